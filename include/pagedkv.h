@@ -74,7 +74,8 @@ typedef enum pa_status {
   PA_ERR_OOM = 8,          /* allocator: not enough free blocks */
   PA_ERR_NO_SEQ = 9,       /* allocator: unknown sequence id */
   PA_ERR_SEQ_EXISTS = 10,  /* allocator: sequence id already in use */
-  PA_ERR_REFCOUNT = 11     /* allocator: a reference count or free list is inconsistent */
+  PA_ERR_REFCOUNT = 11,    /* allocator: a reference count or free list is inconsistent */
+  PA_ERR_BAD_POSITION = 12 /* device: rotary position outside [0, max_position) */
 } pa_status;
 
 typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 } pa_dtype;
@@ -475,6 +476,154 @@ int paged_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
 int kv_cache_append(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens,
                     void* k_cache, void* v_cache, int num_heads, int head_dim, int block_size,
                     int num_blocks, int dtype, int32_t* error_record, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Append with rotary positions, in place of kv_cache_append  [P3b]
+ *
+ * One pass over a step's queries, keys and values: queries and keys are rotated by
+ * their positions, keys and values are written into their slots, and each touched
+ * block's channel-wise key bounds are kept up.  The batch is described as for
+ * paged_attn_prefill: sequence i holds L = seq_lens[i] tokens, the last Q_i =
+ * query_start[i+1] - query_start[i] of which are new; token j of them is row t =
+ * query_start[i] + j of q, k and v, and goes to place L - Q_i + j of the sequence.
+ *
+ * Rotation: pairs j = 0 .. R/2 - 1 of every query and key head, R = rotary_dim, with
+ * c = cos_sin[P][j] and s = cos_sin[P][R/2 + j] for the token's position P on the
+ * pair's axis: (x, y) becomes (x c - y s, y c + x s), in fp32, rounded once to
+ * `dtype`.  A pair is dims (j, j + R/2), or (2 j, 2 j + 1) with `interleaved`.  Dims
+ * R and up pass unchanged.
+ *
+ * Bounds: k_min[b][h][d] and k_max[b][h][d] are the smallest and the largest of
+ * the keys (as stored, so exact) in block b.  If the new tokens of a block include
+ * its row 0 the bounds are theirs alone, otherwise they are combined with the ones
+ * stored; a NaN key makes its channel's bounds NaN.  Bounds so never leave out a row
+ * that was written; after a rollback (rows written anew at a shorter length) they may
+ * be wider than needed until kv_block_bounds computes them afresh.
+ *
+ *   q, k, v       device, [total_tokens][heads][head_dim] in `dtype`, 16-byte aligned;
+ *                 token t of q begins at element t * q_stride (a multiple of 8, at
+ *                 least num_heads * head_dim), so that all three may be slices of one
+ *                 projection's output.  q and q_out may both be NULL (num_heads is
+ *                 then ignored): only keys and values.
+ *   query_start   device int32 [num_seqs + 1], nondecreasing, query_start[num_seqs]
+ *                 <= total_tokens.  Tokens outside every sequence's range are padding:
+ *                 nothing is written for them.
+ *   max_query_len host: >= every Q_i
+ *   k_cache, v_cache  device [num_blocks][num_kv_heads][block_size][head_dim]
+ *   k_min, k_max  device [num_blocks][num_kv_heads][head_dim] in `dtype`, 16-byte
+ *                 aligned; or both NULL.  They have block_copy's layout for
+ *                 block_size 1: copy-on-write copies them with the same pairs.
+ *   head_dim      a multiple of 16, at most 256;  block_size: any
+ *   rope          NULL: no rotation
+ *   q_out         device [total_tokens][num_heads][head_dim], contiguous, 16-byte
+ *                 aligned; may be q itself when q_stride is num_heads * head_dim.
+ * The blocks that hold the new tokens must be private to their sequence (the
+ * allocator's copy-on-write guarantees it).  A sequence whose range is inconsistent
+ * (Q_i > L, range outside the tokens, Q_i > max_query_len, L out of range) is
+ * recorded as PA_ERR_BAD_SEQ_LEN and skipped; where query_start decreases, other
+ * sequences may be left out too.  A block number out of range is recorded as
+ * PA_ERR_BAD_BLOCK (index = sequence) and its tokens' keys and values are skipped.  A
+ * position out of range is recorded as PA_ERR_BAD_POSITION (index = token) and the
+ * nearest one in range is used.
+ * ------------------------------------------------------------------------- */
+#define PA_ROPE_MAX_AXES 4
+typedef struct pa_rope {
+  const float* cos_sin;     /* device [max_position][rotary_dim], 16-byte aligned: the
+                               R/2 cosines, then the R/2 sines of a position */
+  int max_position;         /* >= 1 */
+  int rotary_dim;           /* R: a positive multiple of 16, at most head_dim */
+  int interleaved;
+  int num_axes;             /* 1 .. PA_ROPE_MAX_AXES */
+  const int32_t* positions; /* device [num_axes][total_tokens]; NULL (with one axis):
+                               a token's position is its place in the sequence */
+  const uint8_t* pair_axis; /* HOST [rotary_dim / 2]: the axis of each pair; NULL with
+                               one axis */
+} pa_rope;
+
+int kv_cache_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, const int32_t* query_start,
+                         int total_tokens, int max_query_len, void* k_cache, void* v_cache,
+                         void* k_min, void* k_max, const int32_t* block_tables,
+                         const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads,
+                         int head_dim, int block_size, int max_blocks_per_seq, int num_blocks,
+                         const pa_rope* rope, int dtype, void* q_out, int32_t* error_record,
+                         void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Decode over the blocks that matter to each query
+ *
+ * Long contexts: instead of every token's key, a decode step reads a summary of each
+ * block (its key bounds: two rows instead of block_size), keeps the num_selected
+ * blocks that can hold the largest logits, and attends over their tokens alone.
+ * The four calls below and the append above form the step; each also stands by itself
+ * (lists may come from elsewhere).  Query heads may share key heads: num_heads is a
+ * multiple of num_kv_heads, and query head h reads key head h / (num_heads /
+ * num_kv_heads).  Several query tokens of one sequence are passed as several rows with
+ * the same block table and each its own length.
+ * ------------------------------------------------------------------------- */
+
+/* The key bounds (see kv_cache_append_rope) of the blocks of every sequence that hold
+ * a token at or past first_token[i], computed anew from the rows of tokens < L.
+ *   first_token   NULL (all blocks), or device int32 [num_seqs]; values below 0 mean 0
+ *   head_dim      a multiple of 8;  block_size: any
+ * Sequences that share a block must hold the same rows of it, otherwise the bounds are
+ * those of one of them.  A block number out of range is recorded as PA_ERR_BAD_BLOCK
+ * and skipped; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and skipped. */
+int kv_block_bounds(const void* k_cache, const int32_t* block_tables, const int32_t* seq_lens,
+                    const int32_t* first_token, int num_seqs, int num_kv_heads, int head_dim,
+                    int block_size, int max_blocks_per_seq, int num_blocks, int dtype, void* k_min,
+                    void* k_max, int32_t* error_record, void* stream);
+
+/* scores[i][h][b] = scale * max over the query heads g of key head h of
+ *   sum_d max(q[i][g][d], 0) * k_max[blk][h][d] + min(q[i][g][d], 0) * k_min[blk][h][d]
+ * with blk = block_tables[i][b], for b < ceil(L / block_size): no key of the block has a
+ * larger logit for any of these heads.  -infinity for the other b < max_blocks_per_seq.
+ * A NaN among the products makes the score NaN.
+ *   q             device [num_seqs][num_heads][head_dim] in `dtype`, 16-byte aligned
+ *   head_dim      64, 128 or 256;  scale > 0
+ *   scores        device float [num_seqs][num_kv_heads][max_blocks_per_seq]
+ * A block number out of range is recorded as PA_ERR_BAD_BLOCK and block 0 is read; a
+ * length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
+int paged_block_scores(const void* q, const void* k_min, const void* k_max,
+                       const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                       int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+                       float* scores, int32_t* error_record, void* stream);
+
+/* selected[i][h][0 .. num_selected) = the logical blocks to attend to, in increasing
+ * order, then -1.  With B = ceil(L / block_size) <= num_selected all of them; otherwise
+ * the first sink_blocks, the last recent_blocks, and of the others those with the largest
+ * scores.  Equal scores (0 and -0 are equal): the lower block first.  A NaN counts as
+ * larger than every number, so that a broken block is kept and shows.
+ *   scores        device float [num_seqs][num_kv_heads][max_blocks_per_seq]; entries past a
+ *                 sequence's blocks are not read
+ *   num_selected  >= 1, >= sink_blocks + recent_blocks
+ * A length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
+int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seqs,
+                       int num_kv_heads, int block_size, int max_blocks_per_seq, int num_selected,
+                       int sink_blocks, int recent_blocks, int32_t* selected,
+                       int32_t* error_record, void* stream);
+
+/* out[i][g] = sum_t softmax(scale * <q[i][g], k_t>)_t v_t over the tokens t < L of the
+ * logical blocks listed in selected[i][h], for each query head g of key head h.  A row
+ * without tokens is zero.
+ *   selected      device int32 [num_seqs][num_kv_heads][num_selected], in any order; an
+ *                 entry of -1, or of a block at or past ceil(L / block_size), holds no
+ *                 tokens.  A block listed twice counts twice.  An entry below -1 or at or
+ *                 past max_blocks_per_seq is recorded as PA_ERR_BAD_BLOCK (index = i *
+ *                 num_kv_heads + h) and skipped.
+ *   head_dim      64, 128 or 256;  block_size: a multiple of 16, or 8
+ *   out           device [num_seqs][num_heads][head_dim] in `out_dtype`, 16-byte aligned
+ * Arithmetic as in paged_attn_prefill: logits and sums in fp32, probabilities as a pair of
+ * half-precision numbers.  num_blocks * num_kv_heads * block_size must be < 2^31.
+ * A block-table entry out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and block 0
+ * is read; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
+int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, const int32_t* seq_lens,
+                      const int32_t* selected, int num_selected, int num_seqs, int num_heads,
+                      int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                      int num_blocks, float scale, int dtype, void* out, int out_dtype,
+                      int32_t* error_record, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Copy-on-write block copy  [P3d]

@@ -26,6 +26,11 @@ SOURCES = [
     "paged_attn_shared.cu",
     "paged_prefill.cu",
     "kv_cache_append.cu",
+    "kv_append_rope.cu",
+    "block_bounds.cu",
+    "block_scores.cu",
+    "block_select.cu",
+    "paged_attn_sparse.cu",
     "block_copy.cu",
     "api.cu",
     "allocator.cpp",

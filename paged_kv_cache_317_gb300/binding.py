@@ -28,6 +28,7 @@ STATUS = {
     0: "PA_OK", 1: "PA_ERR_INVALID_ARG", 2: "PA_ERR_UNSUPPORTED", 3: "PA_ERR_CUDA",
     4: "PA_ERR_BAD_BLOCK", 5: "PA_ERR_BAD_SLOT", 6: "PA_ERR_BAD_SEQ_LEN", 7: "PA_ERR_TIMEOUT",
     8: "PA_ERR_OOM", 9: "PA_ERR_NO_SEQ", 10: "PA_ERR_SEQ_EXISTS", 11: "PA_ERR_REFCOUNT",
+    12: "PA_ERR_BAD_POSITION",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -41,6 +42,12 @@ class pa_decode_opts(ctypes.Structure):
                 ("seq_order", c_void_p), ("work_items", c_void_p), ("num_work_items", c_int),
                 ("shared_records", c_void_p), ("num_shared", c_int), ("early_inputs", c_int),
                 ("tail_start", c_void_p), ("counts", c_void_p)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("cos_sin", c_void_p), ("max_position", c_int), ("rotary_dim", c_int),
+                ("interleaved", c_int), ("num_axes", c_int), ("positions", c_void_p),
+                ("pair_axis", ctypes.c_char_p)]
 
 
 ABI_VERSION = 3             # PAGEDKV_VERSION of include/pagedkv.h
@@ -229,6 +236,22 @@ SIGNATURES = {
                                           c_int, c_void_p, c_int, c_int, c_void_p, c_void_p]),
     "kv_cache_append": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int,
                                 c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "kv_cache_append_rope": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                     c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                     c_int, c_int, c_int, ctypes.POINTER(pa_rope), c_int,
+                                     c_void_p, c_void_p, c_void_p]),
+    "kv_block_bounds": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                c_void_p]),
+    "paged_block_scores": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                   c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_int,
+                                   c_void_p, c_void_p, c_void_p]),
+    "paged_block_select": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int,
+                                   c_int, c_void_p, c_void_p, c_void_p]),
+    "paged_attn_sparse": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                  c_float, c_int, c_void_p, c_int, c_void_p, c_void_p]),
     "block_copy": (c_int, [ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p), c_int, c_void_p,
                            c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "pa_decode_partition_tokens": (c_int, [c_void_p, c_int, c_int, c_int, c_int, P_int32]),
@@ -524,6 +547,260 @@ def block_copy(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor
                                    B, _DTYPE[k_caches[0].dtype], _ptr(error_record),
                                    _stream(stream))
     _check(st, "block_copy")
+
+
+# ------------------------------------------- rotated append, block-sparse decode
+def _take(device, dtype, **tensors):
+    """Every tensor (None: skipped) is a contiguous CUDA tensor of the type on the device
+    that launches go to."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on device {t.get_device()}, the current one is {device}")
+
+
+def _shape(name, t, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _half(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16 and t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    return t.dtype
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device.index != device:
+        raise ValueError(f"stream is on device {stream.device.index}, the current one is {device}")
+    return stream.cuda_stream
+
+
+def _new_out(shape, dtype, device, stream):
+    """An output of the stream that the kernel runs on, so that its memory is not handed
+    out again before the kernel is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _tokens(name, t, dtype, device):
+    """[T, heads, head_dim] of which only the step from token to token is free."""
+    if t.dim() != 3 or not t.is_cuda or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a [tokens, heads, head_dim] {dtype} tensor on the "
+                         "current CUDA device")
+    step, (n, heads, dim) = t.stride(0), t.shape
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return step if n > 1 else heads * dim
+
+
+def rope_cos_sin(max_position: int, rotary_dim: int, base: float = 10000.0,
+                 device="cuda") -> torch.Tensor:
+    """The cos_sin table of kv_cache_append_rope, float32 [max_position, rotary_dim], for
+    angles position * base^(-2 j / rotary_dim); computed in 64 bits, so that far positions
+    keep their angles."""
+    rates = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+                            / rotary_dim)
+    angles = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * rates
+    return torch.cat([angles.cos(), angles.sin()], dim=1).float()
+
+
+def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                         query_start: torch.Tensor, max_query_len: int, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, cos_sin: Optional[torch.Tensor],
+                         interleaved: bool = False, positions: Optional[torch.Tensor] = None,
+                         pair_axis: Optional[Sequence[int]] = None,
+                         k_min: Optional[torch.Tensor] = None,
+                         k_max: Optional[torch.Tensor] = None,
+                         q_out: Optional[torch.Tensor] = None,
+                         error_record: Optional[torch.Tensor] = None,
+                         stream=None) -> Optional[torch.Tensor]:
+    """Rotate a step's queries and keys, write keys and values into the paged caches and keep
+    the key bounds of the touched blocks; returns the rotated queries.
+    q [T,Hq,D] (None: keys and values only), k, v [T,H,D], each free to step from token to
+    token (slices of one projection); query_start int32 [N+1]; block_tables int32 [N,MB];
+    seq_lens int32 [N], the new tokens counted; cos_sin float32 [max_position, rotary_dim]
+    (rope_cos_sin; None: no rotation); positions: optional int32 [T], or [axes,T] with
+    pair_axis, the axis of each rotary pair; k_min, k_max: optional bounds [B,H,D]
+    (copy-on-write them with block_copy over [B,H,1,D] views); q_out: optional [T,Hq,D]."""
+    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
+    B, H, bs, D = k_cache.shape
+    N, MB = block_tables.shape
+    T = k.shape[0]
+    _take(device, dtype, k_cache=k_cache, v_cache=v_cache, k_min=k_min, k_max=k_max, q_out=q_out)
+    _take(device, torch.int32, query_start=query_start, block_tables=block_tables,
+          seq_lens=seq_lens, positions=positions, error_record=error_record)
+    _take(device, torch.float32, cos_sin=cos_sin)
+    k_step, v_step = _tokens("k", k, dtype, device), _tokens("v", v, dtype, device)
+    _shape("k", k, (T, H, D))
+    _shape("v", v, (T, H, D))
+    _shape("v_cache", v_cache, (B, H, bs, D))
+    _shape("k_min", k_min, (B, H, D))
+    _shape("k_max", k_max, (B, H, D))
+    _shape("query_start", query_start, (N + 1,))
+    _shape("seq_lens", seq_lens, (N,))
+    if (k_min is None) != (k_max is None):
+        raise ValueError("k_min and k_max must be given together")
+    q_step = Hq = 0
+    if q is not None:
+        q_step, Hq = _tokens("q", q, dtype, device), q.shape[1]
+        _shape("q", q, (T, Hq, D))
+        if q_out is None:
+            q_out = _new_out((T, Hq, D), dtype, q.device, stream)
+        _shape("q_out", q_out, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope = None
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_position, rotary_dim]")
+        axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+        if positions is not None:
+            _shape("positions", positions, (T,) if positions.dim() == 1 else (axes, T))
+        if pair_axis is not None:
+            pair_axis = bytes(pair_axis)
+            if len(pair_axis) != cos_sin.shape[1] // 2:
+                raise ValueError("pair_axis must hold one axis for each of the "
+                                 f"{cos_sin.shape[1] // 2} rotary pairs")
+        elif axes > 1:
+            raise ValueError("positions of several axes need pair_axis")
+        rope = pa_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                       1 if interleaved else 0, axes, _address(positions), pair_axis)
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need cos_sin")
+    _check(load_library().kv_cache_append_rope(
+        _address(q), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step, query_start.data_ptr(),
+        T, int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(), _address(k_min),
+        _address(k_max), block_tables.data_ptr(), seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B,
+        rope, _DTYPE[dtype], _address(q_out), _address(error_record),
+        _raw_stream(stream, device)), "kv_cache_append_rope")
+    return q_out
+
+
+def kv_block_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                    k_min: torch.Tensor, k_max: torch.Tensor,
+                    first_token: Optional[torch.Tensor] = None,
+                    error_record: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Compute k_min, k_max [B,H,D] of every sequence's blocks from k_cache [B,H,bs,D] and the
+    rows below seq_lens; first_token: optional int32 [N], only the blocks that hold a token
+    at or past it."""
+    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
+    B, H, bs, D = k_cache.shape
+    N, MB = block_tables.shape
+    _take(device, dtype, k_cache=k_cache, k_min=k_min, k_max=k_max)
+    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens,
+          first_token=first_token, error_record=error_record)
+    _shape("k_min", k_min, (B, H, D))
+    _shape("k_max", k_max, (B, H, D))
+    _shape("seq_lens", seq_lens, (N,))
+    _shape("first_token", first_token, (N,))
+    _check(load_library().kv_block_bounds(
+        k_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), _address(first_token),
+        N, H, D, bs, MB, B, _DTYPE[dtype], k_min.data_ptr(), k_max.data_ptr(),
+        _address(error_record), _raw_stream(stream, device)), "kv_block_bounds")
+
+
+def paged_block_scores(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor,
+                       block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                       block_size: int, out: Optional[torch.Tensor] = None,
+                       error_record: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """float32 [N,H,MB]: for each block of a sequence the largest logit that one of its keys can
+    have with a query head of key head H, -inf past the sequence's blocks.  q [N,Hq,D], Hq a
+    multiple of H; k_min, k_max [B,H,D]."""
+    device, dtype = torch.cuda.current_device(), _half("k_min", k_min)
+    B, H, D = k_min.shape
+    N, MB = block_tables.shape
+    Hq = q.shape[1]
+    _take(device, dtype, q=q, k_min=k_min, k_max=k_max)
+    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens,
+          error_record=error_record)
+    _shape("q", q, (N, Hq, D))
+    _shape("k_max", k_max, (B, H, D))
+    _shape("seq_lens", seq_lens, (N,))
+    if out is None:
+        out = _new_out((N, H, MB), torch.float32, q.device, stream)
+    else:
+        _take(device, torch.float32, out=out)
+        _shape("out", out, (N, H, MB))
+    _check(load_library().paged_block_scores(
+        q.data_ptr(), k_min.data_ptr(), k_max.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), N, Hq, H, D, int(block_size), MB, B, float(scale), _DTYPE[dtype],
+        out.data_ptr(), _address(error_record), _raw_stream(stream, device)),
+        "paged_block_scores")
+    return out
+
+
+def paged_block_select(scores: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
+                       num_selected: int, sink_blocks: int = 0, recent_blocks: int = 0,
+                       out: Optional[torch.Tensor] = None,
+                       error_record: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """int32 [N,H,num_selected]: the blocks with the largest scores [N,H,MB], the first
+    sink_blocks and the last recent_blocks always among them, in increasing order and then
+    -1."""
+    device = torch.cuda.current_device()
+    N, H, MB = scores.shape
+    _take(device, torch.float32, scores=scores)
+    _take(device, torch.int32, seq_lens=seq_lens, out=out, error_record=error_record)
+    _shape("seq_lens", seq_lens, (N,))
+    if out is None:
+        out = _new_out((N, H, max(int(num_selected), 0)), torch.int32, scores.device, stream)
+    else:
+        _shape("out", out, (N, H, int(num_selected)))
+    _check(load_library().paged_block_select(
+        scores.data_ptr(), seq_lens.data_ptr(), N, H, int(block_size), MB, int(num_selected),
+        int(sink_blocks), int(recent_blocks), out.data_ptr(), _address(error_record),
+        _raw_stream(stream, device)), "paged_block_select")
+    return out
+
+
+def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                      selected: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                      out_dtype=torch.float32, error_record: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Decode attention over the tokens of the listed blocks alone.  q [N,Hq,D]; caches
+    [B,H,bs,D], Hq a multiple of H; block_tables int32 [N,MB]; seq_lens int32 [N]; selected
+    int32 [N,H,S], logical blocks of the sequence, -1 for none (paged_block_select)."""
+    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
+    B, H, bs, D = k_cache.shape
+    N, MB = block_tables.shape
+    Hq, S = q.shape[1], selected.shape[-1]
+    _take(device, dtype, q=q, k_cache=k_cache, v_cache=v_cache)
+    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens, selected=selected,
+          error_record=error_record)
+    _shape("q", q, (N, Hq, D))
+    _shape("v_cache", v_cache, (B, H, bs, D))
+    _shape("seq_lens", seq_lens, (N,))
+    _shape("selected", selected, (N, H, S))
+    if out is None:
+        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
+    else:
+        _take(device, out.dtype, out=out)
+        _shape("out", out, (N, Hq, D))
+    if out.dtype not in _DTYPE:
+        raise ValueError(f"out must be float16, bfloat16 or float32, got {out.dtype}")
+    _check(load_library().paged_attn_sparse(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),
+        _DTYPE[dtype], out.data_ptr(), _DTYPE[out.dtype], _address(error_record),
+        _raw_stream(stream, device)), "paged_attn_sparse")
+    return out
 
 
 # --------------------------------------------------------------- allocator

@@ -1,0 +1,403 @@
+"""paged_block_scores, paged_block_select and paged_attn_sparse on the GPU against the fp64
+oracle, each by itself and as the decode step that they form.
+
+Tolerances (derived, u = 2^-23: a sum on the tensor cores may drop a unit in the last place
+at each addition):
+* scores: 2 D products, exact in fp32, and their sum: (2 D + 4) u times the sum of the terms'
+  magnitudes.
+* attention: a logit is off by at most d = (D + 4) u * max_t scale sum_d |q_d k_td|, so a
+  weight by a factor within e^(+-d); the probabilities enter the product as two half-precision
+  numbers, off by 2^-17 (bf16) of the weight at most; exponentials, n products and sums add
+  (n + 16) u.  Numerator and denominator both, so the result is within twice that of the sum of
+  w_t |v_t|; a half-precision output is rounded by half a step on top.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import bits, half_ulp
+from oracle import sparse as OS
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def B(lib):
+    from paged_kv_cache_317_gb300 import binding
+    return binding
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def make(seed, lens, Hq, H, D, bs, dtype, wide=0):
+    """Caches with NaN in every row without a token, tables (wider than needed by `wide`)."""
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dtype)
+    lens = np.asarray(lens, np.int32)
+    N, nb = len(lens), -(-lens // bs)
+    MB, total = max(1, int(nb.max())) + wide, int(nb.sum()) + 3
+    tables = np.full((N, MB), -1, np.int32)
+    tables[np.arange(MB)[None, :] < nb[:, None]] = rng.permutation(total)[:int(nb.sum())]
+    live = np.zeros((total, bs), bool)
+    for i in range(N):
+        for t in range(int(lens[i])):
+            live[tables[i, t // bs], t % bs] = True
+    dead = torch.from_numpy(~live).cuda()[:, None, :, None]
+    kc, vc = (randn(total, H, bs, D).masked_fill(dead, NAN) for _ in range(2))
+    lo, hi = (torch.full((total, H, D), NAN, dtype=dtype, device="cuda") for _ in range(2))
+    wlo, whi = f64(lo).copy(), f64(hi).copy()
+    OS.block_bounds(f64(kc), tables, lens, wlo, whi)
+    lo, hi = torch.from_numpy(wlo).cuda().to(dtype), torch.from_numpy(whi).cuda().to(dtype)
+    return dict(lens=lens, tables=tables, kc=kc, vc=vc, lo=lo, hi=hi, q=randn(N, Hq, D), bs=bs,
+                scale=float(np.float32(D ** -0.5)), D=D, H=H)
+
+
+def scores_of(B, b, **kw):
+    return B.paged_block_scores(b["q"], b["lo"], b["hi"], dev(b["tables"]), dev(b["lens"]), b["scale"],
+                                b["bs"], **kw)
+
+
+def attend(B, b, selected, **kw):
+    return B.paged_attn_sparse(b["q"], b["kc"], b["vc"], dev(b["tables"]), dev(b["lens"]),
+                               dev(selected), b["scale"], **kw)
+
+
+def check_scores(got, b, dtype=None):
+    want, size = OS.block_scores(f64(b["q"]), f64(b["lo"]), f64(b["hi"]), b["tables"], b["lens"],
+                                 b["scale"], b["bs"])
+    got = f64(got)
+    past = np.isneginf(want)
+    assert np.array_equal(np.isneginf(got), past)
+    err = np.abs(got[~past] - want[~past])
+    assert (err <= (2 * b["D"] + 4) * U * size[~past] + 1e-30).all(), err.max()
+
+
+def check_attention(out, b, selected, kc=None, vc=None):
+    """NaN rows are cut by the oracle; a NaN in the result is an error here."""
+    ref, spread, reach = OS.sparse_attention(f64(b["q"]), f64(b["kc"] if kc is None else kc),
+                                             f64(b["vc"] if vc is None else vc), b["tables"],
+                                             b["lens"], selected, b["scale"])
+    n = selected.shape[-1] * b["bs"]
+    d = (b["D"] + 4) * U * reach[..., None]
+    split = 2.0 ** -17
+    bound = 2 * (np.expm1(2 * d) + split + (n + 16) * U) * spread
+    if out.dtype != torch.float32:
+        bound = bound + half_ulp(np.abs(ref) + bound, out.dtype)
+    err = np.abs(f64(out) - ref)
+    assert (err <= bound).all(), (np.nanmax(err), bound.max(), np.isnan(err).sum())
+
+
+def lists(rng, b, keep, spoil=True):
+    """Distinct blocks in any order with -1 (and blocks past the end) between them."""
+    N, H, MB = len(b["lens"]), b["H"], b["tables"].shape[1]
+    out = np.full((N, H, keep), -1, np.int32)
+    for i in range(N):
+        held = -(-int(b["lens"][i]) // b["bs"])
+        for h in range(H):
+            n = min(held, rng.integers(0, keep + 1)) if spoil else min(held, keep)
+            at = rng.choice(keep, n, replace=False)
+            out[i, h, at] = rng.choice(held, n, replace=False) if n else 0
+            if spoil and held < MB and n < keep:
+                out[i, h, np.flatnonzero(out[i, h] == -1)[0]] = rng.integers(held, MB)
+    return out
+
+
+SHAPES = [
+    # lens, Hq, H, D, bs
+    ([1], 1, 1, 64, 16),
+    ([17, 0, 33, 16, 200], 8, 8, 128, 16),
+    ([40, 7, 1, 100, 31], 8, 2, 128, 8),
+    ([333, 64], 16, 1, 64, 32),
+    ([65, 129, 2], 15, 3, 256, 16),
+    ([130], 32, 1, 128, 48),
+    ([1000, 3], 14, 2, 128, 64),
+    ([50, 90], 80, 2, 256, 8),
+    ([90, 47], 34, 2, 64, 16),
+]
+IDS = ["x".join(map(str, s[1:])) for s in SHAPES]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_scores_match_the_oracle(B, shape, dtype):
+    b = make(1, *shape, dtype, wide=2)
+    rec = B.new_error_record()
+    check_scores(scores_of(B, b, error_record=rec), b)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("keep", [1, 3, 40])
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_attention_matches_the_oracle(B, shape, keep, dtype):
+    b = make(2, *shape, dtype, wide=2)
+    sel = lists(np.random.default_rng(keep), b, keep)
+    rec = B.new_error_record()
+    for out_dtype in (torch.float32, dtype):
+        check_attention(attend(B, b, sel, out_dtype=out_dtype, error_record=rec), b, sel)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("seqs,keep,H,G", [(1, 300, 1, 4), (2, 600, 2, 1), (1, 1500, 1, 8), (70, 33, 2, 2)])
+def test_long_lists(B, seqs, keep, H, G):
+    rng = np.random.default_rng(keep)
+    lens = rng.integers(keep * 16, keep * 18, seqs)
+    b = make(3, lens, H * G, H, 128, 16, torch.bfloat16)
+    sel = lists(rng, b, keep, spoil=False)
+    check_attention(attend(B, b, sel), b, sel)
+
+
+def test_all_blocks_listed_equals_the_dense_decode(B):
+    b = make(4, [130, 16, 77, 1], 4, 4, 128, 16, torch.bfloat16)
+    every = np.broadcast_to(np.arange(9, dtype=np.int32), (4, 4, 9))
+    dense = B.paged_attn_decode(b["q"], b["kc"], b["vc"], dev(b["tables"]), dev(b["lens"]), b["scale"])
+    out = attend(B, b, every)
+    check_attention(out, b, every)
+    assert float((out - dense).abs().max()) < 2e-3
+
+
+def test_rows_without_tokens_are_zero(B):
+    b = make(5, [0, 20, 40], 4, 2, 64, 16, torch.float16, wide=3)
+    sel = np.array([[[0, 1]] * 2, [[-1, -1], [4, 2]], [[1, -1], [-1, -1]]], np.int32)
+    rec = B.new_error_record()
+    out = attend(B, b, sel, error_record=rec)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    assert (out[:2] == 0).all() and (out[2, 2:] == 0).all() and (out[2, :2] != 0).any()
+    none = np.zeros((3, 2, 0), np.int32)
+    assert (attend(B, b, none) == 0).all()
+
+
+def test_a_block_listed_twice_counts_twice(B):
+    b = make(6, [40], 2, 1, 64, 16, torch.float16)
+    sel = np.array([[[1, 2, 1]]], np.int32)
+    check_attention(attend(B, b, sel), b, sel)
+
+
+def test_infinite_keys_in_listed_blocks(B):
+    b = make(7, [40], 1, 1, 64, 16, torch.bfloat16)
+    b["q"].abs_()
+    sel = np.array([[[0, 1, 2]]], np.int32)
+    b["kc"][int(b["tables"][0, 0])] = -INF          # a whole block of logits -inf: weight 0
+    ref = np.array([[[1, 2, -1]]], np.int32)
+    check_attention(attend(B, b, sel), b, ref)
+    b["kc"][:] = -INF                               # every logit -inf: no softmax
+    assert torch.isnan(attend(B, b, sel)).all()
+    assert (scores_of(B, make(7, [0], 1, 1, 64, 16, torch.bfloat16)) == -INF).all()
+
+
+def test_nan_bounds_make_nan_scores_that_are_kept(B):
+    b = make(8, [100], 4, 2, 128, 16, torch.float16)
+    b["lo"][int(b["tables"][0, 3]), 1, 5] = NAN
+    s = scores_of(B, b)
+    assert torch.isnan(s[0, 1, 3]) and int(torch.isnan(s).sum()) == 1
+    assert 3 in B.paged_block_select(s, dev(b["lens"]), 16, 1)[0, 1].tolist()
+
+
+def test_bad_entries_are_recorded(B):
+    b = make(9, [40, 70], 4, 2, 64, 16, torch.float16)
+    rec = B.new_error_record()
+    sel = np.array([[[0, 5], [0, 1]], [[-2, 1], [0, 1]]], np.int32)
+    out = attend(B, b, sel, error_record=rec)
+    got = B.pa_error_read(rec)
+    assert got[0] == 4 and got[1] == 2 and (got[2], got[3]) in ((0, 5), (2, -2))
+    check_attention(out, b, np.array([[[0, -1], [0, 1]], [[-1, 1], [0, 1]]]))
+    B.pa_error_clear(rec)
+    good = b["tables"].copy()
+    b["tables"][1, 0] = len(b["kc"])
+    b["tables"][0, 0] = 0                            # block 0 read in place of a bad one
+    sel = np.zeros((2, 2, 1), np.int32)
+    clean = torch.where(torch.isnan(b["kc"]), 0, b["kc"]), torch.where(torch.isnan(b["vc"]), 0, b["vc"])
+    bad = dict(b, kc=clean[0], vc=clean[1])
+    out = attend(B, bad, sel, error_record=rec)
+    assert B.pa_error_read(rec) == [4, 1, 1, len(b["kc"])]
+    bad["tables"] = np.where(b["tables"] == len(b["kc"]), 0, b["tables"])
+    check_attention(out, bad, sel)
+    B.pa_error_clear(rec)
+    lo, hi = torch.nan_to_num(b["lo"]), torch.nan_to_num(b["hi"])
+    s = scores_of(B, dict(b, lo=lo, hi=hi), error_record=rec)
+    assert B.pa_error_read(rec) == [4, 1, 1, len(b["kc"])]
+    check_scores(s, dict(bad, lo=lo, hi=hi))
+    # lengths out of range are clamped
+    b["tables"], b["lens"] = good, np.array([-1, 81], np.int32)
+    for call in (lambda: scores_of(B, b, error_record=rec), lambda: attend(B, b, sel, error_record=rec),
+                 lambda: B.paged_block_select(torch.zeros(2, 2, 5, device="cuda"), dev(b["lens"]), 16, 2,
+                                              error_record=rec)):
+        B.pa_error_clear(rec)
+        call()
+        got = B.pa_error_read(rec)
+        assert got[0] == 6 and got[1] == 2 and (got[2], got[3]) in ((0, -1), (1, 81))
+
+
+# ------------------------------------------------------------------------------ select
+@pytest.mark.parametrize("width,lens,keep,sink,recent", [
+    (1, [1, 0], 1, 0, 0), (7, [7, 3, 5], 3, 1, 1), (40, [40, 33, 2], 4, 2, 2),
+    (300, [300, 257, 256, 1], 50, 0, 3), (1031, [1031, 800], 64, 4, 8),
+    (2100, [2100, 2049], 1000, 1, 1), (5000, [4999], 1, 0, 1), (9001, [9001, 4097], 300, 0, 0),
+    (20000, [20000, 19999, 7], 2000, 1, 4)])
+@pytest.mark.parametrize("kind", ["normal", "ties", "odd"])
+def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
+    rng = np.random.default_rng(width)
+    s = rng.standard_normal((len(lens), 3, width)).astype(np.float32)
+    if kind == "ties":
+        s = np.round(s)                              # also -0 and 0
+    elif kind == "odd":
+        s = np.round(s * 4)
+        for v in (NAN, -NAN, INF, -INF, 1e-42, -1e-42, -0.0):
+            s[rng.random(s.shape) < 0.05] = v
+        s[0, 0] = 2.5
+    rec = B.new_error_record()
+    got = B.paged_block_select(torch.from_numpy(s).cuda(), dev(lens), 1, keep, sink, recent,
+                               error_record=rec)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, keep, sink, recent))
+
+
+def test_select_reads_nothing_past_a_sequence(B):
+    s = torch.full((1, 1, 50), NAN, device="cuda")
+    s[..., :30] = torch.arange(30, device="cuda").flip(0).float()
+    assert B.paged_block_select(s, dev([30 * 8 - 7]), 8, 4)[0, 0].tolist() == [0, 1, 2, 3]
+
+
+# ---------------------------------------------------------------------------- the step
+def _step(B, b, st, keep, q, k, v, start, most, rec, out=None):
+    """Append with rotation, score, select, attend."""
+    turned = B.kv_cache_append_rope(q, k, v, start, most, b["kc"], b["vc"], st["tables"], st["lens"],
+                                    st["cos_sin"], k_min=b["lo"], k_max=b["hi"], q_out=st.get("q_out"),
+                                    error_record=rec)
+    s = B.paged_block_scores(turned, b["lo"], b["hi"], st["tables"], st["lens"], b["scale"], b["bs"],
+                             out=st.get("scores"), error_record=rec)
+    sel = B.paged_block_select(s, st["lens"], b["bs"], keep, 1, 2, out=st.get("sel"), error_record=rec)
+    return turned, s, sel, B.paged_attn_sparse(turned, b["kc"], b["vc"], st["tables"], st["lens"], sel,
+                                               b["scale"], out=out, out_dtype=q.dtype, error_record=rec)
+
+
+@pytest.mark.parametrize("dtype,Hq,H,D,bs", [(torch.bfloat16, 8, 2, 128, 16), (torch.float16, 4, 4, 64, 8)])
+def test_prompts_then_decode_steps(B, dtype, Hq, H, D, bs):
+    """Prompts through the rotated append and the dense prefill; then decode steps whose lists
+    agree with the scores and whose outputs agree with the oracle; the dense decode over the
+    same caches where every block fits the list."""
+    prompts, steps, keep = [150, 33, 7], 20, 5
+    N, T = len(prompts), sum(prompts)
+    final = np.array(prompts, np.int32) + steps
+    b = make(20, final, Hq, H, D, bs, dtype)
+    b["kc"].fill_(NAN), b["vc"].fill_(NAN), b["lo"].fill_(NAN), b["hi"].fill_(NAN)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dtype)
+    st = {"tables": dev(b["tables"]), "lens": dev(prompts), "cos_sin": B.rope_cos_sin(400, D)}
+    start = np.concatenate([[0], np.cumsum(prompts)])
+    rec = B.new_error_record()
+    q, k, v = randn(T, Hq, D), randn(T, H, D), randn(T, H, D)
+    turned = B.kv_cache_append_rope(q, k, v, dev(start), max(prompts), b["kc"], b["vc"], st["tables"],
+                                    st["lens"], st["cos_sin"], k_min=b["lo"], k_max=b["hi"],
+                                    error_record=rec)
+    if Hq == H:
+        pre = B.paged_attn_prefill(turned, dev(start), max(prompts), b["kc"], b["vc"], st["tables"],
+                                   st["lens"], b["scale"], error_record=rec)
+        assert torch.isfinite(pre).all()
+    lens = np.array(prompts, np.int32)
+    for step in range(steps):
+        lens = lens + 1
+        st["lens"] = dev(lens)
+        turned, s, sel, out = _step(B, b, st, keep, randn(N, Hq, D), randn(N, H, D), randn(N, H, D),
+                                    dev(np.arange(N + 1)), 1, rec)
+        now = dict(b, lens=lens, q=turned)
+        if step % 6 == 0 or step == steps - 1:
+            check_scores(s, now)
+            sel_h = sel.cpu().numpy()
+            assert np.array_equal(sel_h, OS.block_select(s.cpu().numpy(), lens, bs, keep, 1, 2))
+            check_attention(out, now, sel_h)
+            lo, hi = torch.empty_like(b["lo"]), torch.empty_like(b["hi"])
+            B.kv_block_bounds(b["kc"], st["tables"], st["lens"], lo, hi, error_record=rec)
+            held = sorted({int(x) for i in range(N) for x in b["tables"][i, :-(-int(lens[i]) // bs)]})
+            assert torch.equal(lo[held], b["lo"][held]) and torch.equal(hi[held], b["hi"][held])
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+
+
+def test_two_captured_steps_replay_side_by_side(B):
+    """Two steps captured into graphs of their own share no scratch: replayed on two streams at
+    once, each gives what it gives alone, with lengths and inputs written into its buffers."""
+    graphs = []
+    for seed in (30, 31):
+        b = make(seed, [200, 90, 33], 8, 2, 128, 16, torch.bfloat16)
+        st = {"tables": dev(b["tables"]), "lens": dev(b["lens"]), "cos_sin": B.rope_cos_sin(256, 128)}
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+        q, k, v = randn(3, 8, 128), randn(3, 2, 128), randn(3, 2, 128)
+        start, rec = dev(np.arange(4)), B.new_error_record()
+        want = _step(B, b, st, 4, q, k, v, start, 1, rec)
+        st["q_out"], st["scores"], st["sel"] = (torch.empty_like(x) for x in want[:3])
+        out = torch.empty_like(want[3])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _step(B, b, st, 4, q, k, v, start, 1, rec, out=out)
+        graphs.append((g, want, out, st, rec, b, q, k, v, start))   # a graph keeps no tensor alive
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, *_), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for g, want, out, st, rec, *_ in graphs:
+        assert torch.equal(out, want[3]) and torch.equal(st["sel"], want[2])
+        assert torch.equal(st["scores"], want[1]) and B.pa_error_read(rec) == [0, 0, 0, 0]
+
+
+def test_the_same_call_gives_the_same_bits(B):
+    b = make(40, np.random.default_rng(0).integers(1, 3000, 20), 16, 2, 128, 16, torch.bfloat16)
+    first = None
+    for _ in range(5):
+        s = scores_of(B, b)
+        sel = B.paged_block_select(s, dev(b["lens"]), 16, 64, 1, 2)
+        out = B.paged_attn_sparse(b["q"], b["kc"], b["vc"], dev(b["tables"]), dev(b["lens"]), sel, b["scale"])
+        now = (bits(s.to(torch.bfloat16)), sel.cpu().numpy(), out.cpu().numpy())
+        if first is not None:
+            assert all(np.array_equal(x, y) for x, y in zip(first, now))
+        first = now
+
+
+def test_a_given_stream_and_offsets_past_32_bits(B):
+    """A cache of over 2^32 elements: blocks at its far end, on another stream."""
+    H, D, bs, nb = 2, 128, 16, (1 << 20) + 64
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    kc = torch.zeros((nb, H, bs, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    lo, hi = (torch.zeros((nb, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    tables = np.array([[nb - 1, nb - 40, 3]], np.int32)
+    for t in tables[0]:
+        for c in (kc, vc):
+            c[int(t)] = torch.randn((H, bs, D), generator=gen, device="cuda").to(torch.bfloat16)
+    q = torch.randn((1, 4, D), generator=gen, device="cuda").to(torch.bfloat16)
+    lens = np.array([41], np.int32)
+    k = torch.randn((1, H, D), generator=gen, device="cuda").to(torch.bfloat16)
+    lens_d, tables_d, start = dev(lens), dev(tables), dev([0, 1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.kv_block_bounds(kc, tables_d, lens_d, lo, hi, stream=side)
+    B.kv_cache_append_rope(None, k, k, start, 1, kc, vc, tables_d, lens_d, None, k_min=lo, k_max=hi,
+                           stream=side)
+    s = B.paged_block_scores(q, lo, hi, tables_d, lens_d, 0.1, bs, stream=side)
+    sel = B.paged_block_select(s, lens_d, bs, 3, stream=side)
+    out = B.paged_attn_sparse(q, kc, vc, tables_d, lens_d, sel, 0.1, stream=side)
+    side.synchronize()
+    pick = [int(t) for t in tables[0]]
+    small = dict(tables=np.array([[0, 1, 2]]), lens=lens, kc=kc[pick], vc=vc[pick], lo=lo[pick], hi=hi[pick],
+                 q=q, bs=bs, scale=float(np.float32(0.1)), D=D, H=H)
+    assert sel.tolist() == [[[0, 1, 2], [0, 1, 2]]]
+    assert torch.equal(small["kc"][2, :, 8], k[0])
+    check_scores(s, small)
+    check_attention(out, small, sel.cpu().numpy())
