@@ -26,13 +26,6 @@ struct ScoreParams {
   float scale;
 };
 
-// The larger of two, NaN if either is.
-__device__ __forceinline__ float max_nan(float x, float y) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-  return r;
-}
-
 template <class Tag, int D>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
   using T = typename Tag::T;

@@ -177,6 +177,13 @@ __device__ __forceinline__ void store_out(void* out, size_t elem, const float* v
   }
 }
 
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 // Host-side helpers -------------------------------------------------------
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

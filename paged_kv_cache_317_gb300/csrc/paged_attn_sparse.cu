@@ -1,114 +1,513 @@
 // Decode attention over listed blocks.
 //
-// One warp takes one (sequence, query head): the lanes share the channels, and the tokens
-// of the listed blocks go by one at a time with a running maximum and sum.
+// A row is one (sequence, key head) with its list and the query heads that share the key
+// head.  The tokens of the listed blocks are cut into chunks of 16; a cluster of thread
+// blocks takes a row, and the chunks go round its warps, so that lists that end early
+// still load every warp alike.
+//  * Each warp runs a pipeline of its own: its lanes look up the next 32 of its chunks
+//    (list entry, block table, length) at once, one lane starts the K and V copies of a
+//    chunk (a 3-D TMA box of 16 rows x D channels in 128-byte swizzled columns) into the
+//    warp's ring of stages, and the warp waits on the stage's barrier.  No warp waits for
+//    another before the end.
+//  * Per chunk, on mma.sync m16n8k16 with the 16 tokens as the rows and the query heads as
+//    the columns: S^T = K.Q^T in fp32, the running maximum and sum of each column in log2
+//    units, O^T += V^T.P^T with P as a high and a low half-precision number.  Up to 8 query
+//    heads cost one product, up to 16 two; K and V are read once for all of them.
+//  * At the end the warps' (m, l, O) are joined in shared memory, and those of the cluster's
+//    blocks over distributed shared memory, in a fixed order: no workspace, no second
+//    kernel, the same bits on every run.
+// Two operations per cached byte and query head: bound by HBM.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
+#include "mma.cuh"
+#include "tma.cuh"
 
 namespace pagedkv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kChunk = 16;       // tokens per stage
+constexpr int kWarps = 4;        // warps per thread block
+constexpr int kMaxStages = 8;
+constexpr int kMaxCluster = 8;
+constexpr int kAlign = 1024;     // a swizzled box must start on 1024 bytes
+constexpr int kHeader = 1024;    // barriers and the chunks' row counts
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct SparseParams {
   const void* q;
-  const void* k_cache;
-  const void* v_cache;
   const int32_t* block_tables;
   const int32_t* seq_lens;
   const int32_t* selected;
   void* out;
   int32_t* err;
-  int num_selected, num_seqs, num_heads, num_kv_heads, block_size, max_blocks, num_blocks;
-  int out_dtype;
-  float scale;
+  int num_selected, num_heads, num_kv_heads, block_size, max_blocks, num_blocks;
+  int group, tiles;     // query heads per key head; tiles of 8 NT of them
+  int out_dtype, stages;
+  float qscale;         // scale * log2(e)
 };
 
-template <class Tag, int D>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_sparse_kernel(const SparseParams p) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of another block of the cluster, at the same address as `addr` here.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
+// Partials of a column: m = running maximum (NaN once a logit was), l = sum of 2^(s - m);
+// m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity).  The weight
+// of a partial in a join whose maximum is M:
+__device__ __forceinline__ float weight_of(float m, float M) {
+  return m == -INFINITY ? 0.f : exp2f(m - M);
+}
+// 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
+__device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
+  if (M == -INFINITY) return tokens ? NAN : 0.f;
+  return 1.f / l;
+}
+
+template <int D>
+struct Geo {
+  static constexpr int kTileBytes = kChunk * D * 2;  // one chunk of K or V
+  static constexpr int kPitch = D + 4;               // floats per column of the joined O
+};
+
+template <class Tag, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32)
+    paged_attn_sparse_kernel(const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_v, const SparseParams p) {
+  using Gm = Geo<D>;
   using T = typename Tag::T;
-  constexpr int DPL = D / 32;
+  constexpr int kCols = 8 * NT;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.num_seqs) * p.num_heads) return;
-  const int seq = static_cast<int>(row / p.num_heads), g = static_cast<int>(row % p.num_heads);
-  const int group = p.num_heads / p.num_kv_heads, head = g / group;
-  const bool reports = lane == 0 && g % group == 0;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int S = p.stages;
+  const int row = blockIdx.x / ranks;  // (sequence, key head, tile)
+  const int tile = row % p.tiles;
+  const int sh = row / p.tiles;        // sequence * key heads + key head
+  const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
+  const int cols = min(kCols, p.group - tile * kCols);
+  const size_t q0 = static_cast<size_t>(seq) * p.num_heads + head * p.group + tile * kCols;
+
   int L = __ldg(p.seq_lens + seq);
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
-    if (lane == 0 && g == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
+    if (threadIdx.x == 0 && rank == 0 && head == 0 && tile == 0)
+      report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     L = min(max(L, 0), cap);
   }
-  float q[DPL], acc[DPL];
-#pragma unroll
-  for (int j = 0; j < DPL; ++j) {
-    q[j] = static_cast<float>(static_cast<const T*>(p.q)[row * D + lane * DPL + j]);
-    acc[j] = 0.f;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem) + warp * kMaxStages;
+  int* rows_of = reinterpret_cast<int*>(smem + kWarps * kMaxStages * 8) + warp * kMaxStages;
+  const uint32_t base = smem_addr(smem);
+  uint8_t* ring0 = smem + (((base + kHeader + kAlign - 1) & ~uint32_t(kAlign - 1)) - base);
+  uint8_t* ring = ring0 + static_cast<size_t>(warp) * S * 2 * Gm::kTileBytes;
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
   }
-  float m = -INFINITY, l = 0.f;
-  bool some = false;
-  const size_t list = (static_cast<size_t>(seq) * p.num_kv_heads + head) * p.num_selected;
-  for (int e = 0; e < p.num_selected; ++e) {
-    const int b = __ldg(p.selected + list + e);
+  __syncwarp();
+
+  // ------------------------------------------------------- the warp's chunks
+  // Chunk c of a row is 16 tokens of list entry c / (bs / 16), or with 8-token blocks
+  // entries 2 c and 2 c + 1.  This warp takes c = me, me + all, ...; its lanes look up 32 of
+  // them at a time and `mask` names those with tokens that are not issued yet.
+  const int me = rank * kWarps + warp, all = ranks * kWarps;
+  const bool small = p.block_size == 8;
+  const int sub = small ? 1 : p.block_size / kChunk;
+  const long long chunks = small ? (p.num_selected + 1) / 2
+                                 : static_cast<long long>(p.num_selected) * sub;
+  const int32_t* list = p.selected + static_cast<size_t>(sh) * p.num_selected;
+  const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
+  // Row coordinate of (entry e, its 16-token part) in the cache seen as rows of D, and the
+  // number of tokens there (0: none).
+  auto look_up = [&](int e, int part, int height, int& y) -> int {
+    const int b = __ldg(list + e);
     if (b < -1 || b >= p.max_blocks) {
-      if (reports) report_error(p.err, PA_ERR_BAD_BLOCK, static_cast<long long>(seq) * p.num_kv_heads + head, b);
-      continue;
+      if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, sh, b);
+      return 0;
     }
-    if (b < 0) continue;
-    const long long t0 = static_cast<long long>(b) * p.block_size;
-    const int rows = static_cast<int>(min(static_cast<long long>(p.block_size), L - t0));
-    if (rows <= 0) continue;
-    some = true;
-    int blk = __ldg(p.block_tables + static_cast<size_t>(seq) * p.max_blocks + b);
+    if (b < 0) return 0;
+    const int rows = min(height, L - b * p.block_size - part * kChunk);
+    if (rows <= 0) return 0;
+    int blk = __ldg(table + b);
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-      if (reports && head == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
+      if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       blk = 0;
     }
-    const size_t at = (static_cast<size_t>(blk) * p.num_kv_heads + head) * p.block_size * D + lane * DPL;
-    for (int r = 0; r < rows; ++r) {
-      const T* k = static_cast<const T*>(p.k_cache) + at + static_cast<size_t>(r) * D;
-      const T* v = static_cast<const T*>(p.v_cache) + at + static_cast<size_t>(r) * D;
-      float s = 0.f;
+    y = (blk * p.num_kv_heads + head) * p.block_size + part * kChunk;
+    return rows;
+  };
+  long long next = me;
+  unsigned mask = 0;
+  int y_lo = 0, y_hi = 0, rows_lo = 0, rows_hi = 0;
+  auto refill = [&]() {
+    while (mask == 0 && next < chunks) {
+      const long long c = next + static_cast<long long>(lane) * all;
+      rows_lo = rows_hi = 0;
+      if (c < chunks) {
+        if (small) {
+          const int e = static_cast<int>(2 * c);
+          rows_lo = look_up(e, 0, 8, y_lo);
+          if (e + 1 < p.num_selected) rows_hi = look_up(e + 1, 0, 8, y_hi);
+        } else {
+          const int rows = look_up(static_cast<int>(c / sub), static_cast<int>(c % sub), 16, y_lo);
+          rows_lo = min(rows, 8);
+          rows_hi = rows - rows_lo;
+        }
+      }
+      mask = __ballot_sync(kFullMask, rows_lo + rows_hi > 0);
+      next += 32ll * all;
+    }
+  };
+  // Starts the copies of the next chunk into a stage; false when there is none.
+  auto issue = [&](int s) -> bool {
+    if (mask == 0) refill();
+    if (mask == 0) return false;
+    const int j = __ffs(mask) - 1;
+    mask &= mask - 1;
+    const int ylo = __shfl_sync(kFullMask, y_lo, j), yhi = __shfl_sync(kFullMask, y_hi, j);
+    const int rlo = __shfl_sync(kFullMask, rows_lo, j), rhi = __shfl_sync(kFullMask, rows_hi, j);
+    if (lane == 0) {
+      rows_of[s] = rlo | (rhi << 8);
+      uint8_t* dst = ring + s * 2 * Gm::kTileBytes;
+      if (!small) {
+        mbar_arrive_expect_tx(&full[s], 2 * Gm::kTileBytes);
+        tma_load_3d(dst, &tm_k, 0, ylo, 0, &full[s]);
+        tma_load_3d(dst + Gm::kTileBytes, &tm_v, 0, ylo, 0, &full[s]);
+      } else {
+        constexpr int kHalf = Gm::kTileBytes / 2;
+        mbar_arrive_expect_tx(&full[s], (rlo > 0 ? 2 * kHalf : 0) + (rhi > 0 ? 2 * kHalf : 0));
+        if (rlo > 0) {
+          tma_load_3d(dst, &tm_k, 0, ylo, 0, &full[s]);
+          tma_load_3d(dst + Gm::kTileBytes, &tm_v, 0, ylo, 0, &full[s]);
+        }
+        if (rhi > 0) {
+          tma_load_3d(dst + kHalf, &tm_k, 0, yhi, 0, &full[s]);
+          tma_load_3d(dst + Gm::kTileBytes + kHalf, &tm_v, 0, yhi, 0, &full[s]);
+        }
+      }
+    }
+    return true;
+  };
+  int issued = 0, done = 0;
+  while (issued < S && issue(issued)) ++issued;
+
+  // -------------------------------------------------------------- the queries
+  // Q^T as B fragments: column g of an 8-column tile is query head g of the tile.
+  const int g = lane >> 2, tq = lane & 3;
+  uint32_t qf[NT][D / 16][2];
 #pragma unroll
-      for (int j = 0; j < DPL; ++j) s = fmaf(q[j], static_cast<float>(k[j]), s);
+  for (int t = 0; t < NT; ++t) {
+    const bool have = t * 8 + g < cols;
+    const T* src = static_cast<const T*>(p.q) + (q0 + (have ? t * 8 + g : 0)) * D + 2 * tq;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(kFullMask, s, off);
-      s *= p.scale;
-      const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = expf(m - base), w = expf(s - base);
-      l = fmaf(l, alpha, w);
-#pragma unroll
-      for (int j = 0; j < DPL; ++j) acc[j] = fmaf(acc[j], alpha, w * static_cast<float>(v[j]));
-      m = mn;
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qf[t][kk][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16)) : 0u;
+      qf[t][kk][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8)) : 0u;
     }
   }
-  const float inv = some ? 1.f / l : 0.f;
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
 #pragma unroll
-  for (int j = 0; j < DPL; ++j) acc[j] *= inv;
-  store_out<DPL>(p.out, row * D + lane * DPL, acc, p.out_dtype);
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int dd = 0; dd < D / 16; ++dd) o[t][dd][0] = o[t][dd][1] = o[t][dd][2] = o[t][dd][3] = 0.f;
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+  }
+
+  // ldmatrix rows of this lane.  A tile is [D / 64 column groups][16 rows][128 bytes], with
+  // 8-token blocks two of [D / 64][8][128]; token t's 16-byte piece c of a column group sits
+  // at c ^ (t & 7).  K (A operand): matrices (tokens 0-7, d + 0..7), (8-15, d + 0..7), (0-7,
+  // d + 8..15), (8-15, d + 8..15).  V (A operand of V^T, transposed): (tokens 0-7, d + 0..7),
+  // (0-7, d + 8..15), (8-15, d + 0..7), (8-15, d + 8..15).
+  const int mi = lane >> 3, r8 = lane & 7;
+  const uint32_t group_bytes = small ? 1024u : 2048u;
+  const uint32_t half_bytes = small ? Gm::kTileBytes / 2 : 1024u;
+  const uint32_t k_row = (mi & 1) * half_bytes + r8 * 128, v_row = (mi >> 1) * half_bytes + r8 * 128;
+  const int k_half = mi >> 1, v_half = mi & 1;
+  const uint32_t ring_addr = smem_addr(ring);
+
+  bool aborted = false;
+  while (done < issued) {
+    const int s = done % S;
+    if (!__all_sync(kFullMask, mbar_wait_bounded(&full[s], (done / S) & 1))) {
+      if (lane == 0) report_error(p.err, PA_ERR_TIMEOUT, seq, done);
+      aborted = true;
+      break;
+    }
+    const int rows = rows_of[s];
+    const int rlo = rows & 255, rhi = rows >> 8;
+    const uint32_t kt = ring_addr + s * 2 * Gm::kTileBytes, vt = kt + Gm::kTileBytes;
+
+    float sc[NT][4];  // (token g, column 2 tq), (g, 2 tq + 1), (g + 8, ...)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t a[4];
+      const int c = ((kk & 3) << 1) | k_half;
+      ldsm_x4(kt + (kk >> 2) * group_bytes + k_row + ((c ^ r8) << 4), a);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma(sc[t], a, qf[t][kk][0], qf[t][kk][1], Tag{});
+    }
+    const bool partial = rlo + rhi < kChunk;
+    uint32_t bh[NT][2], bl[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[t][e] *= p.qscale;
+      if (partial) {
+        if (g >= rlo) sc[t][0] = sc[t][1] = -INFINITY;
+        if (g >= rhi) sc[t][2] = sc[t][3] = -INFINITY;
+      }
+      float c0 = max_nan(sc[t][0], sc[t][2]), c1 = max_nan(sc[t][1], sc[t][3]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        c0 = max_nan(c0, __shfl_xor_sync(kFullMask, c0, off));
+        c1 = max_nan(c1, __shfl_xor_sync(kFullMask, c1, off));
+      }
+      const float n0 = max_nan(m[t][0], c0), n1 = max_nan(m[t][1], c1);
+      // all -infinity so far: any finite base gives them the weight 0
+      const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+      const float a0 = exp2f(m[t][0] - b0), a1 = exp2f(m[t][1] - b1);
+      const float p0 = exp2f(sc[t][0] - b0), p1 = exp2f(sc[t][1] - b1);
+      const float p2 = exp2f(sc[t][2] - b0), p3 = exp2f(sc[t][3] - b1);
+      l[t][0] = fmaf(l[t][0], a0, p0 + p2);
+      l[t][1] = fmaf(l[t][1], a1, p1 + p3);
+      if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {
+#pragma unroll
+        for (int dd = 0; dd < D / 16; ++dd) {
+          o[t][dd][0] *= a0;
+          o[t][dd][1] *= a1;
+          o[t][dd][2] *= a0;
+          o[t][dd][3] *= a1;
+        }
+      }
+      m[t][0] = n0;
+      m[t][1] = n1;
+      uint32_t hi_a, lo_a, hi_b, lo_b;
+      split2(p0, p1, hi_a, lo_a, Tag{});
+      split2(p2, p3, hi_b, lo_b, Tag{});
+      bh[t][0] = movmatrix_trans(hi_a);
+      bh[t][1] = movmatrix_trans(hi_b);
+      bl[t][0] = movmatrix_trans(lo_a);
+      bl[t][1] = movmatrix_trans(lo_b);
+    }
+    // rows without a token may hold anything, NaN too: 0 in the product
+    uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
+    if (partial) {
+      keep_lo = (2 * tq < rlo ? 0xffffu : 0u) | (2 * tq + 1 < rlo ? 0xffff0000u : 0u);
+      keep_hi = (2 * tq < rhi ? 0xffffu : 0u) | (2 * tq + 1 < rhi ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int dd = 0; dd < D / 16; ++dd) {
+      uint32_t a[4];
+      const int c = ((dd & 3) << 1) | v_half;
+      ldsm_x4_trans(vt + (dd >> 2) * group_bytes + v_row + ((c ^ r8) << 4), a);
+      if (partial) {
+        a[0] &= keep_lo;
+        a[1] &= keep_lo;
+        a[2] &= keep_hi;
+        a[3] &= keep_hi;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma(o[t][dd], a, bh[t][0], bh[t][1], Tag{});
+        mma(o[t][dd], a, bl[t][0], bl[t][1], Tag{});
+      }
+    }
+    __syncwarp();  // the stage is read
+    ++done;
+    if (issue(s)) ++issued;
+  }
+  if (aborted) {  // no copy may land in shared memory after the block has exited
+    for (int i = done; i < issued; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1);
+  }
+
+  // ------------------------------------------------------------------ the join
+  // O of the warps as [warp][column][kPitch], then (m, l) as [warp][column]; the block's own
+  // sums replace warp 0's.
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(ring0);
+  float2* jml = reinterpret_cast<float2*>(jo + kWarps * kCols * Gm::kPitch);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[t][e];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
+      const int col = t * 8 + 2 * tq + e;
+      if (m[t][e] == -INFINITY && done > 0) sum = -1.f;  // tokens, but no weight
+      if (g == 0) jml[warp * kCols + col] = make_float2(m[t][e], sum);
+      float* dst = jo + (warp * kCols + col) * Gm::kPitch + g;
+#pragma unroll
+      for (int dd = 0; dd < D / 16; ++dd) {
+        dst[dd * 16] = o[t][dd][e];
+        dst[dd * 16 + 8] = o[t][dd][2 + e];
+      }
+    }
+  }
+  __syncthreads();
+  auto join = [&](auto ml_of, auto o_of, int n, int col, int d, float& M, float& sum, bool& tokens) {
+    M = -INFINITY;
+    sum = 0.f;
+    tokens = false;
+    for (int i = 0; i < n; ++i) M = max_nan(M, ml_of(i, col).x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float2 ml = ml_of(i, col);
+      const float w = weight_of(ml.x, M);
+      tokens |= ml.y < 0.f || ml.x != -INFINITY;
+      if (ml.x != -INFINITY) {
+        const float4 v = o_of(i, col, d);
+        sum = fmaf(w, ml.y, sum);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
+    }
+    return acc;
+  };
+  auto finish = [&](float4 acc, float M, float sum, bool tokens, int col, int d) {
+    const float inv = inverse_of(M, sum, tokens);
+    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    store_out<4>(p.out, (q0 + col) * D + d, v, p.out_dtype);
+  };
+  auto ml_here = [&](int w, int col) { return jml[w * kCols + col]; };
+  auto o_here = [&](int w, int col, int d) {
+    return *reinterpret_cast<const float4*>(jo + (w * kCols + col) * Gm::kPitch + d);
+  };
+  if (ranks == 1) {
+    for (int i = threadIdx.x; i < cols * (D / 4); i += kWarps * 32) {
+      const int col = i / (D / 4), d = i % (D / 4) * 4;
+      float M, sum;
+      bool tokens;
+      const float4 acc = join(ml_here, o_here, kWarps, col, d, M, sum, tokens);
+      finish(acc, M, sum, tokens, col, d);
+    }
+    return;
+  }
+  float2* block_ml = jml + kWarps * kCols;
+  for (int i = threadIdx.x; i < cols * (D / 4); i += kWarps * 32) {
+    const int col = i / (D / 4), d = i % (D / 4) * 4;
+    float M, sum;
+    bool tokens;
+    const float4 acc = join(ml_here, o_here, kWarps, col, d, M, sum, tokens);
+    *reinterpret_cast<float4*>(jo + col * Gm::kPitch + d) = acc;  // only this thread reads it before
+    if (d == 0) block_ml[col] = make_float2(M, M == -INFINITY && tokens ? -1.f : sum);
+  }
+  cluster_sync();
+  const uint32_t o_addr = smem_addr(jo), ml_addr = smem_addr(block_ml);
+  auto ml_peer = [&](int r, int col) { return ld_peer2(peer_addr(ml_addr + col * 8, r)); };
+  auto o_peer = [&](int r, int col, int d) {
+    return ld_peer4(peer_addr(o_addr + (col * Gm::kPitch + d) * 4, r));
+  };
+  for (int i = rank * kWarps * 32 + threadIdx.x; i < cols * (D / 4); i += ranks * kWarps * 32) {
+    const int col = i / (D / 4), d = i % (D / 4) * 4;
+    float M, sum;
+    bool tokens;
+    const float4 acc = join(ml_peer, o_peer, ranks, col, d, M, sum, tokens);
+    finish(acc, M, sum, tokens, col, d);
+  }
+  cluster_sync();  // no block leaves while another may read its memory
+}
+
+template <int D, int NT>
+size_t smem_bytes(int stages) {
+  const size_t ring = static_cast<size_t>(kWarps) * stages * 2 * Geo<D>::kTileBytes;
+  const size_t join = static_cast<size_t>(kWarps) * 8 * NT * Geo<D>::kPitch * sizeof(float) +
+                      (kWarps + 1) * 8 * NT * sizeof(float2);
+  return kHeader + kAlign + (ring > join ? ring : join);
+}
+
+template <class Tag, int D, int NT>
+int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seqs,
+           cudaStream_t stream) {
+  p.tiles = (p.group + 8 * NT - 1) / (8 * NT);
+  const long long rows = static_cast<long long>(num_seqs) * p.num_kv_heads * p.tiles;
+  p.stages = D == 256 ? 2 : 3;
+  const long long held = p.num_selected < p.max_blocks ? p.num_selected : p.max_blocks;
+  const long long chunks = (held * p.block_size + kChunk - 1) / kChunk;
+  int ranks = 1;
+  while (ranks < kMaxCluster && rows * ranks < 152 * 4 && chunks >= 4ll * kWarps * ranks) ranks *= 2;
+  if (rows * ranks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  // the caches as [D / 64][rows][64]: one box is a chunk, or half of one with 8-token blocks
+  const cuuint64_t cache_rows = static_cast<cuuint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
+  const cuuint64_t dims[3] = {64, cache_rows, D / 64};
+  const cuuint64_t strides[2] = {D * 2, 128};
+  const cuuint32_t box[3] = {64, p.block_size == 8 ? 8u : 16u, D / 64};
+  CUtensorMap tk, tv;
+  const bool bf16 = std::is_same<Tag, BF16>::value;
+  if (!encode_tensor_map(&tk, bf16, k_cache, 3, dims, strides, box) ||
+      !encode_tensor_map(&tv, bf16, v_cache, 3, dims, strides, box))
+    return PA_ERR_CUDA;
+  const size_t smem = smem_bytes<D, NT>(p.stages);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(paged_attn_sparse_kernel<Tag, D, NT>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * ranks));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, paged_attn_sparse_kernel<Tag, D, NT>, tk, tv, p) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <class Tag, int D>
-int launch(const SparseParams& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.num_seqs) * p.num_heads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_attn_sparse_kernel<Tag, D>, p) != cudaSuccess)
-    return PA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, int num_seqs,
+              cudaStream_t stream) {
+  return p.group <= 8 ? launch<Tag, D, 1>(p, k_cache, v_cache, num_seqs, stream)
+                      : launch<Tag, D, 2>(p, k_cache, v_cache, num_seqs, stream);
 }
 
 }  // namespace
@@ -133,7 +532,7 @@ extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void*
     return PA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
   if (static_cast<long long>(max_blocks_per_seq) * block_size > (1ll << 30) || num_seqs > 65535 ||
-      num_heads > 65535)
+      num_heads > 65535 || num_selected > (1 << 30))
     return PA_ERR_INVALID_ARG;
   if (static_cast<long long>(num_blocks) * num_kv_heads * block_size >= (1ll << 31))
     return PA_ERR_INVALID_ARG;
@@ -143,20 +542,33 @@ extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void*
     return PA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return PA_ERR_INVALID_ARG;
-  const SparseParams p{q, k_cache, v_cache, block_tables, seq_lens, selected, out, error_record,
-                       num_selected, num_seqs, num_heads, num_kv_heads, block_size,
-                       max_blocks_per_seq, num_blocks, out_dtype, scale};
+  SparseParams p{};
+  p.q = q;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.selected = selected;
+  p.out = out;
+  p.err = error_record;
+  p.num_selected = num_selected;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.group = num_heads / num_kv_heads;
+  p.out_dtype = out_dtype;
+  p.qscale = scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PA_BF16) {
     switch (head_dim) {
-      case 64: return launch<BF16, 64>(p, st);
-      case 128: return launch<BF16, 128>(p, st);
-      default: return launch<BF16, 256>(p, st);
+      case 64: return launch_nt<BF16, 64>(p, k_cache, v_cache, num_seqs, st);
+      case 128: return launch_nt<BF16, 128>(p, k_cache, v_cache, num_seqs, st);
+      default: return launch_nt<BF16, 256>(p, k_cache, v_cache, num_seqs, st);
     }
   }
   switch (head_dim) {
-    case 64: return launch<F16, 64>(p, st);
-    case 128: return launch<F16, 128>(p, st);
-    default: return launch<F16, 256>(p, st);
+    case 64: return launch_nt<F16, 64>(p, k_cache, v_cache, num_seqs, st);
+    case 128: return launch_nt<F16, 128>(p, k_cache, v_cache, num_seqs, st);
+    default: return launch_nt<F16, 256>(p, k_cache, v_cache, num_seqs, st);
   }
 }

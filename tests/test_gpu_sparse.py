@@ -220,7 +220,7 @@ def test_bad_entries_are_recorded(B):
     clean = torch.where(torch.isnan(b["kc"]), 0, b["kc"]), torch.where(torch.isnan(b["vc"]), 0, b["vc"])
     bad = dict(b, kc=clean[0], vc=clean[1])
     out = attend(B, bad, sel, error_record=rec)
-    assert B.pa_error_read(rec) == [4, 1, 1, len(b["kc"])]
+    assert B.pa_error_read(rec) == [4, 2, 1, len(b["kc"])]     # by both key heads' lists
     bad["tables"] = np.where(b["tables"] == len(b["kc"]), 0, b["tables"])
     check_attention(out, bad, sel)
     B.pa_error_clear(rec)
