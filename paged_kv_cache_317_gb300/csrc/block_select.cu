@@ -1,10 +1,15 @@
 // Block selection: the best num_selected of a row's scores, in increasing block order.
 //
 // One thread block per (sequence, key head).  A score becomes a 32-bit key that orders as
-// the scores do; the key of the last block that is kept is found one 8-bit digit at a
-// time from histograms of the keys that agree with it so far (four passes over the row);
-// a last pass in block order writes the blocks above it, and of those equal to it the
-// lowest.  The sums are of whole numbers, so the result is the same on every run.
+// the scores do.  The key of the last block that is kept is found 11 bits at a time from
+// histograms of the keys that agree with it so far (the first digit holds sign, exponent and
+// two bits of the fraction, so that ordinary scores spread over the bins), and no further than
+// needed to tell the kept from the others.  Then each warp goes over a contiguous part of the
+// row twice: it counts the blocks above that key and equal to it, and, knowing the counts of
+// the parts before, writes them; of the equal ones the lowest.  The sums are of whole numbers,
+// so the result is the same on every run.  The row is read once from memory and from the L1
+// cache after that; bound by latency (of the launch and of a dozen barriers) for one sequence
+// and by instructions for batches.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -12,7 +17,7 @@
 namespace pagedkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kBits = 11, kBins = 1 << kBits;
 
 struct SelectParams {
   const float* scores;
@@ -29,12 +34,15 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const SelectParams p) {
+  constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int head = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
+  const int lane = tid & 31, warp = tid >> 5;
   const size_t row = static_cast<size_t>(seq) * p.num_kv_heads + head;
-  int L = __ldg(p.seq_lens + seq);
+  int L = p.seq_lens[seq];
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
     if (head == 0 && tid == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
@@ -49,64 +57,102 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
   const float* s = p.scores + row * p.max_blocks;
   const int begin = p.sink, end = nb - p.recent;  // the blocks that compete
   int want = p.num_selected - p.sink - p.recent;  // how many of them are kept
-  __shared__ int hist[256];
-  __shared__ int digit_of, above_of;
-  __shared__ int warp_sum[2][kThreads / 32];
-  uint32_t prefix = 0;  // the last kept key's leading digits
+  __shared__ int hist[kBins];
+  __shared__ int warp_sum[kWarps];
+  __shared__ int found[3];  // the digit, the keys above it, the keys that have it
+  uint32_t prefix = 0, known = 0;  // the last kept key's leading bits, and which they are
+  int equal = 0;                   // keys that agree with it in those
   if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      hist[tid] = 0;
+    for (int top = 32; top > 0; top -= kBits) {
+      const int shift = max(top - kBits, 0);
+      const uint32_t digits = (1u << (top - shift)) - 1;
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = begin + tid; i < end; i += kThreads) {
         const uint32_t k = key_of(s[i]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-          atomicAdd(&hist[(k >> shift) & 255], 1);
+        if ((k & known) == prefix) atomicAdd(&hist[(k >> shift) & digits], 1);
       }
       __syncthreads();
-      if (tid == 0) {
-        int above = 0, d = 255;
-        for (; d > 0 && above + hist[d] < want; --d) above += hist[d];
-        digit_of = d;
-        above_of = above;
+      // thread t sums the bins kBins - 1 - t kPer and the kPer - 1 below; then the sums of all
+      // bins above, warp by warp
+      int mine = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) mine += hist[kBins - 1 - tid * kPer - j];
+      int upto = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kFullMask, upto, off);
+        if (lane >= off) upto += v;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) upto += warp_sum[w];
+      int above = upto - mine;
+      if (above < want && upto >= want) {  // in one thread
+        int bin = kBins - 1 - tid * kPer;
+        while (above + hist[bin] < want) above += hist[bin--];
+        found[0] = bin;
+        found[1] = above;
+        found[2] = hist[bin];
       }
       __syncthreads();
-      prefix |= static_cast<uint32_t>(digit_of) << shift;
-      want -= above_of;  // now counted among the keys that agree so far
+      prefix |= static_cast<uint32_t>(found[0]) << shift;
+      known |= digits << shift;
+      want -= found[1];
+      equal = found[2];
+      if (equal == want) break;  // every key that agrees so far is kept
     }
+  } else {
+    known = prefix = 0xffffffffu;  // none above it, and none of the equal ones is kept
   }
-  // want: how many of the keys equal to prefix are kept (the lowest blocks)
-  int written = 0, equal_seen = 0;
-  const bool any = p.num_selected > p.sink + p.recent;
-  for (int base = 0; base < nb; base += kThreads) {
-    const int i = base + tid;
-    bool above = false, equal = false;
-    if (i < nb) {
-      if (i < begin || i >= end) {
-        above = true;
-      } else if (any) {
-        const uint32_t k = key_of(s[i]);
-        above = k > prefix;
-        equal = k == prefix;
-      }
+  // kept: the blocks that do not compete, the keys above, and `want` of the equal ones
+  const int part = (nb + kWarps - 1) / kWarps, first = min(nb, warp * part);
+  const int last = min(nb, first + part);
+  auto classify = [&](int i, bool& over, bool& same) {
+    over = same = false;
+    if (i >= last) return;
+    if (i < begin || i >= end) {
+      over = true;
+      return;
     }
-    const int lane = tid & 31, warp = tid >> 5;
-    const unsigned eq = __ballot_sync(kFullMask, equal);
-    if (lane == 0) warp_sum[0][warp] = __popc(eq);
-    __syncthreads();
-    int before = equal_seen;
-    for (int w = 0; w < warp; ++w) before += warp_sum[0][w];
-    const bool keep = above || (equal && before + __popc(eq & ((1u << lane) - 1)) < want);
+    const uint32_t k = key_of(s[i]) & known;
+    over = k > prefix;
+    same = k == prefix;
+  };
+  int overs = 0, sames = 0;
+#pragma unroll 4
+  for (int i = first; i < last; i += 32) {
+    bool over, same;
+    classify(i + lane, over, same);
+    overs += over;
+    sames += same;
+  }
+  overs = __reduce_add_sync(kFullMask, overs);
+  sames = __reduce_add_sync(kFullMask, sames);
+  __syncthreads();
+  if (lane == 0) {
+    warp_sum[warp] = overs;
+    hist[warp] = sames;
+  }
+  __syncthreads();
+  int at = 0, seen = 0;  // kept and equal blocks before this warp's part
+  for (int w = 0; w < warp; ++w) {
+    at += warp_sum[w];
+    seen += hist[w];
+  }
+  at += min(seen, want);
+  const unsigned below = (1u << lane) - 1;
+#pragma unroll 2
+  for (int i = first; i < last; i += 32) {
+    bool over, same;
+    classify(i + lane, over, same);
+    const unsigned eq = __ballot_sync(kFullMask, same);
+    const bool keep = over || (same && seen + __popc(eq & below) < want);
     const unsigned kp = __ballot_sync(kFullMask, keep);
-    if (lane == 0) warp_sum[1][warp] = __popc(kp);
-    __syncthreads();
-    int at = written;
-    for (int w = 0; w < warp; ++w) at += warp_sum[1][w];
-    if (keep) out[at + __popc(kp & ((1u << lane) - 1))] = i;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      equal_seen += warp_sum[0][w];
-      written += warp_sum[1][w];
-    }
-    __syncthreads();
+    if (keep) out[at + __popc(kp & below)] = i + lane;
+    seen += __popc(eq);
+    at += __popc(kp);
   }
 }
 
@@ -133,13 +179,16 @@ extern "C" int paged_block_select(const float* scores, const int32_t* seq_lens, 
                        max_blocks_per_seq, num_selected, sink_blocks, recent_blocks};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(num_kv_heads, num_seqs);
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_block_select_kernel, p) != cudaSuccess) return PA_ERR_CUDA;
+  const bool wide = max_blocks_per_seq > 16384;
+  cfg.blockDim = dim3(wide ? 1024 : 512);
+  if (cudaLaunchKernelEx(&cfg, wide ? paged_block_select_kernel<1024> : paged_block_select_kernel<512>,
+                         p) != cudaSuccess)
+    return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
