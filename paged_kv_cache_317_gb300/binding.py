@@ -550,35 +550,41 @@ def block_copy(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor
 
 
 # ------------------------------------------- rotated append, block-sparse decode
-def _take(device, dtype, **tensors):
-    """Every tensor (None: skipped) is a contiguous CUDA tensor of the type on the device
-    that launches go to."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != device:
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _need_all(device, specs):
+    """Every (name, tensor, dtype, shape) is a contiguous tensor of that type and shape on the
+    device that launches go to; a tensor of None is skipped.  One comparison chain per tensor:
+    these checks are most of a small call's time."""
+    for name, t, dtype, shape in specs:
+        if t is not None and (t.get_device() != device or t.dtype is not dtype
+                              or t.shape != shape or not t.is_contiguous()):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            if t.dtype is not dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
             raise ValueError(f"{name} is on device {t.get_device()}, the current one is {device}")
 
 
-def _shape(name, t, shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-
-
-def _half(name, t):
+def _half(name, t, rank):
+    """The shape and type of a half-precision tensor."""
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16 and t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
         raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
-    return t.dtype
+    shape = t.shape
+    if len(shape) != rank:
+        raise ValueError(f"{name} must have {rank} dimensions, got {list(shape)}")
+    return shape, t.dtype
 
 
 def _raw_stream(stream, device):
     if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(device)
         return torch.cuda.current_stream(device).cuda_stream
     if stream.device.index != device:
         raise ValueError(f"stream is on device {stream.device.index}, the current one is {device}")
@@ -598,15 +604,25 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _tokens(name, t, dtype, device):
-    """[T, heads, head_dim] of which only the step from token to token is free."""
-    if t.dim() != 3 or not t.is_cuda or t.dtype != dtype or t.get_device() != device:
-        raise ValueError(f"{name} must be a [tokens, heads, head_dim] {dtype} tensor on the "
-                         "current CUDA device")
-    step, (n, heads, dim) = t.stride(0), t.shape
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+def _record(t, device):
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype is not torch.int32 or t.numel() < 4:
+        raise ValueError("error_record must be an int32 CUDA tensor of four entries on the "
+                         "current device (new_error_record)")
+    return t.data_ptr()
+
+
+def _token_step(name, t, dtype, device, shape):
+    """The elements from token to token of [T, heads, head_dim], whose other steps are those
+    of a contiguous tensor."""
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)} on the "
+                         "current device")
+    step, head, one = t.stride()
+    if (one != 1 and shape[2] > 1) or (head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return step if n > 1 else heads * dim
+    return step if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rope_cos_sin(max_position: int, rotary_dim: int, base: float = 10000.0,
@@ -639,40 +655,41 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     (rope_cos_sin; None: no rotation); positions: optional int32 [T], or [axes,T] with
     pair_axis, the axis of each rotary pair; k_min, k_max: optional bounds [B,H,D]
     (copy-on-write them with block_copy over [B,H,1,D] views); q_out: optional [T,Hq,D]."""
-    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
-    B, H, bs, D = k_cache.shape
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
     T = k.shape[0]
-    _take(device, dtype, k_cache=k_cache, v_cache=v_cache, k_min=k_min, k_max=k_max, q_out=q_out)
-    _take(device, torch.int32, query_start=query_start, block_tables=block_tables,
-          seq_lens=seq_lens, positions=positions, error_record=error_record)
-    _take(device, torch.float32, cos_sin=cos_sin)
-    k_step, v_step = _tokens("k", k, dtype, device), _tokens("v", v, dtype, device)
-    _shape("k", k, (T, H, D))
-    _shape("v", v, (T, H, D))
-    _shape("v_cache", v_cache, (B, H, bs, D))
-    _shape("k_min", k_min, (B, H, D))
-    _shape("k_max", k_max, (B, H, D))
-    _shape("query_start", query_start, (N + 1,))
-    _shape("seq_lens", seq_lens, (N,))
+    _need_all(device, (("k_cache", k_cache, dtype, (B, H, bs, D)),
+                       ("v_cache", v_cache, dtype, (B, H, bs, D)),
+                       ("block_tables", block_tables, i32, (N, MB)),
+                       ("seq_lens", seq_lens, i32, (N,)),
+                       ("query_start", query_start, i32, (N + 1,)),
+                       ("k_min", k_min, dtype, (B, H, D)), ("k_max", k_max, dtype, (B, H, D))))
+    k_step = _token_step("k", k, dtype, device, (T, H, D))
+    v_step = _token_step("v", v, dtype, device, (T, H, D))
     if (k_min is None) != (k_max is None):
         raise ValueError("k_min and k_max must be given together")
     q_step = Hq = 0
     if q is not None:
-        q_step, Hq = _tokens("q", q, dtype, device), q.shape[1]
-        _shape("q", q, (T, Hq, D))
+        Hq = q.shape[1]
+        q_step = _token_step("q", q, dtype, device, (T, Hq, D))
         if q_out is None:
             q_out = _new_out((T, Hq, D), dtype, q.device, stream)
-        _shape("q_out", q_out, (T, Hq, D))
+        else:
+            _need_all(device, (("q_out", q_out, dtype, (T, Hq, D)),))
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope = None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
-        axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+        _need_all(device, (("cos_sin", cos_sin, torch.float32, cos_sin.shape),))
+        axes = 1
         if positions is not None:
-            _shape("positions", positions, (T,) if positions.dim() == 1 else (axes, T))
+            if positions.dim() == 2:
+                axes = positions.shape[0]
+            _need_all(device, (("positions", positions, i32,
+                                (T,) if positions.dim() == 1 else (axes, T)),))
         if pair_axis is not None:
             pair_axis = bytes(pair_axis)
             if len(pair_axis) != cos_sin.shape[1] // 2:
@@ -688,7 +705,7 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
         _address(q), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step, query_start.data_ptr(),
         T, int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(), _address(k_min),
         _address(k_max), block_tables.data_ptr(), seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B,
-        rope, _DTYPE[dtype], _address(q_out), _address(error_record),
+        rope, _DTYPE[dtype], _address(q_out), _record(error_record, device),
         _raw_stream(stream, device)), "kv_cache_append_rope")
     return q_out
 
@@ -700,20 +717,17 @@ def kv_block_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens:
     """Compute k_min, k_max [B,H,D] of every sequence's blocks from k_cache [B,H,bs,D] and the
     rows below seq_lens; first_token: optional int32 [N], only the blocks that hold a token
     at or past it."""
-    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
-    B, H, bs, D = k_cache.shape
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
-    _take(device, dtype, k_cache=k_cache, k_min=k_min, k_max=k_max)
-    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens,
-          first_token=first_token, error_record=error_record)
-    _shape("k_min", k_min, (B, H, D))
-    _shape("k_max", k_max, (B, H, D))
-    _shape("seq_lens", seq_lens, (N,))
-    _shape("first_token", first_token, (N,))
+    _need_all(device, (("k_cache", k_cache, dtype, (B, H, bs, D)),
+                       ("k_min", k_min, dtype, (B, H, D)), ("k_max", k_max, dtype, (B, H, D)),
+                       ("block_tables", block_tables, i32, (N, MB)),
+                       ("seq_lens", seq_lens, i32, (N,)), ("first_token", first_token, i32, (N,))))
     _check(load_library().kv_block_bounds(
         k_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), _address(first_token),
         N, H, D, bs, MB, B, _DTYPE[dtype], k_min.data_ptr(), k_max.data_ptr(),
-        _address(error_record), _raw_stream(stream, device)), "kv_block_bounds")
+        _record(error_record, device), _raw_stream(stream, device)), "kv_block_bounds")
 
 
 def paged_block_scores(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor,
@@ -723,25 +737,20 @@ def paged_block_scores(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor
     """float32 [N,H,MB]: for each block of a sequence the largest logit that one of its keys can
     have with a query head of key head H, -inf past the sequence's blocks.  q [N,Hq,D], Hq a
     multiple of H; k_min, k_max [B,H,D]."""
-    device, dtype = torch.cuda.current_device(), _half("k_min", k_min)
-    B, H, D = k_min.shape
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, D), dtype = _half("k_min", k_min, 3)
     N, MB = block_tables.shape
     Hq = q.shape[1]
-    _take(device, dtype, q=q, k_min=k_min, k_max=k_max)
-    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens,
-          error_record=error_record)
-    _shape("q", q, (N, Hq, D))
-    _shape("k_max", k_max, (B, H, D))
-    _shape("seq_lens", seq_lens, (N,))
     if out is None:
         out = _new_out((N, H, MB), torch.float32, q.device, stream)
-    else:
-        _take(device, torch.float32, out=out)
-        _shape("out", out, (N, H, MB))
+    _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_min", k_min, dtype, (B, H, D)),
+                       ("k_max", k_max, dtype, (B, H, D)),
+                       ("block_tables", block_tables, i32, (N, MB)),
+                       ("seq_lens", seq_lens, i32, (N,)), ("out", out, torch.float32, (N, H, MB))))
     _check(load_library().paged_block_scores(
         q.data_ptr(), k_min.data_ptr(), k_max.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), N, Hq, H, D, int(block_size), MB, B, float(scale), _DTYPE[dtype],
-        out.data_ptr(), _address(error_record), _raw_stream(stream, device)),
+        out.data_ptr(), _record(error_record, device), _raw_stream(stream, device)),
         "paged_block_scores")
     return out
 
@@ -753,18 +762,15 @@ def paged_block_select(scores: torch.Tensor, seq_lens: torch.Tensor, block_size:
     """int32 [N,H,num_selected]: the blocks with the largest scores [N,H,MB], the first
     sink_blocks and the last recent_blocks always among them, in increasing order and then
     -1."""
-    device = torch.cuda.current_device()
+    device, i32 = torch.cuda.current_device(), torch.int32
     N, H, MB = scores.shape
-    _take(device, torch.float32, scores=scores)
-    _take(device, torch.int32, seq_lens=seq_lens, out=out, error_record=error_record)
-    _shape("seq_lens", seq_lens, (N,))
     if out is None:
-        out = _new_out((N, H, max(int(num_selected), 0)), torch.int32, scores.device, stream)
-    else:
-        _shape("out", out, (N, H, int(num_selected)))
+        out = _new_out((N, H, max(int(num_selected), 0)), i32, scores.device, stream)
+    _need_all(device, (("scores", scores, torch.float32, (N, H, MB)),
+                       ("seq_lens", seq_lens, i32, (N,)), ("out", out, i32, (N, H, num_selected))))
     _check(load_library().paged_block_select(
         scores.data_ptr(), seq_lens.data_ptr(), N, H, int(block_size), MB, int(num_selected),
-        int(sink_blocks), int(recent_blocks), out.data_ptr(), _address(error_record),
+        int(sink_blocks), int(recent_blocks), out.data_ptr(), _record(error_record, device),
         _raw_stream(stream, device)), "paged_block_select")
     return out
 
@@ -777,28 +783,23 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     """Decode attention over the tokens of the listed blocks alone.  q [N,Hq,D]; caches
     [B,H,bs,D], Hq a multiple of H; block_tables int32 [N,MB]; seq_lens int32 [N]; selected
     int32 [N,H,S], logical blocks of the sequence, -1 for none (paged_block_select)."""
-    device, dtype = torch.cuda.current_device(), _half("k_cache", k_cache)
-    B, H, bs, D = k_cache.shape
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
-    Hq, S = q.shape[1], selected.shape[-1]
-    _take(device, dtype, q=q, k_cache=k_cache, v_cache=v_cache)
-    _take(device, torch.int32, block_tables=block_tables, seq_lens=seq_lens, selected=selected,
-          error_record=error_record)
-    _shape("q", q, (N, Hq, D))
-    _shape("v_cache", v_cache, (B, H, bs, D))
-    _shape("seq_lens", seq_lens, (N,))
-    _shape("selected", selected, (N, H, S))
+    Hq, S = q.shape[1], selected.shape[2]
     if out is None:
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
-    else:
-        _take(device, out.dtype, out=out)
-        _shape("out", out, (N, Hq, D))
     if out.dtype not in _DTYPE:
         raise ValueError(f"out must be float16, bfloat16 or float32, got {out.dtype}")
+    _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_cache", k_cache, dtype, (B, H, bs, D)),
+                       ("v_cache", v_cache, dtype, (B, H, bs, D)),
+                       ("block_tables", block_tables, i32, (N, MB)),
+                       ("seq_lens", seq_lens, i32, (N,)),
+                       ("selected", selected, i32, (N, H, S)), ("out", out, out.dtype, (N, Hq, D))))
     _check(load_library().paged_attn_sparse(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),
-        _DTYPE[dtype], out.data_ptr(), _DTYPE[out.dtype], _address(error_record),
+        _DTYPE[dtype], out.data_ptr(), _DTYPE[out.dtype], _record(error_record, device),
         _raw_stream(stream, device)), "paged_attn_sparse")
     return out
 

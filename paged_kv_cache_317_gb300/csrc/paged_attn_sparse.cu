@@ -24,6 +24,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "mma.cuh"
 #include "tma.cuh"
@@ -51,39 +52,6 @@ struct SparseParams {
   int out_dtype, stages;
   float qscale;         // scale * log2(e)
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Shared memory of another block of the cluster, at the same address as `addr` here.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
-  return v;
-}
 
 // Partials of a column: m = running maximum (NaN once a logit was), l = sum of 2^(s - m);
 // m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity).  The weight
@@ -480,10 +448,11 @@ int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seq
       !encode_tensor_map(&tv, bf16, v_cache, 3, dims, strides, box))
     return PA_ERR_CUDA;
   const size_t smem = smem_bytes<D, NT>(p.stages);
+  // Always the same value, so that concurrent callers never lower it for one another, and on
+  // every launch that needs it (it is lost with the context).
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(paged_attn_sparse_kernel<Tag, D, NT>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * ranks));

@@ -244,7 +244,8 @@ def test_bad_entries_are_recorded(B):
     (1, [1, 0], 1, 0, 0), (7, [7, 3, 5], 3, 1, 1), (40, [40, 33, 2], 4, 2, 2),
     (300, [300, 257, 256, 1], 50, 0, 3), (1031, [1031, 800], 64, 4, 8),
     (2100, [2100, 2049], 1000, 1, 1), (5000, [4999], 1, 0, 1), (9001, [9001, 4097], 300, 0, 0),
-    (20000, [20000, 19999, 7], 2000, 1, 4)])
+    (20000, [20000, 19999, 7], 2000, 1, 4), (70001, [70001, 69000], 500, 3, 5),
+    (400000 - 6784, [393000, 5], 20000, 1, 9)])
 @pytest.mark.parametrize("kind", ["normal", "ties", "odd"])
 def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
     rng = np.random.default_rng(width)
@@ -261,6 +262,17 @@ def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
                                error_record=rec)
     assert B.pa_error_read(rec) == [0, 0, 0, 0]
     assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, keep, sink, recent))
+
+
+@pytest.mark.parametrize("rows", [1, 3, 20, 80, 160])
+def test_select_with_rows_split_over_a_cluster(B, rows):
+    """Few long rows are split over several thread blocks, many are not: the same lists."""
+    rng = np.random.default_rng(rows)
+    s = np.round(rng.standard_normal((rows, 1, 9000)) * 8).astype(np.float32)
+    lens = rng.integers(1, 9001, rows)
+    lens[0] = 9000
+    got = B.paged_block_select(torch.from_numpy(s).cuda(), dev(lens), 1, 200, 1, 2)
+    assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, 200, 1, 2))
 
 
 def test_select_reads_nothing_past_a_sequence(B):
