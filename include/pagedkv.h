@@ -598,7 +598,7 @@ int paged_block_scores(const void* q, const void* k_min, const void* k_max,
  *   scores        device float [num_seqs][num_kv_heads][max_blocks_per_seq]; entries past a
  *                 sequence's blocks are not read
  *   num_selected  >= 1, >= sink_blocks + recent_blocks
- *   max_blocks_per_seq  at most 393216
+ *   max_blocks_per_seq  at most 131072
  * A length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
 int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seqs,
                        int num_kv_heads, int block_size, int max_blocks_per_seq, int num_selected,

@@ -1,8 +1,9 @@
 // Channel-wise smallest and largest key of cached blocks, computed anew.
 //
 // A thread takes 8 channels (16 bytes) of one (sequence, block, key head) and walks the
-// block's rows below the sequence's length.  Every key byte is read once and two rows per
-// block are written: the kernel is bound by HBM.
+// block's rows below the sequence's length, kBatch loads in flight at a time; past the last
+// row it reads that row again, which changes no minimum.  Every key byte is read once from
+// memory and two rows per block are written: the kernel is bound by HBM.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -24,17 +25,17 @@ struct BoundsParams {
   int num_kv_heads, head_dim, block_size, max_blocks, num_blocks;
 };
 
-template <class Tag>
+template <class Tag, int kBatch>
 __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int seq = blockIdx.y;
-  const int L = __ldg(p.seq_lens + seq);
+  const int L = p.seq_lens[seq];
   if (L < 0 || L > static_cast<long long>(p.max_blocks) * p.block_size) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     return;
   }
-  const int first = p.first_token ? max(__ldg(p.first_token + seq), 0) : 0;
+  const int first = p.first_token ? max(p.first_token[seq], 0) : 0;
   const int pieces = p.head_dim / 8;                 // 16-byte pieces of a row
   const int per_block = p.num_kv_heads * pieces;     // threads of a block
   const int b0 = first / p.block_size;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsP
     const int b = b0 + static_cast<int>(i / per_block);
     const int rem = static_cast<int>(i % per_block);
     const int head = rem / pieces, x = rem % pieces;
-    const int blk = __ldg(p.block_tables + static_cast<size_t>(seq) * p.max_blocks + b);
+    const int blk = p.block_tables[static_cast<size_t>(seq) * p.max_blocks + b];
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
       if (rem == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       continue;
@@ -54,12 +55,16 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsP
     const int rows = min(p.block_size, L - b * p.block_size);
     const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
     const uint4* src = static_cast<const uint4*>(p.k_cache) + bh * p.block_size * pieces + x;
-    uint4 lo = __ldg(src), hi = lo;
-#pragma unroll 8
-    for (int r = 1; r < rows; ++r) {
-      const uint4 u = __ldg(src + static_cast<size_t>(r) * pieces);
-      lo = min8(lo, u, Tag{});
-      hi = max8(hi, u, Tag{});
+    uint4 lo = *src, hi = lo;
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+      uint4 u[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) u[j] = src[static_cast<size_t>(min(r0 + j, rows - 1)) * pieces];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        lo = min8(lo, u[j], Tag{});
+        hi = max8(hi, u[j], Tag{});
+      }
     }
     static_cast<uint4*>(p.k_min)[bh * pieces + x] = lo;
     static_cast<uint4*>(p.k_max)[bh * pieces + x] = hi;
@@ -103,7 +108,14 @@ extern "C" int kv_block_bounds(const void* k_cache, const int32_t* block_tables,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<BF16>, p)
-                                         : cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<F16>, p);
+  // as many loads in flight as a block has rows, up to 16 (32 sequences of up to 16384 tokens,
+  // blocks of 16 rows: 99.5 us with 16, 130 us with 8)
+  cudaError_t e;
+  if (block_size <= 8)
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<BF16, 8>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<F16, 8>, p);
+  else
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<BF16, 16>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_block_bounds_kernel<F16, 16>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

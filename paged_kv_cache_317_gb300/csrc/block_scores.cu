@@ -3,13 +3,15 @@
 // With lo <= k <= hi in every channel, q.k <= sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d: a
 // matrix product of the queries' positive and negative parts with the two bounds, of which
 // the largest over the query heads of a key head is kept.
-//  * One warp takes 16 blocks of one key head, on mma.sync m16n8k16 with the blocks as the
-//    rows, the channels of hi and then of lo as the inner dimension and the query heads, 8 at
-//    a time, as the columns.  Consecutive warps take consecutive heads, whose bounds lie side
-//    by side.
+//  * One warp takes up to 64 blocks of one key head, 16 at a time, on mma.sync m16n8k16 with
+//    the blocks as the rows, the channels of hi and then of lo as the inner dimension and the
+//    query heads, 8 at a time, as the columns.  Consecutive warps take consecutive heads,
+//    whose bounds lie side by side.
 //  * A product does not mind in which order the channels come, as long as both operands agree:
-//    each lane loads 16 consecutive bytes of its rows and of its head's query and uses them as
-//    fragments where they are.  No shared memory, no shuffles on the way in.
+//    each lane takes 16 consecutive bytes of its rows and of its head's query and uses them as
+//    fragments where they are.  The lane that uses a piece of a bound also copies it,
+//    asynchronously, into a ring in shared memory: the ring only stands in for registers, so
+//    that the next 16 blocks are on their way during the products, and needs no barriers.
 //  * Products of two half-precision numbers are exact in fp32, sums are kept in fp32.
 // 4 operations per bound and query head: bound by HBM for batches, by latency for one sequence.
 #include <cuda_runtime.h>
@@ -24,7 +26,8 @@ namespace pagedkv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRows = 16;  // blocks per warp
+constexpr int kRows = 16;    // blocks per matrix product
+constexpr int kMaxTiles = 4; // of 16 blocks per warp
 
 struct ScoreParams {
   const void* q;
@@ -35,104 +38,156 @@ struct ScoreParams {
   float* scores;
   int32_t* err;
   int num_heads, num_kv_heads, block_size, max_blocks, num_blocks;
+  int tiles;  // of 16 blocks per warp
   float scale;
 };
 
+__device__ __forceinline__ void copy_async16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D>
+constexpr int stages_of() { return D == 256 ? 2 : 3; }
+template <int D>
+constexpr int smem_of() { return kWarps * stages_of<D>() * (D / 8) * 32 * 16; }
+
 template <class Tag, int D>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
-  constexpr int kPieces = D / 8;             // 16-byte pieces of a row
-  constexpr int kSteps = D / 32;             // pieces of a row that one lane loads
-  constexpr int kBatch = kSteps < 4 ? kSteps : 4;  // of them at a time
+  constexpr int kPieces = D / 8;         // 16-byte pieces of a row
+  constexpr int kSteps = D / 32;         // pieces of a row that one lane takes
+  constexpr int kStages = stages_of<D>();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
+  extern __shared__ uint4 ring[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.y;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
   const int head = static_cast<int>(item % p.num_kv_heads);
-  const long long b0 = item / p.num_kv_heads * kRows;
+  const long long b0 = item / p.num_kv_heads * (kRows * p.tiles);  // the warp's first block
+  if (b0 >= p.max_blocks) return;
+  // Block numbers of blocks b0 + lane and b0 + 32 + lane, fetched along with the length,
+  // before it says which ones count.
+  const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
+  int blk[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    blk[e] = table[min(b0 + 32 * e + lane, static_cast<long long>(p.max_blocks - 1))];
   int L = p.seq_lens[seq];
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     L = min(max(L, 0), cap);
   }
-  if (b0 >= p.max_blocks) return;
   const int nb = static_cast<int>((static_cast<long long>(L) + p.block_size - 1) / p.block_size);
   float* out = p.scores + (static_cast<size_t>(seq) * p.num_kv_heads + head) * p.max_blocks;
-  if (b0 >= nb) {
-    if (lane < kRows && b0 + lane < p.max_blocks) out[b0 + lane] = -INFINITY;
-    return;
-  }
-  const int g = lane >> 2, tq = lane & 3;
-  const int row0 = static_cast<int>(b0) + g;  // this lane's blocks: row0 and row0 + 8
-  const uint4* lo[2];
-  const uint4* hi[2];
+  const int end = static_cast<int>(min(b0 + kRows * p.tiles, static_cast<long long>(p.max_blocks)));
+  for (int b = max(static_cast<int>(b0), nb) + lane; b < end; b += 32) out[b] = -INFINITY;
+  if (b0 >= nb) return;
+  const int first = static_cast<int>(b0), held = min(end, nb) - first;  // blocks with a score
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int b = min(row0 + 8 * e, nb - 1);  // rows past the last block repeat it, unused
-    int blk = p.block_tables[static_cast<size_t>(seq) * p.max_blocks + b];
-    if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-      if (head == 0 && tq == 0 && b == row0 + 8 * e) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
-      blk = 0;
+    if (32 * e + lane < held && static_cast<unsigned>(blk[e]) >= static_cast<unsigned>(p.num_blocks)) {
+      if (head == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk[e]);
+      blk[e] = 0;
     }
-    const size_t at = (static_cast<size_t>(blk) * p.num_kv_heads + head) * kPieces + tq;
-    lo[e] = static_cast<const uint4*>(p.k_min) + at;
-    hi[e] = static_cast<const uint4*>(p.k_max) + at;
   }
+  const int g = lane >> 2, tq = lane & 3;
+  uint4* mine = ring + static_cast<size_t>(warp) * kStages * kPieces * 32 + lane;
+  // The lane's pieces of rows g and g + 8 of tile t: hi then lo, into stage t % kStages.
+  auto issue = [&](int t) {
+    if (16 * t < held) {
+      uint4* dst = mine + (t % kStages) * kPieces * 32;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int b = __shfl_sync(kFullMask, t < 2 ? blk[0] : blk[1], (t & 1) * 16 + 8 * e + g);
+        if (16 * t + 8 * e + g < held) {  // the other rows' products are not used
+          const size_t at = (static_cast<size_t>(b) * p.num_kv_heads + head) * kPieces + tq;
+          const uint4* hi = static_cast<const uint4*>(p.k_max) + at;
+          const uint4* lo = static_cast<const uint4*>(p.k_min) + at;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            copy_async16(dst + (4 * i + e) * 32, hi + 4 * i);
+            copy_async16(dst + (4 * i + 2 + e) * 32, lo + 4 * i);
+          }
+        }
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int t = 0; t < kStages - 1; ++t) issue(t);
+
   const int group = p.num_heads / p.num_kv_heads;
   const uint4* q = static_cast<const uint4*>(p.q) +
                    (static_cast<size_t>(seq) * p.num_heads + static_cast<size_t>(head) * group) * kPieces + tq;
-  float best[2] = {-INFINITY, -INFINITY};
-  for (int h0 = 0; h0 < group; h0 += 8) {
-    // columns past the last head repeat it
-    const uint4* qh = q + static_cast<size_t>(min(h0 + g, group - 1)) * kPieces;
-    float up[4] = {0.f, 0.f, 0.f, 0.f}, down[4] = {0.f, 0.f, 0.f, 0.f};
+  uint4 x[kSteps];
+  for (int t = 0; 16 * t < held; ++t) {
+    issue(t + kStages - 1);
+    if (t == 0) {  // after the copies are on their way
 #pragma unroll
-    for (int i0 = 0; i0 < kSteps; i0 += kBatch) {
-      uint4 a[kBatch][4], x[kBatch];
+      for (int i = 0; i < kSteps; ++i) x[i] = q[min(g, group - 1) * kPieces + 4 * i];
+    }
+    copy_wait<kStages - 1>();
+    const uint4* src = mine + (t % kStages) * kPieces * 32;
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int h0 = 0; h0 < group; h0 += 8) {
+      if (group > 8) {  // columns past the last head repeat it
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        a[i][0] = hi[0][(i0 + i) * 4];
-        a[i][1] = hi[1][(i0 + i) * 4];
-        a[i][2] = lo[0][(i0 + i) * 4];
-        a[i][3] = lo[1][(i0 + i) * 4];
-        x[i] = qh[(i0 + i) * 4];
+        for (int i = 0; i < kSteps; ++i) x[i] = q[static_cast<size_t>(min(h0 + g, group - 1)) * kPieces + 4 * i];
       }
+      float up[4] = {0.f, 0.f, 0.f, 0.f}, down[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
+      for (int i = 0; i < kSteps; ++i) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const uint4 qp = max8(x[i], zero, Tag{}), qn = min8(x[i], zero, Tag{});
-        const uint32_t u0[4] = {a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y};
-        const uint32_t u1[4] = {a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w};
-        const uint32_t v0[4] = {a[i][2].x, a[i][3].x, a[i][2].y, a[i][3].y};
-        const uint32_t v1[4] = {a[i][2].z, a[i][3].z, a[i][2].w, a[i][3].w};
+        const uint4 h_0 = src[(4 * i) * 32], h_1 = src[(4 * i + 1) * 32];
+        const uint4 l_0 = src[(4 * i + 2) * 32], l_1 = src[(4 * i + 3) * 32];
+        const uint32_t u0[4] = {h_0.x, h_1.x, h_0.y, h_1.y}, u1[4] = {h_0.z, h_1.z, h_0.w, h_1.w};
+        const uint32_t v0[4] = {l_0.x, l_1.x, l_0.y, l_1.y}, v1[4] = {l_0.z, l_1.z, l_0.w, l_1.w};
         mma(up, u0, qp.x, qp.y, Tag{});
         mma(down, v0, qn.x, qn.y, Tag{});
         mma(up, u1, qp.z, qp.w, Tag{});
         mma(down, v1, qn.z, qn.w, Tag{});
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        best[e] = max_nan(best[e], max_nan(up[2 * e] + down[2 * e], up[2 * e + 1] + down[2 * e + 1]));
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      best[e] = max_nan(best[e], max_nan(up[2 * e] + down[2 * e], up[2 * e + 1] + down[2 * e + 1]));
+    for (int e = 0; e < 2; ++e) {
+      best[e] = max_nan(best[e], __shfl_xor_sync(kFullMask, best[e], 1));
+      best[e] = max_nan(best[e], __shfl_xor_sync(kFullMask, best[e], 2));
+      if (tq == 0 && 16 * t + 8 * e + g < held) out[first + 16 * t + 8 * e + g] = best[e] * p.scale;
+    }
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    best[e] = max_nan(best[e], __shfl_xor_sync(kFullMask, best[e], 1));
-    best[e] = max_nan(best[e], __shfl_xor_sync(kFullMask, best[e], 2));
-    const int b = row0 + 8 * e;
-    if (tq == 0 && b < p.max_blocks) out[b] = b < nb ? best[e] * p.scale : -INFINITY;
-  }
+  copy_wait<0>();
 }
 
 template <class Tag, int D>
-int launch(const ScoreParams& p, int num_seqs, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  const long long items = static_cast<long long>((p.max_blocks + kRows - 1) / kRows) * p.num_kv_heads;
-  const long long blocks = (items + kWarps - 1) / kWarps;
+int launch(ScoreParams p, int num_seqs, cudaStream_t stream) {
+  // 64 blocks per warp, down to 16 while that leaves fewer than 8 warps for each SM
+  const auto warps = [&](int tiles) {
+    return (p.max_blocks + kRows * tiles - 1) / (kRows * tiles) * static_cast<long long>(p.num_kv_heads);
+  };
+  p.tiles = kMaxTiles;
+  while (p.tiles > 1 && warps(p.tiles) * num_seqs < 152 * 8) p.tiles /= 2;
+  const long long blocks = (warps(p.tiles) + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  constexpr int smem = smem_of<D>();
+  // on every launch that needs it (the attribute is lost with the context)
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(paged_block_scores_kernel<Tag, D>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), num_seqs);
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -169,7 +224,7 @@ extern "C" int paged_block_scores(const void* q, const void* k_min, const void* 
   if (!q || !k_min || !k_max || !block_tables || !seq_lens || !scores) return PA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_min) || !aligned16(k_max)) return PA_ERR_INVALID_ARG;
   const ScoreParams p{q, k_min, k_max, block_tables, seq_lens, scores, error_record, num_heads,
-                      num_kv_heads, block_size, max_blocks_per_seq, num_blocks, scale};
+                      num_kv_heads, block_size, max_blocks_per_seq, num_blocks, 0, scale};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PA_BF16) {
     switch (head_dim) {

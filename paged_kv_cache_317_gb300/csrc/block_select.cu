@@ -1,17 +1,18 @@
 // Block selection: the best num_selected of a row's scores, in increasing block order.
 //
 // A cluster of thread blocks (one, but for few long rows) per (sequence, key head), each with
-// a contiguous part of the row.  A score becomes a 32-bit key that orders as the scores do, and
-// the keys stay in shared memory.  The key of the last block that is kept is found 11 bits at a
-// time from histograms of the keys that agree with it so far (the first digit holds sign,
-// exponent and two bits of the fraction, so that ordinary scores spread over the bins), and no
-// further than needed to tell the kept from the others; the blocks of a cluster add up each
-// other's histograms.  Then each thread counts the blocks above that key and equal to it in a
-// run of its own, a scan of the counts says where its run goes, and it writes them; of the
-// equal ones the lowest.  Runs of odd length keep the threads of a warp on different banks.
-// The sums are of whole numbers, so the result is the same on every run.  The row is read once;
-// bound by latency (the launch and some ten barriers) for one sequence and by instructions for
-// batches.
+// a contiguous part of the row, of which each warp has a contiguous part in turn: up to 32
+// groups of 32 scores, one of each group per lane, read once and kept in registers.  A score
+// becomes a 32-bit key that orders as the scores do.  The key of the last block that is kept
+// is found 11 bits at a time from histograms of the keys that agree with it so far (the first
+// digit holds sign, exponent and two bits of the fraction, so that ordinary scores spread over
+// the bins), and no further than needed to tell the kept from the others; the blocks of a
+// cluster add up each other's histograms.  Then two votes per group tell which of its blocks
+// are above that key and which equal to it; lane j takes the votes of group j, a scan of
+// their counts over lanes, warps and blocks says where its blocks go, and it writes them, of
+// the equal ones the lowest.  The sums are of whole numbers, so the result is the same on every
+// run.  Bound by latency (the launch and some ten barriers) for one sequence and by
+// instructions for batches.
 #include <cuda_runtime.h>
 
 #include "cluster.cuh"
@@ -22,8 +23,8 @@ namespace {
 
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxKeys = 49152;  // per thread block: 192 KB of shared memory
-constexpr int kAhead = 8;        // loads in flight per thread
+constexpr int kGroups = 32;  // groups of 32 keys per warp: one vote per lane
+constexpr int kStep = 8;     // of them between two looks at how many there are
 
 struct SelectParams {
   const float* scores;
@@ -49,15 +50,31 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
   return x;
 }
 
+// hist[bin] += 1 where bit j of `which` is set: predicated, for a branch per key costs more than
+// the rest of a pass.
+__device__ __forceinline__ void count_if(uint32_t which, int j, int* hist, uint32_t bin) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 b;\n\t"
+      "and.b32 b, %0, %1;\n\t"
+      "setp.ne.u32 p, b, 0;\n\t"
+      "@p red.shared::cta.add.u32 [%2], 1;\n\t}" ::"r"(which),
+      "r"(1u << j), "r"(smem_addr(hist + bin))
+      : "memory");
+}
+
+// Bits 0 .. n - 1, for any n.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
+
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
   static_assert(kThreads <= kBins, "a thread has a bin at least");
-  extern __shared__ uint32_t keys[];
   __shared__ __align__(16) int hist[2][kBins];
   __shared__ uint32_t warp_sum[2][kWarps];
-  __shared__ int found[3];       // the digit, the keys above it, the keys that have it
-  __shared__ uint32_t block_sum;
+  __shared__ int found[3];  // the digit, the keys above it, the keys that have it
+  __shared__ uint32_t part_sum[kWarps], block_sum;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int head = blockIdx.x / ranks, seq = blockIdx.y;
@@ -78,30 +95,37 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
       out[i] = i < nb ? i : -1;
     return;
   }
-  const int part = (nb + ranks - 1) / ranks;
-  const int base = min(nb, rank * part), n = min(part, nb - base);
-  const float* s = p.scores + row * p.max_blocks + base;
-  // of this part, the blocks begin .. end - 1 compete; `want` of the row's are kept
-  const int begin = p.sink - base, end = nb - p.recent - base;
+  // Groups of 32 blocks per warp of the row, at most kGroups as the capacity is in range.
+  const int groups = (nb + 32 * kWarps * ranks - 1) / (32 * kWarps * ranks);
+  const int base = (rank * kWarps + warp) * groups * 32;  // the warp's first block
+  const float* s = p.scores + row * p.max_blocks + base + lane;
+  // Of this lane's groups, the ones that have a block, and those whose block competes; `want`
+  // of the row's are kept.
+  const int mine = nb - base - lane;  // group j has a block if 32 j < mine
+  const uint32_t have = bits_below(min((mine + 31) >> 5, groups));
+  const uint32_t in = bits_below(min((mine - p.recent + 31) >> 5, groups)) &
+                      ~bits_below((p.sink - base - lane + 31) >> 5);
   int want = p.num_selected - p.sink - p.recent;
-  __syncthreads();
-  for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
-    float x[kAhead];
+  uint32_t key[kGroups];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kThreads;
-      x[j] = i < n ? s[i] : 0.f;
-    }
+  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
+    if (j0 < groups) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kThreads;
-      const uint32_t k = key_of(x[j]);
-      if (i < n) keys[i] = k;
-      if (i < n && i >= begin && i < end) atomicAdd(&hist[0][k >> (32 - kBits)], 1);
+      for (int j = j0; j < j0 + kStep; ++j)
+        key[j] = __float_as_uint(have >> j & 1 ? s[32 * j] : 0.f);
     }
   }
-  const int run = ((n + kThreads - 1) / kThreads) | 1;
-  const int first = min(n, tid * run), last = min(n, first + run);
+  __syncthreads();  // hist[0] is zero
+#pragma unroll
+  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
+    if (j0 < groups) {
+#pragma unroll
+      for (int j = j0; j < j0 + kStep; ++j) {
+        key[j] = key_of(__uint_as_float(key[j]));
+        count_if(in, j, hist[0], key[j] >> (32 - kBits));
+      }
+    }
+  }
   uint32_t prefix = 0xffffffffu, known = 0xffffffffu;  // want = 0: nothing above, none of the equal
   if (want > 0) {
     prefix = known = 0;  // the last kept key's leading bits, and which they are
@@ -109,10 +133,13 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
       const int shift = max(top - kBits, 0);
       const uint32_t digits = (1u << (top - shift)) - 1;
       if (top < 32) {
-        const int from = max(first, begin), to = min(last, end);
-        for (int i = from; i < to; ++i) {
-          const uint32_t k = keys[i];
-          if ((k & known) == prefix) atomicAdd(&hist[turn][(k >> shift) & digits], 1);
+#pragma unroll
+        for (int j0 = 0; j0 < kGroups; j0 += kStep) {
+          if (j0 < groups) {
+#pragma unroll
+            for (int j = j0; j < j0 + kStep; ++j)
+              count_if((key[j] & known) == prefix ? in : 0u, j, hist[turn], (key[j] >> shift) & digits);
+          }
         }
       }
       if (ranks > 1) cluster_sync();
@@ -136,15 +163,14 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
       // the other histogram, for the next digit: its readers are past the barrier above
 #pragma unroll
       for (int j = 0; j < kPer; ++j) hist[turn ^ 1][bin0 + j] = 0;
-      int mine = 0;
+      int sum = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) mine += bin[j];
-      uint32_t upto = warp_scan(mine, lane);
+      for (int j = 0; j < kPer; ++j) sum += bin[j];
+      uint32_t upto = warp_scan(sum, lane);
       if (lane == 31) warp_sum[turn][warp] = upto;
       __syncthreads();
-      const uint32_t sums = warp_scan(lane < kWarps ? warp_sum[turn][lane] : 0u, lane);
-      if (warp > 0) upto += __shfl_sync(kFullMask, sums, max(warp - 1, 0));
-      int above = static_cast<int>(upto) - mine;
+      upto += __reduce_add_sync(kFullMask, lane < warp ? warp_sum[turn][lane] : 0u);
+      int above = static_cast<int>(upto) - sum;
       if (above < want && static_cast<int>(upto) >= want) {  // in one thread
 #pragma unroll
         for (int j = kPer - 1; j >= 0; --j) {
@@ -162,59 +188,63 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
       want -= found[1];
       if (found[2] == want) break;  // every key that agrees so far is kept
     }
-  } else {
-    __syncthreads();
   }
   // kept: the blocks that do not compete, the keys above, and `want` of the equal ones
-  uint32_t count = 0;  // above in the upper half, equal in the lower (n < 2^16)
-  for (int i = first; i < last; ++i) {
-    const uint32_t k = keys[i] & known;
-    const bool in = i >= begin && i < end;
-    count += !in || k > prefix ? 0x10000u : k == prefix ? 1u : 0u;
+  uint32_t over_here = 0, same_here = 0;  // of group `lane`
+#pragma unroll
+  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
+    if (j0 < groups) {
+#pragma unroll
+      for (int j = j0; j < j0 + kStep; ++j) {
+        const uint32_t k = key[j] & known;
+        const bool inside = in >> j & 1;
+        const unsigned over = __ballot_sync(kFullMask, (have >> j & 1) && (!inside || k > prefix));
+        const unsigned same = __ballot_sync(kFullMask, inside && k == prefix);
+        if (lane == j) {
+          over_here = over;
+          same_here = same;
+        }
+      }
+    }
   }
+  // above in the upper half, equal in the lower (a thread block has at most 2^14 keys)
+  const uint32_t count = static_cast<uint32_t>(__popc(over_here)) << 16 | __popc(same_here);
   uint32_t upto = warp_scan(count, lane);
-  if (lane == 31) warp_sum[0][warp] = upto;
+  if (lane == 31) part_sum[warp] = upto;
   __syncthreads();
-  const uint32_t sums = warp_scan(lane < kWarps ? warp_sum[0][lane] : 0u, lane);
-  if (warp > 0) upto += __shfl_sync(kFullMask, sums, max(warp - 1, 0));
-  upto -= count;  // before this thread's run, within the block
-  int over = static_cast<int>(upto >> 16), same = static_cast<int>(upto & 0xffffu);
+  upto += __reduce_add_sync(kFullMask, lane < warp ? part_sum[lane] : 0u);
+  int at = 0, same = 0;
   if (ranks > 1) {
-    if (tid == kThreads - 1) block_sum = upto + count;
+    if (tid == kThreads - 1) block_sum = upto;
     cluster_sync();
-    const uint32_t at = smem_addr(&block_sum);
+    const uint32_t sum_at = smem_addr(&block_sum);
     for (int r = 0; r < rank; ++r) {
-      const uint32_t v = ld_peer_u32(peer_addr(at, r));
-      over += static_cast<int>(v >> 16);
+      const uint32_t v = ld_peer_u32(peer_addr(sum_at, r));
+      at += static_cast<int>(v >> 16);
       same += static_cast<int>(v & 0xffffu);
     }
   }
-  int at = over + min(same, want);
-  if (count != 0) {
-    for (int i = first; i < last; ++i) {
-      const uint32_t k = keys[i] & known;
-      const bool in = i >= begin && i < end;
-      bool keep = !in || k > prefix;
-      if (in && k == prefix) keep = same++ < want;
-      if (keep) out[at++] = base + i;
+  upto -= count;
+  at += static_cast<int>(upto >> 16);
+  same += static_cast<int>(upto & 0xffffu);
+  at += min(same, want);
+  int left = max(want - same, 0);  // equal ones that are still kept
+  for (uint32_t bits = over_here | same_here; bits != 0; bits &= bits - 1) {
+    const int i = __ffs(bits) - 1;
+    if (same_here >> i & 1) {
+      if (left == 0) continue;
+      --left;
     }
+    out[at++] = base + 32 * lane + i;
   }
   if (ranks > 1) cluster_sync();  // no block leaves while another may read its memory
 }
 
 template <int kThreads>
-int launch(const SelectParams& p, int num_seqs, int ranks, size_t smem, cudaStream_t stream) {
-  // Always the same value, so that concurrent callers never lower it for one another, and on
-  // every launch that needs it (it is lost with the context).
-  if (smem > 24 * 1024 &&
-      cudaFuncSetAttribute(paged_block_select_kernel<kThreads>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMaxKeys * static_cast<int>(sizeof(uint32_t))) != cudaSuccess)
-    return PA_ERR_CUDA;
+int launch(const SelectParams& p, int num_seqs, int ranks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_kv_heads) * ranks, num_seqs);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -250,17 +280,14 @@ extern "C" int paged_block_select(const float* scores, const int32_t* seq_lens, 
   if (!scores || !seq_lens || !selected) return PA_ERR_INVALID_ARG;
   const SelectParams p{scores, seq_lens, selected, error_record, num_kv_heads, block_size,
                        max_blocks_per_seq, num_selected, sink_blocks, recent_blocks};
-  // Parts of at least 2048 keys while there are SMs to spare, and at most kMaxKeys.
+  // Parts of at least 2048 keys while there are SMs to spare, and at most the 16384 of 16 warps.
   const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
   int ranks = 1;
-  while (ranks < kMaxCluster &&
-         ((rows * ranks < 152 && max_blocks_per_seq > 4096 * ranks) ||
-          max_blocks_per_seq > kMaxKeys * ranks))
+  while (ranks < kMaxCluster && ((rows * ranks < 152 && max_blocks_per_seq > 4096 * ranks) ||
+                                 max_blocks_per_seq > 16384 * ranks))
     ranks *= 2;
-  const int part = (max_blocks_per_seq + ranks - 1) / ranks;
-  if (part > kMaxKeys) return PA_ERR_UNSUPPORTED;
-  const size_t smem = static_cast<size_t>(part) * sizeof(uint32_t);
+  if (max_blocks_per_seq > 16384 * ranks) return PA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return part <= 8192 ? launch<256>(p, num_seqs, ranks, smem, st)
-                      : launch<1024>(p, num_seqs, ranks, smem, st);
+  return max_blocks_per_seq <= 8192 * ranks ? launch<256>(p, num_seqs, ranks, st)
+                                            : launch<512>(p, num_seqs, ranks, st);
 }

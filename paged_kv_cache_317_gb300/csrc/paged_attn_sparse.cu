@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int cols = min(kCols, p.group - tile * kCols);
   const size_t q0 = static_cast<size_t>(seq) * p.num_heads + head * p.group + tile * kCols;
 
-  int L = __ldg(p.seq_lens + seq);
+  int L = p.seq_lens[seq];
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
     if (threadIdx.x == 0 && rank == 0 && head == 0 && tile == 0)
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   // Row coordinate of (entry e, its 16-token part) in the cache seen as rows of D, and the
   // number of tokens there (0: none).
   auto look_up = [&](int e, int part, int height, int& y) -> int {
-    const int b = __ldg(list + e);
+    const int b = list[e];
     if (b < -1 || b >= p.max_blocks) {
       if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, sh, b);
       return 0;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (b < 0) return 0;
     const int rows = min(height, L - b * p.block_size - part * kChunk);
     if (rows <= 0) return 0;
-    int blk = __ldg(table + b);
+    int blk = table[b];
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
       if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       blk = 0;
@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     const T* src = static_cast<const T*>(p.q) + (q0 + (have ? t * 8 + g : 0)) * D + 2 * tq;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      qf[t][kk][0] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16)) : 0u;
-      qf[t][kk][1] = have ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8)) : 0u;
+      qf[t][kk][0] = have ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
+      qf[t][kk][1] = have ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
     }
   }
   float o[NT][D / 16][4];

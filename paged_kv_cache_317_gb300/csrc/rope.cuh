@@ -39,8 +39,7 @@ inline int rope_params(const pa_rope& r, int head_dim, RopeParams& p) {
 
 // A token's position on an axis as given, then kept in range.
 __device__ __forceinline__ int raw_position(const RopeParams& p, int axis, int token, int place) {
-  return p.positions ? __ldg(p.positions + static_cast<size_t>(axis) * p.total_tokens + token)
-                     : place;
+  return p.positions ? p.positions[static_cast<size_t>(axis) * p.total_tokens + token] : place;
 }
 __device__ __forceinline__ int position(const RopeParams& p, int axis, int token, int place) {
   return min(max(raw_position(p, axis, token, place), 0), p.max_position - 1);
@@ -60,32 +59,33 @@ __device__ __forceinline__ uint4 from_float8(const float (&f)[8], Tag) {
                     pack2(f[6], f[7], kType));
 }
 
-// Rotates pairs j0 .. j0 + 7 of one token, in fp32, each result rounded once to the
-// storage type.  Half-split pairs: the first elements in a, the second ones in b;
-// interleaved: a and b are 16 consecutive elements, pair after pair.
+// One token's cosines and sines, each from its axis's row of the table, into `out`, by a warp.
+__device__ __forceinline__ void stage_row(const RopeParams& p, int token, int place, float* out,
+                                          int lane) {
+  const int half = p.rotary_dim / 2;
+  for (int j = lane; j < half; j += 32) {
+    const int axis = p.num_axes > 1 ? p.pair_axis[j] : 0;
+    const float* row =
+        p.cos_sin + static_cast<size_t>(position(p, axis, token, place)) * p.rotary_dim;
+    out[j] = row[j];
+    out[half + j] = row[half + j];
+  }
+}
+
+// Rotates 8 pairs of one token, in fp32, each result rounded once to the storage type.  cs:
+// their cosines, the sines rotary_dim / 2 further.  Half-split pairs: the first elements in a,
+// the second ones in b; interleaved: a and b are 16 consecutive elements, pair after pair.
 template <class Tag>
-__device__ __forceinline__ void rotate(const RopeParams& p, int token, int place, int j0, uint4& a,
-                                       uint4& b, Tag) {
+__device__ __forceinline__ void rotate(const RopeParams& p, const float* cs, uint4& a, uint4& b,
+                                       Tag) {
   const int half = p.rotary_dim / 2;
   float c[8], s[8];
-  if (p.num_axes == 1) {
-    const float* row =
-        p.cos_sin + static_cast<size_t>(position(p, 0, token, place)) * p.rotary_dim + j0;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + e));
-      const float4 w = __ldg(reinterpret_cast<const float4*>(row + half + e));
-      c[e] = u.x; c[e + 1] = u.y; c[e + 2] = u.z; c[e + 3] = u.w;
-      s[e] = w.x; s[e + 1] = w.y; s[e + 2] = w.z; s[e + 3] = w.w;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int at = position(p, p.pair_axis[j0 + e], token, place);
-      const float* row = p.cos_sin + static_cast<size_t>(at) * p.rotary_dim + j0 + e;
-      c[e] = __ldg(row);
-      s[e] = __ldg(row + half);
-    }
+  for (int e = 0; e < 8; e += 4) {
+    const float4 u = *reinterpret_cast<const float4*>(cs + e);
+    const float4 w = *reinterpret_cast<const float4*>(cs + half + e);
+    c[e] = u.x; c[e + 1] = u.y; c[e + 2] = u.z; c[e + 3] = u.w;
+    s[e] = w.x; s[e + 1] = w.y; s[e + 2] = w.z; s[e + 3] = w.w;
   }
   float fa[8], fb[8];
   to_float8(a, fa, Tag{});

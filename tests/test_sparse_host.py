@@ -94,7 +94,7 @@ def test_select_refuses(lib):
                dict(sink=3, recent=2), dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), dict(N=65536),
                dict(MB=1 << 28), dict(s=None), dict(sl=None), dict(out=None)):
         assert call(**kw) == INV, kw
-    assert call(MB=393217, bs=1) == UNS            # more blocks than a row may have
+    assert call(MB=131073, bs=1) == UNS            # more blocks than a row may have
 
 
 def test_attention_refuses(lib):
