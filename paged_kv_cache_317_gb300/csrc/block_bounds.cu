@@ -25,6 +25,16 @@ struct BoundsParams {
   int num_kv_heads, head_dim, block_size, max_blocks, num_blocks;
 };
 
+// A load that stays where it is written: left to itself the compiler moves the loads of a batch
+// towards their uses, to save registers (32 sequences of up to 16384 tokens: 108 us, 102 us so).
+__device__ __forceinline__ uint4 load(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <class Tag, int kBatch>
 __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -55,11 +65,12 @@ __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsP
     const int rows = min(p.block_size, L - b * p.block_size);
     const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
     const uint4* src = static_cast<const uint4*>(p.k_cache) + bh * p.block_size * pieces + x;
-    uint4 lo = *src, hi = lo;
+    uint4 lo, hi;
     for (int r0 = 0; r0 < rows; r0 += kBatch) {
       uint4 u[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) u[j] = src[static_cast<size_t>(min(r0 + j, rows - 1)) * pieces];
+      for (int j = 0; j < kBatch; ++j) u[j] = load(src + static_cast<size_t>(min(r0 + j, rows - 1)) * pieces);
+      if (r0 == 0) lo = hi = u[0];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         lo = min8(lo, u[j], Tag{});

@@ -51,16 +51,12 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int D>
-constexpr int stages_of() { return D == 256 ? 2 : 3; }
-template <int D>
-constexpr int smem_of() { return kWarps * stages_of<D>() * (D / 8) * 32 * 16; }
-
-template <class Tag, int D>
+// kStages: 16-block tiles in the ring; 1 where a warp has one tile, else 2 (48 contexts: 38.6 us
+// with 2, 42.7 us with 3, 63 us with 4: more warps on an SM count for more than deeper rings).
+template <class Tag, int D, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
   constexpr int kPieces = D / 8;         // 16-byte pieces of a row
   constexpr int kSteps = D / 32;         // pieces of a row that one lane takes
-  constexpr int kStages = stages_of<D>();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint4 ring[];
@@ -168,20 +164,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
   copy_wait<0>();
 }
 
-template <class Tag, int D>
-int launch(ScoreParams p, int num_seqs, cudaStream_t stream) {
-  // 64 blocks per warp, down to 16 while that leaves fewer than 8 warps for each SM
-  const auto warps = [&](int tiles) {
-    return (p.max_blocks + kRows * tiles - 1) / (kRows * tiles) * static_cast<long long>(p.num_kv_heads);
-  };
-  p.tiles = kMaxTiles;
-  while (p.tiles > 1 && warps(p.tiles) * num_seqs < 152 * 8) p.tiles /= 2;
-  const long long blocks = (warps(p.tiles) + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
-  constexpr int smem = smem_of<D>();
+template <class Tag, int D, int kStages>
+int launch(const ScoreParams& p, long long blocks, int num_seqs, cudaStream_t stream) {
+  constexpr int smem = kWarps * kStages * (D / 8) * 32 * 16;
   // on every launch that needs it (the attribute is lost with the context)
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(paged_block_scores_kernel<Tag, D>,
+      cudaFuncSetAttribute(paged_block_scores_kernel<Tag, D, kStages>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
@@ -194,9 +182,23 @@ int launch(ScoreParams p, int num_seqs, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_block_scores_kernel<Tag, D>, p) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, paged_block_scores_kernel<Tag, D, kStages>, p) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <class Tag, int D>
+int launch(ScoreParams p, int num_seqs, cudaStream_t stream) {
+  // 64 blocks per warp, down to 16 while that leaves fewer than 8 warps for each SM
+  const auto warps = [&](int tiles) {
+    return (p.max_blocks + kRows * tiles - 1) / (kRows * tiles) * static_cast<long long>(p.num_kv_heads);
+  };
+  p.tiles = kMaxTiles;
+  while (p.tiles > 1 && warps(p.tiles) * num_seqs < 152 * 8) p.tiles /= 2;
+  const long long blocks = (warps(p.tiles) + kWarps - 1) / kWarps;
+  if (blocks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  return p.tiles == 1 ? launch<Tag, D, 1>(p, blocks, num_seqs, stream)
+                      : launch<Tag, D, 2>(p, blocks, num_seqs, stream);
 }
 
 }  // namespace

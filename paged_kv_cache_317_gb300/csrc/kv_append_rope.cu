@@ -1,16 +1,17 @@
 // Append with rotary positions: one pass that rotates a step's queries and keys,
 // writes keys and values into their slots and keeps the touched blocks' key bounds.
 //
-// The work is cut into tiles: the new tokens of one sequence that fall into one
-// block.  A thread takes 16 dims (two 16-byte pieces, 8 rotary pairs) of one head of
-// q, k or v and walks the tile's rows, so that a key thread sees every new key of its
-// block and channel and holds their minimum and maximum in registers: the bounds need
-// no atomics and no second pass, and come out the same on every run.
-// The cosines and sines of a tile with several rows or axes are brought into shared
-// memory once for all of the thread block's heads, while the first rows are loading.
-// The rotation is 3 operations per element, the traffic one read and one write of
-// each q, k and v element: the kernel is bound by HBM for prompts and by latency for
-// decode steps.
+// A step of one token a sequence (kv_append_step_kernel): a thread takes 16 dims (two
+// 16-byte pieces, 8 rotary pairs) of one head of one token's q, k or v.  Bound by latency,
+// and by HBM for large batches.
+//
+// Prompts (kv_append_rope_kernel): the work is cut into tiles, the new tokens of one sequence
+// that fall into one block, and a thread block takes 8 heads of q, k or v of a tile.  A thread
+// keeps the cosines and sines of its row and 8 pairs in registers and goes over the heads, 4
+// at a time.  Rotated keys also go to shared memory, where each channel's minimum and maximum
+// over the tile's rows are taken: as the tile holds every new key of its block, the bounds
+// need no atomics and no second pass, and come out the same on every run.  One read and one
+// write of each element, 3 operations: bound by HBM.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -20,6 +21,8 @@ namespace pagedkv {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kHeads = 8;  // heads of a thread block, for prompts
+constexpr int kBatch = 4;  // heads that a thread loads at a time
 
 struct AppendRopeParams {
   const void* q;  // null: keys and values only
@@ -62,160 +65,210 @@ __device__ __forceinline__ long long first_slot(const AppendRopeParams& p, int s
   return static_cast<long long>(p.query_start[seq]) / p.block_size + 2ll * seq;
 }
 
-// kRows: rows of cosines and sines in shared memory; kBatch: rows that a thread loads at a time.
-// A step of one token a sequence needs one row of each, and leaves the SM to more threads (256 x
-// 40 heads: 7.0 us, against 8.5 us with the 16 and 4 of prompts).
-template <class Tag, int kRows, int kBatch>
+// What a thread block works on: `rows` new tokens of sequence `seq`, from row `token` of q, k
+// and v and place `place` of the sequence, all in its logical block `block`.
+struct Tile {
+  int seq, rows, token, place, block;
+};
+
+// The physical block of a tile; false (and recorded, by one thread of the tile) if it is none.
+__device__ __forceinline__ bool physical_block(const AppendRopeParams& p, const Tile& t, bool reports,
+                                               int& blk) {
+  blk = p.block_tables[static_cast<size_t>(t.seq) * p.max_blocks + t.block];
+  if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks)) return true;
+  if (reports) report_error(p.err, PA_ERR_BAD_BLOCK, t.seq, blk);
+  return false;
+}
+
+// The two pieces of dims that slice x of a head covers, and whether it is rotated.
+__device__ __forceinline__ bool dims_of(const RopeParams& r, int x, bool rotated, int& da, int& db) {
+  const int half = r.rotary_dim / 2;
+  da = 16 * x;
+  db = 16 * x + 8;
+  if (!rotated || 8 * x >= half) return false;
+  if (!r.interleaved) {
+    da = 8 * x;
+    db = 8 * x + half;
+  }
+  return true;
+}
+
+template <class Tag>
+__device__ __forceinline__ void merge_bounds(const AppendRopeParams& p, size_t at, uint4 lo, uint4 hi,
+                                             bool stored, Tag) {
+  using T = typename Tag::T;
+  uint4* mn = reinterpret_cast<uint4*>(static_cast<T*>(p.k_min) + at);
+  uint4* mx = reinterpret_cast<uint4*>(static_cast<T*>(p.k_max) + at);
+  *mn = stored ? min8(lo, *mn, Tag{}) : lo;
+  *mx = stored ? max8(hi, *mx, Tag{}) : hi;
+}
+
+// Six blocks an SM: 256 x 40 heads take 6.4 us, 7.0 us with the five that the compiler's own
+// choice of registers allows.
+template <class Tag>
+__global__ void __launch_bounds__(kThreads, 6) kv_append_step_kernel(const AppendRopeParams p) {
+  using T = typename Tag::T;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int seq = blockIdx.x;
+  Range rg;
+  if (!range_of(p, seq, rg)) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, rg.len);
+    return;
+  }
+  if (rg.count == 0) return;
+  const int per_head = p.head_dim / 16;
+  const int task = blockIdx.y * kThreads + threadIdx.x;
+  const int vhead = task / per_head, x = task - vhead * per_head;
+  if (vhead >= p.num_heads + 2 * p.num_kv_heads) return;
+  const int part = vhead < p.num_heads ? 0 : vhead < p.num_heads + p.num_kv_heads ? 1 : 2;
+  const int head = vhead - (part == 0 ? 0 : part == 1 ? p.num_heads : p.num_heads + p.num_kv_heads);
+  const Tile t{seq, 1, rg.first, rg.len - 1, (rg.len - 1) / p.block_size};
+  if (task == 0 && p.rope.cos_sin != nullptr) check_positions(p.rope, t.token, t.place, p.err);
+  int da, db, blk = 0;
+  const bool turn = dims_of(p.rope, x, part < 2, da, db);
+  if (part > 0 && !physical_block(p, t, part == 1 && head == 0 && x == 0, blk)) return;
+  const int row = t.place - t.block * p.block_size;
+
+  const size_t step = part == 0 ? p.q_stride : part == 1 ? p.k_stride : p.v_stride;
+  const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) + t.token * step +
+                 static_cast<size_t>(head) * p.head_dim;
+  const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
+  T* dst = part == 0 ? static_cast<T*>(p.q_out) +
+                           (static_cast<size_t>(t.token) * p.num_heads + head) * p.head_dim
+                     : static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
+                           (bh * p.block_size + row) * p.head_dim;
+  uint4 a = *reinterpret_cast<const uint4*>(src + da), b = *reinterpret_cast<const uint4*>(src + db);
+  if (turn) {
+    float c[8], s[8];
+    load_cos_sin(p.rope, t.token, t.place, 8 * x, c, s);
+    rotate(p.rope, c, s, a, b, Tag{});
+  }
+  *reinterpret_cast<uint4*>(dst + da) = a;
+  *reinterpret_cast<uint4*>(dst + db) = b;
+  if (part == 1 && p.k_min != nullptr) {  // rows below are in the stored bounds
+    merge_bounds(p, bh * p.head_dim + da, a, a, row > 0, Tag{});
+    merge_bounds(p, bh * p.head_dim + db, b, b, row > 0, Tag{});
+  }
+}
+
+template <class Tag>
 __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRopeParams p) {
   using T = typename Tag::T;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int slot = blockIdx.x;
-  int seq = slot, tile = 0;
-  if constexpr (kRows > 1) {
-    if (slot >= p.tiles) {  // check the sequences' ranges; tiles skip the bad ones silently
-      const int i = (slot - p.tiles) * kThreads + threadIdx.x;
-      Range r;
-      if (blockIdx.y == 0 && i < p.num_seqs && !range_of(p, i, r))
-        report_error(p.err, PA_ERR_BAD_SEQ_LEN, i, r.len);
-      return;
-    }
+  if (slot >= p.tiles) {  // check the sequences' ranges; tiles skip the bad ones silently
+    const int i = (slot - p.tiles) * kThreads + threadIdx.x;
+    Range r;
+    if (blockIdx.y == 0 && i < p.num_seqs && !range_of(p, i, r))
+      report_error(p.err, PA_ERR_BAD_SEQ_LEN, i, r.len);
+    return;
+  }
+  Tile t{};
+  {
     int lo = 0, hi = p.num_seqs - 1;  // the last sequence whose slots begin at or before this one
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first_slot(p, mid) <= slot) lo = mid;
       else hi = mid - 1;
     }
-    seq = lo;
-    const long long t = slot - first_slot(p, seq);
-    if (t < 0) return;
-    tile = static_cast<int>(t);
+    t.seq = lo;
+    const long long nth = slot - first_slot(p, t.seq);
+    Range rg;
+    if (nth < 0 || !range_of(p, t.seq, rg) || rg.count == 0) return;
+    const int place0 = rg.len - rg.count;  // place of the sequence's first new token
+    const long long block = place0 / p.block_size + nth;
+    const long long from = max(block * p.block_size, static_cast<long long>(place0));
+    const long long to = min((block + 1) * p.block_size, static_cast<long long>(rg.len));
+    if (from >= to) return;  // a slot without a tile
+    t.rows = static_cast<int>(to - from);
+    t.token = rg.first + static_cast<int>(from - place0);
+    t.place = static_cast<int>(from);
+    t.block = static_cast<int>(block);
   }
-  Range rg;
-  if (!range_of(p, seq, rg)) {
-    if (kRows == 1 && threadIdx.x == 0 && blockIdx.y == 0)
-      report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, rg.len);
-    return;
-  }
-  if (rg.count == 0) return;
-  const int place0 = rg.len - rg.count;  // place of the sequence's first new token
-  const int block = place0 / p.block_size + tile;  // logical block of this tile
-  const long long lo_place = max(static_cast<long long>(block) * p.block_size,
-                                 static_cast<long long>(place0));
-  const long long hi_place = min((static_cast<long long>(block) + 1) * p.block_size,
-                                 static_cast<long long>(rg.len));
-  if (lo_place >= hi_place) return;  // a slot without a tile
-  const int rows = static_cast<int>(hi_place - lo_place);
-  const int token0 = rg.first + static_cast<int>(lo_place - place0);
-  const int row0 = static_cast<int>(lo_place - static_cast<long long>(block) * p.block_size);
-
-  const bool staged = p.rope.cos_sin != nullptr && (rows > 1 || p.rope.num_axes > 1);
+  const int row0 = t.place - t.block * p.block_size;
   if (p.rope.cos_sin != nullptr && blockIdx.y == 0)
-    for (int r = threadIdx.x; r < rows; r += kThreads)
-      check_positions(p.rope, token0 + r, static_cast<int>(lo_place) + r, p.err);
+    for (int r = threadIdx.x; r < t.rows; r += kThreads)
+      check_positions(p.rope, t.token + r, t.place + r, p.err);
 
-  const int per_head = p.head_dim / 16;
-  const int task = blockIdx.y * kThreads + threadIdx.x;
-  const int vhead = task / per_head, x = task - vhead * per_head;
-  const bool idle = vhead >= p.num_heads + 2 * p.num_kv_heads;
-  const int part = vhead < p.num_heads ? 0 : vhead < p.num_heads + p.num_kv_heads ? 1 : 2;
-  const int head = vhead - (part == 0 ? 0 : part == 1 ? p.num_heads : p.num_heads + p.num_kv_heads);
-
-  // dims of the two pieces (pairs >= R/2: not turned)
-  const int half = p.rope.rotary_dim / 2;
-  int da = 16 * x, db = 16 * x + 8;
-  const bool turn = !idle && part < 2 && 8 * x < half;
-  if (turn && !p.rope.interleaved) {
-    da = 8 * x;
-    db = 8 * x + half;
-  }
-
+  // this block's heads
+  const int q_chunks = (p.num_heads + kHeads - 1) / kHeads;
+  const int kv_chunks = (p.num_kv_heads + kHeads - 1) / kHeads;
+  const int chunk = blockIdx.y;
+  const int part = chunk < q_chunks ? 0 : chunk < q_chunks + kv_chunks ? 1 : 2;
+  const int h0 = (part == 0 ? chunk : (chunk - q_chunks) % kv_chunks) * kHeads;
+  const int h1 = min(h0 + kHeads, part == 0 ? p.num_heads : p.num_kv_heads);
   int blk = 0;
-  bool store = !idle;
-  if (part > 0) {
-    blk = p.block_tables[static_cast<size_t>(seq) * p.max_blocks + block];
-    if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-      if (part == 1 && head == 0 && x == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
-      store = false;
-    }
-  }
+  if (part > 0 && !physical_block(p, t, part == 1 && h0 == 0 && threadIdx.x == 0, blk)) return;
 
-  const T* src;
-  T* dst;
-  size_t src_step, dst_step;
-  if (part == 0) {
-    src_step = p.q_stride;
-    dst_step = static_cast<size_t>(p.num_heads) * p.head_dim;
-    src = static_cast<const T*>(p.q) + token0 * src_step + static_cast<size_t>(head) * p.head_dim;
-    dst = static_cast<T*>(p.q_out) + token0 * dst_step + static_cast<size_t>(head) * p.head_dim;
-  } else {
-    src_step = part == 1 ? p.k_stride : p.v_stride;
-    dst_step = p.head_dim;
-    src = static_cast<const T*>(part == 1 ? p.k : p.v) + token0 * src_step +
-          static_cast<size_t>(head) * p.head_dim;
-    dst = static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
-          ((static_cast<size_t>(blk) * p.num_kv_heads + head) * p.block_size + row0) * p.head_dim;
-  }
+  // Thread (x, r, h): slice x of the head, row r of `span` at a time, and of the heads every
+  // `lanes`-th from h on.
+  const int per_head = p.head_dim / 16;
+  int span = 1;
+  while (2 * span * per_head <= kThreads && span < t.rows) span *= 2;
+  const int lanes = kThreads / (span * per_head);
+  const int x = threadIdx.x % per_head, r = threadIdx.x / per_head % span;
+  const int h = threadIdx.x / (per_head * span);
+  int da, db;
+  const bool turn = dims_of(p.rope, x, part < 2, da, db);
+  const bool bounds = part == 1 && p.k_min != nullptr;
+  const int pieces = p.head_dim / 8;
+  __shared__ uint4 keys[kThreads * kBatch * 2];  // [head of the batch][row][piece]
 
-  __shared__ __align__(16) float table[kRows * 256];
-  const bool bounds = part == 1 && p.k_min != nullptr && store;
-  uint4 lo[2], hi[2];
-  for (int r0 = 0; r0 < rows; r0 += kBatch) {
-    uint4 a[kBatch], b[kBatch];
+  const size_t step = part == 0 ? p.q_stride : part == 1 ? p.k_stride : p.v_stride;
+  const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v);
+  T* dst = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_cache : p.v_cache);
+  for (int pass = 0; pass < t.rows; pass += span) {
+    const bool active = pass + r < t.rows && h < lanes;
+    const int token = t.token + pass + r;
+    float c[8], s[8];
+    if (turn && active) load_cos_sin(p.rope, token, t.place + pass + r, 8 * x, c, s);
+    for (int hb = h0; hb < h1; hb += kBatch * lanes) {
+      uint4 a[kBatch], b[kBatch];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      if (store && r0 + e < rows) {
-        a[e] = *reinterpret_cast<const uint4*>(src + (r0 + e) * src_step + da);
-        b[e] = *reinterpret_cast<const uint4*>(src + (r0 + e) * src_step + db);
-      }
-    }
-    if (staged && r0 % kRows == 0) {  // rows r0 .. r0 + kRows - 1
-      if (r0 > 0) __syncthreads();
-      for (int r = threadIdx.x >> 5; r < min(kRows, rows - r0); r += kThreads / 32)
-        stage_row(p.rope, token0 + r0 + r, static_cast<int>(lo_place) + r0 + r,
-                  table + r * p.rope.rotary_dim, threadIdx.x & 31);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      if (store && r0 + e < rows) {
-        if (turn) {
-          const float* cs =
-              staged ? table + (r0 % kRows + e) * p.rope.rotary_dim
-                     : p.rope.cos_sin + static_cast<size_t>(position(p.rope, 0, token0, static_cast<int>(lo_place))) *
-                                            p.rope.rotary_dim;
-          rotate(p.rope, cs + 8 * x, a[e], b[e], Tag{});
+      for (int i = 0; i < kBatch; ++i) {
+        const int head = hb + h + lanes * i;
+        if (active && head < h1) {
+          const T* from = src + token * step + static_cast<size_t>(head) * p.head_dim;
+          a[i] = *reinterpret_cast<const uint4*>(from + da);
+          b[i] = *reinterpret_cast<const uint4*>(from + db);
         }
-        *reinterpret_cast<uint4*>(dst + (r0 + e) * dst_step + da) = a[e];
-        *reinterpret_cast<uint4*>(dst + (r0 + e) * dst_step + db) = b[e];
-        if (bounds) {
-          if (r0 + e == 0) {
-            lo[0] = hi[0] = a[e];
-            lo[1] = hi[1] = b[e];
-          } else {
-            lo[0] = min8(lo[0], a[e], Tag{});
-            lo[1] = min8(lo[1], b[e], Tag{});
-            hi[0] = max8(hi[0], a[e], Tag{});
-            hi[1] = max8(hi[1], b[e], Tag{});
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int head = hb + h + lanes * i;
+        if (active && head < h1) {
+          if (turn) rotate(p.rope, c, s, a[i], b[i], Tag{});
+          const size_t row =
+              part == 0 ? static_cast<size_t>(token) * p.num_heads + head
+                        : (static_cast<size_t>(blk) * p.num_kv_heads + head) * p.block_size + row0 + pass + r;
+          *reinterpret_cast<uint4*>(dst + row * p.head_dim + da) = a[i];
+          *reinterpret_cast<uint4*>(dst + row * p.head_dim + db) = b[i];
+          if (bounds) {
+            uint4* k = keys + ((h + lanes * i) * span + r) * pieces;
+            k[da / 8] = a[i];
+            k[db / 8] = b[i];
           }
         }
       }
-    }
-  }
-  if (bounds) {
-    const size_t at = (static_cast<size_t>(blk) * p.num_kv_heads + head) * p.head_dim;
-    uint4* mn[2] = {reinterpret_cast<uint4*>(static_cast<T*>(p.k_min) + at + da),
-                    reinterpret_cast<uint4*>(static_cast<T*>(p.k_min) + at + db)};
-    uint4* mx[2] = {reinterpret_cast<uint4*>(static_cast<T*>(p.k_max) + at + da),
-                    reinterpret_cast<uint4*>(static_cast<T*>(p.k_max) + at + db)};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (row0 > 0) {  // rows below are in the stored bounds
-        lo[e] = min8(lo[e], *mn[e], Tag{});
-        hi[e] = max8(hi[e], *mx[e], Tag{});
+      if (bounds) {
+        __syncthreads();
+        const int n = min(span, t.rows - pass);
+        for (int j = threadIdx.x; j < min(kBatch * lanes, h1 - hb) * pieces; j += kThreads) {
+          const int slot_head = j / pieces, piece = j % pieces;
+          const uint4* k = keys + slot_head * span * pieces + piece;
+          uint4 mn = k[0], mx = k[0];
+          for (int i = 1; i < n; ++i) {
+            mn = min8(mn, k[i * pieces], Tag{});
+            mx = max8(mx, k[i * pieces], Tag{});
+          }
+          // Rows below are in the stored bounds; those of an earlier pass this thread stored.
+          merge_bounds(p, (static_cast<size_t>(blk) * p.num_kv_heads + hb + slot_head) * p.head_dim + 8 * piece,
+                       mn, mx, row0 + pass > 0, Tag{});
+        }
+        __syncthreads();
       }
-      *mn[e] = lo[e];
-      *mx[e] = hi[e];
     }
   }
 }
@@ -289,12 +342,15 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.rope.total_tokens = total_tokens;
-  // one token a sequence: a tile each; otherwise the slots of first_slot, and behind
-  // them blocks that check the ranges
-  p.tiles = max_query_len == 1 ? num_seqs : total_tokens / block_size + 2 * num_seqs;
-  const int checkers = max_query_len == 1 ? 0 : (num_seqs + kThreads - 1) / kThreads;
-  const long long tasks = (num_heads + 2ll * num_kv_heads) * (head_dim / 16);
-  const long long groups = (tasks + kThreads - 1) / kThreads;
+  // One token a sequence: a thread for 16 dims of each head.  Otherwise the tile slots of
+  // first_slot, with behind them blocks that check the ranges, by chunks of heads.
+  const bool one = max_query_len == 1;
+  p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;
+  const int checkers = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
+  const auto chunks = [](long long n, long long size) { return (n + size - 1) / size; };
+  const long long groups =
+      one ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads)
+          : chunks(num_heads, kHeads) + 2 * chunks(num_kv_heads, kHeads);
   if (groups > 65535) return PA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + checkers), static_cast<unsigned>(groups));
@@ -306,11 +362,11 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
-  if (max_query_len == 1)
-    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<BF16, 1, 1>, p)
-                         : cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<F16, 1, 1>, p);
+  if (one)
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_step_kernel<BF16>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_append_step_kernel<F16>, p);
   else
-    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<BF16, 16, 4>, p)
-                         : cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<F16, 16, 4>, p);
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<BF16>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<F16>, p);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -426,16 +426,52 @@ size_t smem_bytes(int stages) {
   return kHeader + kAlign + (ring > join ? ring : join);
 }
 
+// Thread blocks per row and stages per ring: of the choices, the one with the least time by a
+// model of the launch.  `slots` blocks are resident at a time and share the memory's rate; the
+// blocks of the last, partly filled wave run at the rate that their own copies in flight allow.
+// Clusters wait for their slowest block and for free places on neighbouring SMs, which costs an
+// eighth, so only launches of few rows have them.  On GB300 (D = 128, us):
+//   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
+//   1280 rows of 0.5 MB:  ranks 1 with stages 2: 100, 3: 106 (two blocks an SM instead of three)
+struct Shape {
+  int ranks, stages;
+};
+Shape shape_for(long long rows, double row_bytes, size_t smem2, size_t smem3, double stage_bytes,
+                int most_per_sm) {
+  constexpr double kRate = 6.8e6, kLatency = 1.5;  // bytes per us; us from a copy's start to its reuse
+  Shape best{1, 2};
+  double least = 1e30;
+  for (int stages = 2; stages <= 3; ++stages) {
+    const size_t smem = stages == 2 ? smem2 : smem3;
+    if (smem > 227 * 1024) continue;
+    const int fit = static_cast<int>(228 * 1024 / (smem + 1024));
+    const long long slots = 152ll * (fit < most_per_sm ? fit : most_per_sm);
+    for (int ranks = 1; ranks <= kMaxCluster; ranks *= 2) {
+      const long long blocks = rows * ranks, full = blocks / slots, rest = blocks - full * slots;
+      const double bytes = row_bytes / ranks, alone = bytes * kLatency / (kWarps * stages * stage_bytes);
+      const double shared = rest * bytes / kRate;
+      double us = full * slots * bytes / kRate + (rest == 0 ? 0. : shared > alone ? shared : alone);
+      if (ranks > 1) us = us * 1.125 + 1.;
+      if (us < least) {
+        least = us;
+        best = {ranks, stages};
+      }
+    }
+  }
+  return best;
+}
+
 template <class Tag, int D, int NT>
 int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seqs,
            cudaStream_t stream) {
   p.tiles = (p.group + 8 * NT - 1) / (8 * NT);
   const long long rows = static_cast<long long>(num_seqs) * p.num_kv_heads * p.tiles;
-  p.stages = D == 256 ? 2 : 3;
   const long long held = p.num_selected < p.max_blocks ? p.num_selected : p.max_blocks;
   const long long chunks = (held * p.block_size + kChunk - 1) / kChunk;
-  int ranks = 1;
-  while (ranks < kMaxCluster && rows * ranks < 152 * 4 && chunks >= 4ll * kWarps * ranks) ranks *= 2;
+  const Shape shape = shape_for(rows, chunks * 2 * Geo<D>::kTileBytes, smem_bytes<D, NT>(2),
+                                smem_bytes<D, NT>(3), 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4);
+  const int ranks = shape.ranks;
+  p.stages = shape.stages;
   if (rows * ranks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
   // the caches as [D / 64][rows][64]: one box is a chunk, or half of one with 8-token blocks
   const cuuint64_t cache_rows = static_cast<cuuint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;

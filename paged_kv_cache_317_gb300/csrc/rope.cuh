@@ -13,7 +13,9 @@ struct RopeParams {
   const int32_t* positions;
   int max_position, rotary_dim, interleaved, num_axes, total_tokens;
   uint8_t pair_axis[128];  // head_dim <= 256
+  uint8_t quad_axis[32];   // the axis of pairs 4 i .. 4 i + 3, kMixed if they differ
 };
+constexpr uint8_t kMixed = 255;
 
 // Checks a caller's pa_rope and copies it; returns a pa_status.
 inline int rope_params(const pa_rope& r, int head_dim, RopeParams& p) {
@@ -32,6 +34,8 @@ inline int rope_params(const pa_rope& r, int head_dim, RopeParams& p) {
     for (int j = 0; j < r.rotary_dim / 2; ++j) {
       if (r.pair_axis[j] >= r.num_axes) return PA_ERR_INVALID_ARG;
       p.pair_axis[j] = r.pair_axis[j];
+      if (j % 4 == 0) p.quad_axis[j / 4] = r.pair_axis[j];
+      else if (p.quad_axis[j / 4] != r.pair_axis[j]) p.quad_axis[j / 4] = kMixed;
     }
   }
   return PA_OK;
@@ -59,34 +63,38 @@ __device__ __forceinline__ uint4 from_float8(const float (&f)[8], Tag) {
                     pack2(f[6], f[7], kType));
 }
 
-// One token's cosines and sines, each from its axis's row of the table, into `out`, by a warp.
-__device__ __forceinline__ void stage_row(const RopeParams& p, int token, int place, float* out,
-                                          int lane) {
+// The cosines and sines of pairs j0 .. j0 + 7 of one token, each from its axis's row.
+__device__ __forceinline__ void load_cos_sin(const RopeParams& p, int token, int place, int j0,
+                                             float (&c)[8], float (&s)[8]) {
   const int half = p.rotary_dim / 2;
-  for (int j = lane; j < half; j += 32) {
-    const int axis = p.num_axes > 1 ? p.pair_axis[j] : 0;
-    const float* row =
-        p.cos_sin + static_cast<size_t>(position(p, axis, token, place)) * p.rotary_dim;
-    out[j] = row[j];
-    out[half + j] = row[half + j];
+#pragma unroll
+  for (int e = 0; e < 8; e += 4) {
+    const int axis = p.num_axes == 1 ? 0 : p.quad_axis[(j0 + e) / 4];
+    if (axis != kMixed) {
+      const float* row = p.cos_sin +
+                         static_cast<size_t>(position(p, axis, token, place)) * p.rotary_dim + j0 + e;
+      const float4 u = *reinterpret_cast<const float4*>(row);
+      const float4 w = *reinterpret_cast<const float4*>(row + half);
+      c[e] = u.x; c[e + 1] = u.y; c[e + 2] = u.z; c[e + 3] = u.w;
+      s[e] = w.x; s[e + 1] = w.y; s[e + 2] = w.z; s[e + 3] = w.w;
+    } else {
+#pragma unroll
+      for (int i = e; i < e + 4; ++i) {
+        const int at = position(p, p.pair_axis[j0 + i], token, place);
+        const float* row = p.cos_sin + static_cast<size_t>(at) * p.rotary_dim + j0 + i;
+        c[i] = row[0];
+        s[i] = row[half];
+      }
+    }
   }
 }
 
-// Rotates 8 pairs of one token, in fp32, each result rounded once to the storage type.  cs:
-// their cosines, the sines rotary_dim / 2 further.  Half-split pairs: the first elements in a,
-// the second ones in b; interleaved: a and b are 16 consecutive elements, pair after pair.
+// Rotates 8 pairs of one token, in fp32, each result rounded once to the storage type.
+// Half-split pairs: the first elements in a, the second ones in b; interleaved: a and b are 16
+// consecutive elements, pair after pair.
 template <class Tag>
-__device__ __forceinline__ void rotate(const RopeParams& p, const float* cs, uint4& a, uint4& b,
-                                       Tag) {
-  const int half = p.rotary_dim / 2;
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; e += 4) {
-    const float4 u = *reinterpret_cast<const float4*>(cs + e);
-    const float4 w = *reinterpret_cast<const float4*>(cs + half + e);
-    c[e] = u.x; c[e + 1] = u.y; c[e + 2] = u.z; c[e + 3] = u.w;
-    s[e] = w.x; s[e + 1] = w.y; s[e + 2] = w.z; s[e + 3] = w.w;
-  }
+__device__ __forceinline__ void rotate(const RopeParams& p, const float (&c)[8], const float (&s)[8],
+                                       uint4& a, uint4& b, Tag) {
   float fa[8], fb[8];
   to_float8(a, fa, Tag{});
   to_float8(b, fb, Tag{});
