@@ -37,9 +37,9 @@ __device__ __forceinline__ uint4 load(const uint4* p) {
 
 template <class Tag, int kBatch>
 __global__ void __launch_bounds__(kThreads) kv_block_bounds_kernel(const BoundsParams p) {
+  const int seq = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int seq = blockIdx.y;
   const int L = p.seq_lens[seq];
   if (L < 0 || L > static_cast<long long>(p.max_blocks) * p.block_size) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);

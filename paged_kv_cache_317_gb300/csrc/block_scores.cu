@@ -57,14 +57,14 @@ template <class Tag, int D, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
   constexpr int kPieces = D / 8;         // 16-byte pieces of a row
   constexpr int kSteps = D / 32;         // pieces of a row that one lane takes
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint4 ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.y;
   const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
   const int head = static_cast<int>(item % p.num_kv_heads);
   const long long b0 = item / p.num_kv_heads * (kRows * p.tiles);  // the warp's first block
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (b0 >= p.max_blocks) return;
   // Block numbers of blocks b0 + lane and b0 + 32 + lane, fetched along with the length,
   // before it says which ones count.

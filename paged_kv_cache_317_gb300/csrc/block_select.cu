@@ -79,9 +79,9 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int head = blockIdx.x / ranks, seq = blockIdx.y;
   for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
+  const size_t row = static_cast<size_t>(seq) * p.num_kv_heads + head;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const size_t row = static_cast<size_t>(seq) * p.num_kv_heads + head;
   int L = p.seq_lens[seq];
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {

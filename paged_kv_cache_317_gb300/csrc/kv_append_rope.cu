@@ -6,7 +6,7 @@
 // and by HBM for large batches.
 //
 // Prompts (kv_append_rope_kernel): the work is cut into tiles, the new tokens of one sequence
-// that fall into one block, and a thread block takes 8 heads of q, k or v of a tile.  A thread
+// that fall into one block, and a thread block takes up to 32 heads of q, k or v of a tile.  A thread
 // keeps the cosines and sines of its row and 8 pairs in registers and goes over the heads, 4
 // at a time.  Rotated keys also go to shared memory, where each channel's minimum and maximum
 // over the tile's rows are taken: as the tile holds every new key of its block, the bounds
@@ -21,7 +21,6 @@ namespace pagedkv {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHeads = 8;  // heads of a thread block, for prompts
 constexpr int kBatch = 4;  // heads that a thread loads at a time
 
 struct AppendRopeParams {
@@ -41,6 +40,7 @@ struct AppendRopeParams {
   int total_tokens, max_query_len, num_seqs, num_heads, num_kv_heads, head_dim;
   int block_size, max_blocks, num_blocks;
   int tiles;  // tile slots of the grid; blocks past them check the sequences
+  int heads;  // of a thread block, for prompts
   RopeParams rope;
 };
 
@@ -71,10 +71,12 @@ struct Tile {
   int seq, rows, token, place, block;
 };
 
-// The physical block of a tile; false (and recorded, by one thread of the tile) if it is none.
-__device__ __forceinline__ bool physical_block(const AppendRopeParams& p, const Tile& t, bool reports,
-                                               int& blk) {
-  blk = p.block_tables[static_cast<size_t>(t.seq) * p.max_blocks + t.block];
+__device__ __forceinline__ int table_entry(const AppendRopeParams& p, const Tile& t) {
+  return p.block_tables[static_cast<size_t>(t.seq) * p.max_blocks + t.block];
+}
+// Whether a table entry names a block; if not it is recorded, by one thread of the tile.
+__device__ __forceinline__ bool is_block(const AppendRopeParams& p, const Tile& t, int blk,
+                                         bool reports) {
   if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.num_blocks)) return true;
   if (reports) report_error(p.err, PA_ERR_BAD_BLOCK, t.seq, blk);
   return false;
@@ -108,42 +110,43 @@ __device__ __forceinline__ void merge_bounds(const AppendRopeParams& p, size_t a
 template <class Tag>
 __global__ void __launch_bounds__(kThreads, 6) kv_append_step_kernel(const AppendRopeParams p) {
   using T = typename Tag::T;
+  const int seq = blockIdx.x;
+  const int per_head = p.head_dim / 16;
+  const int task = blockIdx.y * kThreads + threadIdx.x;
+  const int vhead = task / per_head, x = task - vhead * per_head;
+  const int part = vhead < p.num_heads ? 0 : vhead < p.num_heads + p.num_kv_heads ? 1 : 2;
+  const int head = vhead - (part == 0 ? 0 : part == 1 ? p.num_heads : p.num_heads + p.num_kv_heads);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int seq = blockIdx.x;
+  if (vhead >= p.num_heads + 2 * p.num_kv_heads) return;
   Range rg;
   if (!range_of(p, seq, rg)) {
     if (threadIdx.x == 0 && blockIdx.y == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, rg.len);
     return;
   }
   if (rg.count == 0) return;
-  const int per_head = p.head_dim / 16;
-  const int task = blockIdx.y * kThreads + threadIdx.x;
-  const int vhead = task / per_head, x = task - vhead * per_head;
-  if (vhead >= p.num_heads + 2 * p.num_kv_heads) return;
-  const int part = vhead < p.num_heads ? 0 : vhead < p.num_heads + p.num_kv_heads ? 1 : 2;
-  const int head = vhead - (part == 0 ? 0 : part == 1 ? p.num_heads : p.num_heads + p.num_kv_heads);
   const Tile t{seq, 1, rg.first, rg.len - 1, (rg.len - 1) / p.block_size};
   if (task == 0 && p.rope.cos_sin != nullptr) check_positions(p.rope, t.token, t.place, p.err);
-  int da, db, blk = 0;
+  int da, db;
   const bool turn = dims_of(p.rope, x, part < 2, da, db);
-  if (part > 0 && !physical_block(p, t, part == 1 && head == 0 && x == 0, blk)) return;
+  const int blk = part > 0 ? table_entry(p, t) : 0;
   const int row = t.place - t.block * p.block_size;
 
   const size_t step = part == 0 ? p.q_stride : part == 1 ? p.k_stride : p.v_stride;
   const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) + t.token * step +
                  static_cast<size_t>(head) * p.head_dim;
-  const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
-  T* dst = part == 0 ? static_cast<T*>(p.q_out) +
-                           (static_cast<size_t>(t.token) * p.num_heads + head) * p.head_dim
-                     : static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
-                           (bh * p.block_size + row) * p.head_dim;
   uint4 a = *reinterpret_cast<const uint4*>(src + da), b = *reinterpret_cast<const uint4*>(src + db);
   if (turn) {
     float c[8], s[8];
     load_cos_sin(p.rope, t.token, t.place, 8 * x, c, s);
     rotate(p.rope, c, s, a, b, Tag{});
   }
+  if (part > 0 && !is_block(p, t, blk, part == 1 && head == 0 && x == 0)) return;
+  const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
+  T* dst = part == 0 ? static_cast<T*>(p.q_out) +
+                           (static_cast<size_t>(t.token) * p.num_heads + head) * p.head_dim
+                     : static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
+                           (bh * p.block_size + row) * p.head_dim;
   *reinterpret_cast<uint4*>(dst + da) = a;
   *reinterpret_cast<uint4*>(dst + db) = b;
   if (part == 1 && p.k_min != nullptr) {  // rows below are in the stored bounds
@@ -167,11 +170,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
   }
   Tile t{};
   {
-    int lo = 0, hi = p.num_seqs - 1;  // the last sequence whose slots begin at or before this one
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first_slot(p, mid) <= slot) lo = mid;
-      else hi = mid - 1;
+    // the last sequence whose slots begin at or before this one: each warp looks at 32 at once
+    int lo = 0, size = p.num_seqs;
+    while (size > 1) {
+      const int step = (size + 31) / 32, at = lo + static_cast<int>(threadIdx.x & 31) * step;
+      const bool before = at < lo + size && first_slot(p, at) <= slot;
+      const int n = max(__popc(__ballot_sync(kFullMask, before)), 1);
+      size = min(step, lo + size - (lo + (n - 1) * step));
+      lo += (n - 1) * step;
     }
     t.seq = lo;
     const long long nth = slot - first_slot(p, t.seq);
@@ -193,14 +199,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
       check_positions(p.rope, t.token + r, t.place + r, p.err);
 
   // this block's heads
-  const int q_chunks = (p.num_heads + kHeads - 1) / kHeads;
-  const int kv_chunks = (p.num_kv_heads + kHeads - 1) / kHeads;
+  const int q_chunks = (p.num_heads + p.heads - 1) / p.heads;
+  const int kv_chunks = (p.num_kv_heads + p.heads - 1) / p.heads;
   const int chunk = blockIdx.y;
   const int part = chunk < q_chunks ? 0 : chunk < q_chunks + kv_chunks ? 1 : 2;
-  const int h0 = (part == 0 ? chunk : (chunk - q_chunks) % kv_chunks) * kHeads;
-  const int h1 = min(h0 + kHeads, part == 0 ? p.num_heads : p.num_kv_heads);
-  int blk = 0;
-  if (part > 0 && !physical_block(p, t, part == 1 && h0 == 0 && threadIdx.x == 0, blk)) return;
+  const int h0 = (part == 0 ? chunk : (chunk - q_chunks) % kv_chunks) * p.heads;
+  const int h1 = min(h0 + p.heads, part == 0 ? p.num_heads : p.num_kv_heads);
+  const int blk = part > 0 ? table_entry(p, t) : 0;
 
   // Thread (x, r, h): slice x of the head, row r of `span` at a time, and of the heads every
   // `lanes`-th from h on.
@@ -223,7 +228,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
     const bool active = pass + r < t.rows && h < lanes;
     const int token = t.token + pass + r;
     float c[8], s[8];
-    if (turn && active) load_cos_sin(p.rope, token, t.place + pass + r, 8 * x, c, s);
     for (int hb = h0; hb < h1; hb += kBatch * lanes) {
       uint4 a[kBatch], b[kBatch];
 #pragma unroll
@@ -234,6 +238,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
           a[i] = *reinterpret_cast<const uint4*>(from + da);
           b[i] = *reinterpret_cast<const uint4*>(from + db);
         }
+      }
+      if (hb == h0) {  // with the first loads on their way
+        if (turn && active) load_cos_sin(p.rope, token, t.place + pass + r, 8 * x, c, s);
+        if (pass == 0 && part > 0 && !is_block(p, t, blk, part == 1 && h0 == 0 && threadIdx.x == 0))
+          return;
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -348,9 +357,13 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;
   const int checkers = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
   const auto chunks = [](long long n, long long size) { return (n + size - 1) / size; };
+  const auto head_chunks = [&] { return chunks(num_heads, p.heads) + 2 * chunks(num_kv_heads, p.heads); };
+  // 32 heads a thread block, down to 8 while that leaves fewer than 8 blocks for each SM (24
+  // prompts of up to 700 tokens, 32 + 2 x 8 heads: 43.6 us with 32, 44.5 with 16, 47.4 with 8)
+  p.heads = 32;
+  while (!one && p.heads > 8 && (total_tokens / block_size + 1) * head_chunks() < 152 * 8) p.heads /= 2;
   const long long groups =
-      one ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads)
-          : chunks(num_heads, kHeads) + 2 * chunks(num_kv_heads, kHeads);
+      one ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads) : head_chunks();
   if (groups > 65535) return PA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + checkers), static_cast<unsigned>(groups));

@@ -54,11 +54,8 @@ struct SparseParams {
 };
 
 // Partials of a column: m = running maximum (NaN once a logit was), l = sum of 2^(s - m);
-// m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity).  The weight
-// of a partial in a join whose maximum is M:
-__device__ __forceinline__ float weight_of(float m, float M) {
-  return m == -INFINITY ? 0.f : exp2f(m - M);
-}
+// m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity), which have
+// no weight in a join.
 // 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
 __device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
   if (M == -INFINITY) return tokens ? NAN : 0.f;
@@ -78,8 +75,10 @@ __global__ void __launch_bounds__(kWarps * 32)
   using Gm = Geo<D>;
   using T = typename Tag::T;
   constexpr int kCols = 8 * NT;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {  // arguments, not memory of the kernel before
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+  }
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
@@ -90,14 +89,6 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
   const int cols = min(kCols, p.group - tile * kCols);
   const size_t q0 = static_cast<size_t>(seq) * p.num_heads + head * p.group + tile * kCols;
-
-  int L = p.seq_lens[seq];
-  const int cap = p.max_blocks * p.block_size;
-  if (L < 0 || L > cap) {
-    if (threadIdx.x == 0 && rank == 0 && head == 0 && tile == 0)
-      report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
-    L = min(max(L, 0), cap);
-  }
 
   uint64_t* full = reinterpret_cast<uint64_t*>(smem) + warp * kMaxStages;
   int* rows_of = reinterpret_cast<int*>(smem + kWarps * kMaxStages * 8) + warp * kMaxStages;
@@ -110,6 +101,10 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   __syncwarp();
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int L = p.seq_lens[seq];
+
   // ------------------------------------------------------- the warp's chunks
   // Chunk c of a row is 16 tokens of list entry c / (bs / 16), or with 8-token blocks
   // entries 2 c and 2 c + 1.  This warp takes c = me, me + all, ...; its lanes look up 32 of
@@ -117,14 +112,32 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int me = rank * kWarps + warp, all = ranks * kWarps;
   const bool small = p.block_size == 8;
   const int sub = small ? 1 : p.block_size / kChunk;
-  const long long chunks = small ? (p.num_selected + 1) / 2
-                                 : static_cast<long long>(p.num_selected) * sub;
+  const int chunks = small ? (p.num_selected + 1) / 2 : p.num_selected * sub;
   const int32_t* list = p.selected + static_cast<size_t>(sh) * p.num_selected;
   const int32_t* table = p.block_tables + static_cast<size_t>(seq) * p.max_blocks;
-  // Row coordinate of (entry e, its 16-token part) in the cache seen as rows of D, and the
-  // number of tokens there (0: none).
-  auto look_up = [&](int e, int part, int height, int& y) -> int {
-    const int b = list[e];
+  int next = me;  // chunk of lane 0 at the next look-up
+  int b_lo, b_hi, blk_lo, blk_hi;
+  // List entries and block numbers of the next 32 chunks.  The length is not needed for them.
+  auto fetch = [&]() {
+    const int c = next + lane * all;
+    b_lo = b_hi = -1;
+    if (c < chunks) {
+      b_lo = list[small ? 2 * c : c / sub];
+      if (small && 2 * c + 1 < p.num_selected) b_hi = list[2 * c + 1];
+    }
+    blk_lo = static_cast<unsigned>(b_lo) < static_cast<unsigned>(p.max_blocks) ? table[b_lo] : 0;
+    blk_hi = static_cast<unsigned>(b_hi) < static_cast<unsigned>(p.max_blocks) ? table[b_hi] : 0;
+  };
+  fetch();
+  const int cap = p.max_blocks * p.block_size;
+  if (L < 0 || L > cap) {
+    if (threadIdx.x == 0 && rank == 0 && head == 0 && tile == 0)
+      report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
+    L = min(max(L, 0), cap);
+  }
+  // The tokens of block b from its row 16 part on, at most `height`, and their row in the cache
+  // seen as rows of D.
+  auto rows_in = [&](int b, int blk, int part, int height, int& y) -> int {
     if (b < -1 || b >= p.max_blocks) {
       if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, sh, b);
       return 0;
@@ -132,7 +145,6 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (b < 0) return 0;
     const int rows = min(height, L - b * p.block_size - part * kChunk);
     if (rows <= 0) return 0;
-    int blk = table[b];
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
       if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       blk = 0;
@@ -140,26 +152,25 @@ __global__ void __launch_bounds__(kWarps * 32)
     y = (blk * p.num_kv_heads + head) * p.block_size + part * kChunk;
     return rows;
   };
-  long long next = me;
   unsigned mask = 0;
   int y_lo = 0, y_hi = 0, rows_lo = 0, rows_hi = 0;
+  bool fetched = true;
   auto refill = [&]() {
     while (mask == 0 && next < chunks) {
-      const long long c = next + static_cast<long long>(lane) * all;
+      if (!fetched) fetch();
+      fetched = false;
+      const int c = next + lane * all;
       rows_lo = rows_hi = 0;
-      if (c < chunks) {
-        if (small) {
-          const int e = static_cast<int>(2 * c);
-          rows_lo = look_up(e, 0, 8, y_lo);
-          if (e + 1 < p.num_selected) rows_hi = look_up(e + 1, 0, 8, y_hi);
-        } else {
-          const int rows = look_up(static_cast<int>(c / sub), static_cast<int>(c % sub), 16, y_lo);
-          rows_lo = min(rows, 8);
-          rows_hi = rows - rows_lo;
-        }
+      if (small) {
+        rows_lo = rows_in(b_lo, blk_lo, 0, 8, y_lo);
+        rows_hi = rows_in(b_hi, blk_hi, 0, 8, y_hi);
+      } else {
+        const int rows = rows_in(b_lo, blk_lo, c % sub, 16, y_lo);
+        rows_lo = min(rows, 8);
+        rows_hi = rows - rows_lo;
       }
       mask = __ballot_sync(kFullMask, rows_lo + rows_hi > 0);
-      next += 32ll * all;
+      next += 32 * all;
     }
   };
   // Starts the copies of the next chunk into a stage; false when there is none.
@@ -353,27 +364,40 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
   __syncthreads();
-  auto join = [&](auto ml_of, auto o_of, int n, int col, int d, float& M, float& sum, bool& tokens) {
+  // Column col, channels d .. d + 3 of the first n of up to kMost partials; their loads do not
+  // wait for one another.
+  auto join = [&](auto most, auto ml_of, auto o_of, int n, int col, int d, float& M, float& sum,
+                  bool& tokens) {
+    constexpr int kMost = decltype(most)::value;
+    float2 ml[kMost];
+    float4 v[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      ml[i] = i < n ? ml_of(i, col) : make_float2(-INFINITY, 0.f);
+      if (i < n) v[i] = o_of(i, col, d);
+    }
     M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) M = max_nan(M, ml[i].x);
     sum = 0.f;
     tokens = false;
-    for (int i = 0; i < n; ++i) M = max_nan(M, ml_of(i, col).x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float2 ml = ml_of(i, col);
-      const float w = weight_of(ml.x, M);
-      tokens |= ml.y < 0.f || ml.x != -INFINITY;
-      if (ml.x != -INFINITY) {
-        const float4 v = o_of(i, col, d);
-        sum = fmaf(w, ml.y, sum);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      tokens |= ml[i].y < 0.f || ml[i].x != -INFINITY;
+      if (ml[i].x != -INFINITY) {
+        const float w = exp2f(ml[i].x - M);
+        sum = fmaf(w, ml[i].y, sum);
+        acc.x = fmaf(w, v[i].x, acc.x);
+        acc.y = fmaf(w, v[i].y, acc.y);
+        acc.z = fmaf(w, v[i].z, acc.z);
+        acc.w = fmaf(w, v[i].w, acc.w);
       }
     }
     return acc;
   };
+  constexpr std::integral_constant<int, kWarps> warps{};
+  constexpr std::integral_constant<int, kMaxCluster> blocks{};
   auto finish = [&](float4 acc, float M, float sum, bool tokens, int col, int d) {
     const float inv = inverse_of(M, sum, tokens);
     const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
@@ -388,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const int col = i / (D / 4), d = i % (D / 4) * 4;
       float M, sum;
       bool tokens;
-      const float4 acc = join(ml_here, o_here, kWarps, col, d, M, sum, tokens);
+      const float4 acc = join(warps, ml_here, o_here, kWarps, col, d, M, sum, tokens);
       finish(acc, M, sum, tokens, col, d);
     }
     return;
@@ -398,7 +422,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int col = i / (D / 4), d = i % (D / 4) * 4;
     float M, sum;
     bool tokens;
-    const float4 acc = join(ml_here, o_here, kWarps, col, d, M, sum, tokens);
+    const float4 acc = join(warps, ml_here, o_here, kWarps, col, d, M, sum, tokens);
     *reinterpret_cast<float4*>(jo + col * Gm::kPitch + d) = acc;  // only this thread reads it before
     if (d == 0) block_ml[col] = make_float2(M, M == -INFINITY && tokens ? -1.f : sum);
   }
@@ -408,14 +432,24 @@ __global__ void __launch_bounds__(kWarps * 32)
   auto o_peer = [&](int r, int col, int d) {
     return ld_peer4(peer_addr(o_addr + (col * Gm::kPitch + d) * 4, r));
   };
-  for (int i = rank * kWarps * 32 + threadIdx.x; i < cols * (D / 4); i += ranks * kWarps * 32) {
-    const int col = i / (D / 4), d = i % (D / 4) * 4;
-    float M, sum;
-    bool tokens;
-    const float4 acc = join(ml_peer, o_peer, ranks, col, d, M, sum, tokens);
-    finish(acc, M, sum, tokens, col, d);
+  // Each block finishes every ranks-th piece; it is done with its peers' memory before it stores.
+  constexpr int kMine = (kCols * (D / 4) + kWarps * 32 - 1) / (kWarps * 32);
+  float4 acc[kMine];
+  float M[kMine], sum[kMine];
+  bool tokens[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = (threadIdx.x + k * kWarps * 32) * ranks + rank;
+    if (i < cols * (D / 4))
+      acc[k] = join(blocks, ml_peer, o_peer, ranks, i / (D / 4), i % (D / 4) * 4, M[k], sum[k], tokens[k]);
   }
-  cluster_sync();  // no block leaves while another may read its memory
+  cluster_arrive();
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int i = (threadIdx.x + k * kWarps * 32) * ranks + rank;
+    if (i < cols * (D / 4)) finish(acc[k], M[k], sum[k], tokens[k], i / (D / 4), i % (D / 4) * 4);
+  }
+  cluster_wait();  // no block leaves while another may read its memory
 }
 
 template <int D, int NT>
@@ -537,7 +571,8 @@ extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void*
     return PA_ERR_UNSUPPORTED;
   if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
   if (static_cast<long long>(max_blocks_per_seq) * block_size > (1ll << 30) || num_seqs > 65535 ||
-      num_heads > 65535 || num_selected > (1 << 30))
+      num_heads > 65535 ||
+      static_cast<long long>(num_selected) * block_size > (1ll << 33))
     return PA_ERR_INVALID_ARG;
   if (static_cast<long long>(num_blocks) * num_kv_heads * block_size >= (1ll << 31))
     return PA_ERR_INVALID_ARG;
