@@ -673,10 +673,7 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     if q is not None:
         Hq = q.shape[1]
         q_step = _token_step("q", q, dtype, device, (T, Hq, D))
-        if q_out is None:
-            q_out = _new_out((T, Hq, D), dtype, q.device, stream)
-        else:
-            _need_all(device, (("q_out", q_out, dtype, (T, Hq, D)),))
+        _need_all(device, (("q_out", q_out, dtype, (T, Hq, D)),))
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope = None
@@ -701,6 +698,8 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
                        1 if interleaved else 0, axes, _address(positions), pair_axis)
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need cos_sin")
+    if q is not None and q_out is None:
+        q_out = _new_out((T, Hq, D), dtype, q.device, stream)
     _check(load_library().kv_cache_append_rope(
         _address(q), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step, query_start.data_ptr(),
         T, int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(), _address(k_min),
@@ -741,12 +740,12 @@ def paged_block_scores(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor
     (B, H, D), dtype = _half("k_min", k_min, 3)
     N, MB = block_tables.shape
     Hq = q.shape[1]
-    if out is None:
-        out = _new_out((N, H, MB), torch.float32, q.device, stream)
     _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_min", k_min, dtype, (B, H, D)),
                        ("k_max", k_max, dtype, (B, H, D)),
                        ("block_tables", block_tables, i32, (N, MB)),
                        ("seq_lens", seq_lens, i32, (N,)), ("out", out, torch.float32, (N, H, MB))))
+    if out is None:
+        out = _new_out((N, H, MB), torch.float32, q.device, stream)
     _check(load_library().paged_block_scores(
         q.data_ptr(), k_min.data_ptr(), k_max.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), N, Hq, H, D, int(block_size), MB, B, float(scale), _DTYPE[dtype],
@@ -764,10 +763,10 @@ def paged_block_select(scores: torch.Tensor, seq_lens: torch.Tensor, block_size:
     -1."""
     device, i32 = torch.cuda.current_device(), torch.int32
     N, H, MB = scores.shape
-    if out is None:
-        out = _new_out((N, H, max(int(num_selected), 0)), i32, scores.device, stream)
     _need_all(device, (("scores", scores, torch.float32, (N, H, MB)),
                        ("seq_lens", seq_lens, i32, (N,)), ("out", out, i32, (N, H, num_selected))))
+    if out is None:
+        out = _new_out((N, H, max(int(num_selected), 0)), i32, scores.device, stream)
     _check(load_library().paged_block_select(
         scores.data_ptr(), seq_lens.data_ptr(), N, H, int(block_size), MB, int(num_selected),
         int(sink_blocks), int(recent_blocks), out.data_ptr(), _record(error_record, device),
@@ -787,15 +786,17 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
     Hq, S = q.shape[1], selected.shape[2]
-    if out is None:
-        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
-    if out.dtype not in _DTYPE:
-        raise ValueError(f"out must be float16, bfloat16 or float32, got {out.dtype}")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPE:
+        raise ValueError(f"out must be float16, bfloat16 or float32, got {out_dtype}")
     _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_cache", k_cache, dtype, (B, H, bs, D)),
                        ("v_cache", v_cache, dtype, (B, H, bs, D)),
                        ("block_tables", block_tables, i32, (N, MB)),
                        ("seq_lens", seq_lens, i32, (N,)),
-                       ("selected", selected, i32, (N, H, S)), ("out", out, out.dtype, (N, Hq, D))))
+                       ("selected", selected, i32, (N, H, S)), ("out", out, out_dtype, (N, Hq, D))))
+    if out is None:
+        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
     _check(load_library().paged_attn_sparse(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),

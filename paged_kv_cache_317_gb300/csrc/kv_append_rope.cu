@@ -222,21 +222,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
   __shared__ uint4 keys[kThreads * kBatch * 2];  // [head of the batch][row][piece]
 
   const size_t step = part == 0 ? p.q_stride : part == 1 ? p.k_stride : p.v_stride;
-  const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v);
-  T* dst = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_cache : p.v_cache);
+  const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) +
+                 static_cast<size_t>(h0 + h) * p.head_dim;
+  // elements from head to head of the output
+  const size_t head_step = part == 0 ? p.head_dim : static_cast<size_t>(p.block_size) * p.head_dim;
   for (int pass = 0; pass < t.rows; pass += span) {
     const bool active = pass + r < t.rows && h < lanes;
     const int token = t.token + pass + r;
+    const T* from = src + token * step;
     float c[8], s[8];
     for (int hb = h0; hb < h1; hb += kBatch * lanes) {
       uint4 a[kBatch], b[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int head = hb + h + lanes * i;
-        if (active && head < h1) {
-          const T* from = src + token * step + static_cast<size_t>(head) * p.head_dim;
-          a[i] = *reinterpret_cast<const uint4*>(from + da);
-          b[i] = *reinterpret_cast<const uint4*>(from + db);
+        if (active && hb + h + lanes * i < h1) {
+          const T* at = from + (hb - h0 + lanes * i) * p.head_dim;
+          a[i] = *reinterpret_cast<const uint4*>(at + da);
+          b[i] = *reinterpret_cast<const uint4*>(at + db);
         }
       }
       if (hb == h0) {  // with the first loads on their way
@@ -244,16 +246,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
         if (pass == 0 && part > 0 && !is_block(p, t, blk, part == 1 && h0 == 0 && threadIdx.x == 0))
           return;
       }
+      const size_t row = part == 0 ? static_cast<size_t>(token) * p.num_heads
+                                   : static_cast<size_t>(blk) * p.num_kv_heads * p.block_size + row0 + pass + r;
+      T* to = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_cache : p.v_cache) +
+              row * p.head_dim + (hb + h) * head_step;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int head = hb + h + lanes * i;
-        if (active && head < h1) {
+        if (active && hb + h + lanes * i < h1) {
           if (turn) rotate(p.rope, c, s, a[i], b[i], Tag{});
-          const size_t row =
-              part == 0 ? static_cast<size_t>(token) * p.num_heads + head
-                        : (static_cast<size_t>(blk) * p.num_kv_heads + head) * p.block_size + row0 + pass + r;
-          *reinterpret_cast<uint4*>(dst + row * p.head_dim + da) = a[i];
-          *reinterpret_cast<uint4*>(dst + row * p.head_dim + db) = b[i];
+          *reinterpret_cast<uint4*>(to + da) = a[i];
+          *reinterpret_cast<uint4*>(to + db) = b[i];
+          to += lanes * head_step;
           if (bounds) {
             uint4* k = keys + ((h + lanes * i) * span + r) * pieces;
             k[da / 8] = a[i];
