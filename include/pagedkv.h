@@ -498,7 +498,8 @@ int kv_cache_append(const void* k, const void* v, const int64_t* slot_mapping, i
  * its row 0 the bounds are theirs alone, otherwise they are combined with the ones
  * stored; a NaN key makes its channel's bounds NaN.  Bounds so never leave out a row
  * that was written; after a rollback (rows written anew at a shorter length) they may
- * be wider than needed until kv_block_bounds computes them afresh.
+ * be wider than needed until kv_block_bounds computes them afresh.  kv_cache_append and
+ * paged_attn_decode_append leave the bounds alone: after them, kv_block_bounds.
  *
  *   q, k, v       device, [total_tokens][heads][head_dim] in `dtype`, 16-byte aligned;
  *                 token t of q begins at element t * q_stride (a multiple of 8, at

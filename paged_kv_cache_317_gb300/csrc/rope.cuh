@@ -30,7 +30,7 @@ inline int rope_params(const pa_rope& r, int head_dim, RopeParams& p) {
   p.rotary_dim = r.rotary_dim;
   p.interleaved = r.interleaved != 0;
   p.num_axes = r.num_axes;
-  if (r.num_axes > 1) {
+  if (r.pair_axis) {
     for (int j = 0; j < r.rotary_dim / 2; ++j) {
       if (r.pair_axis[j] >= r.num_axes) return PA_ERR_INVALID_ARG;
       p.pair_axis[j] = r.pair_axis[j];

@@ -178,6 +178,19 @@ def test_many_sequences_of_mixed_lengths(B):
     check(B, st, out, before)
 
 
+@pytest.mark.parametrize("Hq,H,D,bs", [(12, 10, 16, 8), (40, 3, 32, 16), (33, 33, 16, 4)])
+def test_large_batches_of_prompts(B, Hq, H, D, bs):
+    """Enough tiles that a thread block takes all of its 32 heads."""
+    rng = np.random.default_rng(Hq)
+    lens = rng.integers(1, 900, 40)
+    news = np.maximum(lens - rng.integers(0, 30, 40), 0)
+    st = make(Hq, lens, news, Hq, H, D, 16, bs, torch.float16, axes=2)
+    before, rec = snapshot(st), B.new_error_record()
+    out = call(B, st, error_record=rec)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    check(B, st, out, before)
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [1, 30, 7]])
 def test_without_rotation_it_is_the_plain_append(B, news):
     st = make(7, [33, 64, 7], news, 4, 4, 64, 0, 16, torch.float16)

@@ -47,7 +47,7 @@ def test_append_rope_refuses(lib, binding):
     for kw, want in ((dict(rotary_dim=0), INV), (dict(rotary_dim=24), UNS), (dict(rotary_dim=80), UNS),
                      (dict(max_position=0), INV), (dict(num_axes=0), INV), (dict(num_axes=5), INV),
                      (dict(cos_sin=None), INV), (dict(cos_sin=P + 4), INV), (dict(num_axes=2), INV),
-                     (dict(num_axes=2, positions=P), INV),
+                     (dict(num_axes=2, positions=P), INV), (dict(pair_axis=bytes([1] * 32)), INV),
                      (dict(num_axes=2, positions=P, pair_axis=bytes([0] * 31 + [2])), INV)):
         assert call(rope=_rope(binding, **kw)) == want, kw
 
