@@ -2,17 +2,22 @@
 //
 // A cluster of thread blocks (one, but for few long rows) per (sequence, key head), each with
 // a contiguous part of the row, of which each warp has a contiguous part in turn: up to 32
-// groups of 32 scores, one of each group per lane, read once and kept in registers.  A score
-// becomes a 32-bit key that orders as the scores do.  The key of the last block that is kept
-// is found 11 bits at a time from histograms of the keys that agree with it so far (the first
-// digit holds sign, exponent and two bits of the fraction, so that ordinary scores spread over
-// the bins), and no further than needed to tell the kept from the others; the blocks of a
-// cluster add up each other's histograms.  Then two votes per group tell which of its blocks
-// are above that key and which equal to it; lane j takes the votes of group j, a scan of
-// their counts over lanes, warps and blocks says where its blocks go, and it writes them, of
-// the equal ones the lowest.  The sums are of whole numbers, so the result is the same on every
-// run.  Bound by latency (the launch and some ten barriers) for one sequence and by
-// instructions for batches.
+// groups of 32 scores, one of each group per lane, read once and kept in registers.  Three
+// steps find the last score that is kept:
+//  1. With one thread block, the scores between the row's smallest and largest are spread evenly
+//     over 2048 bins (subtraction, product and rounding keep their order) and counted.  Every
+//     score above the bin in which the count reaches num_selected is kept, and as a rule that
+//     bin holds a handful.  Skipped where a score is NaN or infinite.
+//  2. If the bin holds more than are wanted, its scores, listed in shared memory, are each
+//     ranked among one another.  Where they are too many, or step 1 was skipped, a score becomes
+//     a 32-bit key that orders as the scores do, and the last kept key is found 11 bits at a
+//     time from histograms of the keys that agree with it so far; the blocks of a cluster add up
+//     each other's histograms.
+//  3. A vote per group (two, where equal scores are kept in part) tells which of its blocks are
+//     kept; lane j takes the votes of group j, a scan of their counts over lanes, warps and
+//     blocks says where its blocks go, and it writes them, of equal ones the lowest.
+// Sums are of whole numbers, so the result is the same on every run.  Bound by latency (the
+// launch and some ten barriers) for one sequence and by instructions for batches.
 #include <cuda_runtime.h>
 
 #include "cluster.cuh"
@@ -23,7 +28,6 @@ namespace {
 
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMaxCluster = 8;
-constexpr int kGroups = 32;  // groups of 32 keys per warp: one vote per lane
 constexpr int kStep = 8;     // of them between two looks at how many there are
 
 struct SelectParams {
@@ -39,6 +43,11 @@ __device__ __forceinline__ uint32_t key_of(float s) {
   if (s != s) return 0xffffffffu;
   const uint32_t u = __float_as_uint(s + 0.f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// The score of a key (any NaN for that of NaN).
+__device__ __forceinline__ float score_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {
@@ -67,18 +76,35 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1;
 }
 
-template <int kThreads>
+// f(j) for the groups j < `groups`, and up to kStep - 1 more, which no mask names.  Unrolled, so
+// that the scores stay in registers.
+template <int kGroups, class F>
+__device__ __forceinline__ void each_group(int groups, F f) {
+#pragma unroll
+  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
+    if (j0 < groups) {
+#pragma unroll
+      for (int j = j0; j < j0 + kStep; ++j) f(j);
+    }
+  }
+}
+
+// kGroups: groups of 32 scores per warp, at most 32, one vote for each lane.  Rows of up to 2048
+// blocks take 8: less code to fetch (one 30k context: 4.0 us, 4.5 us with 32).
+template <int kThreads, int kGroups>
 __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
   static_assert(kThreads <= kBins, "a thread has a bin at least");
   __shared__ __align__(16) int hist[2][kBins];
-  __shared__ uint32_t warp_sum[2][kWarps];
-  __shared__ int found[3];  // the digit, the keys above it, the keys that have it
+  __shared__ uint32_t warp_sum[2][kWarps], warp_range[2][kWarps];
+  __shared__ int found[3];  // the bin, the scores above it, the scores in it
   __shared__ uint32_t part_sum[kWarps], block_sum;
+  __shared__ int listed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int head = blockIdx.x / ranks, seq = blockIdx.y;
   for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
+  if (tid == 0) listed = 0;
   const size_t row = static_cast<size_t>(seq) * p.num_kv_heads + head;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -99,113 +125,180 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
   const int groups = (nb + 32 * kWarps * ranks - 1) / (32 * kWarps * ranks);
   const int base = (rank * kWarps + warp) * groups * 32;  // the warp's first block
   const float* s = p.scores + row * p.max_blocks + base + lane;
-  // Of this lane's groups, the ones that have a block, and those whose block competes; `want`
-  // of the row's are kept.
+  // Bit j of a mask is this lane's block of group j.  `kept` will be; of `open`, the blocks whose
+  // scores compete, `want` of the row's are kept.
   const int mine = nb - base - lane;  // group j has a block if 32 j < mine
   const uint32_t have = bits_below(min((mine + 31) >> 5, groups));
-  const uint32_t in = bits_below(min((mine - p.recent + 31) >> 5, groups)) &
-                      ~bits_below((p.sink - base - lane + 31) >> 5);
+  uint32_t open = bits_below(min((mine - p.recent + 31) >> 5, groups)) &
+                  ~bits_below((p.sink - base - lane + 31) >> 5);
+  uint32_t kept = have & ~open;
   int want = p.num_selected - p.sink - p.recent;
-  uint32_t key[kGroups];
+  float x[kGroups];
+  each_group<kGroups>(groups, [&](int j) { x[j] = have >> j & 1 ? s[32 * j] : 0.f; });
+
+  // The bin of hist[turn] in which the count from the top reaches `want`, into `found`.
+  auto find = [&](int turn) {
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    // thread t has the bins kBins - 1 - t kPer and the kPer - 1 below
+    const int bin0 = kBins - (tid + 1) * kPer;
+    int bin[kPer];
+    if (ranks == 1) {
 #pragma unroll
-  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
-    if (j0 < groups) {
+      for (int j = 0; j < kPer; ++j) bin[j] = hist[turn][bin0 + j];
+    } else {
 #pragma unroll
-      for (int j = j0; j < j0 + kStep; ++j)
-        key[j] = __float_as_uint(have >> j & 1 ? s[32 * j] : 0.f);
-    }
-  }
-  __syncthreads();  // hist[0] is zero
+      for (int j = 0; j < kPer; ++j) bin[j] = 0;
+      const uint32_t at = smem_addr(&hist[turn][bin0]);
+      for (int r = 0; r < ranks; ++r) {
+        const uint32_t peer = peer_addr(at, r);
 #pragma unroll
-  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
-    if (j0 < groups) {
-#pragma unroll
-      for (int j = j0; j < j0 + kStep; ++j) {
-        key[j] = key_of(__uint_as_float(key[j]));
-        count_if(in, j, hist[0], key[j] >> (32 - kBits));
+        for (int j = 0; j < kPer; ++j) bin[j] += static_cast<int>(ld_peer_u32(peer + 4 * j));
       }
     }
-  }
-  uint32_t prefix = 0xffffffffu, known = 0xffffffffu;  // want = 0: nothing above, none of the equal
+    // the other histogram, for the next count: its readers are past the barrier above
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) hist[turn ^ 1][bin0 + j] = 0;
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sum += bin[j];
+    uint32_t upto = warp_scan(sum, lane);
+    if (lane == 31) warp_sum[turn][warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(kFullMask, lane < warp ? warp_sum[turn][lane] : 0u);
+    int above = static_cast<int>(upto) - sum;
+    if (above < want && static_cast<int>(upto) >= want) {  // in one thread
+#pragma unroll
+      for (int j = kPer - 1; j >= 0; --j) {
+        if (above < want && above + bin[j] >= want) {
+          found[0] = bin0 + j;
+          found[1] = above;
+          found[2] = bin[j];
+        }
+        above += bin[j];
+      }
+    }
+    __syncthreads();
+    want -= found[1];
+    return found[0];
+  };
+
+  bool ties = false;  // more open blocks than wanted, of the same score
   if (want > 0) {
-    prefix = known = 0;  // the last kept key's leading bits, and which they are
-    for (int top = 32, turn = 0; top > 0; top -= kBits, turn ^= 1) {
+    int turn = 0;
+    bool ranked = false;  // `open` are the blocks with the last kept score
+    ties = true;
+    if (ranks == 1) {
+      float low = INFINITY, high = -INFINITY;  // high is NaN if a score is
+      each_group<kGroups>(groups, [&](int j) {
+        if (open >> j & 1) {
+          low = fminf(low, x[j]);
+          high = max_nan(high, x[j]);
+        }
+      });
+      const uint32_t low_key = __reduce_min_sync(kFullMask, key_of(low));
+      const uint32_t high_key = __reduce_max_sync(kFullMask, key_of(high));
+      if (lane == 0) {
+        warp_range[0][warp] = low_key;
+        warp_range[1][warp] = high_key;
+      }
+      __syncthreads();
+      low = score_of(__reduce_min_sync(kFullMask, lane < kWarps ? warp_range[0][lane] : 0xffffffffu));
+      high = score_of(__reduce_max_sync(kFullMask, lane < kWarps ? warp_range[1][lane] : 0u));
+      // (not so if a score is NaN or infinite, or if all are nearly equal)
+      const float scale = (kBins - 1) / (high - low);
+      if (low > -INFINITY && high < INFINITY && scale > 0.f && scale < 1e38f) {
+        // (v - low) scale to the nearest whole number, in the low bits of a sum with 1.5 * 2^23
+        constexpr float kMagic = 12582912.f;
+        auto bin_of = [&](float v) { return __float_as_int(fmaf(v - low, scale, kMagic)) - 0x4b400000; };
+        each_group<kGroups>(groups, [&](int j) { count_if(open, j, hist[0], bin_of(x[j])); });
+        const int last = find(0);
+        turn = 1;
+        ties = found[2] != want;
+        uint32_t same = 0;
+        each_group<kGroups>(groups, [&](int j) {
+          const int bin = bin_of(x[j]);
+          if (bin > last) kept |= open & (1u << j);
+          if (bin == last) same |= 1u << j;
+        });
+        open &= same;
+        const int n = found[2];
+        if (ties && n <= kThreads) {  // list the bin's scores (over hist[0]) and rank each
+          const bool some = __any_sync(kFullMask, open != 0);
+          if (some)
+            each_group<kGroups>(groups, [&](int j) {
+              if (open >> j & 1) hist[0][atomicAdd(&listed, 1)] = static_cast<int>(key_of(x[j]));
+            });
+          __syncthreads();
+          if (tid < n) {
+            const uint32_t k = static_cast<uint32_t>(hist[0][tid]);
+            int above = 0, equal = 0;
+            for (int i = 0; i < n; ++i) {
+              const uint32_t v = static_cast<uint32_t>(hist[0][i]);
+              above += v > k;
+              equal += v == k;
+            }
+            if (above < want && above + equal >= want) {  // in one thread, or alike in several
+              found[0] = static_cast<int>(k);
+              found[1] = above;
+              found[2] = equal;
+            }
+          }
+          __syncthreads();
+          const uint32_t k = static_cast<uint32_t>(found[0]);
+          want -= found[1];
+          ties = found[2] != want;
+          ranked = true;
+          if (some) {
+            same = 0;
+            each_group<kGroups>(groups, [&](int j) {
+              const uint32_t v = key_of(x[j]);
+              if (v > k) kept |= open & (1u << j);
+              if (v == k) same |= 1u << j;
+            });
+            open &= same;
+          }
+        }
+      }
+    } else {
+      __syncthreads();  // hist[0] is zero
+    }
+    uint32_t prefix = 0, known = 0;  // the last kept key's leading bits, and which they are
+    for (int top = 32; ties && !ranked && top > 0; top -= kBits, turn ^= 1) {
       const int shift = max(top - kBits, 0);
       const uint32_t digits = (1u << (top - shift)) - 1;
-      if (top < 32) {
-#pragma unroll
-        for (int j0 = 0; j0 < kGroups; j0 += kStep) {
-          if (j0 < groups) {
-#pragma unroll
-            for (int j = j0; j < j0 + kStep; ++j)
-              count_if((key[j] & known) == prefix ? in : 0u, j, hist[turn], (key[j] >> shift) & digits);
-          }
-        }
+      if (__any_sync(kFullMask, open != 0)) {
+        each_group<kGroups>(groups, [&](int j) {
+          const uint32_t k = key_of(x[j]);
+          count_if((k & known) == prefix ? open : 0u, j, hist[turn], (k >> shift) & digits);
+        });
       }
-      if (ranks > 1) cluster_sync();
-      else __syncthreads();
-      // thread t has the bins kBins - 1 - t kPer and the kPer - 1 below
-      const int bin0 = kBins - (tid + 1) * kPer;
-      int bin[kPer];
-      if (ranks == 1) {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) bin[j] = hist[turn][bin0 + j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) bin[j] = 0;
-        const uint32_t at = smem_addr(&hist[turn][bin0]);
-        for (int r = 0; r < ranks; ++r) {
-          const uint32_t peer = peer_addr(at, r);
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) bin[j] += static_cast<int>(ld_peer_u32(peer + 4 * j));
-        }
-      }
-      // the other histogram, for the next digit: its readers are past the barrier above
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) hist[turn ^ 1][bin0 + j] = 0;
-      int sum = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) sum += bin[j];
-      uint32_t upto = warp_scan(sum, lane);
-      if (lane == 31) warp_sum[turn][warp] = upto;
-      __syncthreads();
-      upto += __reduce_add_sync(kFullMask, lane < warp ? warp_sum[turn][lane] : 0u);
-      int above = static_cast<int>(upto) - sum;
-      if (above < want && static_cast<int>(upto) >= want) {  // in one thread
-#pragma unroll
-        for (int j = kPer - 1; j >= 0; --j) {
-          if (above < want && above + bin[j] >= want) {
-            found[0] = bin0 + j;
-            found[1] = above;
-            found[2] = bin[j];
-          }
-          above += bin[j];
-        }
-      }
-      __syncthreads();
-      prefix |= static_cast<uint32_t>(found[0]) << shift;
+      prefix |= static_cast<uint32_t>(find(turn)) << shift;
       known |= digits << shift;
-      want -= found[1];
-      if (found[2] == want) break;  // every key that agrees so far is kept
+      ties = found[2] != want;
     }
+    if (known != 0 && __any_sync(kFullMask, open != 0)) {
+      uint32_t same = 0;
+      each_group<kGroups>(groups, [&](int j) {
+        const uint32_t k = key_of(x[j]) & known;
+        if (k > prefix) kept |= open & (1u << j);
+        if (k == prefix) same |= 1u << j;
+      });
+      open &= same;
+    }
+    if (!ties) kept |= open;
   }
-  // kept: the blocks that do not compete, the keys above, and `want` of the equal ones
+  // kept: the blocks of `kept` and, with ties, `want` of the row's open ones
   uint32_t over_here = 0, same_here = 0;  // of group `lane`
-#pragma unroll
-  for (int j0 = 0; j0 < kGroups; j0 += kStep) {
-    if (j0 < groups) {
-#pragma unroll
-      for (int j = j0; j < j0 + kStep; ++j) {
-        const uint32_t k = key[j] & known;
-        const bool inside = in >> j & 1;
-        const unsigned over = __ballot_sync(kFullMask, (have >> j & 1) && (!inside || k > prefix));
-        const unsigned same = __ballot_sync(kFullMask, inside && k == prefix);
-        if (lane == j) {
-          over_here = over;
-          same_here = same;
-        }
-      }
-    }
+  each_group<kGroups>(groups, [&](int j) {
+    const unsigned over = __ballot_sync(kFullMask, kept >> j & 1);
+    if (lane == j) over_here = over;
+  });
+  if (ties) {
+    each_group<kGroups>(groups, [&](int j) {
+      const unsigned same = __ballot_sync(kFullMask, open >> j & 1);
+      if (lane == j) same_here = same;
+    });
   }
   // above in the upper half, equal in the lower (a thread block has at most 2^14 keys)
   const uint32_t count = static_cast<uint32_t>(__popc(over_here)) << 16 | __popc(same_here);
@@ -240,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
   if (ranks > 1) cluster_sync();  // no block leaves while another may read its memory
 }
 
-template <int kThreads>
+template <int kThreads, int kGroups>
 int launch(const SelectParams& p, int num_seqs, int ranks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_kv_heads) * ranks, num_seqs);
@@ -254,7 +347,7 @@ int launch(const SelectParams& p, int num_seqs, int ranks, cudaStream_t stream) 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, paged_block_select_kernel<kThreads>, p) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, paged_block_select_kernel<kThreads, kGroups>, p) != cudaSuccess)
     return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -288,6 +381,7 @@ extern "C" int paged_block_select(const float* scores, const int32_t* seq_lens, 
     ranks *= 2;
   if (max_blocks_per_seq > 16384 * ranks) return PA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return max_blocks_per_seq <= 8192 * ranks ? launch<256>(p, num_seqs, ranks, st)
-                                            : launch<512>(p, num_seqs, ranks, st);
+  if (max_blocks_per_seq <= 2048 * ranks) return launch<256, 8>(p, num_seqs, ranks, st);
+  if (max_blocks_per_seq <= 8192 * ranks) return launch<256, 32>(p, num_seqs, ranks, st);
+  return launch<512, 32>(p, num_seqs, ranks, st);
 }

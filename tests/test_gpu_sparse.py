@@ -246,7 +246,7 @@ def test_bad_entries_are_recorded(B):
     (2100, [2100, 2049], 1000, 1, 1), (5000, [4999], 1, 0, 1), (9001, [9001, 4097], 300, 0, 0),
     (20000, [20000, 19999, 7], 2000, 1, 4), (70001, [70001, 69000], 500, 3, 5),
     (131072, [131072, 5], 20000, 1, 9)])
-@pytest.mark.parametrize("kind", ["normal", "ties", "odd"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "odd", "wide"])
 def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
     rng = np.random.default_rng(width)
     s = rng.standard_normal((len(lens), 3, width)).astype(np.float32)
@@ -257,6 +257,10 @@ def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
         for v in (NAN, -NAN, INF, -INF, 1e-42, -1e-42, -0.0):
             s[rng.random(s.shape) < 0.05] = v
         s[0, 0] = 2.5
+    elif kind == "wide":                             # finite, of every size
+        s = (s * np.float32(10.0) ** rng.integers(-44, 38, s.shape)).astype(np.float32)
+        s[-1] = 1 + rng.integers(0, 9, s[-1].shape) * np.float32(2.0 ** -23)
+        s[0, 1] = np.float32(3e38) * rng.choice([-1, 1], width)
     rec = B.new_error_record()
     got = B.paged_block_select(torch.from_numpy(s).cuda(), dev(lens), 1, keep, sink, recent,
                                error_record=rec)
