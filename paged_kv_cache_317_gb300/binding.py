@@ -553,13 +553,14 @@ def block_copy(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _need_all(device, specs):
-    """Every (name, tensor, dtype, shape) is a contiguous tensor of that type and shape on the
-    device that launches go to; a tensor of None is skipped.  One comparison chain per tensor:
-    these checks are most of a small call's time."""
-    for name, t, dtype, shape in specs:
+def _need_all(device, dtype, names, *tensors):
+    """Every (tensor, shape) is a contiguous tensor of that type and shape on the device that
+    launches go to; a tensor of None is skipped.  These checks are a good part of a small call's
+    time, so the names are only looked at when one fails."""
+    for t, shape in tensors:
         if t is not None and (t.get_device() != device or t.dtype is not dtype
                               or t.shape != shape or not t.is_contiguous()):
+            name = names.split()[[u is t for u, _ in tensors].index(True)]
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")
             if t.dtype is not dtype:
@@ -619,10 +620,12 @@ def _token_step(name, t, dtype, device, shape):
     if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)} on the "
                          "current device")
+    if t.is_contiguous():
+        return shape[1] * shape[2]
     step, head, one = t.stride()
     if (one != 1 and shape[2] > 1) or (head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return step if shape[0] > 1 else shape[1] * shape[2]
+    return step
 
 
 def rope_cos_sin(max_position: int, rotary_dim: int, base: float = 10000.0,
@@ -659,12 +662,11 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
     T = k.shape[0]
-    _need_all(device, (("k_cache", k_cache, dtype, (B, H, bs, D)),
-                       ("v_cache", v_cache, dtype, (B, H, bs, D)),
-                       ("block_tables", block_tables, i32, (N, MB)),
-                       ("seq_lens", seq_lens, i32, (N,)),
-                       ("query_start", query_start, i32, (N + 1,)),
-                       ("k_min", k_min, dtype, (B, H, D)), ("k_max", k_max, dtype, (B, H, D))))
+    cache, bound = (B, H, bs, D), (B, H, D)
+    _need_all(device, dtype, "k_cache v_cache k_min k_max", (k_cache, cache), (v_cache, cache),
+              (k_min, bound), (k_max, bound))
+    _need_all(device, i32, "block_tables seq_lens query_start", (block_tables, (N, MB)),
+              (seq_lens, (N,)), (query_start, (N + 1,)))
     k_step = _token_step("k", k, dtype, device, (T, H, D))
     v_step = _token_step("v", v, dtype, device, (T, H, D))
     if (k_min is None) != (k_max is None):
@@ -673,29 +675,31 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     if q is not None:
         Hq = q.shape[1]
         q_step = _token_step("q", q, dtype, device, (T, Hq, D))
-        _need_all(device, (("q_out", q_out, dtype, (T, Hq, D)),))
+        if q_out is not None:
+            _need_all(device, dtype, "q_out", (q_out, (T, Hq, D)))
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope = None
     if cos_sin is not None:
-        if cos_sin.dim() != 2:
+        table = cos_sin.shape
+        if len(table) != 2:
             raise ValueError("cos_sin must be [max_position, rotary_dim]")
-        _need_all(device, (("cos_sin", cos_sin, torch.float32, cos_sin.shape),))
+        _need_all(device, torch.float32, "cos_sin", (cos_sin, table))
         axes = 1
         if positions is not None:
             if positions.dim() == 2:
                 axes = positions.shape[0]
-            _need_all(device, (("positions", positions, i32,
-                                (T,) if positions.dim() == 1 else (axes, T)),))
+            _need_all(device, i32, "positions",
+                      (positions, (T,) if positions.dim() == 1 else (axes, T)))
         if pair_axis is not None:
             pair_axis = bytes(pair_axis)
-            if len(pair_axis) != cos_sin.shape[1] // 2:
+            if len(pair_axis) != table[1] // 2:
                 raise ValueError("pair_axis must hold one axis for each of the "
-                                 f"{cos_sin.shape[1] // 2} rotary pairs")
+                                 f"{table[1] // 2} rotary pairs")
         elif axes > 1:
             raise ValueError("positions of several axes need pair_axis")
-        rope = pa_rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-                       1 if interleaved else 0, axes, _address(positions), pair_axis)
+        rope = pa_rope(cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, axes,
+                       None if positions is None else positions.data_ptr(), pair_axis)
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need cos_sin")
     if q is not None and q_out is None:
@@ -719,10 +723,11 @@ def kv_block_bounds(k_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens:
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
-    _need_all(device, (("k_cache", k_cache, dtype, (B, H, bs, D)),
-                       ("k_min", k_min, dtype, (B, H, D)), ("k_max", k_max, dtype, (B, H, D)),
-                       ("block_tables", block_tables, i32, (N, MB)),
-                       ("seq_lens", seq_lens, i32, (N,)), ("first_token", first_token, i32, (N,))))
+    bound = (B, H, D)
+    _need_all(device, dtype, "k_cache k_min k_max", (k_cache, (B, H, bs, D)), (k_min, bound),
+              (k_max, bound))
+    _need_all(device, i32, "block_tables seq_lens first_token", (block_tables, (N, MB)),
+              (seq_lens, (N,)), (first_token, (N,)))
     _check(load_library().kv_block_bounds(
         k_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), _address(first_token),
         N, H, D, bs, MB, B, _DTYPE[dtype], k_min.data_ptr(), k_max.data_ptr(),
@@ -740,12 +745,13 @@ def paged_block_scores(q: torch.Tensor, k_min: torch.Tensor, k_max: torch.Tensor
     (B, H, D), dtype = _half("k_min", k_min, 3)
     N, MB = block_tables.shape
     Hq = q.shape[1]
-    _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_min", k_min, dtype, (B, H, D)),
-                       ("k_max", k_max, dtype, (B, H, D)),
-                       ("block_tables", block_tables, i32, (N, MB)),
-                       ("seq_lens", seq_lens, i32, (N,)), ("out", out, torch.float32, (N, H, MB))))
+    bound = (B, H, D)
+    _need_all(device, dtype, "q k_min k_max", (q, (N, Hq, D)), (k_min, bound), (k_max, bound))
+    _need_all(device, i32, "block_tables seq_lens", (block_tables, (N, MB)), (seq_lens, (N,)))
     if out is None:
         out = _new_out((N, H, MB), torch.float32, q.device, stream)
+    else:
+        _need_all(device, torch.float32, "out", (out, (N, H, MB)))
     _check(load_library().paged_block_scores(
         q.data_ptr(), k_min.data_ptr(), k_max.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), N, Hq, H, D, int(block_size), MB, B, float(scale), _DTYPE[dtype],
@@ -763,8 +769,8 @@ def paged_block_select(scores: torch.Tensor, seq_lens: torch.Tensor, block_size:
     -1."""
     device, i32 = torch.cuda.current_device(), torch.int32
     N, H, MB = scores.shape
-    _need_all(device, (("scores", scores, torch.float32, (N, H, MB)),
-                       ("seq_lens", seq_lens, i32, (N,)), ("out", out, i32, (N, H, num_selected))))
+    _need_all(device, torch.float32, "scores", (scores, (N, H, MB)))
+    _need_all(device, i32, "seq_lens out", (seq_lens, (N,)), (out, (N, H, num_selected)))
     if out is None:
         out = _new_out((N, H, max(int(num_selected), 0)), i32, scores.device, stream)
     _check(load_library().paged_block_select(
@@ -790,13 +796,14 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         out_dtype = out.dtype
     if out_dtype not in _DTYPE:
         raise ValueError(f"out must be float16, bfloat16 or float32, got {out_dtype}")
-    _need_all(device, (("q", q, dtype, (N, Hq, D)), ("k_cache", k_cache, dtype, (B, H, bs, D)),
-                       ("v_cache", v_cache, dtype, (B, H, bs, D)),
-                       ("block_tables", block_tables, i32, (N, MB)),
-                       ("seq_lens", seq_lens, i32, (N,)),
-                       ("selected", selected, i32, (N, H, S)), ("out", out, out_dtype, (N, Hq, D))))
+    cache = (B, H, bs, D)
+    _need_all(device, dtype, "q k_cache v_cache", (q, (N, Hq, D)), (k_cache, cache), (v_cache, cache))
+    _need_all(device, i32, "block_tables seq_lens selected", (block_tables, (N, MB)),
+              (seq_lens, (N,)), (selected, (N, H, S)))
     if out is None:
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
+    else:
+        _need_all(device, out_dtype, "out", (out, (N, Hq, D)))
     _check(load_library().paged_attn_sparse(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),
