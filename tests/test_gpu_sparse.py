@@ -417,3 +417,16 @@ def test_a_given_stream_and_offsets_past_32_bits(B):
     assert torch.equal(small["kc"][2, :, 8], k[0])
     check_scores(s, small)
     check_attention(out, small, sel.cpu().numpy())
+
+
+def test_the_example_runs(B):
+    """paged_kv_cache_317_gb300/examples/sparse_step.py: its output is the oracle's for its lists."""
+    import os
+    import runpy
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = runpy.run_path(os.path.join(root, "paged_kv_cache_317_gb300", "examples", "sparse_step.py"))
+    lens, sel = env["lengths"].cpu().numpy(), env["blocks"].cpu().numpy()
+    assert lens.tolist() == [5001, 301] and (sel[1, :, 19:] == -1).all() and (sel[0] >= 0).all()
+    b = dict(lens=lens, tables=env["tables"].cpu().numpy(), kc=env["kc"], vc=env["vc"], q=env["q"], bs=16,
+             scale=128 ** -0.5, D=128)
+    check_attention(env["out"], b, sel)

@@ -133,3 +133,11 @@ def test_rope_table_shape_and_values(binding):
     assert t.shape == (5, 8) and t.dtype == torch.float32
     assert torch.equal(t[0], torch.tensor([1.0] * 4 + [0.0] * 4))
     assert abs(float(t[3, 1]) - float(torch.cos(torch.tensor(3 * 100.0 ** -0.25)))) < 1e-6
+
+
+def test_the_example_is_the_one_shown():
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = open(os.path.join(root, "paged_kv_cache_317_gb300", "examples", "sparse_step.py")).read()
+    body = code.split('"""', 2)[2].strip()
+    assert body in open(os.path.join(root, "README.md")).read()
