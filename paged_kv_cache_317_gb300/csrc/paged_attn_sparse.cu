@@ -53,7 +53,7 @@ struct SparseParams {
   float qscale;         // scale * log2(e)
 };
 
-// Partials of a column: m = running maximum (NaN once a logit was), l = sum of 2^(s - m);
+// Partials of a column: m = running maximum (NaN once a logit was), l = sum of the weights;
 // m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity), which have
 // no weight in a join.
 // 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
@@ -75,6 +75,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   using Gm = Geo<D>;
   using T = typename Tag::T;
   constexpr int kCols = 8 * NT;
+  // Weights are kept as 2^(s - m + kLift), sums and products alike: fp16 has no numbers below
+  // 2^-24, and a long list's many small weights would be lost next to one of 1.
+  constexpr float kLift = std::is_same<Tag, F16>::value ? 12.f : 0.f;
   if (threadIdx.x == 0) {  // arguments, not memory of the kernel before
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
@@ -285,8 +288,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       // all -infinity so far: any finite base gives them the weight 0
       const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
       const float a0 = exp2f(m[t][0] - b0), a1 = exp2f(m[t][1] - b1);
-      const float p0 = exp2f(sc[t][0] - b0), p1 = exp2f(sc[t][1] - b1);
-      const float p2 = exp2f(sc[t][2] - b0), p3 = exp2f(sc[t][3] - b1);
+      const float s0 = kLift - b0, s1 = kLift - b1;
+      const float p0 = exp2f(sc[t][0] + s0), p1 = exp2f(sc[t][1] + s1);
+      const float p2 = exp2f(sc[t][2] + s0), p3 = exp2f(sc[t][3] + s1);
       l[t][0] = fmaf(l[t][0], a0, p0 + p2);
       l[t][1] = fmaf(l[t][1], a1, p1 + p3);
       if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {

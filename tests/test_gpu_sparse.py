@@ -9,7 +9,8 @@ at each addition):
   weight by a factor within e^(+-d); the probabilities enter the product as two half-precision
   numbers, off by 2^-17 (bf16) of the weight at most; exponentials, n products and sums add
   (n + 16) u.  Numerator and denominator both, so the result is within twice that of the sum of
-  w_t |v_t|; a half-precision output is rounded by half a step on top.
+  w_t |v_t|; a half-precision output is rounded by half a step on top.  fp16 has steps of 2^-24 at
+  least and holds 2^12 times the weight: 2^-37 (of a largest weight of 1) per token and |v| besides.
 """
 
 import numpy as np
@@ -92,6 +93,8 @@ def check_attention(out, b, selected, kc=None, vc=None):
     d = (b["D"] + 4) * U * reach[..., None]
     split = 2.0 ** -17
     bound = 2 * (np.expm1(2 * d) + split + (n + 16) * U) * spread
+    if b["q"].dtype == torch.float16:
+        bound = bound + n * 2.0 ** -37 * float(torch.nan_to_num(b["vc"].float()).abs().max())
     if out.dtype != torch.float32:
         bound = bound + half_ulp(np.abs(ref) + bound, out.dtype)
     err = np.abs(f64(out) - ref)
@@ -194,6 +197,21 @@ def test_infinite_keys_in_listed_blocks(B):
     b["kc"][:] = -INF                               # every logit -inf: no softmax
     assert torch.isnan(attend(B, b, sel)).all()
     assert (scores_of(B, make(7, [0], 1, 1, 64, 16, torch.bfloat16)) == -INF).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_small_weights_next_to_a_large_one(B, dtype):
+    """8000 weights of 2^-25.5 of the largest, whose value is 0: they are all of the result."""
+    b = make(10, [8001], 1, 1, 64, 16, dtype)
+    b["kc"].fill_(0), b["vc"].fill_(1), b["q"].fill_(0)
+    b["q"][..., 0] = 1
+    first = int(b["tables"][0, 0])
+    b["kc"][first, 0, 0, 0], b["vc"][first, 0, 0] = 17.625, 0     # 25.43 / log2(e)
+    b["scale"] = 1.0
+    sel = np.arange(501, dtype=np.int32)[None, None]
+    out = attend(B, b, sel)
+    check_attention(out, b, sel)
+    assert float(out.min()) > 1e-4
 
 
 def test_nan_bounds_make_nan_scores_that_are_kept(B):
