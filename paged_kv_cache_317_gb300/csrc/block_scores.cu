@@ -7,11 +7,11 @@
 //    the blocks as the rows, the channels of hi and then of lo as the inner dimension and the
 //    query heads, 8 at a time, as the columns.  Consecutive warps take consecutive heads,
 //    whose bounds lie side by side.
+//  * A warp copies whole rows, asynchronously, into a ring of its own in shared memory: the next
+//    16 blocks are on their way during the products (64-byte pieces of rows instead: 38.5 us).
 //  * A product does not mind in which order the channels come, as long as both operands agree:
 //    each lane takes 16 consecutive bytes of its rows and of its head's query and uses them as
-//    fragments where they are.  The lane that uses a piece of a bound also copies it,
-//    asynchronously, into a ring in shared memory: the ring only stands in for registers, so
-//    that the next 16 blocks are on their way during the products, and needs no barriers.
+//    fragments where they are.
 //  * Products of two half-precision numbers are exact in fp32, sums are kept in fp32.
 // 4 operations per bound and query head: bound by HBM for batches, by latency for one sequence.
 #include <cuda_runtime.h>
@@ -51,8 +51,8 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// kStages: 16-block tiles in the ring; 1 where a warp has one tile, else 2 (48 contexts: 38.6 us
-// with 2, 42.7 us with 3, 63 us with 4: more warps on an SM count for more than deeper rings).
+// kStages: 16-block tiles in the ring; 1 where a warp has one tile, else 2 (48 contexts, 225 MB:
+// 37.0 us with 2, 40.6 us with 3: more warps on an SM count for more than deeper rings).
 template <class Tag, int D, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
   constexpr int kPieces = D / 8;         // 16-byte pieces of a row
@@ -93,23 +93,23 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
     }
   }
   const int g = lane >> 2, tq = lane & 3;
-  uint4* mine = ring + static_cast<size_t>(warp) * kStages * kPieces * 32 + lane;
-  // The lane's pieces of rows g and g + 8 of tile t: hi then lo, into stage t % kStages.
+  // A stage is hi then lo, [16 rows][pieces], odd rows with their 64-byte halves exchanged, so that
+  // the rows g and g + 1 that a quarter of a warp reads at the same pieces lie on other banks.
+  uint4* mine = ring + static_cast<size_t>(warp) * kStages * kPieces * 32;
+  // Copies tile t into stage t % kStages, whole rows at a time: kPieces lanes to a row.
+  const int my_row = lane / kPieces, my_piece = lane % kPieces;
   auto issue = [&](int t) {
     if (16 * t < held) {
-      uint4* dst = mine + (t % kStages) * kPieces * 32;
+      uint4* dst = mine + (t % kStages) * kPieces * 32 + lane / kPieces * kPieces;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int b = __shfl_sync(kFullMask, t < 2 ? blk[0] : blk[1], (t & 1) * 16 + 8 * e + g);
-        if (16 * t + 8 * e + g < held) {  // the other rows' products are not used
-          const size_t at = (static_cast<size_t>(b) * p.num_kv_heads + head) * kPieces + tq;
-          const uint4* hi = static_cast<const uint4*>(p.k_max) + at;
-          const uint4* lo = static_cast<const uint4*>(p.k_min) + at;
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            copy_async16(dst + (4 * i + e) * 32, hi + 4 * i);
-            copy_async16(dst + (4 * i + 2 + e) * 32, lo + 4 * i);
-          }
+      for (int r0 = 0; r0 < kRows; r0 += 32 / kPieces) {
+        const int r = r0 + my_row;
+        const int b = __shfl_sync(kFullMask, t < 2 ? blk[0] : blk[1], (t & 1) * 16 + r);
+        if (16 * t + r < held) {  // the other rows' products are not used
+          const size_t at = (static_cast<size_t>(b) * p.num_kv_heads + head) * kPieces + my_piece;
+          const int to = r0 * kPieces + (my_piece ^ ((r & 1) << 2));
+          copy_async16(dst + to, static_cast<const uint4*>(p.k_max) + at);
+          copy_async16(dst + kRows * kPieces + to, static_cast<const uint4*>(p.k_min) + at);
         }
       }
     }
@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
       for (int i = 0; i < kSteps; ++i) x[i] = q[min(g, group - 1) * kPieces + 4 * i];
     }
     copy_wait<kStages - 1>();
-    const uint4* src = mine + (t % kStages) * kPieces * 32;
+    __syncwarp();
+    const uint4* src = mine + (t % kStages) * kPieces * 32 + g * kPieces;
     float best[2] = {-INFINITY, -INFINITY};
     for (int h0 = 0; h0 < group; h0 += 8) {
       if (group > 8) {  // columns past the last head repeat it
@@ -141,8 +142,9 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
       for (int i = 0; i < kSteps; ++i) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const uint4 qp = max8(x[i], zero, Tag{}), qn = min8(x[i], zero, Tag{});
-        const uint4 h_0 = src[(4 * i) * 32], h_1 = src[(4 * i + 1) * 32];
-        const uint4 l_0 = src[(4 * i + 2) * 32], l_1 = src[(4 * i + 3) * 32];
+        const int at = (4 * i + tq) ^ ((g & 1) << 2);
+        const uint4 h_0 = src[at], h_1 = src[8 * kPieces + at];
+        const uint4 l_0 = src[16 * kPieces + at], l_1 = src[24 * kPieces + at];
         const uint32_t u0[4] = {h_0.x, h_1.x, h_0.y, h_1.y}, u1[4] = {h_0.z, h_1.z, h_0.w, h_1.w};
         const uint32_t v0[4] = {l_0.x, l_1.x, l_0.y, l_1.y}, v1[4] = {l_0.z, l_1.z, l_0.w, l_1.w};
         mma(up, u0, qp.x, qp.y, Tag{});
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
       best[e] = max_nan(best[e], __shfl_xor_sync(kFullMask, best[e], 2));
       if (tq == 0 && 16 * t + 8 * e + g < held) out[first + 16 * t + 8 * e + g] = best[e] * p.scale;
     }
+    __syncwarp();  // the stage is read
   }
   copy_wait<0>();
 }
