@@ -601,6 +601,13 @@ def _new_out(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(t, stream):
+    """_new_out of t's shape, type and device (a microsecond less than by giving them)."""
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _new_out(t.shape, t.dtype, t.device, stream)
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -703,7 +710,7 @@ def kv_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Te
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need cos_sin")
     if q is not None and q_out is None:
-        q_out = _new_out((T, Hq, D), dtype, q.device, stream)
+        q_out = _new_like(q, stream)
     _check(load_library().kv_cache_append_rope(
         _address(q), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step, query_start.data_ptr(),
         T, int(max_query_len), k_cache.data_ptr(), v_cache.data_ptr(), _address(k_min),
@@ -800,10 +807,12 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     _need_all(device, dtype, "q k_cache v_cache", (q, (N, Hq, D)), (k_cache, cache), (v_cache, cache))
     _need_all(device, i32, "block_tables seq_lens selected", (block_tables, (N, MB)),
               (seq_lens, (N,)), (selected, (N, H, S)))
-    if out is None:
-        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
-    else:
+    if out is not None:
         _need_all(device, out_dtype, "out", (out, (N, Hq, D)))
+    elif out_dtype is dtype:
+        out = _new_like(q, stream)
+    else:
+        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
     _check(load_library().paged_attn_sparse(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),

@@ -448,3 +448,58 @@ def test_the_example_runs(B):
     b = dict(lens=lens, tables=env["tables"].cpu().numpy(), kc=env["kc"], vc=env["vc"], q=env["q"], bs=16,
              scale=128 ** -0.5, D=128)
     check_attention(env["out"], b, sel)
+
+
+def test_a_million_tokens(B):
+    b = make(50, [(1 << 20) - 7], 4, 1, 64, 16, torch.bfloat16)
+    rec = B.new_error_record()
+    s = scores_of(B, b, error_record=rec)
+    check_scores(s, b)
+    sel = B.paged_block_select(s, dev(b["lens"]), 16, 4096, 1, 4, error_record=rec)
+    assert np.array_equal(sel.cpu().numpy(), OS.block_select(s.cpu().numpy(), b["lens"], 16, 4096, 1, 4))
+    check_attention(attend(B, b, sel.cpu().numpy(), error_record=rec), b, sel.cpu().numpy())
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+
+
+def test_the_largest_batch(B):
+    """65535 sequences, the most a call takes, two tokens each in a block of its own; one more is
+    refused."""
+    N, D, bs = 65535, 64, 8
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.float16)
+    kc, vc = randn(N + 1, 1, bs, D), randn(N + 1, 1, bs, D)
+    lo, hi = torch.empty_like(kc[:, :, 0]), torch.empty_like(kc[:, :, 0])
+    tables = torch.arange(N + 1, dtype=torch.int32, device="cuda").flip(0)[:, None].contiguous()
+    lens = torch.full((N + 1,), 2, dtype=torch.int32, device="cuda")
+    start = torch.arange(N + 2, dtype=torch.int32, device="cuda")
+    q, k, v = randn(N + 1, 2, D), randn(N + 1, 1, D), randn(N + 1, 1, D)
+    table, rec = B.rope_cos_sin(8, D), B.new_error_record()
+
+    def step(n):
+        B.kv_block_bounds(kc, tables[:n], lens[:n] - 1, lo, hi, error_record=rec)
+        turned = B.kv_cache_append_rope(q[:n], k[:n], v[:n], start[:n + 1], 1, kc, vc, tables[:n], lens[:n],
+                                        table, k_min=lo, k_max=hi, error_record=rec)
+        s = B.paged_block_scores(turned, lo, hi, tables[:n], lens[:n], 0.125, bs, error_record=rec)
+        sel = B.paged_block_select(s, lens[:n], bs, 1, error_record=rec)
+        return turned, s, B.paged_attn_sparse(turned, kc, vc, tables[:n], lens[:n], sel, 0.125,
+                                              error_record=rec)
+
+    turned, s, out = step(N)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    pick = np.array([0, 1, 30000, N - 1])
+    blocks = [N - int(i) for i in pick]
+    small = dict(tables=np.arange(4)[:, None], lens=np.full(4, 2), kc=kc[blocks], vc=vc[blocks], lo=lo[blocks],
+                 hi=hi[blocks], q=turned[pick], bs=bs, scale=0.125, D=D, H=1)
+    check_scores(s[pick], small)
+    check_attention(out[pick], small, np.zeros((4, 1, 1), np.int32))
+    # prompts: two tokens of each
+    starts = 2 * start[:N + 1]
+    two = randn(2 * N, 1, D)
+    B.kv_cache_append_rope(None, two, two, starts, 2, kc, vc, tables[:N], lens[:N], None, k_min=lo, k_max=hi,
+                           error_record=rec)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    at = torch.from_numpy(pick).cuda()
+    assert torch.equal(kc[blocks, 0, 1], two[2 * at + 1, 0]) and torch.equal(vc[blocks, 0, 0], two[2 * at, 0])
+    assert torch.equal(lo[blocks, 0], torch.minimum(two[2 * at, 0], two[2 * at + 1, 0]))
+    with pytest.raises(B.PagedKVError, match="INVALID_ARG"):
+        step(N + 1)
