@@ -161,6 +161,20 @@ def test_long_lists(B, seqs, keep, H, G):
     check_attention(attend(B, b, sel), b, sel)
 
 
+def test_short_lists_spread_over_clusters(B):
+    """Few rows, one query head in the last tile of a group: the clusters' blocks have next to
+    nothing to do after they have read one another's sums, and must still wait for one another
+    before they leave."""
+    b = make(11, [3, 0, 1, 1, 2], 66, 2, 128, 48, torch.float16, wide=3)
+    sel = lists(np.random.default_rng(0), b, 7)
+    tables, lens, sel_d = dev(b["tables"]), dev(b["lens"]), dev(sel)
+    first = attend(B, b, sel)
+    check_attention(first, b, sel)
+    for _ in range(3000):
+        out = B.paged_attn_sparse(b["q"], b["kc"], b["vc"], tables, lens, sel_d, b["scale"])
+    assert torch.equal(out, first)
+
+
 def test_all_blocks_listed_equals_the_dense_decode(B):
     b = make(4, [130, 16, 77, 1], 4, 4, 128, 16, torch.bfloat16)
     every = np.broadcast_to(np.arange(9, dtype=np.int32), (4, 4, 9))
