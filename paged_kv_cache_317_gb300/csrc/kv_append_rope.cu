@@ -357,7 +357,7 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   // first_slot, with behind them blocks that check the ranges, by chunks of heads.
   const bool one = max_query_len == 1;
   p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;
-  const int checkers = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
+  const int range_blocks = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
   const auto chunks = [](long long n, long long size) { return (n + size - 1) / size; };
   const auto head_chunks = [&] { return chunks(num_heads, p.heads) + 2 * chunks(num_kv_heads, p.heads); };
   // 32 heads a thread block, down to 8 while that leaves fewer than 8 blocks for each SM (24
@@ -368,7 +368,7 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
       one ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads) : head_chunks();
   if (groups > 65535) return PA_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + checkers), static_cast<unsigned>(groups));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + range_blocks), static_cast<unsigned>(groups));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
