@@ -616,16 +616,24 @@ int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seq
  *                 num_kv_heads + h) and skipped.
  *   head_dim      64, 128 or 256;  block_size: a multiple of 16, or 8
  *   out           device [num_seqs][num_heads][head_dim] in `out_dtype`, 16-byte aligned
+ *   workspace     device, 16-byte aligned, at least paged_attn_sparse_workspace_size(...)
+ *                 bytes, scratch of this call alone; or NULL: a list is then read by at most 8
+ *                 thread blocks, which is slow where few rows have long lists (the size is 0
+ *                 otherwise).
  * Arithmetic as in paged_attn_prefill: logits and sums in fp32, probabilities as a pair of
  * half-precision numbers.  num_blocks * num_kv_heads * block_size must be < 2^31.
  * A block-table entry out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and block 0
  * is read; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
+size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int block_size, int max_blocks_per_seq,
+                                        int num_selected);
 int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_tables, const int32_t* seq_lens,
                       const int32_t* selected, int num_selected, int num_seqs, int num_heads,
                       int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                       int num_blocks, float scale, int dtype, void* out, int out_dtype,
-                      int32_t* error_record, void* stream);
+                      void* workspace, size_t workspace_bytes, int32_t* error_record,
+                      void* stream);
 
 /* ---------------------------------------------------------------------------
  * Copy-on-write block copy  [P3d]

@@ -251,7 +251,9 @@ SIGNATURES = {
                                    c_int, c_void_p, c_void_p, c_void_p]),
     "paged_attn_sparse": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                   c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
-                                  c_float, c_int, c_void_p, c_int, c_void_p, c_void_p]),
+                                  c_float, c_int, c_void_p, c_int, c_void_p, c_size_t, c_void_p,
+                                  c_void_p]),
+    "paged_attn_sparse_workspace_size": (c_size_t, [c_int] * 7),
     "block_copy": (c_int, [ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p), c_int, c_void_p,
                            c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "pa_decode_partition_tokens": (c_int, [c_void_p, c_int, c_int, c_int, c_int, P_int32]),
@@ -787,14 +789,23 @@ def paged_block_select(scores: torch.Tensor, seq_lens: torch.Tensor, block_size:
     return out
 
 
+def paged_attn_sparse_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                     max_blocks_per_seq, num_selected) -> int:
+    """Workspace bytes of a paged_attn_sparse call (0 but for few rows with long lists)."""
+    return int(load_library().paged_attn_sparse_workspace_size(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_selected))
+
+
 def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                       block_tables: torch.Tensor, seq_lens: torch.Tensor,
                       selected: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
-                      out_dtype=torch.float32, error_record: Optional[torch.Tensor] = None,
-                      stream=None) -> torch.Tensor:
+                      out_dtype=torch.float32, workspace: Optional[torch.Tensor] = None,
+                      error_record: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Decode attention over the tokens of the listed blocks alone.  q [N,Hq,D]; caches
     [B,H,bs,D], Hq a multiple of H; block_tables int32 [N,MB]; seq_lens int32 [N]; selected
-    int32 [N,H,S], logical blocks of the sequence, -1 for none (paged_block_select)."""
+    int32 [N,H,S], logical blocks of the sequence, -1 for none (paged_block_select); workspace:
+    optional contiguous tensor of at least paged_attn_sparse_workspace_size(...) bytes, made here
+    if it is needed and not given."""
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
@@ -813,11 +824,19 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         out = _new_like(q, stream)
     else:
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
-    _check(load_library().paged_attn_sparse(
+    lib = load_library()
+    if workspace is None:
+        need = lib.paged_attn_sparse_workspace_size(N, Hq, H, D, bs, MB, S)
+        if need:
+            workspace = _new_out((need,), torch.uint8, q.device, stream)
+    else:
+        _need_all(device, workspace.dtype, "workspace", (workspace, workspace.shape))
+        need = workspace.numel() * workspace.element_size()
+    _check(lib.paged_attn_sparse(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
         seq_lens.data_ptr(), selected.data_ptr(), S, N, Hq, H, D, bs, MB, B, float(scale),
-        _DTYPE[dtype], out.data_ptr(), _DTYPE[out.dtype], _record(error_record, device),
-        _raw_stream(stream, device)), "paged_attn_sparse")
+        _DTYPE[dtype], out.data_ptr(), _DTYPE[out_dtype], _address(workspace), need,
+        _record(error_record, device), _raw_stream(stream, device)), "paged_attn_sparse")
     return out
 
 

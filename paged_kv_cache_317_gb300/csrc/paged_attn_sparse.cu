@@ -14,8 +14,9 @@
 //    units, O^T += V^T.P^T with P as a high and a low half-precision number.  Up to 8 query
 //    heads cost one product, up to 16 two; K and V are read once for all of them.
 //  * At the end the warps' (m, l, O) are joined in shared memory, and those of the cluster's
-//    blocks over distributed shared memory, in a fixed order: no workspace, no second
-//    kernel, the same bits on every run.
+//    blocks over distributed shared memory, in a fixed order: the same bits on every run.  Only
+//    where a few rows have long lists are a row's chunks spread over several clusters, whose sums
+//    go through a workspace to a second kernel.
 // Two operations per cached byte and query head: bound by HBM.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,6 +37,7 @@ constexpr int kChunk = 16;       // tokens per stage
 constexpr int kWarps = 4;        // warps per thread block
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxParts = 64;    // clusters per row
 constexpr int kAlign = 1024;     // a swizzled box must start on 1024 bytes
 constexpr int kHeader = 1024;    // barriers and the chunks' row counts
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,6 +51,9 @@ struct SparseParams {
   int32_t* err;
   int num_selected, num_heads, num_kv_heads, block_size, max_blocks, num_blocks;
   int group, tiles;     // query heads per key head; tiles of 8 NT of them
+  int parts;            // clusters per row
+  float* part_o;        // [row][part][8 NT][D], with parts > 1
+  float2* part_ml;      // [row][part][8 NT]
   int out_dtype, stages;
   float qscale;         // scale * log2(e)
 };
@@ -86,7 +91,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int S = p.stages;
-  const int row = blockIdx.x / ranks;  // (sequence, key head, tile)
+  const int cluster = blockIdx.x / ranks;
+  const int row = cluster / p.parts, part = cluster - row * p.parts;  // row: (sequence, key head, tile)
   const int tile = row % p.tiles;
   const int sh = row / p.tiles;        // sequence * key heads + key head
   const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   // Chunk c of a row is 16 tokens of list entry c / (bs / 16), or with 8-token blocks
   // entries 2 c and 2 c + 1.  This warp takes c = me, me + all, ...; its lanes look up 32 of
   // them at a time and `mask` names those with tokens that are not issued yet.
-  const int me = rank * kWarps + warp, all = ranks * kWarps;
+  const int me = (part * ranks + rank) * kWarps + warp, all = p.parts * ranks * kWarps;
   const bool small = p.block_size == 8;
   const int sub = small ? 1 : p.block_size / kChunk;
   const int chunks = small ? (p.num_selected + 1) / 2 : p.num_selected * sub;
@@ -134,25 +140,25 @@ __global__ void __launch_bounds__(kWarps * 32)
   fetch();
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
-    if (threadIdx.x == 0 && rank == 0 && head == 0 && tile == 0)
+    if (threadIdx.x == 0 && rank == 0 && part == 0 && head == 0 && tile == 0)
       report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     L = min(max(L, 0), cap);
   }
-  // The tokens of block b from its row 16 part on, at most `height`, and their row in the cache
+  // The tokens of block b from its row 16 from on, at most `height`, and their row in the cache
   // seen as rows of D.
-  auto rows_in = [&](int b, int blk, int part, int height, int& y) -> int {
+  auto rows_in = [&](int b, int blk, int from, int height, int& y) -> int {
     if (b < -1 || b >= p.max_blocks) {
-      if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, sh, b);
+      if (from == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, sh, b);
       return 0;
     }
     if (b < 0) return 0;
-    const int rows = min(height, L - b * p.block_size - part * kChunk);
+    const int rows = min(height, L - b * p.block_size - from * kChunk);
     if (rows <= 0) return 0;
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-      if (part == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
+      if (from == 0 && tile == 0) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       blk = 0;
     }
-    y = (blk * p.num_kv_heads + head) * p.block_size + part * kChunk;
+    y = (blk * p.num_kv_heads + head) * p.block_size + from * kChunk;
     return rows;
   };
   unsigned mask = 0;
@@ -451,9 +457,62 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
     const int i = (threadIdx.x + k * kWarps * 32) * ranks + rank;
-    if (i < cols * (D / 4)) finish(acc[k], M[k], sum[k], tokens[k], i / (D / 4), i % (D / 4) * 4);
+    if (i < cols * (D / 4)) {
+      const int col = i / (D / 4), d = i % (D / 4) * 4;
+      if (p.parts == 1) {
+        finish(acc[k], M[k], sum[k], tokens[k], col, d);
+      } else {
+        const size_t at = static_cast<size_t>(cluster) * kCols + col;
+        *reinterpret_cast<float4*>(p.part_o + at * D + d) = acc[k];
+        if (d == 0) p.part_ml[at] = make_float2(M[k], M[k] == -INFINITY && tokens[k] ? -1.f : sum[k]);
+      }
+    }
   }
   cluster_wait();  // no block leaves while another may read its memory
+}
+
+// Joins the parts of a row: a thread block per query head, four channels a thread.
+template <int D, int NT>
+__global__ void __launch_bounds__(D / 4) paged_attn_sparse_join_kernel(const SparseParams p) {
+  constexpr int kCols = 8 * NT, kAhead = 8;
+  const int seq = blockIdx.x / p.num_heads, g = blockIdx.x - seq * p.num_heads;
+  const int head = g / p.group, r = g - head * p.group;
+  const size_t row = (static_cast<size_t>(seq) * p.num_kv_heads + head) * p.tiles + r / kCols;
+  const size_t at = row * p.parts * kCols + r % kCols;
+  const int d = threadIdx.x * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float M = -INFINITY, sum = 0.f;
+  bool tokens = false;
+#pragma unroll 8
+  for (int i = 0; i < p.parts; ++i) M = max_nan(M, p.part_ml[at + i * kCols].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < p.parts; i0 += kAhead) {
+    float2 ml[kAhead];
+    float4 v[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const size_t from = at + static_cast<size_t>(min(i0 + j, p.parts - 1)) * kCols;
+      ml[j] = p.part_ml[from];
+      v[j] = *reinterpret_cast<const float4*>(p.part_o + from * D + d);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i0 + j >= p.parts) break;
+      tokens |= ml[j].y < 0.f || ml[j].x != -INFINITY;
+      if (ml[j].x != -INFINITY) {
+        const float w = exp2f(ml[j].x - M);
+        sum = fmaf(w, ml[j].y, sum);
+        acc.x = fmaf(w, v[j].x, acc.x);
+        acc.y = fmaf(w, v[j].y, acc.y);
+        acc.z = fmaf(w, v[j].z, acc.z);
+        acc.w = fmaf(w, v[j].w, acc.w);
+      }
+    }
+  }
+  const float inv = inverse_of(M, sum, tokens);
+  const float out[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  store_out<4>(p.out, static_cast<size_t>(blockIdx.x) * D + d, out, p.out_dtype);
 }
 
 template <int D, int NT>
@@ -464,53 +523,103 @@ size_t smem_bytes(int stages) {
   return kHeader + kAlign + (ring > join ? ring : join);
 }
 
-// Thread blocks per row and stages per ring: of the choices, the one with the least time by a
-// model of the launch.  `slots` blocks are resident at a time and share the memory's rate; the
-// blocks of the last, partly filled wave run at the rate that their own copies in flight allow.
-// Clusters wait for their slowest block and for free places on neighbouring SMs, which costs an
-// eighth, so only launches of few rows have them.  On GB300 (D = 128, us):
+// Thread blocks per cluster, clusters per row and stages per ring: of the choices, the one with
+// the least time by a model of the launch.  `slots` blocks are resident at a time and share the
+// memory's rate; the blocks of the last, partly filled wave run at the rate that their own copies
+// in flight allow.  Clusters wait for their slowest block and for free places on neighbouring
+// SMs, which costs an eighth, so only launches of few rows have them; several clusters per row
+// cost a second kernel, so only few rows with long lists do.  On GB300 (D = 128, us):
 //   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
 //   1280 rows of 0.5 MB:  ranks 1 with stages 2: 100, 3: 106 (two blocks an SM instead of three)
 struct Shape {
-  int ranks, stages;
+  int ranks, parts, stages;
 };
 Shape shape_for(long long rows, double row_bytes, size_t smem2, size_t smem3, double stage_bytes,
-                int most_per_sm) {
+                int most_per_sm, int most_parts) {
   constexpr double kRate = 6.8e6, kLatency = 1.5;  // bytes per us; us from a copy's start to its reuse
-  Shape best{1, 2};
+  Shape best{1, 1, 2};
   double least = 1e30;
   for (int stages = 2; stages <= 3; ++stages) {
     const size_t smem = stages == 2 ? smem2 : smem3;
     if (smem > 227 * 1024) continue;
     const int fit = static_cast<int>(228 * 1024 / (smem + 1024));
     const long long slots = 152ll * (fit < most_per_sm ? fit : most_per_sm);
-    for (int ranks = 1; ranks <= kMaxCluster; ranks *= 2) {
-      const long long blocks = rows * ranks, full = blocks / slots, rest = blocks - full * slots;
-      const double bytes = row_bytes / ranks, alone = bytes * kLatency / (kWarps * stages * stage_bytes);
+    for (int all = 1; all <= kMaxCluster * most_parts; all *= 2) {  // blocks per row
+      const long long blocks = rows * all, full = blocks / slots, rest = blocks - full * slots;
+      const double bytes = row_bytes / all, alone = bytes * kLatency / (kWarps * stages * stage_bytes);
       const double shared = rest * bytes / kRate;
       double us = full * slots * bytes / kRate + (rest == 0 ? 0. : shared > alone ? shared : alone);
-      if (ranks > 1) us = us * 1.125 + 1.;
+      if (all > 1) us = us * 1.125 + 1.;
+      if (all > kMaxCluster) us += 3.;
       if (us < least) {
         least = us;
-        best = {ranks, stages};
+        best = {all < kMaxCluster ? all : kMaxCluster, all <= kMaxCluster ? 1 : all / kMaxCluster, stages};
       }
     }
   }
   return best;
 }
 
+template <int D, int NT>
+Shape shape_of(long long rows, int num_selected, int max_blocks, int block_size, bool parts) {
+  const long long held = num_selected < max_blocks ? num_selected : max_blocks;
+  const long long chunks = (held * block_size + kChunk - 1) / kChunk;
+  return shape_for(rows, static_cast<double>(chunks) * 2 * Geo<D>::kTileBytes, smem_bytes<D, NT>(2),
+                   smem_bytes<D, NT>(3), 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4,
+                   parts ? kMaxParts : 1);
+}
+
+long long rows_of(int num_seqs, int num_kv_heads, int group, int cols) {
+  return static_cast<long long>(num_seqs) * num_kv_heads * ((group + cols - 1) / cols);
+}
+
+template <int D, int NT>
+size_t workspace_for(long long rows, int parts) {
+  if (parts == 1) return 0;
+  return static_cast<size_t>(rows) * parts * 8 * NT * (D * sizeof(float) + sizeof(float2));
+}
+
+template <int D, int NT>
+size_t workspace_size(int num_seqs, int num_kv_heads, int group, int num_selected, int max_blocks,
+                      int block_size) {
+  const long long rows = rows_of(num_seqs, num_kv_heads, group, 8 * NT);
+  return workspace_for<D, NT>(rows, shape_of<D, NT>(rows, num_selected, max_blocks, block_size, true).parts);
+}
+
+template <class... Kernel, class... Args>
+bool launch_dependent(void (*kernel)(Kernel...), dim3 grid, dim3 block, size_t smem, int cluster,
+                      cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
+}
+
 template <class Tag, int D, int NT>
-int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seqs,
-           cudaStream_t stream) {
+int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seqs, void* workspace,
+           size_t workspace_bytes, cudaStream_t stream) {
   p.tiles = (p.group + 8 * NT - 1) / (8 * NT);
-  const long long rows = static_cast<long long>(num_seqs) * p.num_kv_heads * p.tiles;
-  const long long held = p.num_selected < p.max_blocks ? p.num_selected : p.max_blocks;
-  const long long chunks = (held * p.block_size + kChunk - 1) / kChunk;
-  const Shape shape = shape_for(rows, chunks * 2 * Geo<D>::kTileBytes, smem_bytes<D, NT>(2),
-                                smem_bytes<D, NT>(3), 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4);
+  const long long rows = rows_of(num_seqs, p.num_kv_heads, p.group, 8 * NT);
+  const Shape shape = shape_of<D, NT>(rows, p.num_selected, p.max_blocks, p.block_size, workspace != nullptr);
   const int ranks = shape.ranks;
   p.stages = shape.stages;
-  if (rows * ranks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  p.parts = shape.parts;
+  if (rows * ranks * p.parts > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  if (p.parts > 1) {
+    if (workspace_bytes < workspace_for<D, NT>(rows, p.parts)) return PA_ERR_INVALID_ARG;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * p.parts * 8 * NT * D);
+  }
   // the caches as [D / 64][rows][64]: one box is a chunk, or half of one with 8-token blocks
   const cuuint64_t cache_rows = static_cast<cuuint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   const cuuint64_t dims[3] = {64, cache_rows, D / 64};
@@ -528,29 +637,23 @@ int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seq
       cudaFuncSetAttribute(paged_attn_sparse_kernel<Tag, D, NT>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
     return PA_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * ranks));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ranks;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, paged_attn_sparse_kernel<Tag, D, NT>, tk, tv, p) != cudaSuccess)
+  if (!launch_dependent(paged_attn_sparse_kernel<Tag, D, NT>, dim3(static_cast<unsigned>(rows * ranks * p.parts)),
+                        dim3(kWarps * 32), smem, ranks, stream, tk, tv, p))
     return PA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (p.parts > 1 &&
+      !launch_dependent(paged_attn_sparse_join_kernel<D, NT>,
+                        dim3(static_cast<unsigned>(num_seqs) * static_cast<unsigned>(p.num_heads)),
+                        dim3(D / 4), 0, 1, stream, p))
+    return PA_ERR_CUDA;
+  return PA_OK;
 }
 
 template <class Tag, int D>
 int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, int num_seqs,
-              cudaStream_t stream) {
-  return p.group <= 8 ? launch<Tag, D, 1>(p, k_cache, v_cache, num_seqs, stream)
-                      : launch<Tag, D, 2>(p, k_cache, v_cache, num_seqs, stream);
+              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return p.group <= 8
+             ? launch<Tag, D, 1>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, stream)
+             : launch<Tag, D, 2>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, stream);
 }
 
 }  // namespace
@@ -558,12 +661,35 @@ int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, i
 
 using namespace pagedkv;
 
+extern "C" size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                   int head_dim, int block_size,
+                                                   int max_blocks_per_seq, int num_selected) {
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
+    return 0;
+  const int group = num_heads / num_kv_heads;
+  const auto size = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    return group <= 8 ? workspace_size<D, 1>(num_seqs, num_kv_heads, group, num_selected,
+                                             max_blocks_per_seq, block_size)
+                      : workspace_size<D, 2>(num_seqs, num_kv_heads, group, num_selected,
+                                             max_blocks_per_seq, block_size);
+  };
+  switch (head_dim) {
+    case 64: return size(std::integral_constant<int, 64>{});
+    case 128: return size(std::integral_constant<int, 128>{});
+    case 256: return size(std::integral_constant<int, 256>{});
+    default: return 0;
+  }
+}
+
 extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
                                  const int32_t* block_tables, const int32_t* seq_lens,
                                  const int32_t* selected, int num_selected, int num_seqs,
                                  int num_heads, int num_kv_heads, int head_dim, int block_size,
                                  int max_blocks_per_seq, int num_blocks, float scale, int dtype,
-                                 void* out, int out_dtype, int32_t* error_record, void* stream) {
+                                 void* out, int out_dtype, void* workspace,
+                                 size_t workspace_bytes, int32_t* error_record, void* stream) {
   NvtxRange range("paged_attn_sparse");
   if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
       block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_selected < 0)
@@ -584,7 +710,8 @@ extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void*
   if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !out ||
       (!selected && num_selected > 0))
     return PA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned16(workspace))
     return PA_ERR_INVALID_ARG;
   SparseParams p{};
   p.q = q;
@@ -605,14 +732,14 @@ extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void*
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == PA_BF16) {
     switch (head_dim) {
-      case 64: return launch_nt<BF16, 64>(p, k_cache, v_cache, num_seqs, st);
-      case 128: return launch_nt<BF16, 128>(p, k_cache, v_cache, num_seqs, st);
-      default: return launch_nt<BF16, 256>(p, k_cache, v_cache, num_seqs, st);
+      case 64: return launch_nt<BF16, 64>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
+      case 128: return launch_nt<BF16, 128>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
+      default: return launch_nt<BF16, 256>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
     }
   }
   switch (head_dim) {
-    case 64: return launch_nt<F16, 64>(p, k_cache, v_cache, num_seqs, st);
-    case 128: return launch_nt<F16, 128>(p, k_cache, v_cache, num_seqs, st);
-    default: return launch_nt<F16, 256>(p, k_cache, v_cache, num_seqs, st);
+    case 64: return launch_nt<F16, 64>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
+    case 128: return launch_nt<F16, 128>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
+    default: return launch_nt<F16, 256>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, st);
   }
 }

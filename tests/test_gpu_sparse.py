@@ -161,6 +161,47 @@ def test_long_lists(B, seqs, keep, H, G):
     check_attention(attend(B, b, sel), b, sel)
 
 
+@pytest.mark.parametrize("dtype,D,Hq,H,keep,bs", [(torch.bfloat16, 128, 1, 1, 700, 64),
+                                                  (torch.float16, 256, 9, 1, 600, 32),
+                                                  (torch.bfloat16, 64, 34, 2, 4000, 8)])
+def test_few_rows_with_long_lists(B, dtype, D, Hq, H, keep, bs):
+    """A row's list spread over several clusters, whose sums a second kernel joins; without a
+    workspace over one; rows without tokens, and with less than one chunk a cluster, among them."""
+    rng = np.random.default_rng(D)
+    for lens in ([keep * bs - 3], [bs * keep // 3, 0, 5]):
+        b = make(12, lens, Hq, H, D, bs, dtype, wide=keep - (-(-max(lens) // bs)))
+        sel = lists(rng, b, keep, spoil=len(lens) > 1)
+        need = B.paged_attn_sparse_workspace_size(len(lens), Hq, H, D, bs, b["tables"].shape[1], keep)
+        assert need > 0
+        ws, rec = torch.full((need,), 255, dtype=torch.uint8, device="cuda"), B.new_error_record()
+        for od in (torch.float32, dtype):
+            out = attend(B, b, sel, out_dtype=od, workspace=ws, error_record=rec)
+            check_attention(out, b, sel)
+            assert torch.equal(out, attend(B, b, sel, out_dtype=od))
+        assert B.pa_error_read(rec) == [0, 0, 0, 0]
+        lib, one = B.load_library(), torch.empty_like(b["q"])
+        tables, lens_d, sel_d = dev(b["tables"]), dev(b["lens"]), dev(sel)
+        assert lib.paged_attn_sparse(b["q"].data_ptr(), b["kc"].data_ptr(), b["vc"].data_ptr(),
+                                     tables.data_ptr(), lens_d.data_ptr(),
+                                     sel_d.data_ptr(), keep, len(lens), Hq, H, D, bs,
+                                     b["tables"].shape[1], len(b["kc"]), b["scale"], B._DTYPE[dtype],
+                                     one.data_ptr(), B._DTYPE[dtype], None, 0, None,
+                                     torch.cuda.current_stream().cuda_stream) == 0
+        check_attention(one, b, sel)
+        with pytest.raises(B.PagedKVError, match="INVALID_ARG"):
+            attend(B, b, sel, workspace=ws[:-1])
+    # every logit -infinity in all parts: no softmax; in all but one: that one's alone
+    b["kc"].fill_(-INF), b["q"].abs_(), b["q"].add_(1)
+    sel = lists(rng, b, keep, spoil=False)
+    assert torch.isnan(attend(B, b, sel)[0]).all()
+    b["kc"][int(b["tables"][0, 1])] = 0.5
+    only = np.full_like(sel, -1)
+    only[0, :, 0] = 1
+    only[2] = -1
+    out = attend(B, b, np.where(np.arange(3)[:, None, None] == 2, -1, sel).astype(np.int32))
+    check_attention(out, b, only)
+
+
 def test_short_lists_spread_over_clusters(B):
     """Few rows, one query head in the last tile of a group: the clusters' blocks have next to
     nothing to do after they have read one another's sums, and must still wait for one another

@@ -100,7 +100,7 @@ def test_select_refuses(lib):
 def test_attention_refuses(lib):
     def call(**kw):
         a = dict(q=P, kc=P, vc=P, bt=P, sl=P, sel=P, S=4, N=4, Hq=8, H=2, D=64, bs=16, MB=4, B=64,
-                 scale=0.125, dt=0, out=P, odt=2, err=None, stream=None)
+                 scale=0.125, dt=0, out=P, odt=2, ws=None, wsb=0, err=None, stream=None)
         a.update(kw)
         return lib.paged_attn_sparse(*a.values())
 
@@ -109,8 +109,12 @@ def test_attention_refuses(lib):
                dict(S=-1), dict(scale=float("nan")), dict(scale=float("inf")), dict(N=65536),
                dict(MB=1 << 28), dict(B=1 << 27), dict(q=None), dict(kc=None), dict(vc=None),
                dict(bt=None), dict(sl=None), dict(sel=None), dict(out=None), dict(q=P + 8), dict(kc=P + 8),
-               dict(vc=P + 8), dict(out=P + 8)):
+               dict(vc=P + 8), dict(out=P + 8), dict(ws=P + 8, wsb=1 << 30)):
         assert call(**kw) == INV, kw
+    # few rows with long lists: the workspace given is a byte short
+    long = dict(N=1, S=4096, MB=4096, B=8192)
+    need = lib.paged_attn_sparse_workspace_size(1, 8, 2, 64, 16, 4096, 4096)
+    assert need > 0 and call(ws=P, wsb=need - 1, **long) == INV
     for kw in (dict(D=96), dict(dt=2), dict(odt=3), dict(bs=24), dict(bs=4)):
         assert call(**kw) == UNS, kw
 
@@ -141,3 +145,17 @@ def test_the_example_is_the_one_shown():
     code = open(os.path.join(root, "paged_kv_cache_317_gb300", "examples", "sparse_step.py")).read()
     body = code.split('"""', 2)[2].strip()
     assert body in open(os.path.join(root, "README.md")).read()
+
+
+def test_attention_workspace_sizes(lib):
+    size = lib.paged_attn_sparse_workspace_size
+    assert size(1, 32, 8, 128, 16, 4096, 64) == 0          # short lists: one cluster a row
+    assert size(64, 64, 8, 128, 16, 4096, 128) == 0        # many rows
+    # rows x parts partials of 8 (16) columns: O in fp32, m and l
+    for heads, cols in ((8, 8), (16, 16), (17, 16)):
+        n = size(1, heads, 1, 128, 64, 512, 512)
+        rows = -(-heads // cols)
+        assert n > 0 and n % (rows * cols * (128 * 4 + 8)) == 0
+        assert n // (rows * cols * (128 * 4 + 8)) <= 64
+    assert size(0, 8, 2, 64, 16, 4096, 4096) == size(1, 7, 2, 64, 16, 4096, 4096) == 0
+    assert size(1, 8, 2, 96, 16, 4096, 4096) == size(1, 8, 2, 64, 16, 4096, 0) == 0
