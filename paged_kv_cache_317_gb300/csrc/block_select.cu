@@ -1,23 +1,24 @@
 // Block selection: the best num_selected of a row's scores, in increasing block order.
 //
-// A cluster of thread blocks (one, but for few long rows) per (sequence, key head), each with
+// A cluster of thread blocks (one, but for very long rows) per (sequence, key head), each with
 // a contiguous part of the row, of which each warp has a contiguous part in turn: up to 32
 // groups of 32 scores, one of each group per lane, read once and kept in registers.  Three
 // steps find the last score that is kept:
-//  1. With one thread block, the scores between the row's smallest and largest are spread evenly
-//     over 2048 bins (subtraction, product and rounding keep their order) and counted.  Every
+//  1. The scores between the row's smallest and largest are spread evenly
+//     over the bins (subtraction, product and rounding keep their order) and counted; the blocks
+//     of a cluster add up each other's counts.  Every
 //     score above the bin in which the count reaches num_selected is kept, and as a rule that
 //     bin holds a handful.  Skipped where a score is NaN or infinite.
 //  2. If the bin holds more than are wanted, its scores, listed in shared memory, are each
-//     ranked among one another.  Where they are too many, or step 1 was skipped, a score becomes
-//     a 32-bit key that orders as the scores do, and the last kept key is found 11 bits at a
-//     time from histograms of the keys that agree with it so far; the blocks of a cluster add up
-//     each other's histograms.
+//     ranked among one another.  Where they are too many, or the row is a cluster's, or step 1 was skipped, a score becomes
+//     a 32-bit key that orders as the scores do, and the last kept key is found 9 to 12 bits at
+//     a time from histograms of the keys that agree with it so far.
 //  3. A vote per group (two, where equal scores are kept in part) tells which of its blocks are
 //     kept; lane j takes the votes of group j, a scan of their counts over lanes, warps and
 //     blocks says where its blocks go, and it writes them, of equal ones the lowest.
 // Sums are of whole numbers, so the result is the same on every run.  Bound by latency (the
-// launch and some ten barriers) for one sequence and by instructions for batches.
+// launch and some ten barriers) for one sequence and by instructions for batches: few warps
+// with many groups each for many rows, many warps with few groups for few.
 #include <cuda_runtime.h>
 
 #include "cluster.cuh"
@@ -26,7 +27,6 @@
 namespace pagedkv {
 namespace {
 
-constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = 8;     // of them between two looks at how many there are
 
@@ -89,23 +89,24 @@ __device__ __forceinline__ void each_group(int groups, F f) {
   }
 }
 
-// kGroups: groups of 32 scores per warp, at most 32, one vote for each lane.  Rows of up to 2048
-// blocks take 8: less code to fetch (one 30k context: 4.0 us, 4.5 us with 32).
+// kGroups: groups of 32 scores per warp, at most 32, one vote for each lane.
 template <int kThreads, int kGroups>
 __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const SelectParams p) {
-  constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
-  static_assert(kThreads <= kBins, "a thread has a bin at least");
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kPer = 8, kBins = kPer * kThreads;  // bins per thread, and in all
+  constexpr int kBits = kThreads == 64 ? 9 : kThreads == 128 ? 10 : kThreads == 256 ? 11 : 12;
+  static_assert(kBins == 1 << kBits, "a bin for each digit");
   __shared__ __align__(16) int hist[2][kBins];
   __shared__ uint32_t warp_sum[2][kWarps], warp_range[2][kWarps];
   __shared__ int found[3];  // the bin, the scores above it, the scores in it
-  __shared__ uint32_t part_sum[kWarps], block_sum;
+  __shared__ uint32_t part_sum[kWarps], block_sum, block_range[2];
   __shared__ int listed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
-  const int head = blockIdx.x / ranks, seq = blockIdx.y;
+  const size_t row = blockIdx.x / ranks;
+  const int seq = static_cast<int>(row / p.num_kv_heads), head = static_cast<int>(row % p.num_kv_heads);
   for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
   if (tid == 0) listed = 0;
-  const size_t row = static_cast<size_t>(seq) * p.num_kv_heads + head;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int L = p.seq_lens[seq];
@@ -150,10 +151,17 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
 #pragma unroll
       for (int j = 0; j < kPer; ++j) bin[j] = 0;
       const uint32_t at = smem_addr(&hist[turn][bin0]);
+#pragma unroll 2
       for (int r = 0; r < ranks; ++r) {
         const uint32_t peer = peer_addr(at, r);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) bin[j] += static_cast<int>(ld_peer_u32(peer + 4 * j));
+        for (int j = 0; j < kPer; j += 4) {
+          const uint4 v = ld_peer4_u32(peer + 4 * j);
+          bin[j] += static_cast<int>(v.x);
+          bin[j + 1] += static_cast<int>(v.y);
+          bin[j + 2] += static_cast<int>(v.z);
+          bin[j + 3] += static_cast<int>(v.w);
+        }
       }
     }
     // the other histogram, for the next count: its readers are past the barrier above
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
     int turn = 0;
     bool ranked = false;  // `open` are the blocks with the last kept score
     ties = true;
-    if (ranks == 1) {
+    {
       float low = INFINITY, high = -INFINITY;  // high is NaN if a score is
       each_group<kGroups>(groups, [&](int j) {
         if (open >> j & 1) {
@@ -203,8 +211,21 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
         warp_range[1][warp] = high_key;
       }
       __syncthreads();
-      low = score_of(__reduce_min_sync(kFullMask, lane < kWarps ? warp_range[0][lane] : 0xffffffffu));
-      high = score_of(__reduce_max_sync(kFullMask, lane < kWarps ? warp_range[1][lane] : 0u));
+      uint32_t from = __reduce_min_sync(kFullMask, lane < kWarps ? warp_range[0][lane] : 0xffffffffu);
+      uint32_t to = __reduce_max_sync(kFullMask, lane < kWarps ? warp_range[1][lane] : 0u);
+      if (ranks > 1) {
+        if (tid == 0) {
+          block_range[0] = from;
+          block_range[1] = to;
+        }
+        cluster_sync();
+        const uint32_t at = smem_addr(block_range);
+        const uint32_t peer = peer_addr(at, min(lane, ranks - 1));
+        from = __reduce_min_sync(kFullMask, ld_peer_u32(peer));
+        to = __reduce_max_sync(kFullMask, ld_peer_u32(peer + 4));
+      }
+      low = score_of(from);
+      high = score_of(to);
       // (not so if a score is NaN or infinite, or if all are nearly equal)
       const float scale = (kBins - 1) / (high - low);
       if (low > -INFINITY && high < INFINITY && scale > 0.f && scale < 1e38f) {
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
         });
         open &= same;
         const int n = found[2];
-        if (ties && n <= kThreads) {  // list the bin's scores (over hist[0]) and rank each
+        if (ties && ranks == 1 && n <= kThreads) {  // list the bin's scores (over hist[0]) and rank each
           const bool some = __any_sync(kFullMask, open != 0);
           if (some)
             each_group<kGroups>(groups, [&](int j) {
@@ -260,8 +281,6 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
           }
         }
       }
-    } else {
-      __syncthreads();  // hist[0] is zero
     }
     uint32_t prefix = 0, known = 0;  // the last kept key's leading bits, and which they are
     for (int top = 32; ties && !ranked && top > 0; top -= kBits, turn ^= 1) {
@@ -333,11 +352,11 @@ __global__ void __launch_bounds__(kThreads) paged_block_select_kernel(const Sele
   if (ranks > 1) cluster_sync();  // no block leaves while another may read its memory
 }
 
-template <int kThreads, int kGroups>
-int launch(const SelectParams& p, int num_seqs, int ranks, cudaStream_t stream) {
+int launch(void (*kernel)(SelectParams), const SelectParams& p, dim3 grid, int threads, int ranks,
+           cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_kv_heads) * ranks, num_seqs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -347,8 +366,7 @@ int launch(const SelectParams& p, int num_seqs, int ranks, cudaStream_t stream) 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, paged_block_select_kernel<kThreads, kGroups>, p) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -371,17 +389,22 @@ extern "C" int paged_block_select(const float* scores, const int32_t* seq_lens, 
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0) return PA_OK;
   if (!scores || !seq_lens || !selected) return PA_ERR_INVALID_ARG;
+  const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
   const SelectParams p{scores, seq_lens, selected, error_record, num_kv_heads, block_size,
                        max_blocks_per_seq, num_selected, sink_blocks, recent_blocks};
-  // Parts of at least 2048 keys while there are SMs to spare, and at most the 16384 of 16 warps.
-  const long long rows = static_cast<long long>(num_seqs) * num_kv_heads;
-  int ranks = 1;
-  while (ranks < kMaxCluster && ((rows * ranks < 152 && max_blocks_per_seq > 4096 * ranks) ||
-                                 max_blocks_per_seq > 16384 * ranks))
-    ranks *= 2;
-  if (max_blocks_per_seq > 16384 * ranks) return PA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (max_blocks_per_seq <= 2048 * ranks) return launch<256, 8>(p, num_seqs, ranks, st);
-  if (max_blocks_per_seq <= 8192 * ranks) return launch<256, 32>(p, num_seqs, ranks, st);
-  return launch<512, 32>(p, num_seqs, ranks, st);
+  // As many blocks a row as its length takes: up to 16384 scores for each.
+  int ranks = 1;
+  while (ranks < kMaxCluster && max_blocks_per_seq > 16384 * ranks) ranks *= 2;
+  if (max_blocks_per_seq > 16384 * ranks) return PA_ERR_UNSUPPORTED;
+  if (rows * ranks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
+  const dim3 grid(static_cast<unsigned>(rows * ranks));
+  if (rows >= 152 * 4) {
+    if (max_blocks_per_seq <= 1024) return launch(paged_block_select_kernel<64, 16>, p, grid, 64, 1, st);
+    if (max_blocks_per_seq <= 4096) return launch(paged_block_select_kernel<128, 32>, p, grid, 128, 1, st);
+  }
+  if (max_blocks_per_seq <= 2048) return launch(paged_block_select_kernel<256, 8>, p, grid, 256, 1, st);
+  if (max_blocks_per_seq <= 8192 * ranks)
+    return launch(paged_block_select_kernel<256, 32>, p, grid, 256, ranks, st);
+  return launch(paged_block_select_kernel<512, 32>, p, grid, 512, ranks, st);
 }

@@ -341,15 +341,37 @@ def test_select_matches_the_oracle(B, width, lens, keep, sink, recent, kind):
     assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, keep, sink, recent))
 
 
-@pytest.mark.parametrize("rows", [1, 3, 20, 80, 160])
-def test_select_with_rows_split_over_a_cluster(B, rows):
-    """Few long rows are split over several thread blocks, many are not: the same lists."""
-    rng = np.random.default_rng(rows)
-    s = np.round(rng.standard_normal((rows, 1, 9000)) * 8).astype(np.float32)
-    lens = rng.integers(1, 9001, rows)
-    lens[0] = 9000
-    got = B.paged_block_select(torch.from_numpy(s).cuda(), dev(lens), 1, 200, 1, 2)
-    assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, 200, 1, 2))
+@pytest.mark.parametrize("kind", ["normal", "ties", "odd", "wide"])
+@pytest.mark.parametrize("rows,width,keep", [(700, 40, 7), (650, 256, 256), (700, 300, 17), (620, 1024, 100),
+                                             (640, 1500, 64), (610, 2048, 1), (20, 2049, 9), (3, 33000, 200)])
+def test_select_of_many_rows(B, rows, width, keep, kind):
+    """A warp a row, a thread block a row and a cluster a row: by the width and how many rows."""
+    rng = np.random.default_rng(rows + width)
+    s = rng.standard_normal((rows, 1, width)).astype(np.float32)
+    if kind == "ties":
+        s = np.round(s)
+    elif kind == "odd":
+        s = np.round(s * 4)
+        for v in (NAN, -NAN, INF, -INF, 1e-42, -1e-42, -0.0):
+            s[rng.random(s.shape) < 0.03] = v
+        s[1] = -1.5
+    elif kind == "wide":
+        s = (s * np.float32(10.0) ** rng.integers(-44, 38, s.shape)).astype(np.float32)
+    lens = rng.integers(0, width + 1, rows)
+    lens[0] = width
+    sink, recent = (1, 2) if keep > 4 else (0, 0)
+    rec = B.new_error_record()
+    got = B.paged_block_select(torch.from_numpy(s).cuda(), dev(lens), 1, keep, sink, recent, error_record=rec)
+    assert B.pa_error_read(rec) == [0, 0, 0, 0]
+    assert np.array_equal(got.cpu().numpy(), OS.block_select(s, lens, 1, keep, sink, recent))
+
+
+@pytest.mark.parametrize("width", [9, 300, 3000, 40000])
+def test_select_of_the_ends_alone(B, width):
+    """Nothing competes for a place: the first and last blocks, whatever the scores."""
+    s = torch.full((609, 1, width), NAN, device="cuda")
+    got = B.paged_block_select(s, dev([width] * 609), 1, 5, 2, 3)[:, 0].cpu().numpy()
+    assert (got == [0, 1, width - 3, width - 2, width - 1]).all()
 
 
 def test_select_reads_nothing_past_a_sequence(B):
