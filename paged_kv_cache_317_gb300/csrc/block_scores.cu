@@ -57,6 +57,7 @@ template <class Tag, int D, int kStages>
 __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const ScoreParams p) {
   constexpr int kPieces = D / 8;         // 16-byte pieces of a row
   constexpr int kSteps = D / 32;         // pieces of a row that one lane takes
+  constexpr int kAhead = kSteps < 4 ? kSteps : 4;  // of them at a time
   extern __shared__ uint4 ring[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int seq = blockIdx.y;
@@ -121,40 +122,53 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
   const int group = p.num_heads / p.num_kv_heads;
   const uint4* q = static_cast<const uint4*>(p.q) +
                    (static_cast<size_t>(seq) * p.num_heads + static_cast<size_t>(head) * group) * kPieces + tq;
-  uint4 x[kSteps];
   for (int t = 0; 16 * t < held; ++t) {
     issue(t + kStages - 1);
-    if (t == 0) {  // after the copies are on their way
+    uint4 x[kAhead];
+    auto fetch = [&](int h0, int i0) {  // columns past the last head repeat it
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) x[i] = q[min(g, group - 1) * kPieces + 4 * i];
-    }
+      for (int i = 0; i < kAhead; ++i)
+        x[i] = q[static_cast<size_t>(min(h0 + g, group - 1)) * kPieces + 4 * (i0 + i)];
+    };
+    fetch(0, 0);
     copy_wait<kStages - 1>();
     __syncwarp();
     const uint4* src = mine + (t % kStages) * kPieces * 32 + g * kPieces;
     float best[2] = {-INFINITY, -INFINITY};
     for (int h0 = 0; h0 < group; h0 += 8) {
-      if (group > 8) {  // columns past the last head repeat it
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
+        if (h0 + i0 > 0) fetch(h0, i0);
+        // four products to a sum, then the sums: the tensor cores drop bits at every addition
+        float up[kAhead / 2][4], down[kAhead / 2][4];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) x[i] = q[static_cast<size_t>(min(h0 + g, group - 1)) * kPieces + 4 * i];
+        for (int i = 0; i < kAhead / 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up[i][e] = down[i][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 qp = max8(x[i], zero, Tag{}), qn = min8(x[i], zero, Tag{});
+          const int at = (4 * (i0 + i) + tq) ^ ((g & 1) << 2);
+          const uint4 h_0 = src[at], h_1 = src[8 * kPieces + at];
+          const uint4 l_0 = src[16 * kPieces + at], l_1 = src[24 * kPieces + at];
+          const uint32_t u0[4] = {h_0.x, h_1.x, h_0.y, h_1.y}, u1[4] = {h_0.z, h_1.z, h_0.w, h_1.w};
+          const uint32_t v0[4] = {l_0.x, l_1.x, l_0.y, l_1.y}, v1[4] = {l_0.z, l_1.z, l_0.w, l_1.w};
+          mma(up[i / 2], u0, qp.x, qp.y, Tag{});
+          mma(down[i / 2], v0, qn.x, qn.y, Tag{});
+          mma(up[i / 2], u1, qp.z, qp.w, Tag{});
+          mma(down[i / 2], v1, qn.z, qn.w, Tag{});
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead / 2; ++i) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] += up[i][e] + down[i][e];
+        }
       }
-      float up[4] = {0.f, 0.f, 0.f, 0.f}, down[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        const uint4 qp = max8(x[i], zero, Tag{}), qn = min8(x[i], zero, Tag{});
-        const int at = (4 * i + tq) ^ ((g & 1) << 2);
-        const uint4 h_0 = src[at], h_1 = src[8 * kPieces + at];
-        const uint4 l_0 = src[16 * kPieces + at], l_1 = src[24 * kPieces + at];
-        const uint32_t u0[4] = {h_0.x, h_1.x, h_0.y, h_1.y}, u1[4] = {h_0.z, h_1.z, h_0.w, h_1.w};
-        const uint32_t v0[4] = {l_0.x, l_1.x, l_0.y, l_1.y}, v1[4] = {l_0.z, l_1.z, l_0.w, l_1.w};
-        mma(up, u0, qp.x, qp.y, Tag{});
-        mma(down, v0, qn.x, qn.y, Tag{});
-        mma(up, u1, qp.z, qp.w, Tag{});
-        mma(down, v1, qn.z, qn.w, Tag{});
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        best[e] = max_nan(best[e], max_nan(up[2 * e] + down[2 * e], up[2 * e + 1] + down[2 * e + 1]));
+      for (int e = 0; e < 2; ++e) best[e] = max_nan(best[e], max_nan(sum[2 * e], sum[2 * e + 1]));
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

@@ -1,12 +1,14 @@
 // Append with rotary positions: one pass that rotates a step's queries and keys,
 // writes keys and values into their slots and keeps the touched blocks' key bounds.
 //
-// A step of one token a sequence (kv_append_step_kernel): a thread takes 16 dims (two
-// 16-byte pieces, 8 rotary pairs) of one head of one token's q, k or v.  Bound by latency,
-// and by HBM for large batches.
+// The work is cut into tiles, the new tokens of one sequence that fall into one block.
 //
-// Prompts (kv_append_rope_kernel): the work is cut into tiles, the new tokens of one sequence
-// that fall into one block, and a thread block takes up to 32 heads of q, k or v of a tile.  A thread
+// Steps of one to a few tokens a sequence (kv_append_step_kernel): a thread takes 16 dims (two
+// 16-byte pieces, 8 rotary pairs) of one head of q, k or v, and the tile's tokens one after the
+// other.  Bound by latency, and by HBM for large batches.
+//
+// Prompts (kv_append_rope_kernel): a thread block takes up to 32 heads of q, k or v of a tile; of q
+// and v at most 16 tokens of a longer tile.  A thread
 // keeps the cosines and sines of its row and 8 pairs in registers and goes over the heads, 4
 // at a time.  Rotated keys also go to shared memory, where each channel's minimum and maximum
 // over the tile's rows are taken: as the tile holds every new key of its block, the bounds
@@ -22,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 4;  // heads that a thread loads at a time
+constexpr int kFew = 4;    // tokens a sequence of a step
 
 struct AppendRopeParams {
   const void* q;  // null: keys and values only
@@ -41,6 +44,7 @@ struct AppendRopeParams {
   int block_size, max_blocks, num_blocks;
   int tiles;  // tile slots of the grid; blocks past them check the sequences
   int heads;  // of a thread block, for prompts
+  int split;  // tokens of q and v of a thread block, for prompts
   RopeParams rope;
 };
 
@@ -95,6 +99,38 @@ __device__ __forceinline__ bool dims_of(const RopeParams& r, int x, bool rotated
   return true;
 }
 
+// The tile of a slot; false for a slot without one.
+__device__ __forceinline__ bool find_tile(const AppendRopeParams& p, int slot, Tile& t) {
+  // the last sequence whose slots begin at or before this one: each warp looks at 32 at once
+  int lo = 0, size = p.num_seqs;
+  while (size > 1) {
+    const int step = (size + 31) / 32, at = lo + static_cast<int>(threadIdx.x & 31) * step;
+    const bool before = at < lo + size && first_slot(p, at) <= slot;
+    const int n = max(__popc(__ballot_sync(kFullMask, before)), 1);
+    size = min(step, lo + size - (lo + (n - 1) * step));
+    lo += (n - 1) * step;
+  }
+  const long long nth = slot - first_slot(p, lo);
+  Range rg;
+  if (nth < 0 || !range_of(p, lo, rg) || rg.count == 0) return false;
+  const int place0 = rg.len - rg.count;  // place of the sequence's first new token
+  const long long block = place0 / p.block_size + nth;
+  const long long from = max(block * p.block_size, static_cast<long long>(place0));
+  const long long to = min((block + 1) * p.block_size, static_cast<long long>(rg.len));
+  if (from >= to) return false;
+  t = {lo, static_cast<int>(to - from), rg.first + static_cast<int>(from - place0), static_cast<int>(from),
+       static_cast<int>(block)};
+  return true;
+}
+
+// A block behind the tiles: the sequences' ranges, of which tiles skip the bad ones silently.
+__device__ __forceinline__ void check_ranges(const AppendRopeParams& p, int nth) {
+  const int i = nth * kThreads + threadIdx.x;
+  Range r;
+  if (blockIdx.y == 0 && blockIdx.z == 0 && i < p.num_seqs && !range_of(p, i, r))
+    report_error(p.err, PA_ERR_BAD_SEQ_LEN, i, r.len);
+}
+
 template <class Tag>
 __device__ __forceinline__ void merge_bounds(const AppendRopeParams& p, size_t at, uint4 lo, uint4 hi,
                                              bool stored, Tag) {
@@ -105,11 +141,10 @@ __device__ __forceinline__ void merge_bounds(const AppendRopeParams& p, size_t a
   *mx = stored ? max8(hi, *mx, Tag{}) : hi;
 }
 
-// 256 x 40 heads (26 MB): 5.4 us in a graph.
-template <class Tag>
+// kOne: one token a sequence, whose tile needs no search (256 x 40 heads, 26 MB: 5.4 us in a graph).
+template <class Tag, bool kOne>
 __global__ void __launch_bounds__(kThreads) kv_append_step_kernel(const AppendRopeParams p) {
   using T = typename Tag::T;
-  const int seq = blockIdx.x;
   const int per_head = p.head_dim / 16;
   const int task = blockIdx.y * kThreads + threadIdx.x;
   const int vhead = task / per_head, x = task - vhead * per_head;
@@ -117,15 +152,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_step_kernel(const AppendRo
   const int head = vhead - (part == 0 ? 0 : part == 1 ? p.num_heads : p.num_heads + p.num_kv_heads);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (vhead >= p.num_heads + 2 * p.num_kv_heads) return;
-  Range rg;
-  if (!range_of(p, seq, rg)) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, rg.len);
-    return;
+  const int slot = blockIdx.x;
+  Tile t;
+  if constexpr (kOne) {
+    Range rg;
+    if (!range_of(p, slot, rg)) {
+      if (threadIdx.x == 0 && blockIdx.y == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, slot, rg.len);
+      return;
+    }
+    if (rg.count == 0) return;
+    t = {slot, 1, rg.first, rg.len - 1, (rg.len - 1) / p.block_size};
+  } else {
+    if (slot >= p.tiles) {
+      check_ranges(p, slot - p.tiles);
+      return;
+    }
+    if (!find_tile(p, slot, t)) return;
   }
-  if (rg.count == 0) return;
-  const Tile t{seq, 1, rg.first, rg.len - 1, (rg.len - 1) / p.block_size};
-  if (task == 0 && p.rope.cos_sin != nullptr) check_positions(p.rope, t.token, t.place, p.err);
+  if (vhead >= p.num_heads + 2 * p.num_kv_heads) return;
+  if (task == 0 && p.rope.cos_sin != nullptr)
+    for (int r = 0; r < t.rows; ++r) check_positions(p.rope, t.token + r, t.place + r, p.err);
   int da, db;
   const bool turn = dims_of(p.rope, x, part < 2, da, db);
   const int blk = part > 0 ? table_entry(p, t) : 0;
@@ -134,23 +180,32 @@ __global__ void __launch_bounds__(kThreads) kv_append_step_kernel(const AppendRo
   const size_t step = part == 0 ? p.q_stride : part == 1 ? p.k_stride : p.v_stride;
   const T* src = static_cast<const T*>(part == 0 ? p.q : part == 1 ? p.k : p.v) + t.token * step +
                  static_cast<size_t>(head) * p.head_dim;
-  uint4 a = *reinterpret_cast<const uint4*>(src + da), b = *reinterpret_cast<const uint4*>(src + db);
-  if (turn) {
-    float c[8], s[8];
-    load_cos_sin(p.rope, t.token, t.place, 8 * x, c, s);
-    rotate(p.rope, c, s, a, b, Tag{});
-  }
-  if (part > 0 && !is_block(p, t, blk, part == 1 && head == 0 && x == 0)) return;
+  uint4 lo[2], hi[2];
   const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + head;
-  T* dst = part == 0 ? static_cast<T*>(p.q_out) +
-                           (static_cast<size_t>(t.token) * p.num_heads + head) * p.head_dim
-                     : static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
-                           (bh * p.block_size + row) * p.head_dim;
-  *reinterpret_cast<uint4*>(dst + da) = a;
-  *reinterpret_cast<uint4*>(dst + db) = b;
+  for (int r = 0; r < t.rows; ++r) {
+    uint4 a = *reinterpret_cast<const uint4*>(src + r * step + da);
+    uint4 b = *reinterpret_cast<const uint4*>(src + r * step + db);
+    if (turn) {
+      float c[8], s[8];
+      load_cos_sin(p.rope, t.token + r, t.place + r, 8 * x, c, s);
+      rotate(p.rope, c, s, a, b, Tag{});
+    }
+    if (part > 0 && !is_block(p, t, blk, part == 1 && head == 0 && x == 0)) return;
+    T* dst = part == 0 ? static_cast<T*>(p.q_out) +
+                             (static_cast<size_t>(t.token + r) * p.num_heads + head) * p.head_dim
+                       : static_cast<T*>(part == 1 ? p.k_cache : p.v_cache) +
+                             (bh * p.block_size + row + r) * p.head_dim;
+    *reinterpret_cast<uint4*>(dst + da) = a;
+    *reinterpret_cast<uint4*>(dst + db) = b;
+    lo[0] = r == 0 ? a : min8(lo[0], a, Tag{});
+    lo[1] = r == 0 ? b : min8(lo[1], b, Tag{});
+    hi[0] = r == 0 ? a : max8(hi[0], a, Tag{});
+    hi[1] = r == 0 ? b : max8(hi[1], b, Tag{});
+    if constexpr (kOne) break;
+  }
   if (part == 1 && p.k_min != nullptr) {  // rows below are in the stored bounds
-    merge_bounds(p, bh * p.head_dim + da, a, a, row > 0, Tag{});
-    merge_bounds(p, bh * p.head_dim + db, b, b, row > 0, Tag{});
+    merge_bounds(p, bh * p.head_dim + da, lo[0], hi[0], row > 0, Tag{});
+    merge_bounds(p, bh * p.head_dim + db, lo[1], hi[1], row > 0, Tag{});
   }
 }
 
@@ -160,40 +215,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int slot = blockIdx.x;
-  if (slot >= p.tiles) {  // check the sequences' ranges; tiles skip the bad ones silently
-    const int i = (slot - p.tiles) * kThreads + threadIdx.x;
-    Range r;
-    if (blockIdx.y == 0 && i < p.num_seqs && !range_of(p, i, r))
-      report_error(p.err, PA_ERR_BAD_SEQ_LEN, i, r.len);
+  if (slot >= p.tiles) {
+    check_ranges(p, slot - p.tiles);
     return;
   }
-  Tile t{};
-  {
-    // the last sequence whose slots begin at or before this one: each warp looks at 32 at once
-    int lo = 0, size = p.num_seqs;
-    while (size > 1) {
-      const int step = (size + 31) / 32, at = lo + static_cast<int>(threadIdx.x & 31) * step;
-      const bool before = at < lo + size && first_slot(p, at) <= slot;
-      const int n = max(__popc(__ballot_sync(kFullMask, before)), 1);
-      size = min(step, lo + size - (lo + (n - 1) * step));
-      lo += (n - 1) * step;
-    }
-    t.seq = lo;
-    const long long nth = slot - first_slot(p, t.seq);
-    Range rg;
-    if (nth < 0 || !range_of(p, t.seq, rg) || rg.count == 0) return;
-    const int place0 = rg.len - rg.count;  // place of the sequence's first new token
-    const long long block = place0 / p.block_size + nth;
-    const long long from = max(block * p.block_size, static_cast<long long>(place0));
-    const long long to = min((block + 1) * p.block_size, static_cast<long long>(rg.len));
-    if (from >= to) return;  // a slot without a tile
-    t.rows = static_cast<int>(to - from);
-    t.token = rg.first + static_cast<int>(from - place0);
-    t.place = static_cast<int>(from);
-    t.block = static_cast<int>(block);
-  }
-  const int row0 = t.place - t.block * p.block_size;
-  if (p.rope.cos_sin != nullptr && blockIdx.y == 0)
+  Tile t;
+  if (!find_tile(p, slot, t)) return;
+  if (p.rope.cos_sin != nullptr && blockIdx.y == 0 && blockIdx.z == 0)
     for (int r = threadIdx.x; r < t.rows; r += kThreads)
       check_positions(p.rope, t.token + r, t.place + r, p.err);
 
@@ -204,6 +232,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
   const int part = chunk < q_chunks ? 0 : chunk < q_chunks + kv_chunks ? 1 : 2;
   const int h0 = (part == 0 ? chunk : (chunk - q_chunks) % kv_chunks) * p.heads;
   const int h1 = min(h0 + p.heads, part == 0 ? p.num_heads : p.num_kv_heads);
+  const int skip = blockIdx.z * p.split;
+  if (part == 1 ? skip > 0 : skip >= t.rows) return;
+  if (part != 1) {  // keys take the whole tile, for their bounds
+    t.rows = min(p.split, t.rows - skip);
+    t.token += skip;
+    t.place += skip;
+  }
+  const int row0 = t.place - t.block * p.block_size;
   const int blk = part > 0 ? table_entry(p, t) : 0;
 
   // Thread (x, r, h): slice x of the head, row r of `span` at a time, and of the heads every
@@ -353,9 +389,10 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.rope.total_tokens = total_tokens;
-  // One token a sequence: a thread for 16 dims of each head.  Otherwise the tile slots of
-  // first_slot, with behind them blocks that check the ranges, by chunks of heads.
-  const bool one = max_query_len == 1;
+  // A few tokens a sequence: a thread for 16 dims of each head of a tile (217 sequences of 1 or 2
+  // tokens, 48 + 2 x 3 heads: 15 us by chunks of heads).  Otherwise by chunks of heads.  A tile for
+  // each sequence, or the tile slots of first_slot with behind them blocks that check the ranges.
+  const bool one = max_query_len == 1, few = max_query_len <= kFew;
   p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;
   const int range_blocks = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
   const auto chunks = [](long long n, long long size) { return (n + size - 1) / size; };
@@ -363,12 +400,16 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   // 32 heads a thread block, down to 8 while that leaves fewer than 8 blocks for each SM (24
   // prompts of up to 700 tokens, 32 + 2 x 8 heads: 43.6 us with 32, 44.5 with 16, 47.4 with 8)
   p.heads = 32;
-  while (!one && p.heads > 8 && (total_tokens / block_size + 1) * head_chunks() < 152 * 8) p.heads /= 2;
+  while (!few && p.heads > 8 && (total_tokens / block_size + 1) * head_chunks() < 152 * 8) p.heads /= 2;
   const long long groups =
-      one ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads) : head_chunks();
+      few ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads) : head_chunks();
   if (groups > 65535) return PA_ERR_INVALID_ARG;
+  // 16 tokens of q and v a thread block, more only where a tile would need over 64 blocks
+  const int longest = block_size < max_query_len ? block_size : max_query_len;
+  p.split = (longest + 63) / 64 > 16 ? (longest + 63) / 64 : 16;
+  const unsigned splits = few ? 1u : static_cast<unsigned>((longest + p.split - 1) / p.split);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + range_blocks), static_cast<unsigned>(groups));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.tiles + range_blocks), static_cast<unsigned>(groups), splits);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -378,8 +419,11 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   cfg.numAttrs = 1;
   cudaError_t e;
   if (one)
-    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_step_kernel<BF16>, p)
-                         : cudaLaunchKernelEx(&cfg, kv_append_step_kernel<F16>, p);
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_step_kernel<BF16, true>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_append_step_kernel<F16, true>, p);
+  else if (few)
+    e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_step_kernel<BF16, false>, p)
+                         : cudaLaunchKernelEx(&cfg, kv_append_step_kernel<F16, false>, p);
   else
     e = dtype == PA_BF16 ? cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<BF16>, p)
                          : cudaLaunchKernelEx(&cfg, kv_append_rope_kernel<F16>, p);

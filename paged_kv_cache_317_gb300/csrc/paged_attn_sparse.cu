@@ -526,7 +526,7 @@ size_t smem_bytes(int stages) {
 // Thread blocks per cluster, clusters per row and stages per ring: of the choices, the one with
 // the least time by a model of the launch.  `slots` blocks are resident at a time and share the
 // memory's rate; the blocks of the last, partly filled wave run at the rate that their own copies
-// in flight allow.  Clusters wait for their slowest block and for free places on neighbouring
+// in flight allow; each wave takes 2 us besides.  One stage will do where a warp has one chunk.  Clusters wait for their slowest block and for free places on neighbouring
 // SMs, which costs an eighth, so only launches of few rows have them; several clusters per row
 // cost a second kernel, so only few rows with long lists do.  On GB300 (D = 128, us):
 //   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
@@ -534,21 +534,24 @@ size_t smem_bytes(int stages) {
 struct Shape {
   int ranks, parts, stages;
 };
-Shape shape_for(long long rows, double row_bytes, size_t smem2, size_t smem3, double stage_bytes,
+Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], double chunk_bytes,
                 int most_per_sm, int most_parts) {
   constexpr double kRate = 6.8e6, kLatency = 1.5;  // bytes per us; us from a copy's start to its reuse
+  const double row_bytes = chunks * chunk_bytes;
   Shape best{1, 1, 2};
   double least = 1e30;
-  for (int stages = 2; stages <= 3; ++stages) {
-    const size_t smem = stages == 2 ? smem2 : smem3;
+  for (int stages = 1; stages <= 3; ++stages) {
+    const size_t smem = smem_of[stages - 1];
     if (smem > 227 * 1024) continue;
     const int fit = static_cast<int>(228 * 1024 / (smem + 1024));
     const long long slots = 152ll * (fit < most_per_sm ? fit : most_per_sm);
     for (int all = 1; all <= kMaxCluster * most_parts; all *= 2) {  // blocks per row
+      if (stages == 1 && chunks > static_cast<long long>(kWarps) * all) continue;
       const long long blocks = rows * all, full = blocks / slots, rest = blocks - full * slots;
-      const double bytes = row_bytes / all, alone = bytes * kLatency / (kWarps * stages * stage_bytes);
+      const double bytes = row_bytes / all, alone = bytes * kLatency / (kWarps * stages * chunk_bytes);
       const double shared = rest * bytes / kRate;
       double us = full * slots * bytes / kRate + (rest == 0 ? 0. : shared > alone ? shared : alone);
+      us += 2. * (full + (rest > 0 ? 1 : 0));
       if (all > 1) us = us * 1.125 + 1.;
       if (all > kMaxCluster) us += 3.;
       if (us < least) {
@@ -564,8 +567,8 @@ template <int D, int NT>
 Shape shape_of(long long rows, int num_selected, int max_blocks, int block_size, bool parts) {
   const long long held = num_selected < max_blocks ? num_selected : max_blocks;
   const long long chunks = (held * block_size + kChunk - 1) / kChunk;
-  return shape_for(rows, static_cast<double>(chunks) * 2 * Geo<D>::kTileBytes, smem_bytes<D, NT>(2),
-                   smem_bytes<D, NT>(3), 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4,
+  const size_t smem[3] = {smem_bytes<D, NT>(1), smem_bytes<D, NT>(2), smem_bytes<D, NT>(3)};
+  return shape_for(rows, chunks, smem, 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4,
                    parts ? kMaxParts : 1);
 }
 

@@ -153,6 +153,10 @@ CASES = [
     ([9, 50, 3], [9, 20, 3], 3, 3, 48, 16, 5, 1, False),
     ([300], [299], 4, 2, 128, 128, 64, 4, False),
     ([20, 21], [4, 21], 2, 2, 16, 16, 1, 1, False),
+    ([17, 4, 33, 64, 200], [2, 4, 0, 3, 1], 6, 2, 128, 64, 16, 3, False),   # a few tokens each
+    ([9, 5, 3], [3, 3, 2], 40, 5, 64, 64, 2, 1, True),
+    ([700, 130], [600, 130], 3, 2, 64, 32, 500, 1, False),                  # long blocks
+    ([2500], [2400], 1, 1, 32, 32, 2100, 1, True),
 ]
 
 
