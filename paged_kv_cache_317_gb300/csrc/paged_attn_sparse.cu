@@ -17,7 +17,10 @@
 //    blocks over distributed shared memory, in a fixed order: the same bits on every run.  Only
 //    where a few rows have long lists are a row's chunks spread over several clusters, whose sums
 //    go through a workspace to a second kernel.
-// Two operations per cached byte and query head: bound by HBM.
+// Two operations per cached byte and query head: bound by HBM (64 sequences x 8 key heads x 8 query
+// heads, lists of 128 blocks of 16, 527 MB: 83 us, 6.4 TB/s; 32 x 40 heads, 64 blocks, 672 MB: 100
+// us, 6.7 TB/s).  One row alone is a chain of look-ups, copy, products and joins (8 rows of 64
+// blocks: 5.7 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -526,9 +529,10 @@ size_t smem_bytes(int stages) {
 // Thread blocks per cluster, clusters per row and stages per ring: of the choices, the one with
 // the least time by a model of the launch.  `slots` blocks are resident at a time and share the
 // memory's rate; the blocks of the last, partly filled wave run at the rate that their own copies
-// in flight allow; each wave takes 2 us besides.  One stage will do where a warp has one chunk.  Clusters wait for their slowest block and for free places on neighbouring
-// SMs, which costs an eighth, so only launches of few rows have them; several clusters per row
-// cost a second kernel, so only few rows with long lists do.  On GB300 (D = 128, us):
+// in flight allow; each wave takes 2 us besides.  One stage will do where a warp has one chunk.
+// Clusters wait for their slowest block and for free places on neighbouring SMs, which costs an
+// eighth, so only launches of few rows have them; several clusters per row cost a second kernel,
+// so only few rows with long lists do.  On GB300 (D = 128, us):
 //   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
 //   1280 rows of 0.5 MB:  ranks 1 with stages 2: 100, 3: 106 (two blocks an SM instead of three)
 struct Shape {
