@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_block_scores_kernel(const S
   for (int t = 0; t < kStages - 1; ++t) issue(t);
 
   const int group = p.num_heads / p.num_kv_heads;
-  const uint4* q = static_cast<const uint4*>(p.q) +
-                   (static_cast<size_t>(seq) * p.num_heads + static_cast<size_t>(head) * group) * kPieces + tq;
+  const size_t q0 = static_cast<size_t>(seq) * p.num_heads + static_cast<size_t>(head) * group;
+  const uint4* q = static_cast<const uint4*>(p.q) + q0 * kPieces + tq;
   for (int t = 0; 16 * t < held; ++t) {
     issue(t + kStages - 1);
     uint4 x[kAhead];

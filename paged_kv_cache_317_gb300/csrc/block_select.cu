@@ -10,9 +10,9 @@
 //     score above the bin in which the count reaches num_selected is kept, and as a rule that
 //     bin holds a handful.  Skipped where a score is NaN or infinite.
 //  2. If the bin holds more than are wanted, its scores, listed in shared memory, are each
-//     ranked among one another.  Where they are too many, or the row is a cluster's, or step 1 was skipped, a score becomes
-//     a 32-bit key that orders as the scores do, and the last kept key is found 9 to 12 bits at
-//     a time from histograms of the keys that agree with it so far.
+//     ranked among one another.  Where they are too many, or the row is a cluster's, or step 1
+//     was skipped, a score becomes a 32-bit key that orders as the scores do, and the last kept
+//     key is found 9 to 12 bits at a time from histograms of the keys that agree with it so far.
 //  3. A vote per group (two, where equal scores are kept in part) tells which of its blocks are
 //     kept; lane j takes the votes of group j, a scan of their counts over lanes, warps and
 //     blocks says where its blocks go, and it writes them, of equal ones the lowest.

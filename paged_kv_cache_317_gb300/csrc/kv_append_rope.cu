@@ -282,8 +282,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
         if (pass == 0 && part > 0 && !is_block(p, t, blk, part == 1 && h0 == 0 && threadIdx.x == 0))
           return;
       }
-      const size_t row = part == 0 ? static_cast<size_t>(token) * p.num_heads
-                                   : static_cast<size_t>(blk) * p.num_kv_heads * p.block_size + row0 + pass + r;
+      const size_t row =
+          part == 0 ? static_cast<size_t>(token) * p.num_heads
+                    : static_cast<size_t>(blk) * p.num_kv_heads * p.block_size + row0 + pass + r;
       T* to = static_cast<T*>(part == 0 ? p.q_out : part == 1 ? p.k_cache : p.v_cache) +
               row * p.head_dim + (hb + h) * head_step;
 #pragma unroll
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
             mx = max8(mx, k[i * pieces], Tag{});
           }
           // Rows below are in the stored bounds; those of an earlier pass this thread stored.
-          merge_bounds(p, (static_cast<size_t>(blk) * p.num_kv_heads + hb + slot_head) * p.head_dim + 8 * piece,
-                       mn, mx, row0 + pass > 0, Tag{});
+          const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + hb + slot_head;
+          merge_bounds(p, bh * p.head_dim + 8 * piece, mn, mx, row0 + pass > 0, Tag{});
         }
         __syncthreads();
       }

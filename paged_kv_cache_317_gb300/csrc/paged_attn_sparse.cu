@@ -644,8 +644,9 @@ int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seq
       cudaFuncSetAttribute(paged_attn_sparse_kernel<Tag, D, NT>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (!launch_dependent(paged_attn_sparse_kernel<Tag, D, NT>, dim3(static_cast<unsigned>(rows * ranks * p.parts)),
-                        dim3(kWarps * 32), smem, ranks, stream, tk, tv, p))
+  if (!launch_dependent(paged_attn_sparse_kernel<Tag, D, NT>,
+                        dim3(static_cast<unsigned>(rows * ranks * p.parts)), dim3(kWarps * 32), smem,
+                        ranks, stream, tk, tv, p))
     return PA_ERR_CUDA;
   if (p.parts > 1 &&
       !launch_dependent(paged_attn_sparse_join_kernel<D, NT>,
