@@ -44,7 +44,7 @@ struct AppendRopeParams {
   int total_tokens, max_query_len, num_seqs, num_heads, num_kv_heads, head_dim;
   int block_size, max_blocks, num_blocks;
   int tiles;  // tile slots of the grid; blocks past them check the sequences
-  int heads;  // of a thread block, for prompts
+  int heads, key_heads;  // of q and v, and of k, of a thread block, for prompts
   int split;  // tokens of q and v of a thread block, for prompts
   RopeParams rope;
 };
@@ -228,11 +228,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
 
   // this block's heads
   const int q_chunks = (p.num_heads + p.heads - 1) / p.heads;
-  const int kv_chunks = (p.num_kv_heads + p.heads - 1) / p.heads;
+  const int k_chunks = (p.num_kv_heads + p.key_heads - 1) / p.key_heads;
   const int chunk = blockIdx.y;
-  const int part = chunk < q_chunks ? 0 : chunk < q_chunks + kv_chunks ? 1 : 2;
-  const int h0 = (part == 0 ? chunk : (chunk - q_chunks) % kv_chunks) * p.heads;
-  const int h1 = min(h0 + p.heads, part == 0 ? p.num_heads : p.num_kv_heads);
+  const int part = chunk < q_chunks ? 0 : chunk < q_chunks + k_chunks ? 1 : 2;
+  const int size = part == 1 ? p.key_heads : p.heads;
+  const int h0 = (chunk - (part == 0 ? 0 : part == 1 ? q_chunks : q_chunks + k_chunks)) * size;
+  const int h1 = min(h0 + size, part == 0 ? p.num_heads : p.num_kv_heads);
   const int skip = blockIdx.z * p.split;
   if (part == 1 ? skip > 0 : skip >= t.rows) return;
   if (part != 1) {  // keys take the whole tile, for their bounds
@@ -262,12 +263,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
                  static_cast<size_t>(h0 + h) * p.head_dim;
   // elements from head to head of the output
   const size_t head_step = part == 0 ? p.head_dim : static_cast<size_t>(p.block_size) * p.head_dim;
-  for (int pass = 0; pass < t.rows; pass += span) {
-    const bool active = pass + r < t.rows && h < lanes;
-    const int token = t.token + pass + r;
-    const T* from = src + token * step;
-    float c[8], s[8];
-    for (int hb = h0; hb < h1; hb += kBatch * lanes) {
+  const bool many = t.rows > span;  // passes over the rows; then a thread has at most one reduction
+  float c[8], s[8];
+  for (int hb = h0; hb < h1; hb += kBatch * lanes) {
+    const int tasks = min(kBatch * lanes, h1 - hb) * pieces;
+    uint4 mn, mx;
+    for (int pass = 0; pass < t.rows; pass += span) {
+      const bool active = pass + r < t.rows && h < lanes;
+      const int token = t.token + pass + r;
+      const T* from = src + token * step;
       uint4 a[kBatch], b[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -277,11 +281,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
           b[i] = *reinterpret_cast<const uint4*>(at + db);
         }
       }
-      if (hb == h0) {  // with the first loads on their way
-        if (turn && active) load_cos_sin(p.rope, token, t.place + pass + r, 8 * x, c, s);
-        if (pass == 0 && part > 0 && !is_block(p, t, blk, part == 1 && h0 == 0 && threadIdx.x == 0))
-          return;
-      }
+      // with the loads on their way
+      if ((many || hb == h0) && turn && active)
+        load_cos_sin(p.rope, token, t.place + pass + r, 8 * x, c, s);
+      if (hb == h0 && pass == 0 && part > 0 &&
+          !is_block(p, t, blk, part == 1 && h0 == 0 && threadIdx.x == 0))
+        return;
       const size_t row =
           part == 0 ? static_cast<size_t>(token) * p.num_heads
                     : static_cast<size_t>(blk) * p.num_kv_heads * p.block_size + row0 + pass + r;
@@ -304,17 +309,18 @@ __global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const AppendRo
       if (bounds) {
         __syncthreads();
         const int n = min(span, t.rows - pass);
-        for (int j = threadIdx.x; j < min(kBatch * lanes, h1 - hb) * pieces; j += kThreads) {
+        for (int j = threadIdx.x; j < tasks; j += kThreads) {
           const int slot_head = j / pieces, piece = j % pieces;
           const uint4* k = keys + slot_head * span * pieces + piece;
-          uint4 mn = k[0], mx = k[0];
-          for (int i = 1; i < n; ++i) {
+          if (!many || pass == 0) mn = mx = k[0];
+          for (int i = 0; i < n; ++i) {
             mn = min8(mn, k[i * pieces], Tag{});
             mx = max8(mx, k[i * pieces], Tag{});
           }
-          // Rows below are in the stored bounds; those of an earlier pass this thread stored.
-          const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + hb + slot_head;
-          merge_bounds(p, bh * p.head_dim + 8 * piece, mn, mx, row0 + pass > 0, Tag{});
+          if (pass + span >= t.rows) {  // rows below the tile are in the stored bounds
+            const size_t bh = static_cast<size_t>(blk) * p.num_kv_heads + hb + slot_head;
+            merge_bounds(p, bh * p.head_dim + 8 * piece, mn, mx, row0 > 0, Tag{});
+          }
         }
         __syncthreads();
       }
@@ -399,16 +405,24 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;
   const int range_blocks = one ? 0 : (num_seqs + kThreads - 1) / kThreads;
   const auto chunks = [](long long n, long long size) { return (n + size - 1) / size; };
-  const auto head_chunks = [&] { return chunks(num_heads, p.heads) + 2 * chunks(num_kv_heads, p.heads); };
+  const auto head_chunks = [&] {
+    return chunks(num_heads, p.heads) + chunks(num_kv_heads, p.heads) + chunks(num_kv_heads, p.key_heads);
+  };
+  // As many keys' heads a thread block, but 4 where their rows need several passes.
+  const int longest = block_size < max_query_len ? block_size : max_query_len;
+  const auto set_heads = [&](int n) {
+    p.heads = n;
+    p.key_heads = longest * (head_dim / 16) > kThreads ? kBatch : n;
+  };
   // 32 heads a thread block, down to 8 while that leaves fewer than 8 blocks for each SM (24
   // prompts of up to 700 tokens, 32 + 2 x 8 heads: 43.6 us with 32, 44.5 with 16, 47.4 with 8)
-  p.heads = 32;
-  while (!few && p.heads > 8 && (total_tokens / block_size + 1) * head_chunks() < 152 * 8) p.heads /= 2;
+  set_heads(32);
+  while (!few && p.heads > 8 && (total_tokens / block_size + 1) * head_chunks() < 152 * 8)
+    set_heads(p.heads / 2);
   const long long groups =
       few ? chunks((num_heads + 2ll * num_kv_heads) * (head_dim / 16), kThreads) : head_chunks();
   if (groups > 65535) return PA_ERR_INVALID_ARG;
   // 16 tokens of q and v a thread block, more only where a tile would need over 64 blocks
-  const int longest = block_size < max_query_len ? block_size : max_query_len;
   p.split = (longest + 63) / 64 > 16 ? (longest + 63) / 64 : 16;
   const unsigned splits = few ? 1u : static_cast<unsigned>((longest + p.split - 1) / p.split);
   cudaLaunchConfig_t cfg{};
