@@ -18,7 +18,7 @@
 //    where a few rows have long lists are a row's chunks spread over several clusters, whose sums
 //    go through a workspace to a second kernel.
 // Two operations per cached byte and query head: bound by HBM (64 sequences x 8 key heads x 8 query
-// heads, lists of 128 blocks of 16, 527 MB: 83 us, 6.4 TB/s; 32 x 40 heads, 64 blocks, 672 MB: 100
+// heads, lists of 128 blocks of 16, 527 MB: 81 us, 6.5 TB/s; 32 x 40 heads, 64 blocks, 672 MB: 100
 // us, 6.7 TB/s).  One row alone is a chain of look-ups, copy, products and joins (8 rows of 64
 // blocks: 5.7 us).
 #include <cuda_bf16.h>
@@ -529,12 +529,13 @@ size_t smem_bytes(int stages) {
 // Thread blocks per cluster, clusters per row and stages per ring: of the choices, the one with
 // the least time by a model of the launch.  `slots` blocks are resident at a time and share the
 // memory's rate; the blocks of the last, partly filled wave run at the rate that their own copies
-// in flight allow; each wave takes 2 us besides.  One stage will do where a warp has one chunk.
+// in flight allow; each wave takes 2 us besides.  Of equals the deeper ring.
 // Clusters wait for their slowest block and for free places on neighbouring SMs, which costs an
 // eighth, so only launches of few rows have them; several clusters per row cost a second kernel,
 // so only few rows with long lists do.  On GB300 (D = 128, us):
 //   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
 //   1280 rows of 0.5 MB:  ranks 1 with stages 2: 100, 3: 106 (two blocks an SM instead of three)
+//   640 rows of 1 MB, D = 256:  ranks 1 with stages 1: 103, 2: 118 (one block an SM instead of three)
 struct Shape {
   int ranks, parts, stages;
 };
@@ -550,7 +551,6 @@ Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], do
     const int fit = static_cast<int>(228 * 1024 / (smem + 1024));
     const long long slots = 152ll * (fit < most_per_sm ? fit : most_per_sm);
     for (int all = 1; all <= kMaxCluster * most_parts; all *= 2) {  // blocks per row
-      if (stages == 1 && chunks > static_cast<long long>(kWarps) * all) continue;
       const long long blocks = rows * all, full = blocks / slots, rest = blocks - full * slots;
       const double bytes = row_bytes / all, alone = bytes * kLatency / (kWarps * stages * chunk_bytes);
       const double shared = rest * bytes / kRate;
@@ -558,7 +558,7 @@ Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], do
       us += 2. * (full + (rest > 0 ? 1 : 0));
       if (all > 1) us = us * 1.125 + 1.;
       if (all > kMaxCluster) us += 3.;
-      if (us < least) {
+      if (us < least || (us == least && stages > best.stages)) {
         least = us;
         best = {all < kMaxCluster ? all : kMaxCluster, all <= kMaxCluster ? 1 : all / kMaxCluster, stages};
       }
@@ -571,8 +571,11 @@ template <int D, int NT>
 Shape shape_of(long long rows, int num_selected, int max_blocks, int block_size, bool parts) {
   const long long held = num_selected < max_blocks ? num_selected : max_blocks;
   const long long chunks = (held * block_size + kChunk - 1) / kChunk;
+  // thread blocks an SM, as registers allow
+  constexpr int kMost[3][2] = {{6, 4}, {4, 3}, {3, 2}};
+  constexpr int most = kMost[D / 128][NT - 1];
   const size_t smem[3] = {smem_bytes<D, NT>(1), smem_bytes<D, NT>(2), smem_bytes<D, NT>(3)};
-  return shape_for(rows, chunks, smem, 2 * Geo<D>::kTileBytes, D == 64 && NT == 1 ? 6 : 4,
+  return shape_for(rows, chunks, smem, 2 * Geo<D>::kTileBytes, most,
                    parts ? kMaxParts : 1);
 }
 
