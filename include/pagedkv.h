@@ -614,6 +614,8 @@ int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seq
  *                 tokens.  A block listed twice counts twice.  An entry below -1 or at or
  *                 past max_blocks_per_seq is recorded as PA_ERR_BAD_BLOCK (index = i *
  *                 num_kv_heads + h) and skipped.
+ *                 All entries are looked at: num_selected beyond max_blocks_per_seq only
+ *                 costs time.  num_selected * block_size at most 2^33.
  *   head_dim      64, 128 or 256;  block_size: a multiple of 16, or 8
  *   out           device [num_seqs][num_heads][head_dim] in `out_dtype`, 16-byte aligned
  *   workspace     device, 16-byte aligned, at least paged_attn_sparse_workspace_size(...)
