@@ -528,22 +528,24 @@ size_t smem_bytes(int stages) {
 
 // Thread blocks per cluster, clusters per row and stages per ring: of the choices, the one with
 // the least time by a model of the launch.  `slots` blocks are resident at a time and share the
-// memory's rate; the blocks of the last, partly filled wave run at the rate that their own copies
-// in flight allow; each wave takes 2 us besides.  Of equals the deeper ring.
+// memory's rate; the blocks of the last, partly filled wave take what a warp's chunks take one after
+// the other, if that is longer; each wave takes 2 us besides.  Of equals the deeper ring.
 // Clusters wait for their slowest block and for free places on neighbouring SMs, which costs an
 // eighth, so only launches of few rows have them; several clusters per row cost a second kernel,
 // so only few rows with long lists do.  On GB300 (D = 128, us):
 //   512 rows of 1 MB:     ranks 1 with stages 2: 97, 3: 82;  ranks 2: 91 and 95;  ranks 4: 93, 103
 //   1280 rows of 0.5 MB:  ranks 1 with stages 2: 100, 3: 106 (two blocks an SM instead of three)
+//   80 rows of 2 MB:      ranks 1 with stages 2: 54, 3: 55;  ranks 2: 34 and 34;  ranks 4: 30, 43
 //   640 rows of 1 MB, D = 256:  ranks 1 with stages 1: 103, 2: 118 (one block an SM instead of three)
 struct Shape {
   int ranks, parts, stages;
 };
 Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], double chunk_bytes,
                 int most_per_sm, int most_parts) {
-  constexpr double kRate = 6.8e6, kLatency = 1.5;  // bytes per us; us from a copy's start to its reuse
+  constexpr double kRate = 6.8e6;              // bytes per us
+  constexpr double kWait = 1.25, kStep = 0.85;  // us per chunk of a warp: copy and products, products
   const double row_bytes = chunks * chunk_bytes;
-  Shape best{1, 1, 2};
+  Shape best{1, 1, 1};
   double least = 1e30;
   for (int stages = 1; stages <= 3; ++stages) {
     const size_t smem = smem_of[stages - 1];
@@ -552,7 +554,11 @@ Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], do
     const long long slots = 152ll * (fit < most_per_sm ? fit : most_per_sm);
     for (int all = 1; all <= kMaxCluster * most_parts; all *= 2) {  // blocks per row
       const long long blocks = rows * all, full = blocks / slots, rest = blocks - full * slots;
-      const double bytes = row_bytes / all, alone = bytes * kLatency / (kWarps * stages * chunk_bytes);
+      const long long warps = static_cast<long long>(all) * kWarps;
+      const long long each = (chunks + warps - 1) / warps;
+      if (stages > 1 && stages > each) continue;  // nothing to fill them with
+      const double alone = each * (stages == 1 ? kWait : kStep);
+      const double bytes = row_bytes / all;
       const double shared = rest * bytes / kRate;
       double us = full * slots * bytes / kRate + (rest == 0 ? 0. : shared > alone ? shared : alone);
       us += 2. * (full + (rest > 0 ? 1 : 0));
