@@ -825,8 +825,8 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     else:
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
     lib = load_library()
-    if workspace is None:
-        need = lib.paged_attn_sparse_workspace_size(N, Hq, H, D, bs, MB, S)
+    if workspace is None:   # (lists of up to 1024 tokens never need one)
+        need = lib.paged_attn_sparse_workspace_size(N, Hq, H, D, bs, MB, S) if S * bs > 1024 else 0
         if need:
             workspace = _new_out((need,), torch.uint8, q.device, stream)
     else:

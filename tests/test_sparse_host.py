@@ -157,5 +157,9 @@ def test_attention_workspace_sizes(lib):
         rows = -(-heads // cols)
         assert n > 0 and n % (rows * cols * (128 * 4 + 8)) == 0
         assert n // (rows * cols * (128 * 4 + 8)) <= 64
+    for n in (1, 2, 7, 40, 300):                  # lists of up to 1024 tokens never need one
+        for heads, kv in ((1, 1), (8, 1), (32, 8), (64, 2)):
+            for dim in (64, 128, 256):
+                assert size(n, heads, kv, dim, 8, 4096, 128) == size(n, heads, kv, dim, 64, 4096, 16) == 0
     assert size(0, 8, 2, 64, 16, 4096, 4096) == size(1, 7, 2, 64, 16, 4096, 4096) == 0
     assert size(1, 8, 2, 96, 16, 4096, 4096) == size(1, 8, 2, 64, 16, 4096, 0) == 0
