@@ -620,15 +620,22 @@ int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seq
  *   out           device [num_seqs][num_heads][head_dim] in `out_dtype`, 16-byte aligned
  *   workspace     device, 16-byte aligned, at least paged_attn_sparse_workspace_size(...)
  *                 bytes, scratch of this call alone; or NULL: a list is then read by at most 8
- *                 thread blocks, which is slow where few rows have long lists (the size is 0
- *                 otherwise).
+ *                 thread blocks, which is slow where few rows have long lists.
  * Arithmetic as in paged_attn_prefill: logits and sums in fp32, probabilities as a pair of
  * half-precision numbers.  num_blocks * num_kv_heads * block_size must be < 2^31.
  * A block-table entry out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and block 0
- * is read; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped. */
+ * is read; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.
+ *
+ * paged_attn_sparse_workspace_size never falls as num_seqs, num_selected, max_blocks_per_seq or
+ * block_size grow, the others alike: a buffer sized for the largest call serves every smaller
+ * one.  0 where lists hold at most 2048 tokens; at most 1024 partial results of 8 or 16 heads.
+ * paged_attn_sparse_clusters: over how many thread-block clusters the call, given a workspace,
+ * spreads a list.  1: it does not touch the workspace (nor look at its size). */
 size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                         int head_dim, int block_size, int max_blocks_per_seq,
                                         int num_selected);
+int paged_attn_sparse_clusters(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                               int block_size, int max_blocks_per_seq, int num_selected);
 int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_tables, const int32_t* seq_lens,
                       const int32_t* selected, int num_selected, int num_seqs, int num_heads,

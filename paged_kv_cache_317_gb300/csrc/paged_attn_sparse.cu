@@ -41,6 +41,8 @@ constexpr int kWarps = 4;        // warps per thread block
 constexpr int kMaxStages = 8;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxParts = 64;    // clusters per row
+constexpr int kMaxShares = 1024; // clusters of all rows, where rows have several
+constexpr int kWhole = 128;      // a list of at most so many chunks is one cluster's
 constexpr int kAlign = 1024;     // a swizzled box must start on 1024 bytes
 constexpr int kHeader = 1024;    // barriers and the chunks' row counts
 constexpr float kLog2e = 1.4426950408889634f;
@@ -573,33 +575,42 @@ Shape shape_for(long long rows, long long chunks, const size_t (&smem_of)[3], do
   return best;
 }
 
+// The chunks of the longest list that holds no block twice.
+long long chunks_of(int num_selected, int max_blocks, int block_size) {
+  const long long held = num_selected < max_blocks ? num_selected : max_blocks;
+  return (held * block_size + kChunk - 1) / kChunk;
+}
+
+// The clusters that a row may have.  kMaxShares in all fill the card several times over (39 rows of
+// 19058 blocks of 16, 64 channels, 16 query heads: 503 us with 16 clusters a row, 551 us with 32).
+int most_parts(long long rows, long long chunks) {
+  if (chunks <= kWhole || rows > kMaxShares) return 1;
+  return static_cast<int>(rows * kMaxParts < kMaxShares ? kMaxParts : kMaxShares / rows);
+}
+
 template <int D, int NT>
 Shape shape_of(long long rows, int num_selected, int max_blocks, int block_size, bool parts) {
-  const long long held = num_selected < max_blocks ? num_selected : max_blocks;
-  const long long chunks = (held * block_size + kChunk - 1) / kChunk;
+  const long long chunks = chunks_of(num_selected, max_blocks, block_size);
   // thread blocks an SM, as registers allow
   constexpr int kMost[3][2] = {{6, 4}, {4, 3}, {3, 2}};
   constexpr int most = kMost[D / 128][NT - 1];
   const size_t smem[3] = {smem_bytes<D, NT>(1), smem_bytes<D, NT>(2), smem_bytes<D, NT>(3)};
   return shape_for(rows, chunks, smem, 2 * Geo<D>::kTileBytes, most,
-                   parts ? kMaxParts : 1);
+                   parts ? most_parts(rows, chunks) : 1);
 }
 
 long long rows_of(int num_seqs, int num_kv_heads, int group, int cols) {
   return static_cast<long long>(num_seqs) * num_kv_heads * ((group + cols - 1) / cols);
 }
 
+// Enough for the clusters of this call and of every one with fewer rows or shorter lists: what a
+// call itself uses goes up and down with its rows (8 key heads, D = 128, lists of 8192 tokens: 40 shares
+// of rows for 5 sequences, 24 for 6), and one buffer has to serve a batch whose sequences end.
 template <int D, int NT>
-size_t workspace_for(long long rows, int parts) {
-  if (parts == 1) return 0;
-  return static_cast<size_t>(rows) * parts * 8 * NT * (D * sizeof(float) + sizeof(float2));
-}
-
-template <int D, int NT>
-size_t workspace_size(int num_seqs, int num_kv_heads, int group, int num_selected, int max_blocks,
-                      int block_size) {
-  const long long rows = rows_of(num_seqs, num_kv_heads, group, 8 * NT);
-  return workspace_for<D, NT>(rows, shape_of<D, NT>(rows, num_selected, max_blocks, block_size, true).parts);
+size_t workspace_for(long long rows, long long chunks) {
+  if (chunks <= kWhole) return 0;
+  const long long shares = rows * kMaxParts < kMaxShares ? rows * kMaxParts : kMaxShares;
+  return static_cast<size_t>(shares) * 8 * NT * (D * sizeof(float) + sizeof(float2));
 }
 
 template <class... Kernel, class... Args>
@@ -632,7 +643,8 @@ int launch(SparseParams p, const void* k_cache, const void* v_cache, int num_seq
   p.parts = shape.parts;
   if (rows * ranks * p.parts > 0x7fffffffll) return PA_ERR_INVALID_ARG;
   if (p.parts > 1) {
-    if (workspace_bytes < workspace_for<D, NT>(rows, p.parts)) return PA_ERR_INVALID_ARG;
+    if (workspace_bytes < workspace_for<D, NT>(rows, chunks_of(p.num_selected, p.max_blocks, p.block_size)))
+      return PA_ERR_INVALID_ARG;
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * p.parts * 8 * NT * D);
   }
@@ -673,6 +685,26 @@ int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, i
              : launch<Tag, D, 2>(p, k_cache, v_cache, num_seqs, workspace, workspace_bytes, stream);
 }
 
+// f(D, NT) for the sizes of a call; 0 where there is no such call.
+template <class F>
+auto for_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+               int max_blocks_per_seq, int num_selected, F f) {
+  using R = decltype(f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{}));
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
+    return R{0};
+  const auto with = [&](auto dim) {
+    return num_heads / num_kv_heads <= 8 ? f(dim, std::integral_constant<int, 1>{})
+                                         : f(dim, std::integral_constant<int, 2>{});
+  };
+  switch (head_dim) {
+    case 64: return with(std::integral_constant<int, 64>{});
+    case 128: return with(std::integral_constant<int, 128>{});
+    case 256: return with(std::integral_constant<int, 256>{});
+    default: return R{0};
+  }
+}
+
 }  // namespace
 }  // namespace pagedkv
 
@@ -681,23 +713,23 @@ using namespace pagedkv;
 extern "C" size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                                    int head_dim, int block_size,
                                                    int max_blocks_per_seq, int num_selected) {
-  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
-      block_size <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
-    return 0;
-  const int group = num_heads / num_kv_heads;
-  const auto size = [&](auto dim) {
-    constexpr int D = decltype(dim)::value;
-    return group <= 8 ? workspace_size<D, 1>(num_seqs, num_kv_heads, group, num_selected,
-                                             max_blocks_per_seq, block_size)
-                      : workspace_size<D, 2>(num_seqs, num_kv_heads, group, num_selected,
-                                             max_blocks_per_seq, block_size);
-  };
-  switch (head_dim) {
-    case 64: return size(std::integral_constant<int, 64>{});
-    case 128: return size(std::integral_constant<int, 128>{});
-    case 256: return size(std::integral_constant<int, 256>{});
-    default: return 0;
-  }
+  return for_sizes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                   num_selected, [&](auto dim, auto nt) {
+    constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
+    return workspace_for<D, NT>(rows_of(num_seqs, num_kv_heads, num_heads / num_kv_heads, 8 * NT),
+                                chunks_of(num_selected, max_blocks_per_seq, block_size));
+  });
+}
+
+extern "C" int paged_attn_sparse_clusters(int num_seqs, int num_heads, int num_kv_heads,
+                                          int head_dim, int block_size, int max_blocks_per_seq,
+                                          int num_selected) {
+  return for_sizes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                   num_selected, [&](auto dim, auto nt) {
+    constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
+    const long long rows = rows_of(num_seqs, num_kv_heads, num_heads / num_kv_heads, 8 * NT);
+    return shape_of<D, NT>(rows, num_selected, max_blocks_per_seq, block_size, true).parts;
+  });
 }
 
 extern "C" int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
