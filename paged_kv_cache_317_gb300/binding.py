@@ -343,6 +343,22 @@ def _need(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _cache_sizes(name: str, shape, k_cache: torch.Tensor, v_cache: torch.Tensor, *rows: torch.Tensor):
+    """Blocks and block size of the caches, which, like rows of new keys and values, must have the
+    heads and channels of `name` (shape [_, H, D]): these calls know one number of heads, and with
+    fewer in a cache they would address past its end."""
+    _, H, D = shape
+    B, heads, bs, channels = cache = k_cache.shape
+    if heads != H or channels != D or v_cache.shape != cache:
+        raise ValueError(f"the caches must be [blocks, {H}, block_size, {D}], with the heads and channels "
+                         f"of {name}, got {list(cache)} and {list(v_cache.shape)}")
+    for t in rows:
+        if t.shape != shape:
+            raise ValueError(f"rows of new keys and values must have the shape {list(shape)} of {name}, "
+                             f"got {list(t.shape)}")
+    return B, bs
+
+
 # --------------------------------------------------------------- error record
 def new_error_record(device="cuda") -> torch.Tensor:
     return torch.zeros(4, dtype=torch.int32, device=device)
@@ -395,8 +411,8 @@ def paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     counts: optional int32 [2] on the device, the numbers of work items and records
     to run out of the lists given (then capacities), for CUDA-graph replays with
     lists of varying length."""
-    N, H, D = q.shape
-    B, _, bs, _ = k_cache.shape
+    N, H, D = shape = q.shape
+    B, bs = _cache_sizes("q", shape, k_cache, v_cache)
     MB = block_tables.shape[1]
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n)
@@ -437,8 +453,8 @@ def paged_attn_decode_append(q: torch.Tensor, new_k: torch.Tensor, new_v: torch.
                              stream=None) -> torch.Tensor:
     """Append each sequence's last token (new_k/new_v [N,H,D]) into its slot and
     decode over all seq_lens[i] tokens, in one pass."""
-    N, H, D = q.shape
-    B, _, bs, _ = k_cache.shape
+    N, H, D = shape = q.shape
+    B, bs = _cache_sizes("q", shape, k_cache, v_cache, new_k, new_v)
     MB = block_tables.shape[1]
     for t, n in ((q, "q"), (new_k, "new_k"), (new_v, "new_v"), (k_cache, "k_cache"),
                  (v_cache, "v_cache")):
@@ -472,8 +488,8 @@ def paged_attn_prefill(q: torch.Tensor, query_start: torch.Tensor, max_query_len
                        seq_order: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal multi-query attention: q [total,H,D]; query_start int32 [N+1] (device);
     seq_order: optional int32 [N] dispatch order of the sequences on the device."""
-    T, H, D = q.shape
-    B, _, bs, _ = k_cache.shape
+    T, H, D = shape = q.shape
+    B, bs = _cache_sizes("q", shape, k_cache, v_cache)
     N = seq_lens.shape[0]
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n)
@@ -505,8 +521,8 @@ def paged_attn_decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
                               stream=None) -> torch.Tensor:
     """paged_attn_decode with its scratch taken from the library's fixed array:
     allocates nothing (``out`` must be given)."""
-    N, H, D = q.shape
-    B, _, bs, _ = k_cache.shape
+    N, H, D = shape = q.shape
+    B, bs = _cache_sizes("q", shape, k_cache, v_cache)
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
         _need(t, n)
     _need(block_tables, "block_tables", torch.int32)
@@ -524,8 +540,8 @@ def kv_cache_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor
                     k_cache: torch.Tensor, v_cache: torch.Tensor,
                     error_record: Optional[torch.Tensor] = None, stream=None) -> None:
     """k, v [T,H,D]; slot_mapping int64 [T]; caches [B,H,bs,D]."""
-    T, H, D = k.shape
-    B, _, bs, _ = k_cache.shape
+    T, H, D = shape = k.shape
+    B, bs = _cache_sizes("k", shape, k_cache, v_cache, v)
     for t, n in ((k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n)
     _need(slot_mapping, "slot_mapping", torch.int64)
