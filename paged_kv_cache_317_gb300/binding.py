@@ -556,7 +556,14 @@ def block_copy(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor
                stream=None) -> None:
     """Per-layer caches [B,H,bs,D]; pairs int64 [n,2] (src, dst) on the device."""
     n_layers = len(k_caches)
-    B, H, bs, D = k_caches[0].shape
+    B, H, bs, D = shape = k_caches[0].shape
+    dtype = k_caches[0].dtype
+    if len(v_caches) != n_layers:
+        raise ValueError(f"{n_layers} key caches and {len(v_caches)} value caches")
+    for t in (*k_caches, *v_caches):
+        if t.shape != shape or t.dtype != dtype:   # key bounds beside caches: a call of their own
+            raise ValueError(f"the caches of one call must be alike: {list(shape)} in {dtype}, got "
+                             f"{list(t.shape)} in {t.dtype}")
     for t in (*k_caches, *v_caches):
         _need(t, "cache")
     _need(pairs, "pairs", torch.int64)
