@@ -121,9 +121,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
   const int nb = static_cast<int>((static_cast<long long>(L) + p.block_size - 1) / p.block_size);
   int32_t* out = p.selected + row * p.num_selected;
   if (nb <= p.num_selected) {  // alike for all blocks of the cluster
-    // (in 64 bits: num_selected may be the largest 32-bit number)
-    for (long long i = rank * kThreads + tid; i < p.num_selected; i += ranks * kThreads)
-      out[i] = i < nb ? static_cast<int>(i) : -1;
+    // (unsigned: num_selected may be the largest int, and a step goes past it)
+    for (unsigned i = rank * kThreads + tid; i < static_cast<unsigned>(p.num_selected); i += ranks * kThreads)
+      out[i] = i < static_cast<unsigned>(nb) ? static_cast<int>(i) : -1;
     return;
   }
   // Groups of 32 blocks per warp of the row, at most kGroups as the capacity is in range.
