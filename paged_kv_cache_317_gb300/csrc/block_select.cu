@@ -1,14 +1,14 @@
 // Block selection: the best num_selected of a row's scores, in increasing block order.
 //
-// A cluster of thread blocks (one, but for very long rows) per (sequence, key head), each with
-// a contiguous part of the row, of which each warp has a contiguous part in turn: up to 32
+// A thread block (for rows of over 16384 blocks a cluster of them) per (sequence, key head), each
+// with a contiguous part of the row, of which each warp has a contiguous part in turn: up to 32
 // groups of 32 scores, one of each group per lane, read once and kept in registers.  Three
 // steps find the last score that is kept:
-//  1. The scores between the row's smallest and largest are spread evenly
-//     over the bins (subtraction, product and rounding keep their order) and counted; the blocks
-//     of a cluster add up each other's counts.  Every
-//     score above the bin in which the count reaches num_selected is kept, and as a rule that
-//     bin holds a handful.  Skipped where a score is NaN or infinite.
+//  1. The scores between the row's smallest and largest are spread evenly over the bins
+//     (subtraction, product and rounding keep their order) and counted; the blocks of a cluster
+//     add up each other's counts.  Every score above the bin in which the count reaches
+//     num_selected is kept, and as a rule that bin holds a handful.  Skipped where a score is NaN
+//     or infinite.
 //  2. If the bin holds more than are wanted, its scores, listed in shared memory, are each
 //     ranked among one another.  Where they are too many, or the row is a cluster's, or step 1
 //     was skipped, a score becomes a 32-bit key that orders as the scores do, and the last kept
@@ -17,9 +17,10 @@
 //     kept; lane j takes the votes of group j, a scan of their counts over lanes, warps and
 //     blocks says where its blocks go, and it writes them, of equal ones the lowest.
 // Sums are of whole numbers, so the result is the same on every run.  Bound by latency (the
-// launch and some ten barriers) for one sequence (8 rows of 1876 blocks: 3.9 us) and by instructions
-// for batches (1280 rows of up to 8192: 24 us): few warps with many groups each for many rows,
-// many warps with few groups for few (6464 rows of up to 215: 22 us with 2 warps, 45 us with 8).
+// launch and, as a rule, seven barriers) for one sequence (8 rows of 1876 blocks: 3.6 us) and by
+// instructions for batches (1280 rows of up to 8192: 23 us): few warps with many groups each for many
+// rows, many warps with few groups for few (6464 rows of up to 215: 21 us with 2 warps; before the
+// cluster's code left the kernel of one block 22 us, and 45 us with 8 warps).
 #include <cuda_runtime.h>
 
 #include "cluster.cuh"
@@ -29,7 +30,7 @@ namespace pagedkv {
 namespace {
 
 constexpr int kMaxCluster = 8;
-constexpr int kStep = 8;     // of them between two looks at how many there are
+constexpr int kStep = 8;  // groups of a sweep between two looks at how many the warp has
 
 struct SelectParams {
   const float* scores;
@@ -93,7 +94,9 @@ __device__ __forceinline__ void each_group(int groups, F f) {
 // kGroups: groups of 32 scores per warp, at most 32, one vote for each lane.
 // 64 registers a thread: four blocks of 256 threads an SM (1280 rows of up to 8192 blocks: 24.1 us,
 // 25.1 us with the 80 registers and three blocks of the compiler's choice).
-template <int kThreads, int kGroups>
+// kClustered: a row is a cluster's; without that code in it, the kernel of one block does not spill
+// (the same case: 23.0 us, 24.0 us with it).
+template <int kThreads, int kGroups, bool kClustered>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kPer = 8, kBins = kPer * kThreads;  // bins per thread, and in all
@@ -105,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
   __shared__ uint32_t part_sum[kWarps], block_sum, block_range[2];
   __shared__ int listed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int rank = kClustered ? static_cast<int>(cluster_rank()) : 0;
+  const int ranks = kClustered ? static_cast<int>(cluster_size()) : 1;
   const size_t row = blockIdx.x / ranks;
   const int seq = static_cast<int>(row / p.num_kv_heads), head = static_cast<int>(row % p.num_kv_heads);
   for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
@@ -143,12 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
 
   // The bin of hist[turn] in which the count from the top reaches `want`, into `found`.
   auto find = [&](int turn) {
-    if (ranks > 1) cluster_sync();
+    if constexpr (kClustered) cluster_sync();
     else __syncthreads();
     // thread t has the bins kBins - 1 - t kPer and the kPer - 1 below
     const int bin0 = kBins - (tid + 1) * kPer;
     int bin[kPer];
-    if (ranks == 1) {
+    if constexpr (!kClustered) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) bin[j] = hist[turn][bin0 + j];
     } else {
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
       __syncthreads();
       uint32_t from = __reduce_min_sync(kFullMask, lane < kWarps ? warp_range[0][lane] : 0xffffffffu);
       uint32_t to = __reduce_max_sync(kFullMask, lane < kWarps ? warp_range[1][lane] : 0u);
-      if (ranks > 1) {
+      if constexpr (kClustered) {
         if (tid == 0) {
           block_range[0] = from;
           block_range[1] = to;
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
         });
         open &= same;
         const int n = found[2];
-        if (ties && ranks == 1 && n <= kThreads) {  // list the bin's scores (over hist[0]) and rank each
+        if (ties && !kClustered && n <= kThreads) {  // list the bin's scores (over hist[0]) and rank each
           const bool some = __any_sync(kFullMask, open != 0);
           if (some)
             each_group<kGroups>(groups, [&](int j) {
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
   __syncthreads();
   upto += __reduce_add_sync(kFullMask, lane < warp ? part_sum[lane] : 0u);
   int at = 0, same = 0;
-  if (ranks > 1) {
+  if constexpr (kClustered) {
     if (tid == kThreads - 1) block_sum = upto;
     cluster_sync();
     const uint32_t sum_at = smem_addr(&block_sum);
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) paged_block_select_
     }
     out[at++] = base + 32 * lane + i;
   }
-  if (ranks > 1) cluster_sync();  // no block leaves while another may read its memory
+  if constexpr (kClustered) cluster_sync();  // no block leaves while another may read its memory
 }
 
 int launch(void (*kernel)(SelectParams), const SelectParams& p, dim3 grid, int threads, int ranks,
@@ -397,18 +401,19 @@ extern "C" int paged_block_select(const float* scores, const int32_t* seq_lens, 
   const SelectParams p{scores, seq_lens, selected, error_record, num_kv_heads, block_size,
                        max_blocks_per_seq, num_selected, sink_blocks, recent_blocks};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // As many blocks a row as its length takes: up to 16384 scores for each.
+  // As many thread blocks a row as its length takes: up to 16384 scores for each.
   int ranks = 1;
   while (ranks < kMaxCluster && max_blocks_per_seq > 16384 * ranks) ranks *= 2;
   if (max_blocks_per_seq > 16384 * ranks) return PA_ERR_UNSUPPORTED;
   if (rows * ranks > 0x7fffffffll) return PA_ERR_INVALID_ARG;
   const dim3 grid(static_cast<unsigned>(rows * ranks));
+  if (ranks > 1) return launch(paged_block_select_kernel<512, 32, true>, p, grid, 512, ranks, st);
   if (rows >= 152 * 4) {
-    if (max_blocks_per_seq <= 1024) return launch(paged_block_select_kernel<64, 16>, p, grid, 64, 1, st);
-    if (max_blocks_per_seq <= 4096) return launch(paged_block_select_kernel<128, 32>, p, grid, 128, 1, st);
+    if (max_blocks_per_seq <= 1024) return launch(paged_block_select_kernel<64, 16, false>, p, grid, 64, 1, st);
+    if (max_blocks_per_seq <= 4096)
+      return launch(paged_block_select_kernel<128, 32, false>, p, grid, 128, 1, st);
   }
-  if (max_blocks_per_seq <= 2048) return launch(paged_block_select_kernel<256, 8>, p, grid, 256, 1, st);
-  if (max_blocks_per_seq <= 8192 * ranks)
-    return launch(paged_block_select_kernel<256, 32>, p, grid, 256, ranks, st);
-  return launch(paged_block_select_kernel<512, 32>, p, grid, 512, ranks, st);
+  if (max_blocks_per_seq <= 2048) return launch(paged_block_select_kernel<256, 8, false>, p, grid, 256, 1, st);
+  if (max_blocks_per_seq <= 8192) return launch(paged_block_select_kernel<256, 32, false>, p, grid, 256, 1, st);
+  return launch(paged_block_select_kernel<512, 32, false>, p, grid, 512, 1, st);
 }
