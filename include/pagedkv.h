@@ -629,13 +629,14 @@ int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seq
  * paged_attn_sparse_workspace_size never falls as num_seqs, num_selected, max_blocks_per_seq or
  * block_size grow, the others alike: a buffer sized for the largest call serves every smaller
  * one.  0 where lists hold at most 2048 tokens; at most 1024 partial results of 8 or 16 heads.
- * paged_attn_sparse_clusters: over how many thread-block clusters the call, given a workspace,
- * spreads a list.  1: it does not touch the workspace (nor look at its size). */
+ * paged_attn_sparse_workspace_needed is that size where a call of exactly these sizes uses a
+ * workspace, and 0 where it neither touches one nor looks at its size. */
 size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                         int head_dim, int block_size, int max_blocks_per_seq,
                                         int num_selected);
-int paged_attn_sparse_clusters(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                               int block_size, int max_blocks_per_seq, int num_selected);
+size_t paged_attn_sparse_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
+                                          int head_dim, int block_size, int max_blocks_per_seq,
+                                          int num_selected);
 int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_tables, const int32_t* seq_lens,
                       const int32_t* selected, int num_selected, int num_seqs, int num_heads,

@@ -254,7 +254,7 @@ SIGNATURES = {
                                   c_float, c_int, c_void_p, c_int, c_void_p, c_size_t, c_void_p,
                                   c_void_p]),
     "paged_attn_sparse_workspace_size": (c_size_t, [c_int] * 7),
-    "paged_attn_sparse_clusters": (c_int, [c_int] * 7),
+    "paged_attn_sparse_workspace_needed": (c_size_t, [c_int] * 7),
     "block_copy": (c_int, [ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p), c_int, c_void_p,
                            c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "pa_decode_partition_tokens": (c_int, [c_void_p, c_int, c_int, c_int, c_int, P_int32]),
@@ -821,11 +821,11 @@ def paged_attn_sparse_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim
         num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_selected))
 
 
-def paged_attn_sparse_clusters(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
-                               max_blocks_per_seq, num_selected) -> int:
-    """Over how many clusters a paged_attn_sparse call with a workspace spreads a list; 1: it does
-    not touch the workspace."""
-    return int(load_library().paged_attn_sparse_clusters(
+def paged_attn_sparse_workspace_needed(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                       max_blocks_per_seq, num_selected) -> int:
+    """The same where a call of exactly these sizes uses a workspace (few rows with long lists),
+    0 where it does not touch it."""
+    return int(load_library().paged_attn_sparse_workspace_needed(
         num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, num_selected))
 
 
@@ -859,9 +859,8 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
     lib = load_library()
     if workspace is None:   # (lists of up to 2048 tokens never need one)
-        need = 0
-        if S * bs > 2048 and lib.paged_attn_sparse_clusters(N, Hq, H, D, bs, MB, S) > 1:
-            need = lib.paged_attn_sparse_workspace_size(N, Hq, H, D, bs, MB, S)
+        need = lib.paged_attn_sparse_workspace_needed(N, Hq, H, D, bs, MB, S) if S * bs > 2048 else 0
+        if need:
             workspace = _new_out((need,), torch.uint8, q.device, stream)
     else:
         _need_all(device, workspace.dtype, "workspace", (workspace, workspace.shape))

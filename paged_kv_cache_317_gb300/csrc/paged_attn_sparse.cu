@@ -687,12 +687,11 @@ int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, i
 
 // f(D, NT) for the sizes of a call; 0 where there is no such call.
 template <class F>
-auto for_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+size_t for_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                int max_blocks_per_seq, int num_selected, F f) {
-  using R = decltype(f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{}));
   if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
       block_size <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
-    return R{0};
+    return 0;
   const auto with = [&](auto dim) {
     return num_heads / num_kv_heads <= 8 ? f(dim, std::integral_constant<int, 1>{})
                                          : f(dim, std::integral_constant<int, 2>{});
@@ -701,7 +700,7 @@ auto for_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int 
     case 64: return with(std::integral_constant<int, 64>{});
     case 128: return with(std::integral_constant<int, 128>{});
     case 256: return with(std::integral_constant<int, 256>{});
-    default: return R{0};
+    default: return 0;
   }
 }
 
@@ -721,14 +720,15 @@ extern "C" size_t paged_attn_sparse_workspace_size(int num_seqs, int num_heads, 
   });
 }
 
-extern "C" int paged_attn_sparse_clusters(int num_seqs, int num_heads, int num_kv_heads,
-                                          int head_dim, int block_size, int max_blocks_per_seq,
-                                          int num_selected) {
+extern "C" size_t paged_attn_sparse_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
+                                                     int head_dim, int block_size,
+                                                     int max_blocks_per_seq, int num_selected) {
   return for_sizes(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                   num_selected, [&](auto dim, auto nt) {
+                   num_selected, [&](auto dim, auto nt) -> size_t {
     constexpr int D = decltype(dim)::value, NT = decltype(nt)::value;
     const long long rows = rows_of(num_seqs, num_kv_heads, num_heads / num_kv_heads, 8 * NT);
-    return shape_of<D, NT>(rows, num_selected, max_blocks_per_seq, block_size, true).parts;
+    if (shape_of<D, NT>(rows, num_selected, max_blocks_per_seq, block_size, true).parts == 1) return 0;
+    return workspace_for<D, NT>(rows, chunks_of(num_selected, max_blocks_per_seq, block_size));
   });
 }
 

@@ -16,11 +16,6 @@ def binding(lib):
     return binding
 
 
-def _rows(n, heads, kv):
-    cols = 8 if heads // kv <= 8 else 16
-    return n * kv * -(-(heads // kv) // cols), cols
-
-
 @pytest.mark.parametrize("heads,kv,dim", SHAPES)
 @pytest.mark.parametrize("keep", [129, 160, 192, 256, 512, 1000, 8192, 1 << 17])
 def test_the_size_never_falls_as_sequences_are_added(binding, heads, kv, dim, keep):
@@ -41,55 +36,61 @@ def test_the_size_never_falls_with_longer_lists_or_wider_tables(binding, heads, 
 
 
 @pytest.mark.parametrize("heads,kv,dim", SHAPES)
-def test_what_a_call_uses_is_within_the_size(binding, heads, kv, dim):
+def test_what_a_call_needs_is_the_size_or_nothing(binding, heads, kv, dim):
     spread = 0
     for n, keep, bs in itertools.product((1, 2, 3, 5, 7, 9, 11, 12, 17, 39, 153, 400, 2000),
                                          (1, 128, 129, 256, 1024, 5000, 1 << 15), (8, 16, 64)):
         a = (n, heads, kv, dim, bs, 1 << 16, keep)
-        used, size = binding.paged_attn_sparse_clusters(*a), binding.paged_attn_sparse_workspace_size(*a)
-        rows, cols = _rows(n, heads, kv)
-        assert 1 <= used <= 64 and (used == 1 or rows * used * cols * (dim * 4 + 8) <= size)
+        need, size = binding.paged_attn_sparse_workspace_needed(*a), binding.paged_attn_sparse_workspace_size(*a)
+        cols = 8 if heads // kv <= 8 else 16
+        rows = n * kv * -(-(heads // kv) // cols)
+        assert need in (0, size) and size <= min(64 * rows, 1024) * cols * (dim * 4 + 8)
         if keep * bs <= 2048:
-            assert used == 1 and size == 0
-        spread += used > 1
+            assert size == 0
+        spread += need > 0
     assert spread > 20
 
 
 def test_sizes_that_no_call_has(binding):
     for a in ((0, 8, 2, 64, 16, 4096, 4096), (1, 7, 2, 64, 16, 4096, 4096), (1, 8, 2, 96, 16, 4096, 4096),
               (1, 8, 2, 64, 16, 4096, 0), (1, 8, 2, 64, 0, 4096, 9), (1, 8, 2, 64, 16, -1, 9)):
-        assert binding.paged_attn_sparse_clusters(*a) == binding.paged_attn_sparse_workspace_size(*a) == 0
+        assert binding.paged_attn_sparse_workspace_needed(*a) == 0
+        assert binding.paged_attn_sparse_workspace_size(*a) == 0
 
 
 def test_a_buffer_below_the_size_is_refused_where_a_list_is_spread(lib, binding):
     for n in range(1, 18):
         a = (n, 8, 1, 128, 16, 8192, 512)
         size = binding.paged_attn_sparse_workspace_size(*a)
-        if binding.paged_attn_sparse_clusters(*a) > 1:
+        if binding.paged_attn_sparse_workspace_needed(*a):
             assert lib.paged_attn_sparse(P, P, P, P, P, P, 512, n, 8, 1, 128, 16, 8192, 1 << 18, 0.1, 1, P, 1,
                                          P, size - 1, None, None) == 1
-    assert binding.paged_attn_sparse_clusters(1, 8, 1, 128, 16, 8192, 512) > 1
+    assert binding.paged_attn_sparse_workspace_needed(1, 8, 1, 128, 16, 8192, 512) > 0
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("narrow", [False, True], ids=["rows", "lists"])
-def test_one_buffer_serves_a_batch_that_shrinks(binding, narrow):
-    """12 sequences need less at a time than 11, and short lists more than long ones; a buffer made
-    for all of them takes each, and leaves what lies behind it alone."""
-    B, D, bs, keep, width = binding, 128, 16, 512, 600
+@pytest.mark.parametrize("Hq,H,D", [(8, 1, 128), (16, 1, 64), (17, 1, 256), (6, 2, 64)])
+def test_one_buffer_serves_a_batch_that_shrinks(binding, Hq, H, D):
+    """12 sequences use less at a time than 11, and long lists less than short ones; a buffer made for
+    all of them takes each, and what lies behind it stays."""
+    B, bs, keep, width = binding, 16, 512, 600
     gen = torch.Generator(device="cuda").manual_seed(0)
     randn = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
-    kc, vc, q = randn(3000, 1, bs, D), randn(3000, 1, bs, D), randn(12, 8, D)
+    kc, vc, q = randn(3000, H, bs, D), randn(3000, H, bs, D), randn(12, Hq, D)
     rng = np.random.default_rng(0)
     dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
     tables, lens = dev(rng.integers(0, 3000, (12, width))), dev(rng.integers(bs * keep, bs * width + 1, 12))
-    sel = dev(np.sort(rng.permuted(np.tile(np.arange(keep + 80), (12, 1)), axis=1)[:, None, :keep]))
-    need = B.paged_attn_sparse_workspace_size(12, 8, 1, D, bs, width, keep)
+    sel = dev(rng.permuted(np.tile(np.arange(keep + 80), (12, H, 1)), axis=2)[:, :, :keep])
+    need = B.paged_attn_sparse_workspace_size(12, Hq, H, D, bs, width, keep)
     whole = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    used = []
     for n in range(12, 0, -1):
-        for s in ((keep, 300, 129) if narrow else (keep,)):
+        for s in (keep, 300, 129):
             part = sel[:n, :, :s].contiguous()
-            want = B.paged_attn_sparse(q[:n], kc, vc, tables[:n], lens[:n], part, 0.1)
-            got = B.paged_attn_sparse(q[:n], kc, vc, tables[:n], lens[:n], part, 0.1, workspace=whole[:need])
-            assert torch.equal(got, want) and bool(torch.isfinite(got).all())
-    assert bool((whole[need:] == 77).all())
+            args = (q[:n], kc, vc, tables[:n], lens[:n], part, 0.1)
+            whole[:need] = 255
+            got = B.paged_attn_sparse(*args, workspace=whole[:need])
+            used.append(int((whole[:need] != 255).sum()))
+            assert torch.equal(got, B.paged_attn_sparse(*args)) and bool(torch.isfinite(got).all())
+            assert (used[-1] > 0) == (B.paged_attn_sparse_workspace_needed(n, Hq, H, D, bs, width, s) > 0)
+    assert max(used[3:]) > used[0] and bool((whole[need:] == 77).all())
