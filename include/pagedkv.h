@@ -578,8 +578,9 @@ int kv_block_bounds(const void* k_cache, const int32_t* block_tables, const int3
 /* scores[i][h][b] = scale * max over the query heads g of key head h of
  *   sum_d max(q[i][g][d], 0) * k_max[blk][h][d] + min(q[i][g][d], 0) * k_min[blk][h][d]
  * with blk = block_tables[i][b], for b < ceil(L / block_size): no key of the block has a
- * larger logit for any of these heads.  -infinity for the other b < max_blocks_per_seq.
- * A NaN among the products makes the score NaN.
+ * larger logit for any of these heads, but for the roundings of the 2 head_dim products' sum in
+ * fp32 (less than (2 head_dim + 4) 2^-23 of their magnitudes; 2.6e-7 of them in practice).
+ * -infinity for the other b < max_blocks_per_seq.  A NaN among the products makes the score NaN.
  *   q             device [num_seqs][num_heads][head_dim] in `dtype`, 16-byte aligned
  *   head_dim      64, 128 or 256;  scale > 0
  *   scores        device float [num_seqs][num_kv_heads][max_blocks_per_seq]
@@ -622,7 +623,10 @@ int paged_block_select(const float* scores, const int32_t* seq_lens, int num_seq
  *                 bytes, scratch of this call alone; or NULL: a list is then read by at most 8
  *                 thread blocks, which is slow where few rows have long lists.
  * Arithmetic as in paged_attn_prefill: logits and sums in fp32, probabilities as a pair of
- * half-precision numbers.  num_blocks * num_kv_heads * block_size must be < 2^31.
+ * half-precision numbers of the cache's type.  Besides fp32's roundings a result so differs from
+ * the exact one by at most 2^-17 (bf16) or 2^-23 (fp16) of sum_t w_t |v_t|: 1.2e-6 and 2.6e-7 of it
+ * in all as measured, where the dense decode, with weights in fp32, has 1.8e-7.
+ * num_blocks * num_kv_heads * block_size must be < 2^31.
  * A block-table entry out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and block 0
  * is read; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.
  *

@@ -7,14 +7,16 @@
 // 16-byte pieces, 8 rotary pairs) of one head of q, k or v, and the tile's tokens one after the
 // other.  Bound by latency, and by HBM for large batches.
 //
-// Prompts (kv_append_rope_kernel): a thread block takes up to 32 heads of q, k or v of a tile; of q
-// and v at most 16 tokens of a longer tile.  A thread
-// keeps the cosines and sines of its row and 8 pairs in registers and goes over the heads, 4
-// at a time.  Rotated keys also go to shared memory, where each channel's minimum and maximum
-// over the tile's rows are taken: as the tile holds every new key of its block, the bounds
-// need no atomics and no second pass, and come out the same on every run.  One read and one
-// write of each element, 3 operations: bound by HBM (24 prompts of up to 700 tokens, 32 + 2 x 8
-// heads of 128, 240 MB: 43 us, 5.6 TB/s), four blocks of 128 registers a thread on an SM.
+// Prompts (kv_append_rope_kernel): a thread block takes up to 32 heads of q, k or v of a tile, 4 heads
+// of k where a tile's rows need several passes; of q and v 16 tokens of a longer tile, or a 64th of
+// the longest tile if that is more, of k the whole tile.  A thread keeps the cosines and sines of
+// its row and 8 pairs in registers and goes over the heads, 4 at a time.  Rotated keys also go to
+// shared memory, where each channel's minimum and maximum over the tile's rows are taken: as the
+// tile holds every new key of its block, the bounds need no atomics and no second pass, and come
+// out the same on every run.  One read and one write of each element, 3 operations: bound by HBM
+// (24 prompts of up to 700 tokens, 32 + 2 x 8 heads of 128, 240 MB: 43 us, 5.6 TB/s), four blocks of
+// 127 registers a thread on an SM.  With one head a thread block has 2 KB in flight and half its
+// threads idle (63,000 tokens of one head of 64, 50 MB: 62 us).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -142,7 +144,7 @@ __device__ __forceinline__ void merge_bounds(const AppendRopeParams& p, size_t a
   *mx = stored ? max8(hi, *mx, Tag{}) : hi;
 }
 
-// kOne: one token a sequence, whose tile needs no search (256 x 40 heads, 26 MB: 5.4 us in a graph).
+// kOne: one token a sequence, whose tile needs no search (256 x 40 heads, 26 MB: 5.5 us in a graph).
 template <class Tag, bool kOne>
 __global__ void __launch_bounds__(kThreads) kv_append_step_kernel(const AppendRopeParams p) {
   using T = typename Tag::T;
@@ -397,9 +399,10 @@ extern "C" int kv_cache_append_rope(const void* q, int64_t q_stride, const void*
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.rope.total_tokens = total_tokens;
-  // A few tokens a sequence: a thread for 16 dims of each head of a tile (217 sequences of 1 or 2
-  // tokens, 48 + 2 x 3 heads of 64: 6.8 us, by chunks of heads 14.9 us).  Otherwise by chunks of
-  // heads.  A tile for each sequence, or the tile slots of first_slot with behind them blocks that
+  // Up to kFew tokens a sequence: a thread for 16 dims of each head of a tile, otherwise by chunks of
+  // heads (217 sequences of 2, 3, 4 tokens, 48 + 2 x 3 heads of 64: 5.6, 6.6, 7.3 us, by chunks of
+  // heads 13.3, 13.9, 14.4 us; 64 of 3, 4, 6 tokens, 32 + 2 x 8 heads of 128: 5.3, 6.0, 7.5 us, by
+  // chunks 5.9, 5.9, 6.6 us).  A tile for each sequence, or the tile slots of first_slot with behind them blocks that
   // check the ranges.
   const bool one = max_query_len == 1, few = max_query_len <= kFew;
   p.tiles = one ? num_seqs : total_tokens / block_size + 2 * num_seqs;

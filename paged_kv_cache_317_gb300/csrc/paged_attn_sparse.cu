@@ -11,7 +11,8 @@
 //    another before the end.
 //  * Per chunk, on mma.sync m16n8k16 with the 16 tokens as the rows and the query heads as
 //    the columns: S^T = K.Q^T in fp32, the running maximum and sum of each column in log2
-//    units, O^T += V^T.P^T with P as a high and a low half-precision number.  Up to 8 query
+//    units, O^T += V^T.P^T with P as a high and a low half-precision number (off by at most 2^-17
+//    of a weight in bf16, 2^-23 in fp16; with one number it would be 2^-8, 2^-11).  Up to 8 query
 //    heads cost one product, up to 16 two; K and V are read once for all of them.
 //  * At the end the warps' (m, l, O) are joined in shared memory, and those of the cluster's
 //    blocks over distributed shared memory, in a fixed order: the same bits on every run.  Only
@@ -20,7 +21,7 @@
 // Two operations per cached byte and query head: bound by HBM (64 sequences x 8 key heads x 8 query
 // heads, lists of 128 blocks of 16, 527 MB: 81 us, 6.5 TB/s; 32 x 40 heads, 64 blocks, 672 MB: 100
 // us, 6.7 TB/s).  One row alone is a chain of look-ups, copy, products and joins (8 rows of 64
-// blocks: 5.7 us).
+// blocks: 5.6 us; one list of 2048 blocks over 32 clusters: 12.6 us, over one 166 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -591,7 +592,7 @@ int most_parts(long long rows, long long chunks) {
 template <int D, int NT>
 Shape shape_of(long long rows, int num_selected, int max_blocks, int block_size, bool parts) {
   const long long chunks = chunks_of(num_selected, max_blocks, block_size);
-  // thread blocks an SM, as registers allow
+  // thread blocks an SM, as registers allow (64 channels, 8 heads: of 72 registers seven would fit)
   constexpr int kMost[3][2] = {{6, 4}, {4, 3}, {3, 2}};
   constexpr int most = kMost[D / 128][NT - 1];
   const size_t smem[3] = {smem_bytes<D, NT>(1), smem_bytes<D, NT>(2), smem_bytes<D, NT>(3)};
