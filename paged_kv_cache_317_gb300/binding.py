@@ -556,16 +556,18 @@ def block_copy(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor
                stream=None) -> None:
     """Per-layer caches [B,H,bs,D]; pairs int64 [n,2] (src, dst) on the device."""
     n_layers = len(k_caches)
-    B, H, bs, D = shape = k_caches[0].shape
-    dtype = k_caches[0].dtype
+    B, H, bs, D = k_caches[0].shape
+    size = k_caches[0].nbytes
     if len(v_caches) != n_layers:
         raise ValueError(f"{n_layers} key caches and {len(v_caches)} value caches")
-    for t in (*k_caches, *v_caches):
-        if t.shape != shape or t.dtype != dtype:   # key bounds beside caches: a call of their own
-            raise ValueError(f"the caches of one call must be alike: {list(shape)} in {dtype}, got "
-                             f"{list(t.shape)} in {t.dtype}")
-    for t in (*k_caches, *v_caches):
-        _need(t, "cache")
+    caches = (*k_caches, *v_caches)
+    for t in caches:   # one look at each of what may be a hundred; which check failed, afterwards
+        if t.nbytes != size or not t.is_cuda or not t.is_contiguous():
+            for u in caches:   # (key bounds beside caches: a call of their own)
+                if u.nbytes != size:
+                    raise ValueError(f"the caches of one call must be alike: {[B, H, bs, D]} in "
+                                     f"{k_caches[0].dtype}, got {list(u.shape)} in {u.dtype}")
+            _need(t, "cache")
     _need(pairs, "pairs", torch.int64)
     kp = (c_void_p * n_layers)(*[t.data_ptr() for t in k_caches])
     vp = (c_void_p * n_layers)(*[t.data_ptr() for t in v_caches])
