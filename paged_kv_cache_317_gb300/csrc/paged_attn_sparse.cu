@@ -689,7 +689,7 @@ int launch_nt(const SparseParams& p, const void* k_cache, const void* v_cache, i
 // f(D, NT) for the sizes of a call; 0 where there is no such call.
 template <class F>
 size_t for_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-               int max_blocks_per_seq, int num_selected, F f) {
+                 int max_blocks_per_seq, int num_selected, F f) {
   if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
       block_size <= 0 || max_blocks_per_seq <= 0 || num_selected <= 0)
     return 0;
