@@ -75,7 +75,7 @@ typedef enum pa_status {
   PA_ERR_NO_SEQ = 9,       /* allocator: unknown sequence id */
   PA_ERR_SEQ_EXISTS = 10,  /* allocator: sequence id already in use */
   PA_ERR_REFCOUNT = 11,    /* allocator: a reference count or free list is inconsistent */
-  PA_ERR_BAD_POSITION = 12 /* device: rotary position outside [0, max_position) */
+  PA_ERR_BAD_POSITION = 12 /* device: a rotary position, or a kept place, out of range */
 } pa_status;
 
 typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 } pa_dtype;
@@ -650,6 +650,110 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
                       void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A bounded cache: attention that tells what weight each cached token has had, and
+ * eviction of the others
+ *
+ * A sequence may keep fewer tokens than it has had.  weights[i][h][t] adds up the
+ * attention weight that the token at place t of sequence i has had from the query heads
+ * of key head h; paged_block_select over them (block_size 1) lists the places to keep,
+ * and kv_cache_evict moves those to the front.  Query heads may share key heads as above.
+ * Keys carry their rotation in the cache, so places may be renumbered freely; new tokens
+ * keep the positions that they would have had (kv_cache_append_rope's `positions`).
+ *   weights       device float [num_seqs][num_kv_heads][weights_tokens], weights_tokens >=
+ *                 max_blocks_per_seq * block_size; row i belongs to sequence i of the call.
+ *                 Zeroed by the caller when a sequence begins; places at or past L are
+ *                 neither read nor written, so a token's weight begins at the zero there.
+ * ------------------------------------------------------------------------- */
+
+/* paged_attn_prefill for query heads that share key heads: num_heads is a multiple of
+ * num_kv_heads, at most 128 times it, and the query heads of a key head and several tokens
+ * fill a tile together, so that a few drafted tokens read K and V once for all heads.
+ *   k_cache, v_cache  device [num_blocks][num_kv_heads][block_size][head_dim]
+ *   lse           NULL, or device float [total_queries][num_heads]: the natural logarithm of
+ *                 a row's sum of e^(scale * <q, k_t>); rows outside every range are not written
+ *   seq_order     as in pa_prefill_opts, or NULL
+ * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x
+ * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30.  Otherwise, checks
+ * of the batch and arithmetic too, as paged_attn_prefill. */
+int paged_attn_chunk(const void* q, const int32_t* query_start, int total_queries,
+                     int max_query_len, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                     int num_heads, int num_kv_heads, int head_dim, int block_size,
+                     int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out,
+                     int out_dtype, float* lse, const int32_t* seq_order, int32_t* error_record,
+                     void* stream);
+
+/* weights[i][h][t] += sum over the last W_i of sequence i's queries, W_i = Q_i or at most
+ * `window`, and the query heads of key head h, of e^(scale * <q, k_t> - lse), for the places
+ * t that the query sees.  The batch is described as for paged_attn_prefill, lse is what
+ * paged_attn_chunk gave for these queries.
+ *   window        0: all queries of the call
+ * A sequence whose range or length is inconsistent is recorded as PA_ERR_BAD_SEQ_LEN and
+ * skipped; a block number out of range is recorded as PA_ERR_BAD_BLOCK and block 0 is read.
+ * num_heads at most 128 times num_kv_heads; num_blocks * num_kv_heads * block_size < 2^31;
+ * num_seqs x num_kv_heads x ceil(max_blocks_per_seq * block_size / 256) at most 2^30. */
+int paged_chunk_weights(const void* q, const float* lse, const int32_t* query_start,
+                        int total_queries, int max_query_len, const void* k_cache,
+                        const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                        int num_heads, int num_kv_heads, int head_dim, int block_size,
+                        int max_blocks_per_seq, int num_blocks, float scale, int dtype, int window,
+                        float* weights, int64_t weights_tokens, int32_t* error_record, void* stream);
+
+/* Decode attention, out[i][g] = sum_t softmax(scale * <q[i][g], k_t>)_t v_t over the tokens
+ * t < L, and weights[i][h][t] += sum over the query heads g of key head h of those softmax
+ * weights, K and V read once for both.  A row without tokens is zero.
+ *   q, out        device [num_seqs][num_heads][head_dim], 16-byte aligned
+ *   head_dim      64, 128 or 256;  block_size: a multiple of 16, or 8
+ *   workspace     device, 16-byte aligned, scratch of this call alone, at least
+ *                 paged_attn_decode_weights_workspace_size(...) bytes; may be NULL where
+ *                 paged_attn_decode_weights_workspace_needed(...) is 0
+ * Arithmetic as in paged_attn_sparse.  num_blocks * num_kv_heads * block_size must be < 2^31.
+ * A block number out of range is recorded as PA_ERR_BAD_BLOCK and block 0 is read; a length out
+ * of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.
+ *
+ * paged_attn_decode_weights_workspace_size never falls as num_seqs, max_blocks_per_seq or
+ * block_size grow, the others alike: a buffer sized for the largest call serves every smaller
+ * one.  paged_attn_decode_weights_workspace_needed is that size where a call of exactly these
+ * sizes uses a workspace, and 0 where it neither touches one nor looks at its size. */
+size_t paged_attn_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                int head_dim, int block_size,
+                                                int max_blocks_per_seq);
+size_t paged_attn_decode_weights_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
+                                                  int head_dim, int block_size,
+                                                  int max_blocks_per_seq);
+int paged_attn_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                              int num_heads, int num_kv_heads, int head_dim, int block_size,
+                              int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+                              void* out, int out_dtype, float* weights, int64_t weights_tokens,
+                              void* workspace, size_t workspace_bytes, int32_t* error_record,
+                              void* stream);
+
+/* For every sequence i, key head h and place j < min(num_kept, L): place j takes the row of K,
+ * of V and the weight that place s = kept[i][h][j] held before the call.  Places below L without
+ * an entry (kept[i][h][j] = -1, or j >= num_kept) keep their rows and get the weight 0.  With
+ * ascending places, then -1, the sequence is afterwards min(num_kept, L) tokens long.
+ *   kept          device int32 [num_seqs][num_kv_heads][num_kept]: -1, or j <= s < L, as any
+ *                 ascending list has it.  Another entry is recorded as PA_ERR_BAD_POSITION (index =
+ *                 i * num_kv_heads + h, value = s), and place j stays as it is.  L is the length
+ *                 before the call.
+ *   new_tables    NULL: in place; or device int32 [num_seqs][new_max_blocks], the blocks of the
+ *                 new places.  Each entry is the sequence's own block of those places, or a block
+ *                 that no sequence of the call reads (pa_batch_evict sees to it).  In place, the
+ *                 blocks of the new places must be private to their sequence.
+ *   weights       may be NULL
+ *   head_dim      a multiple of 8, at most 1024;  block_size: any
+ * A block number out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and the row is left out;
+ * a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.  Key bounds are left alone:
+ * after it, kv_block_bounds. */
+int kv_cache_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
+                   const int32_t* new_tables, const int32_t* seq_lens, const int32_t* kept,
+                   int num_kept, float* weights, int64_t weights_tokens, int num_seqs,
+                   int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                   int new_max_blocks, int num_blocks, int dtype, int32_t* error_record,
+                   void* stream);
+
+/* ---------------------------------------------------------------------------
  * Copy-on-write block copy  [P3d]
  *
  * For each pair j < num_pairs, (src, dst) = (pairs[2j], pairs[2j+1]), and each
@@ -729,6 +833,13 @@ int pa_batch_fork(pa_allocator* a, const int64_t* parents, const int64_t* childr
 /* n frees (see pa_seq_free).  All-or-nothing: an id that is missing or listed
  * twice returns PA_ERR_NO_SEQ before anything changes. */
 int pa_batch_free(pa_allocator* a, const int64_t* seqs, int32_t n);
+/* Every listed sequence of more than num_kept (>= 1) tokens gets that length.  Of the blocks it
+ * keeps, those that others hold when the call begins are replaced by fresh ones, which are taken
+ * before any block goes back: the tables before and after the call are kv_cache_evict's
+ * block_tables and new_tables.  A block that goes back may be handed out at once; what is then
+ * enqueued on the eviction's stream comes after it.  All-or-nothing: PA_ERR_OOM if the free list
+ * cannot give the fresh blocks, PA_ERR_NO_SEQ for an id that is missing or listed twice. */
+int pa_batch_evict(pa_allocator* a, const int64_t* seqs, int32_t n, int32_t num_kept);
 /* Block tables of the listed sequences as rows of tables[n][max_blocks] (entries
  * past a table's end are -1) and their lengths. PA_ERR_INVALID_ARG if a table
  * does not fit. */

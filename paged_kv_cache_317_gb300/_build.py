@@ -31,6 +31,9 @@ SOURCES = [
     "block_scores.cu",
     "block_select.cu",
     "paged_attn_sparse.cu",
+    "paged_attn_decode_weights.cu",
+    "chunk_weights.cu",
+    "kv_cache_evict.cu",
     "block_copy.cu",
     "api.cu",
     "allocator.cpp",

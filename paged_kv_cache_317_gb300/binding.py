@@ -255,6 +255,22 @@ SIGNATURES = {
                                   c_void_p]),
     "paged_attn_sparse_workspace_size": (c_size_t, [c_int] * 7),
     "paged_attn_sparse_workspace_needed": (c_size_t, [c_int] * 7),
+    "paged_attn_chunk": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                 c_float, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                 c_void_p]),
+    "paged_chunk_weights": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                                    c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                    c_float, c_int, c_int, c_void_p, c_int64, c_void_p, c_void_p]),
+    "paged_attn_decode_weights": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                          c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_int,
+                                          c_void_p, c_int, c_void_p, c_int64, c_void_p, c_size_t,
+                                          c_void_p, c_void_p]),
+    "paged_attn_decode_weights_workspace_size": (c_size_t, [c_int] * 6),
+    "paged_attn_decode_weights_workspace_needed": (c_size_t, [c_int] * 6),
+    "kv_cache_evict": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                               c_void_p, c_int64, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                               c_int, c_void_p, c_void_p]),
     "block_copy": (c_int, [ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p), c_int, c_void_p,
                            c_int, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "pa_decode_partition_tokens": (c_int, [c_void_p, c_int, c_int, c_int, c_int, P_int32]),
@@ -281,6 +297,7 @@ SIGNATURES = {
     "pa_batch_append": (c_int, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, P_int32]),
     "pa_batch_fork": (c_int, [c_void_p, c_void_p, c_void_p, c_int32]),
     "pa_batch_free": (c_int, [c_void_p, c_void_p, c_int32]),
+    "pa_batch_evict": (c_int, [c_void_p, c_void_p, c_int32, c_int32]),
     "pa_batch_block_tables": (c_int, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
     "pa_alloc_stats": (c_int, [c_void_p, P_int32, P_int64, P_int64, P_int64]),
     "pa_alloc_check": (c_int, [c_void_p]),
@@ -875,6 +892,171 @@ def paged_attn_sparse(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return out
 
 
+# --------------------------------------- a bounded cache: attention weights, eviction
+def _weights(t, device, rows, room):
+    """The floats from (sequence, key head) to the next of weights [N,H,T], T at least the places
+    that the block tables have."""
+    if t.dim() != 3 or t.shape[2] < room:
+        raise ValueError(f"weights must be [{rows[0]}, {rows[1]}, at least {room}], got {list(t.shape)}")
+    _need_all(device, torch.float32, "weights", (t, (*rows, t.shape[2])))
+    return t.shape[2]
+
+
+def paged_attn_chunk(q: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
+                     k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                     seq_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                     out_dtype=torch.float32, lse: Optional[torch.Tensor] = None,
+                     seq_order: Optional[torch.Tensor] = None,
+                     error_record: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of each sequence's last tokens over its cached ones, query heads sharing key
+    heads.  q [T,Hq,D]; query_start int32 [N+1]; caches [B,H,bs,D], Hq a multiple of H;
+    block_tables int32 [N,MB]; seq_lens int32 [N], the new tokens counted; lse: optional float32
+    [T,Hq], filled with the logarithm of each row's sum of exponentials; seq_order: optional int32
+    [N] dispatch order of the sequences."""
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
+    N, MB = block_tables.shape
+    T, Hq = q.shape[:2]
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPE:
+        raise ValueError(f"out must be float16, bfloat16 or float32, got {out_dtype}")
+    cache = (B, H, bs, D)
+    _need_all(device, dtype, "q k_cache v_cache", (q, (T, Hq, D)), (k_cache, cache), (v_cache, cache))
+    _need_all(device, i32, "query_start block_tables seq_lens seq_order", (query_start, (N + 1,)),
+              (block_tables, (N, MB)), (seq_lens, (N,)), (seq_order, (N,)))
+    _need_all(device, torch.float32, "lse", (lse, (T, Hq)))
+    if out is not None:
+        _need_all(device, out_dtype, "out", (out, (T, Hq, D)))
+    elif out_dtype is dtype:
+        out = _new_like(q, stream)
+    else:
+        out = _new_out((T, Hq, D), out_dtype, q.device, stream)
+    _check(load_library().paged_attn_chunk(
+        q.data_ptr(), query_start.data_ptr(), T, int(max_query_len), k_cache.data_ptr(),
+        v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B,
+        float(scale), _DTYPE[dtype], out.data_ptr(), _DTYPE[out_dtype], _address(lse),
+        _address(seq_order), _record(error_record, device), _raw_stream(stream, device)),
+        "paged_attn_chunk")
+    return out
+
+
+def paged_chunk_weights(q: torch.Tensor, lse: torch.Tensor, query_start: torch.Tensor,
+                        max_query_len: int, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                        seq_lens: torch.Tensor, scale: float, weights: torch.Tensor, window: int = 0,
+                        error_record: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Add to weights float32 [N,H,places] the attention weight that each cached token has from the
+    last `window` (0: all) of each sequence's queries q [T,Hq,D], summed over them and over the query
+    heads of key head H; lse float32 [T,Hq] as paged_attn_chunk gave it."""
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
+    N, MB = block_tables.shape
+    T, Hq = q.shape[:2]
+    _need_all(device, dtype, "q k_cache", (q, (T, Hq, D)), (k_cache, (B, H, bs, D)))
+    _need_all(device, i32, "query_start block_tables seq_lens", (query_start, (N + 1,)),
+              (block_tables, (N, MB)), (seq_lens, (N,)))
+    _need_all(device, torch.float32, "lse", (lse, (T, Hq)))
+    room = _weights(weights, device, (N, H), MB * bs)
+    _check(load_library().paged_chunk_weights(
+        q.data_ptr(), lse.data_ptr(), query_start.data_ptr(), T, int(max_query_len),
+        k_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B,
+        float(scale), _DTYPE[dtype], int(window), weights.data_ptr(), room,
+        _record(error_record, device), _raw_stream(stream, device)), "paged_chunk_weights")
+
+
+def paged_attn_decode_weights_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                             max_blocks_per_seq) -> int:
+    """Workspace bytes that serve a paged_attn_decode_weights call of these sizes and every one with
+    fewer sequences or narrower tables."""
+    return int(load_library().paged_attn_decode_weights_workspace_size(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq))
+
+
+def paged_attn_decode_weights_workspace_needed(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                               max_blocks_per_seq) -> int:
+    """The same where a call of exactly these sizes uses a workspace, 0 where it does not touch it."""
+    return int(load_library().paged_attn_decode_weights_workspace_needed(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq))
+
+
+def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                              weights: torch.Tensor, out: Optional[torch.Tensor] = None,
+                              out_dtype=torch.float32, workspace: Optional[torch.Tensor] = None,
+                              error_record: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Decode attention, query heads sharing key heads, that adds to weights float32 [N,H,places] the
+    softmax weight of every cached token, summed over the query heads of its key head.  q [N,Hq,D];
+    caches [B,H,bs,D], Hq a multiple of H; block_tables int32 [N,MB]; seq_lens int32 [N]; workspace:
+    optional contiguous tensor of at least paged_attn_decode_weights_workspace_size(...) bytes, made
+    here if it is needed and not given."""
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
+    N, MB = block_tables.shape
+    Hq = q.shape[1]
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _DTYPE:
+        raise ValueError(f"out must be float16, bfloat16 or float32, got {out_dtype}")
+    cache = (B, H, bs, D)
+    _need_all(device, dtype, "q k_cache v_cache", (q, (N, Hq, D)), (k_cache, cache), (v_cache, cache))
+    _need_all(device, i32, "block_tables seq_lens", (block_tables, (N, MB)), (seq_lens, (N,)))
+    room = _weights(weights, device, (N, H), MB * bs)
+    if out is not None:
+        _need_all(device, out_dtype, "out", (out, (N, Hq, D)))
+    elif out_dtype is dtype:
+        out = _new_like(q, stream)
+    else:
+        out = _new_out((N, Hq, D), out_dtype, q.device, stream)
+    lib = load_library()
+    if workspace is None:
+        need = lib.paged_attn_decode_weights_workspace_needed(N, Hq, H, D, bs, MB)
+        if need:
+            workspace = _new_out((need,), torch.uint8, q.device, stream)
+    else:
+        _need_all(device, workspace.dtype, "workspace", (workspace, workspace.shape))
+        need = workspace.numel() * workspace.element_size()
+    _check(lib.paged_attn_decode_weights(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B, float(scale), _DTYPE[dtype], out.data_ptr(),
+        _DTYPE[out_dtype], weights.data_ptr(), room, _address(workspace), need,
+        _record(error_record, device), _raw_stream(stream, device)), "paged_attn_decode_weights")
+    return out
+
+
+def kv_cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   seq_lens: torch.Tensor, kept: torch.Tensor,
+                   weights: Optional[torch.Tensor] = None,
+                   new_tables: Optional[torch.Tensor] = None,
+                   error_record: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Place j of each (sequence, key head) takes the rows of K and V, and the weight, that place
+    kept[i,h,j] held; the weights of the other places become 0.  caches [B,H,bs,D]; block_tables
+    int32 [N,MB]; seq_lens int32 [N], the lengths before; kept int32 [N,H,K], ascending places, then
+    -1 (paged_block_select over the weights, block size 1); weights: optional float32 [N,H,places];
+    new_tables: optional int32 [N,MB'], the tables after BlockAllocator.batch_evict, where other
+    sequences hold blocks of these."""
+    device, i32 = torch.cuda.current_device(), torch.int32
+    (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
+    N, MB = block_tables.shape
+    cache = (B, H, bs, D)
+    _need_all(device, dtype, "k_cache v_cache", (k_cache, cache), (v_cache, cache))
+    if kept.dim() != 3:
+        raise ValueError(f"kept must be [{N}, {H}, places to keep], got {list(kept.shape)}")
+    K = kept.shape[2]
+    width = MB
+    if new_tables is not None:
+        if new_tables.dim() != 2:
+            raise ValueError(f"new_tables must be [{N}, blocks], got {list(new_tables.shape)}")
+        width = new_tables.shape[1]
+    _need_all(device, i32, "block_tables seq_lens kept new_tables", (block_tables, (N, MB)),
+              (seq_lens, (N,)), (kept, (N, H, K)), (new_tables, (N, width)))
+    room = 0 if weights is None else _weights(weights, device, (N, H), MB * bs)
+    _check(load_library().kv_cache_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), _address(new_tables),
+        seq_lens.data_ptr(), kept.data_ptr(), K, _address(weights), room, N, H, D, bs, MB, width, B,
+        _DTYPE[dtype], _record(error_record, device), _raw_stream(stream, device)), "kv_cache_evict")
+
+
 # --------------------------------------------------------------- allocator
 class BlockAllocator:
     """Host block allocator (C++), see pa_alloc_* in include/pagedkv.h."""
@@ -971,6 +1153,15 @@ class BlockAllocator:
         ids = np.ascontiguousarray(seqs, dtype=np.int64)
         _check(self._lib.pa_batch_free(self._h, ids.ctypes.data, ids.shape[0]),
                "pa_batch_free")
+
+    def batch_evict(self, seqs, num_kept: int) -> None:
+        """Cut every listed sequence of more than num_kept tokens to that length, with fresh blocks
+        for those of the kept ones that others hold; all-or-nothing.  The tables before and after
+        are kv_cache_evict's block_tables and new_tables."""
+        import numpy as np
+        ids = np.ascontiguousarray(seqs, dtype=np.int64)
+        _check(self._lib.pa_batch_evict(self._h, ids.ctypes.data, ids.shape[0], int(num_kept)),
+               "pa_batch_evict")
 
     def batch_block_tables(self, seqs, max_blocks: int, out=None):
         """Block tables [n, max_blocks] (-1 past each sequence's blocks) and lengths

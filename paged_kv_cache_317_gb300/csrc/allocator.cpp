@@ -333,6 +333,50 @@ extern "C" int pa_batch_free(pa_allocator* a, const int64_t* seqs, int32_t n) {
   return status;
 }
 
+extern "C" int pa_batch_evict(pa_allocator* a, const int64_t* seqs, int32_t n, int32_t num_kept) {
+  if (!a || n < 0 || num_kept <= 0 || (n > 0 && !seqs)) return PA_ERR_INVALID_ARG;
+  std::vector<pa_allocator::Seq*> cut;    // the sequences that lose tokens
+  std::vector<std::pair<int32_t, int32_t>> shared;  // (which of them, entry of its table) to replace
+  const int32_t keep = a->blocks_for(num_kept);
+  try {
+    std::vector<int64_t> ids(seqs, seqs + n);
+    std::sort(ids.begin(), ids.end());
+    for (int32_t i = 1; i < n; ++i)
+      if (ids[i] == ids[i - 1]) return PA_ERR_NO_SEQ;  // listed twice
+    for (int32_t i = 0; i < n; ++i) {
+      auto it = a->seqs.find(seqs[i]);
+      if (it == a->seqs.end()) return PA_ERR_NO_SEQ;
+      if (it->second.len <= num_kept) continue;
+      for (int32_t j = 0; j < keep; ++j)
+        if (a->refcount[it->second.blocks[j]] > 1)
+          shared.emplace_back(static_cast<int32_t>(cut.size()), j);
+      cut.push_back(&it->second);
+    }
+    if (shared.size() > a->free_stack.size()) return PA_ERR_OOM;
+    // room for every block that may come back, so that nothing below can fail
+    a->free_stack.reserve(static_cast<size_t>(a->num_blocks));
+  } catch (...) {
+    return PA_ERR_OOM;
+  }
+  int status = PA_OK;
+  for (auto& s : shared) {  // the old block is left in `shared`, to be released below
+    int32_t& b = cut[s.first]->blocks[s.second];
+    const int32_t old = b;
+    b = a->take();
+    s.first = old;
+  }
+  for (const auto& s : shared)
+    if (!a->release(s.first)) status = PA_ERR_REFCOUNT;
+  for (pa_allocator::Seq* s : cut) {
+    while (static_cast<int32_t>(s->blocks.size()) > keep) {
+      if (!a->release(s->blocks.back())) status = PA_ERR_REFCOUNT;
+      s->blocks.pop_back();
+    }
+    s->len = num_kept;
+  }
+  return status;
+}
+
 extern "C" int pa_batch_block_tables(const pa_allocator* a, const int64_t* seqs, int32_t n,
                                      int32_t max_blocks, int32_t* tables, int32_t* seq_lens) {
   if (!a || n < 0 || max_blocks <= 0 || (n > 0 && (!seqs || !tables || !seq_lens)))

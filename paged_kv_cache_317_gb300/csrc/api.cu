@@ -19,7 +19,7 @@ extern "C" const char* pa_status_string(int status) {
     case PA_ERR_NO_SEQ: return "unknown sequence";
     case PA_ERR_SEQ_EXISTS: return "sequence already exists";
     case PA_ERR_REFCOUNT: return "allocator state inconsistent";
-    case PA_ERR_BAD_POSITION: return "rotary position out of range";
+    case PA_ERR_BAD_POSITION: return "position out of range";
     default: return "unknown status";
   }
 }

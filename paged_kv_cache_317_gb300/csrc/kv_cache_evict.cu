@@ -1,0 +1,181 @@
+// Eviction: the kept tokens of each key head move to the front of their sequence.
+//
+// Place j of (sequence, key head) takes the row of K, of V and the weight that place kept[j] held.
+// In place this is a gather within one array, safe in order: kept[j] >= j, so a row that is still to
+// be read (for place j' > j, from a place >= j') is never one that place j overwrites.  A thread
+// block, or for few rows a cluster, takes one (sequence, key head) and goes through its list in
+// rounds: every thread loads its pieces of the round's rows into registers, a barrier, every thread
+// stores them.  Loads of later rounds may run ahead of the stores of earlier ones; only the loads of
+// a round itself have to be over, which the barrier sees to.
+// A move and nothing else: bound by HBM for batches, by the chain list entry -> block -> row for one
+// sequence.
+#include <cuda_runtime.h>
+
+#include "cluster.cuh"
+#include "common.cuh"
+
+namespace pagedkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;     // 16-byte pieces of K, and as many of V, that a thread has in flight
+constexpr int kMaxCluster = 8;
+
+struct EvictParams {
+  uint4* k;
+  uint4* v;
+  const int32_t* tables;
+  const int32_t* new_tables;
+  const int32_t* seq_lens;
+  const int32_t* kept;
+  float* weights;
+  int32_t* err;
+  long long weights_row;   // floats from (sequence, key head) to the next
+  int num_kept, num_kv_heads, vecs, block_size, max_blocks, new_max_blocks, num_blocks;
+  int rows;                // rows of a round and thread block
+};
+
+__global__ void __launch_bounds__(kThreads, 4) kv_cache_evict_kernel(const EvictParams p) {
+  const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int sh = blockIdx.x / ranks;
+  const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
+  const bool first = rank == 0 && threadIdx.x == 0;
+  int L = p.seq_lens[seq];
+  const int cap = p.max_blocks * p.block_size;
+  if (L < 0 || L > cap) {
+    if (first && head == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
+    L = min(max(L, 0), cap);
+  }
+  const int32_t* kept = p.kept + static_cast<size_t>(sh) * p.num_kept;
+  const int32_t* table = p.tables + static_cast<size_t>(seq) * p.max_blocks;
+  const int32_t* new_table = p.new_tables + static_cast<size_t>(seq) * p.new_max_blocks;
+  float* weights = p.weights + sh * p.weights_row;
+  const int places = min(p.num_kept, L);
+
+  // the place that place j takes its row from, -1 if none
+  auto source = [&](int j, bool report) -> int {
+    const int s = kept[j];
+    if (s >= j && s < L) return s;
+    if (s != -1 && report) report_error(p.err, PA_ERR_BAD_POSITION, sh, s);
+    return s == -1 ? -1 : -2;
+  };
+  // the row of place j in the cache seen as rows of head_dim
+  auto row_of = [&](const int32_t* from, int blocks, int j, bool report) -> long long {
+    const int b = j / p.block_size;
+    const int blk = b < blocks ? from[b] : -1;
+    if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
+      if (report) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
+      return -1;
+    }
+    return (static_cast<long long>(blk) * p.num_kv_heads + head) * p.block_size + (j - b * p.block_size);
+  };
+
+  for (int j0 = rank * p.rows; j0 - rank * p.rows < places; j0 += ranks * p.rows) {
+    uint4 k[kPieces], v[kPieces];
+    long long to[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = threadIdx.x + u * kThreads, row = i / p.vecs, c = i - row * p.vecs;
+      const int j = j0 + row;
+      to[u] = -1;
+      if (row < p.rows && j < places) {
+        const int s = source(j, c == 0);
+        if (s >= 0) {
+          const long long src = row_of(table, p.max_blocks, s, c == 0);
+          const long long dst = row_of(new_table, p.new_max_blocks, j, c == 0);
+          if (src >= 0 && dst >= 0 && src != dst) {
+            k[u] = __ldcg(p.k + src * p.vecs + c);
+            v[u] = __ldcg(p.v + src * p.vecs + c);
+            to[u] = dst * p.vecs + c;
+          }
+        }
+      }
+    }
+    float w = 0.f;
+    int from = -2;
+    const int j = j0 + static_cast<int>(threadIdx.x);
+    if (p.weights != nullptr && threadIdx.x < p.rows && j < places) {
+      from = source(j, false);
+      if (from >= 0) w = __ldcg(weights + from);
+    }
+    if (ranks == 1) __syncthreads();
+    else cluster_sync();
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      if (to[u] >= 0) {
+        p.k[to[u]] = k[u];
+        p.v[to[u]] = v[u];
+      }
+    }
+    if (from >= -1 && from != j) weights[j] = w;
+  }
+  // every weight has been read
+  if (p.weights != nullptr)
+    for (int j = places + rank * kThreads + static_cast<int>(threadIdx.x); j < L; j += ranks * kThreads)
+      weights[j] = 0.f;
+}
+
+}  // namespace
+}  // namespace pagedkv
+
+using namespace pagedkv;
+
+extern "C" int kv_cache_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
+                              const int32_t* new_tables, const int32_t* seq_lens, const int32_t* kept,
+                              int num_kept, float* weights, int64_t weights_tokens, int num_seqs,
+                              int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                              int new_max_blocks, int num_blocks, int dtype, int32_t* error_record,
+                              void* stream) {
+  NvtxRange range("kv_cache_evict");
+  if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 ||
+      num_blocks <= 0 || num_kept <= 0 || (new_tables && new_max_blocks <= 0))
+    return PA_ERR_INVALID_ARG;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (head_dim % 8 != 0 || head_dim > 1024) return PA_ERR_UNSUPPORTED;
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+  if (cap > (1ll << 30) || num_seqs > 65535 || num_kept > (1 << 30) ||
+      static_cast<long long>(num_seqs) * num_kv_heads > (1ll << 27))
+    return PA_ERR_INVALID_ARG;
+  if (weights && weights_tokens < cap) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !kept) return PA_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+  EvictParams p{};
+  p.k = static_cast<uint4*>(k_cache);
+  p.v = static_cast<uint4*>(v_cache);
+  p.tables = block_tables;
+  p.new_tables = new_tables ? new_tables : block_tables;
+  p.new_max_blocks = new_tables ? new_max_blocks : max_blocks_per_seq;
+  p.seq_lens = seq_lens;
+  p.kept = kept;
+  p.weights = weights;
+  p.weights_row = weights_tokens;
+  p.err = error_record;
+  p.num_kept = num_kept;
+  p.num_kv_heads = num_kv_heads;
+  p.vecs = head_dim / 8;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  const int fit = kThreads * kPieces / p.vecs;
+  p.rows = fit < kThreads ? fit : kThreads;
+  // Few rows: clusters, as far as a round still has work for every block of them.
+  const long long lists = static_cast<long long>(num_seqs) * num_kv_heads;
+  const long long longest = num_kept < cap ? num_kept : cap;
+  int ranks = 1;
+  while (ranks < kMaxCluster && lists * ranks < 304 && longest > static_cast<long long>(ranks) * p.rows)
+    ranks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(lists * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kv_cache_evict_kernel, p) != cudaSuccess || cudaGetLastError() != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}

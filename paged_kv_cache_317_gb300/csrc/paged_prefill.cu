@@ -54,6 +54,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 #include "tma.cuh"
 
 namespace pagedkv {
@@ -101,6 +102,7 @@ struct Cfg {
   static_assert(kSmemBytes <= 227 * 1024, "one block per SM");
 };
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 // A row's exponentials are taken against a reference max that only moves when
 // the running max exceeds it by more than this (log2 units): p <= 2^8, exact in
 // fp32, and O is rescaled only then.
@@ -129,144 +131,15 @@ struct PrefillParams {
   int num_heads, block_size, max_blocks, num_blocks, out_dtype;
   int total_queries;  // rows of q and out
   float qscale;
+  // grouped: query heads per key head, tokens per tile, and ceil(2^16 / group): r / group is
+  // r * inv_group >> 16 for r < 128, group <= 128
+  int num_kv_heads, group, tile_tokens, inv_group;
+  float* lse;         // [total_queries][num_heads], or NULL
 };
 
-// ---------------------------------------------------------------- PTX helpers
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Shared-memory matrix descriptor (tcgen05): start, leading / stride byte
-// offsets (16-byte units), descriptor version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t smem_desc_sw128(const void* p, uint32_t lbo, uint32_t sbo) {
-  const uint32_t a = smem_addr(p);
-  uint64_t d = static_cast<uint64_t>((a >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= 1ull << 46;
-  d |= 2ull << 61;
-  return d;
-}
-
-// Instruction descriptor for kind::f16: fp32 accumulator, A and B both bf16 (or
-// both fp16), A K-major, B K-major or MN-major, shape M x N.
-__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool bf16, bool b_mn_major) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
-         ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Same, with A read from tensor memory (M rows = lanes, K values packed two per
-// 32-bit column).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-               : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-               : "memory");
-}
-
-// Two fp32 lanes at once (sm_100+ packed f32x2 arithmetic, round to nearest:
-// the same results as two scalar operations).
-__device__ __forceinline__ void fma2(float& y0, float& y1, float x0, float x1, float s, float c) {
-  asm("{\n\t.reg .b64 x, s, c, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
-      "mov.b64 c, {%5, %5};\n\tfma.rn.f32x2 d, x, s, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(y0), "=f"(y1)
-      : "f"(x0), "f"(x1), "f"(s), "f"(c));
-}
-
-__device__ __forceinline__ void add2(float& a0, float& a1, float x0, float x1) {
-  asm("{\n\t.reg .b64 a, x, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
-      "add.rn.f32x2 d, a, x;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(x0), "f"(x1));
-}
-
-// (y0, y1) = (a0 - b0, a1 - b1), one packed instruction, same rounding as scalar fp32.
-__device__ __forceinline__ void sub2(float& y0, float& y1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "sub.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(y0), "=f"(y1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
-// 2^x by the SFU's approximate base-2 exponential (PTX ex2.approx.ftz.f32;
-// relative error ~2^-22, 2^-inf = +0).
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// Two floats -> two 16-bit values (bf16 or fp16, round to nearest even), packed.
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  if constexpr (BF16) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  } else {
-    __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ float half_to_float(uint32_t bits16) {
-  if constexpr (BF16) {
-    return __uint_as_float(bits16 << 16);
-  } else {
-    __half h;
-    *reinterpret_cast<uint16_t*>(&h) = static_cast<uint16_t>(bits16);
-    return __half2float(h);
-  }
-}
-
 // One work item: 128-query tile `q0 / kQTile` of sequence `seq`, head `h`.
+// Grouped, `h` is a key head, the tile's rows are (token, query head of the key head), heads innermost,
+// and q0 and pos0 count tokens.
 struct Tile {
   int seq, h, q_begin, q0;
   int rows;  // valid query rows
@@ -280,14 +153,17 @@ struct Tile {
 // later (longer) query tiles of that sequence first, heads innermost.  Every
 // thread decodes the same items from the same device values, so all roles
 // agree on which items exist.
+template <bool kGrouped>
 __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int num_seqs,
                                             int num_qtiles, bool report) {
   Tile w;
   w.valid = false;
-  const int per_seq = p.num_heads * num_qtiles;
+  const int heads = kGrouped ? p.num_kv_heads : p.num_heads;
+  const int tile_tokens = kGrouped ? p.tile_tokens : kQTile;
+  const int per_seq = heads * num_qtiles;
   const int z = it / per_seq, rem = it % per_seq;
-  const int qt = num_qtiles - 1 - rem / p.num_heads;
-  w.h = rem % p.num_heads;
+  const int qt = num_qtiles - 1 - rem / heads;
+  w.h = rem % heads;
   int seq = z;
   if (p.seq_order != nullptr) {
     seq = __ldg(p.seq_order + z);
@@ -306,16 +182,17 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   const bool bad_len = L < 0 || L > cap;
   L = L < 0 ? 0 : (L > cap ? cap : L);
   const bool bad_q = nq < 0 || nq > L || w.q_begin < 0 || w.q_begin > p.total_queries - nq ||
-                     nq > num_qtiles * kQTile;
+                     nq > num_qtiles * tile_tokens;
   if (bad_len || bad_q) {
     if (report && rem == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     if (bad_q) return w;
   }
-  w.q0 = qt * kQTile;
+  w.q0 = qt * tile_tokens;
   if (w.q0 >= nq) return w;
-  w.rows = min(kQTile, nq - w.q0);
+  const int tokens = min(tile_tokens, nq - w.q0);
+  w.rows = kGrouped ? tokens * p.group : tokens;
   w.pos0 = L - nq + w.q0;
-  w.keys = w.pos0 + w.rows;
+  w.keys = w.pos0 + tokens;
   w.T = (w.keys + kKTile - 1) / kKTile;
   w.valid = true;
   return w;
@@ -328,7 +205,7 @@ __device__ __forceinline__ int item_of(int r) {
   return r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -379,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int n_items = num_seqs * p.num_heads * num_qtiles;
+  const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
+  const int n_items = num_seqs * kv_heads * num_qtiles;
 
   // Key tiles are counted across the block's items: tile g of the block uses K
   // and V stage g & 1 and S/P buffer g & 1, and its barriers' phases are g >> 1.
@@ -392,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     bool ok = true;
     for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-      const Tile w = decode_tile(p, it, num_seqs, num_qtiles, !is_v && lane == 0);
+      const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, !is_v && lane == 0);
       if (!w.valid) continue;
       const int32_t* table = p.block_tables + static_cast<size_t>(w.seq) * p.max_blocks;
       int blk = 0, blk_hi = 0;
@@ -457,12 +335,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           const int c = lane - (j & 7) * 4;
           const int k0 = j * kKTile + c * 16;
           if (c >= 0 && c < 4 && k0 < w.keys) {
-            const int row = (blk * p.num_heads + w.h) * p.block_size + k0 % p.block_size;
+            const int row = (blk * kv_heads + w.h) * p.block_size + k0 % p.block_size;
 #pragma unroll
             for (int gr = 0; gr < C::kGroups; ++gr)
               tma_load_2d(dst + gr * kHalfBytes + c * 2048, map, 64 * gr, row, full);
             if (half_blocks && k0 + 8 < w.keys) {
-              const int row_hi = (blk_hi * p.num_heads + w.h) * p.block_size;
+              const int row_hi = (blk_hi * kv_heads + w.h) * p.block_size;
 #pragma unroll
               for (int gr = 0; gr < C::kGroups; ++gr)
                 tma_load_2d(dst + gr * kHalfBytes + c * 2048 + 1024, map, 64 * gr, row_hi, full);
@@ -476,11 +354,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           if (lane == 0) {
             if (q_issued > 0) good = mbar_wait_bounded(&bars->q_empty, (q_issued - 1) & 1);
             if (good) {
-              mbar_arrive_expect_tx(&bars->q_full, C::kQBytes);
+              // (grouped, the rows of the tile past its tokens' heads keep what they held: they are
+              // masked, and rows of a product do not mix)
+              const uint32_t q_bytes =
+                  kGrouped ? C::kGroups * 128u * p.tile_tokens * p.group : C::kQBytes;
+              mbar_arrive_expect_tx(&bars->q_full, q_bytes);
 #pragma unroll
               for (int gr = 0; gr < C::kGroups; ++gr)
-                tma_load_3d(Qs + gr * kQHalfBytes, &tm_q, 64 * gr, w.h, w.q_begin + w.q0,
-                            &bars->q_full);
+                tma_load_3d(Qs + gr * kQHalfBytes, &tm_q, 64 * gr, kGrouped ? w.h * p.group : w.h,
+                            w.q_begin + w.q0, &bars->q_full);
             }
           }
           good = __shfl_sync(kFullMask, good, 0);
@@ -514,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       int g = 0, items = 0;
       bool ok = true;
       for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-        const Tile w = decode_tile(p, it, num_seqs, num_qtiles, false);
+        const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, false);
         if (!w.valid) continue;
         if (!mbar_wait_bounded(&bars->q_full, items & 1)) {
           ok = false;
@@ -588,10 +470,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     int g = 0;
     bool ok = true;
     for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-      const Tile w = decode_tile(p, it, num_seqs, num_qtiles, false);
+      const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, false);
       if (!w.valid) continue;
       const bool row_valid = r < w.rows;
-      const int pos = row_valid ? w.pos0 + r : -1;
+      const int token = kGrouped ? r * p.inv_group >> 16 : r;  // of the tile
+      const int pos = row_valid ? w.pos0 + token : -1;
       float m_ref = -INFINITY, l = 0.f;  // reference max (log2 units) and running sum
       for (int j = 0; j < w.T; ++j) {
         const int gg = g + j, b = gg & 1;
@@ -720,9 +603,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       // neither side has bank conflicts.
       const int esz = p.out_dtype == PA_F32 ? 4 : 2;
       const size_t row_bytes = static_cast<size_t>(p.num_heads) * D * esz;
+      const int first_head = kGrouped ? w.h * p.group : w.h, first = kGrouped ? 0 : warp * 32;
       char* out_warp = static_cast<char*>(p.out) +
-                       (static_cast<size_t>(w.q_begin + w.q0 + warp * 32) * p.num_heads + w.h) *
+                       (static_cast<size_t>(w.q_begin + w.q0 + first) * p.num_heads + first_head) *
                            D * esz;
+      // where the warp's row begins, from out_warp
+      auto row_at = [&](int row) -> size_t {
+        if constexpr (kGrouped) {
+          const int rr = warp * 32 + row, t = rr * p.inv_group >> 16;
+          return t * row_bytes + static_cast<size_t>(rr - t * p.group) * (D * esz);
+        } else {
+          return row * row_bytes;
+        }
+      };
+      if constexpr (kGrouped) {
+        if (p.lse != nullptr && row_valid)  // ln of the sum of e^logit
+          p.lse[static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + first_head +
+                (r - token * p.group)] = (m_ref + log2f(l)) * kLn2;
+      }
       const int warp_rows = w.rows - warp * 32;  // this warp's valid rows (may be <= 0)
       uint8_t* stage = smem + C::kOffStage + warp * 2048;
       auto put = [&](const uint4 (&v)[4], int col_byte) {
@@ -734,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
         for (int i = 0; i < 4; ++i) {
           const int idx = lane + 32 * i, row = idx >> 2, k = idx & 3;
           if (row < warp_rows)
-            *reinterpret_cast<uint4*>(out_warp + row * row_bytes + col_byte + k * 16) =
+            *reinterpret_cast<uint4*>(out_warp + row_at(row) + col_byte + k * 16) =
                 *reinterpret_cast<const uint4*>(stage + row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
         }
         __syncwarp();
@@ -811,28 +709,60 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
 // The kernel always needs opt-in shared memory.  The attribute belongs to the
 // module loaded in the current context and is lost with it (cudaDeviceReset,
 // another driver-API context), so it is set on every launch.
-template <bool BF16, int D>
+template <bool BF16, int D, bool kGrouped>
 cudaError_t ensure_prefill_smem() {
-  return cudaFuncSetAttribute(paged_prefill_kernel<BF16, D>,
+  return cudaFuncSetAttribute(paged_prefill_kernel<BF16, D, kGrouped>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool kGrouped>
 int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const PrefillParams& p, int num_seqs, int num_qtiles, cudaStream_t st) {
-  if (ensure_prefill_smem<BF16, D>() != cudaSuccess) return PA_ERR_CUDA;
+  if (ensure_prefill_smem<BF16, D, kGrouped>() != cudaSuccess) return PA_ERR_CUDA;
   // Persistent: one block per resident slot (Cfg<D>::kMinBlocks per SM), each
   // looping over its share of the (sequence, query tile, head) items.
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_CUDA;
-  const long long items = static_cast<long long>(num_seqs) * p.num_heads * num_qtiles;
+  const long long items =
+      static_cast<long long>(num_seqs) * (kGrouped ? p.num_kv_heads : p.num_heads) * num_qtiles;
   const long long slots = static_cast<long long>(sms) * Cfg<D>::kMinBlocks;
   const unsigned grid = static_cast<unsigned>(items < slots ? items : slots);
-  paged_prefill_kernel<BF16, D>
+  paged_prefill_kernel<BF16, D, kGrouped>
       <<<grid, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, tv, p, num_seqs, num_qtiles);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The tensor maps of a call, and its launch.  A box of the cache is one 16-key chunk, or half of one
+// with 8-token blocks; a box of q the rows of a tile, 64 channels wide.
+template <bool kGrouped>
+int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, const void* v_cache,
+                unsigned long long cache_rows, int num_seqs, int head_dim, int num_qtiles, bool bf16,
+                cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(head_dim),
+                               static_cast<cuuint64_t>(p.num_heads),
+                               static_cast<cuuint64_t>(p.total_queries)};
+  const cuuint64_t qstr[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                              static_cast<cuuint64_t>(head_dim) * 2 * p.num_heads};
+  const cuuint32_t qbox[3] = {64, kGrouped ? static_cast<cuuint32_t>(p.group) : 1u,
+                              kGrouped ? static_cast<cuuint32_t>(p.tile_tokens) : kQTile};
+  const cuuint64_t cdims[2] = {static_cast<cuuint64_t>(head_dim), cache_rows};
+  const cuuint64_t cstr[1] = {static_cast<cuuint64_t>(head_dim) * 2};
+  const cuuint32_t cbox[2] = {64, p.block_size >= 16 ? 16u : 8u};
+  if (!encode_tensor_map(&tq, bf16, q, 3, qdims, qstr, qbox) ||
+      !encode_tensor_map(&tk, bf16, k_cache, 2, cdims, cstr, cbox) ||
+      !encode_tensor_map(&tv, bf16, v_cache, 2, cdims, cstr, cbox))
+    return PA_ERR_CUDA;
+  switch ((bf16 ? 1 : 0) | (head_dim == 64 ? 0 : head_dim == 128 ? 2 : 4)) {
+    case 0: return launch_prefill<false, 64, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 1: return launch_prefill<true, 64, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 2: return launch_prefill<false, 128, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 3: return launch_prefill<true, 128, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 4: return launch_prefill<false, 256, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    default: return launch_prefill<true, 256, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+  }
 }
 
 }  // namespace
@@ -887,23 +817,6 @@ extern "C" int paged_attn_prefill_ex(const void* q, const int32_t* query_start,
   if (static_cast<long long>(num_seqs) * num_heads * qtiles >= (1ll << 30))
     return PA_ERR_INVALID_ARG;
 
-  const bool bf16 = dtype == PA_BF16;
-  CUtensorMap tq, tk, tv;
-  const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(head_dim),
-                               static_cast<cuuint64_t>(num_heads),
-                               static_cast<cuuint64_t>(total_queries)};
-  const cuuint64_t qstr[2] = {static_cast<cuuint64_t>(head_dim) * 2,
-                              static_cast<cuuint64_t>(head_dim) * 2 * num_heads};
-  const cuuint32_t qbox[3] = {64, 1, kQTile};
-  const cuuint64_t cdims[2] = {static_cast<cuuint64_t>(head_dim), cache_rows};
-  const cuuint64_t cstr[1] = {static_cast<cuuint64_t>(head_dim) * 2};
-  // a box is one 16-key chunk, or half of one with 8-token blocks
-  const cuuint32_t cbox[2] = {64, block_size >= 16 ? 16u : 8u};
-  if (!encode_tensor_map(&tq, bf16, q, 3, qdims, qstr, qbox) ||
-      !encode_tensor_map(&tk, bf16, k_cache, 2, cdims, cstr, cbox) ||
-      !encode_tensor_map(&tv, bf16, v_cache, 2, cdims, cstr, cbox))
-    return PA_ERR_CUDA;
-
   PrefillParams p{};
   p.seq_order = opts ? opts->seq_order : nullptr;
   p.query_start = query_start;
@@ -919,13 +832,63 @@ extern "C" int paged_attn_prefill_ex(const void* q, const int32_t* query_start,
   p.total_queries = total_queries;
   p.qscale = scale * kLog2e;
 
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  switch ((bf16 ? 1 : 0) | (head_dim == 64 ? 0 : head_dim == 128 ? 2 : 4)) {
-    case 0: return launch_prefill<false, 64>(tq, tk, tv, p, num_seqs, qtiles, st);
-    case 1: return launch_prefill<true, 64>(tq, tk, tv, p, num_seqs, qtiles, st);
-    case 2: return launch_prefill<false, 128>(tq, tk, tv, p, num_seqs, qtiles, st);
-    case 3: return launch_prefill<true, 128>(tq, tk, tv, p, num_seqs, qtiles, st);
-    case 4: return launch_prefill<false, 256>(tq, tk, tv, p, num_seqs, qtiles, st);
-    default: return launch_prefill<true, 256>(tq, tk, tv, p, num_seqs, qtiles, st);
-  }
+  return run_prefill<false>(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, qtiles,
+                            dtype == PA_BF16, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int total_queries,
+                                int max_query_len, const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                                int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                int max_blocks_per_seq, int num_blocks, float scale, int dtype,
+                                void* out, int out_dtype, float* lse, const int32_t* seq_order,
+                                int32_t* error_record, void* stream) {
+  NvtxRange range("paged_attn_chunk");
+  if (num_seqs < 0 || total_queries < 0 || max_query_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+      num_heads % num_kv_heads != 0 || block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return PA_ERR_INVALID_ARG;
+  const int group = num_heads / num_kv_heads;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      (block_size % 16 != 0 && block_size != 8) || group > kQTile)
+    return PA_ERR_UNSUPPORTED;
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (out_dtype != PA_F16 && out_dtype != PA_BF16 && out_dtype != PA_F32)
+    return PA_ERR_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+  const unsigned long long cache_rows =
+      static_cast<unsigned long long>(num_blocks) * num_kv_heads * block_size;
+  const int tile_tokens = kQTile / group;
+  const long long qtiles = (static_cast<long long>(max_query_len) + tile_tokens - 1) / tile_tokens;
+  // items are numbered in an int inside the kernel (with a grid's worth of headroom)
+  if (cache_rows >= (1ull << 31) ||
+      static_cast<long long>(max_blocks_per_seq) * block_size > (1ll << 30) ||
+      static_cast<long long>(num_seqs) * num_kv_heads * qtiles >= (1ll << 30))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_queries == 0 || max_query_len == 0) return PA_OK;
+  if (!q || !query_start || !k_cache || !v_cache || !block_tables || !seq_lens || !out)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return PA_ERR_INVALID_ARG;
+  PrefillParams p{};
+  p.seq_order = seq_order;
+  p.query_start = query_start;
+  p.seq_lens = seq_lens;
+  p.block_tables = block_tables;
+  p.out = out;
+  p.err = error_record;
+  p.num_heads = num_heads;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.out_dtype = out_dtype;
+  p.total_queries = total_queries;
+  p.qscale = scale * kLog2e;
+  p.num_kv_heads = num_kv_heads;
+  p.group = group;
+  p.tile_tokens = tile_tokens;
+  p.inv_group = (65536 + group - 1) / group;
+  p.lse = lse;
+  return run_prefill<true>(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim,
+                           static_cast<int>(qtiles), dtype == PA_BF16,
+                           static_cast<cudaStream_t>(stream));
 }
