@@ -5,15 +5,17 @@
 // with the rows' lse from the chunk's attention, so one pass over the keys does.
 //
 //  * Work item = (sequence, key head, 256 tokens).  S^T = K.Q^T: the tokens are the rows of the product
-//    (TMEM lanes), so that a token's sum over rows is one thread's.  Two warpgroups take 128 tokens each;
+//    (TMEM lanes), so that a token's sum over rows is one thread's.  Two warpgroups take 128 tokens each
+//    (of every 16 the first and the last 8: a box of 16 rows then is one copy, whatever head_dim);
 //    the query rows, (token, head) packed 128 to a tile, go by as columns.  Every token is one thread's of
 //    one item: no atomics, the same bits on every run.
 //  * Persistent, one thread block an SM.  The items that exist are counted from the lengths, so that none
 //    is dealt out in vain.  Where the window's tiles stay in shared memory a block takes a contiguous run
 //    of items and loads them once a key head; else block b takes items b, b + grid, ...: heads innermost,
 //    so that the items of a causal triangle are shared out alike.
-//  * 10 warps: two softmax warpgroups, a producer (TMA boxes of 16 rows of K through the block table, boxes
-//    of whole tiles of Q), an issuer of the products.  Each warpgroup has two 128-column buffers of S in
+//  * 11 warps: two softmax warpgroups, a producer (TMA boxes of 16 rows of K through the block table, boxes
+//    of whole tiles of Q), an issuer of products for each warpgroup (one thread issues a product in about
+//    the time that it runs, and has barriers to wait for besides).  Each warpgroup has two 128-column buffers of S in
 //    TMEM: one is read while the next product runs.
 //  * Masks only where a tile of rows meets tokens that some of its rows do not see, or ends short.
 //  * Every wait is bounded (one second); on a timeout the block records PA_ERR_TIMEOUT, waits (bounded) for
@@ -23,6 +25,7 @@
 
 #include <cmath>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
@@ -33,21 +36,24 @@ namespace {
 constexpr int kHalf = 128;                 // tokens of a warpgroup (MMA M)
 constexpr int kTokens = 2 * kHalf;         // of an item
 constexpr int kRows = 128;                 // query rows of a tile (MMA N)
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 320;
-constexpr int kLists = 128;                // runs of sequences whose items are counted together
+constexpr int kWarpLoad = 8, kWarpMma = 9;  // and 10: an issuer for each warpgroup
+constexpr int kThreads = 352;
+constexpr int kMaxCluster = 8;
+constexpr int kLists = 128;                // lists of sequences whose items are counted together
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct Cfg {
-  static constexpr int kGroups = D / 64;                  // 64-wide column groups, 128 bytes a row
+  static constexpr int kWide = D / 64;                    // 64-wide column groups, 128 bytes a row
   static constexpr int kKBytes = kTokens * D * 2;         // 32 / 64 / 128 KB
+  static constexpr int kChunkBytes = 16 * D * 2;          // a box: 16 tokens of K
   static constexpr int kQBytes = kRows * D * 2;           // 16 / 32 / 64 KB
   static constexpr int kKStages = D <= 128 ? 2 : 1;
   static constexpr int kQStages = D <= 128 ? 2 : 1;
   static constexpr int kOffQ = kKStages * kKBytes;
   static constexpr int kOffLse = kOffQ + kQStages * kQBytes;       // [warpgroup][2][kRows] floats
-  static constexpr int kOffCount = kOffLse + 4 * kRows * 4;        // [kLists] ints
+  static constexpr int kOffSums = kOffLse + 2 * 2 * kRows * 4;  // [2][kMaxCluster][kTokens] floats
+  static constexpr int kOffCount = kOffSums + 2 * kMaxCluster * kTokens * 4;  // [kLists] ints
   static constexpr int kOffBar = kOffCount + kLists * 4;
   static constexpr int kUsed = kOffBar + 256 + 1024;               // 1 KB to align the base
   // one block an SM, which takes all 512 TMEM columns
@@ -57,8 +63,9 @@ struct Cfg {
 
 struct Bars {
   uint64_t k_full[2], k_free[2], q_full[2], q_free[2];
-  uint64_t s_full[2][2], s_free[2][2];  // [warpgroup][buffer]
-  uint64_t drain;
+  uint64_t s_full[2][2], s_free[2][2];  // [buffer][warpgroup]
+  uint64_t sums_full[2], sums_free[2];  // the cluster's sums of even and odd items: all there; read
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -104,81 +111,114 @@ __device__ __forceinline__ int tiles_of(const Seq& s) {
   return s.W > 0 ? (s.L + kTokens - 1) / kTokens : 0;
 }
 
-struct Item {
+// Items of one key head: its token tiles from `tile` to before `end`.
+struct Run {
   Seq s;
-  int seq, head, t0;
-  int first, tiles;  // tiles of query rows: the first that sees a token of the item, and their number
+  int seq, head, tile, end;
+  int row_tiles;  // tiles of query rows
+
+  // The first tile of rows that sees a token of the tile at t0.
+  __device__ __forceinline__ int first(const ChunkWeightsParams& p, int t0) const {
+    const int before = s.L - s.W;
+    return t0 > before ? (t0 - before) / p.tile_tokens : 0;
+  }
 };
 
-// The items of a thread block, decoded alike by every warp.
+// The items of a thread block or cluster, b of n, decoded alike by every warp.  All of them look up what
+// is next only from run to run: the loops over a run's items have to be small, for code that every role
+// goes through once an item costs a fetch of instructions each time.
 struct Walk {
   const ChunkWeightsParams& p;
-  const int* upto;   // [kLists]: items of the first runs of sequences
-  int run;           // sequences of a run
+  const int* upto;  // [kLists]: items of the first lists of sequences
+  int list;         // sequences of a list
   int m, end, step;
-  Item it;
-  int seq_begin, seq_items;  // the items of it.seq
+  Run run;
 
-  __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, int run)
-      : p(p), upto(upto), run(run), seq_begin(0), seq_items(0) {
+  __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, int list, int b, int n)
+      : p(p), upto(upto), list(list) {
     const long long all = upto[kLists - 1];
-    const int b = static_cast<int>(blockIdx.x), n = static_cast<int>(gridDim.x);
-    step = p.resident ? 1 : n;
+    step = n;
     m = p.resident ? static_cast<int>(all * b / n) : b;
     end = p.resident ? static_cast<int>(all * (b + 1) / n) : static_cast<int>(all);
   }
 
-  // The next item; false past the last.  By whole warps.
+  // The next run; false past the last.  By whole warps.
   __device__ __forceinline__ bool next() {
     if (m >= end) return false;
     const int lane = threadIdx.x & 31;
-    if (m - seq_begin >= seq_items) {
-      const int4 u = reinterpret_cast<const int4*>(upto)[lane];
-      const int r = __reduce_add_sync(kFullMask, (u.x <= m) + (u.y <= m) + (u.z <= m) + (u.w <= m));
-      int left = m - (r > 0 ? upto[r - 1] : 0);
-      for (int s0 = r * run;; s0 += 32) {
-        const int seq = s0 + lane;
-        Seq s{0, 0, 0};
-        if (seq < min(p.num_seqs, (r + 1) * run)) s = sequence(p, seq, false);
-        const int items = tiles_of(s) * p.num_kv_heads;
-        int sum = items;
+    const int4 u = reinterpret_cast<const int4*>(upto)[lane];
+    const int r = __reduce_add_sync(kFullMask, (u.x <= m) + (u.y <= m) + (u.z <= m) + (u.w <= m));
+    int left = m - (r > 0 ? upto[r - 1] : 0);
+    const int last = min(p.num_seqs, (r + 1) * list);
+    for (int s0 = r * list; s0 < last; s0 += 32) {
+      const int seq = s0 + lane;
+      Seq s{0, 0, 0};
+      if (seq < last) s = sequence(p, seq, false);
+      const int items = tiles_of(s) * p.num_kv_heads;
+      int sum = items;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int v = __shfl_up_sync(kFullMask, sum, off);
-          if (lane >= off) sum += v;
-        }
-        const unsigned past = __ballot_sync(kFullMask, sum > left);
-        if (past != 0) {
-          const int at = __ffs(past) - 1;
-          it.seq = s0 + at;
-          it.s.L = __shfl_sync(kFullMask, s.L, at);
-          it.s.W = __shfl_sync(kFullMask, s.W, at);
-          it.s.row0 = __shfl_sync(kFullMask, s.row0, at);
-          seq_items = __shfl_sync(kFullMask, items, at);
-          seq_begin = m - (left - __shfl_sync(kFullMask, sum - items, at));
-          break;
-        }
-        left -= __shfl_sync(kFullMask, sum, 31);
-        if (s0 + 32 >= (r + 1) * run) return false;  // (not reached: the counts say there is one)
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(kFullMask, sum, off);
+        if (lane >= off) sum += v;
       }
+      const unsigned past = __ballot_sync(kFullMask, sum > left);
+      if (past != 0) {
+        const int at = __ffs(past) - 1;
+        run.seq = s0 + at;
+        run.s.L = __shfl_sync(kFullMask, s.L, at);
+        run.s.W = __shfl_sync(kFullMask, s.W, at);
+        run.s.row0 = __shfl_sync(kFullMask, s.row0, at);
+        run.row_tiles = (run.s.W + p.tile_tokens - 1) / p.tile_tokens;
+        left -= __shfl_sync(kFullMask, sum - items, at);
+        break;
+      }
+      left -= __shfl_sync(kFullMask, sum, 31);
     }
-    const int at = m - seq_begin;
-    int tile;
-    if (p.resident) {
-      const int tiles = seq_items / p.num_kv_heads;
-      it.head = at / tiles;
-      tile = at - it.head * tiles;
-    } else {
-      tile = at / p.num_kv_heads;
-      it.head = at - tile * p.num_kv_heads;
+    if (p.resident) {  // a key head's tokens one after the other
+      const int tiles = tiles_of(run.s);
+      run.head = left / tiles;
+      run.tile = left - run.head * tiles;
+      run.end = min(tiles, run.tile + end - m);
+      m += run.end - run.tile;
+    } else {           // heads innermost
+      run.tile = left / p.num_kv_heads;
+      run.head = left - run.tile * p.num_kv_heads;
+      run.end = run.tile + 1;
+      m += step;
     }
-    it.t0 = tile * kTokens;
-    it.tiles = (it.s.W + p.tile_tokens - 1) / p.tile_tokens;
-    it.first = max(0, it.t0 - (it.s.L - it.s.W)) / p.tile_tokens;
-    m += step;
     return true;
   }
 };
+
+// e^(logit - lse) of 32 columns of S, added to the four sums; nl: shared address of -lse in base 2.
+__device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, float qscale, float (&sum)[4]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const float4 v = ld_shared4(nl + 4 * c);
+    float x0, x1, x2, x3;
+    fma2(x0, x1, s[c], s[c + 1], qscale, v.x, v.y);
+    fma2(x2, x3, s[c + 2], s[c + 3], qscale, v.z, v.w);
+    add2(sum[0], sum[1], ex2_approx(x0), ex2_approx(x1));
+    add2(sum[2], sum[3], ex2_approx(x2), ex2_approx(x3));
+  }
+}
+
+// The same for the columns c0 + c < cols whose token, c / group tokens after the tile's first, is not
+// before this thread's, `ahead` after it.  Others may hold anything.
+__device__ __forceinline__ void add_seen_weights(const float (&s)[32], uint32_t nl, float qscale, int c0, int cols,
+                                                 int ahead, int inv_group, float (&sum)[4]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const float4 v = ld_shared4(nl + 4 * c);
+    const float l[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = ex2_approx(fmaf(s[c + i], qscale, l[i]));
+      const int col = c0 + c + i;
+      sum[i] += col < cols && ahead <= (col * inv_group >> 16) ? e : 0.f;
+    }
+  }
+}
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -194,19 +234,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
   const bool half_blocks = p.block_size < 16;
+  const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_free[s], 1);
+      mbar_init(&bars->k_free[s], 2);  // both issuers
       mbar_init(&bars->q_full[s], 1);
-      mbar_init(&bars->q_free[s], 1);
-      for (int g = 0; g < 2; ++g) {
-        mbar_init(&bars->s_full[g][s], 1);
-        mbar_init(&bars->s_free[g][s], kHalf);
-      }
+      mbar_init(&bars->q_free[s], 2);
+      mbar_init(&bars->drain[s], 1);
+      mbar_init(&bars->sums_full[s], ranks > 1 ? (ranks - 1) * kTokens : 1);
+      mbar_init(&bars->sums_free[s], kTokens);
     }
-    mbar_init(&bars->drain, 1);
+    for (int g = 0; g < 4; ++g) {
+      mbar_init(&bars->s_full[g >> 1][g & 1], 1);
+      mbar_init(&bars->s_free[g >> 1][g & 1], kHalf);
+    }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -219,11 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // The items of each run of sequences, then those of all runs up to each.
-  const int run = (p.num_seqs + kLists - 1) / kLists;
+  // The items of each list of sequences, then those of all lists up to each.
+  const int list = (p.num_seqs + kLists - 1) / kLists;
   if (threadIdx.x < kLists) {
     int sum = 0;
-    for (int s = threadIdx.x * run; s < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * run); ++s)
+    for (int s = threadIdx.x * list; s < min(p.num_seqs, (static_cast<int>(threadIdx.x) + 1) * list); ++s)
       sum += tiles_of(sequence(p, s, blockIdx.x == 0)) * p.num_kv_heads;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -241,137 +284,131 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (ranks > 1) cluster_sync();  // peers' barriers are set up
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  Walk walk(p, upto, run);
-  const Item& it = walk.it;
+  Walk walk(p, upto, list, static_cast<int>(blockIdx.x) / ranks, static_cast<int>(gridDim.x) / ranks);
+  const Run& run = walk.run;
 
   int k_loads = 0, q_loads = 0;  // producer, issuer: tiles begun so far
   int mma_started = 0;
   if (warp == kWarpLoad) {
     // --------------------------------------------------------------- producer
+    int good = 1;
+    auto load_q = [&](int j) -> bool {
+      const int qs = q_loads % QS;
+      if (lane == 0) {
+        if (q_loads >= QS) good = mbar_wait_bounded(&bars->q_free[qs], (q_loads / QS - 1) & 1);
+        if (good) {
+          mbar_arrive_expect_tx(&bars->q_full[qs], C::kWide * 128u * p.tile_tokens * p.group);
+#pragma unroll
+          for (int g = 0; g < C::kWide; ++g)
+            tma_load_3d(smem + C::kOffQ + qs * C::kQBytes + g * (kRows * 128), &tm_q, 64 * g,
+                        run.head * p.group, run.s.row0 + j * p.tile_tokens, &bars->q_full[qs]);
+        }
+      }
+      ++q_loads;
+      return __shfl_sync(kFullMask, good, 0) != 0 && __shfl_sync(kFullMask, *abort_flag, 0) == 0;
+    };
     bool ok = true;
-    int held_seq = -1, held_head = -1;  // whose tiles of query rows are in shared memory
     while (ok && walk.next()) {
-      const int32_t* table = p.block_tables + static_cast<size_t>(it.seq) * p.max_blocks;
-      const int tokens = min(kTokens, it.s.L - it.t0);
-      // lane l < 16: the block of tokens t0 + 16 l on (with 8-token blocks also of the 8 after)
-      int y = 0, y_hi = 0;
-      auto y_of = [&](int t) {
+      const int32_t* table = p.block_tables + static_cast<size_t>(run.seq) * p.max_blocks;
+      // lane l < 16 of a tile: the block of tokens t0 + 16 l on (with 8-token blocks also of the 8 after),
+      // as a row of the cache seen as rows of D
+      auto y_of = [&](int t) -> int {
+        if (t >= run.s.L) return -1;
         const int b = t / p.block_size;
         int blk = __ldg(table + b);
         if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-          if (it.head == 0 && (t == b * p.block_size)) report_error(p.err, PA_ERR_BAD_BLOCK, it.seq, blk);
+          if (run.head == 0 && rank == 0 && t == b * p.block_size)
+            report_error(p.err, PA_ERR_BAD_BLOCK, run.seq, blk);
           blk = 0;
         }
-        return (blk * p.num_kv_heads + it.head) * p.block_size + (t - b * p.block_size);
+        return (blk * p.num_kv_heads + run.head) * p.block_size + (t - b * p.block_size);
       };
-      const bool mine = lane * 16 < tokens, mine_hi = half_blocks && lane * 16 + 8 < tokens;
-      if (lane < 16) {
-        if (mine) y = y_of(it.t0 + lane * 16);
-        if (mine_hi) y_hi = y_of(it.t0 + lane * 16 + 8);
-      }
-      const int ks = k_loads % KS;
-      int good = 1;
-      if (lane == 0) {
-        if (k_loads >= KS) good = mbar_wait_bounded(&bars->k_free[ks], (k_loads / KS - 1) & 1);
-        const int unit = half_blocks ? 8 : 16;
-        const int rows = (tokens + unit - 1) / unit * unit;
-        if (good) mbar_arrive_expect_tx(&bars->k_full[ks], static_cast<uint32_t>(rows) * D * 2);
-      }
-      ok = __shfl_sync(kFullMask, good, 0);
-      if (!ok) break;
-      if (lane < 16) {
-        uint8_t* dst = smem + ks * C::kKBytes + lane * 2048;
-#pragma unroll
-        for (int g = 0; g < C::kGroups; ++g) {
-          if (mine) tma_load_2d(dst + g * (kTokens * 128), &tm_k, 64 * g, y, &bars->k_full[ks]);
-          if (mine_hi) tma_load_2d(dst + g * (kTokens * 128) + 1024, &tm_k, 64 * g, y_hi, &bars->k_full[ks]);
+      bool with_q = p.resident != 0;
+      for (int tile = run.tile; ok && tile < run.end; ++tile) {
+        const int t0 = tile * kTokens;
+        const int j0 = p.resident ? 0 : run.first(p, t0) + rank;
+        if (j0 >= run.row_tiles) break;  // other blocks of the cluster have its tiles
+        int y = -1, y_hi = -1;
+        if (lane < 16) {
+          y = y_of(t0 + lane * 16);
+          if (half_blocks) y_hi = y_of(t0 + lane * 16 + 8);
         }
-      }
-      ++k_loads;
-      if (!p.resident || it.seq != held_seq || it.head != held_head) {
-        held_seq = it.seq;
-        held_head = it.head;
-        for (int j = p.resident ? 0 : it.first; ok && j < it.tiles; ++j) {
-          const int qs = q_loads % QS;
-          if (lane == 0) {
-            if (q_loads >= QS) good = mbar_wait_bounded(&bars->q_free[qs], (q_loads / QS - 1) & 1);
-            if (good) {
-              mbar_arrive_expect_tx(&bars->q_full[qs], C::kGroups * 128u * p.tile_tokens * p.group);
-#pragma unroll
-              for (int g = 0; g < C::kGroups; ++g)
-                tma_load_3d(smem + C::kOffQ + qs * C::kQBytes + g * (kRows * 128), &tm_q, 64 * g,
-                            it.head * p.group, it.s.row0 + j * p.tile_tokens, &bars->q_full[qs]);
-            }
-          }
-          ok = __shfl_sync(kFullMask, good, 0);
-          if (ok) ++q_loads;
-          if (__shfl_sync(kFullMask, *abort_flag, 0)) ok = false;
+        const int ks = k_loads % KS;
+        if (lane == 0) {
+          if (k_loads >= KS) good = mbar_wait_bounded(&bars->k_free[ks], (k_loads / KS - 1) & 1);
+          const int unit = half_blocks ? 8 : 16;
+          const int rows = (min(kTokens, run.s.L - t0) + unit - 1) / unit * unit;
+          if (good) mbar_arrive_expect_tx(&bars->k_full[ks], static_cast<uint32_t>(rows) * D * 2);
         }
+        ok = __shfl_sync(kFullMask, good, 0) != 0;
+        if (!ok) break;
+        uint8_t* dst = smem + ks * C::kKBytes + lane * C::kChunkBytes;
+        if (y >= 0) tma_load_3d(dst, &tm_k, 0, y, 0, &bars->k_full[ks]);
+        if (y_hi >= 0) tma_load_3d(dst + C::kChunkBytes / 2, &tm_k, 0, y_hi, 0, &bars->k_full[ks]);
+        ++k_loads;
+        if (__shfl_sync(kFullMask, *abort_flag, 0)) ok = false;
+        if (!p.resident || with_q)
+          for (int j = j0; ok && j < run.row_tiles; j += ranks) ok = load_q(j);
+        with_q = false;
       }
-      if (__shfl_sync(kFullMask, *abort_flag, 0)) ok = false;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
-      report_error(p.err, PA_ERR_TIMEOUT, it.seq, -1);
+      report_error(p.err, PA_ERR_TIMEOUT, run.seq, -1);
     }
-  } else if (warp == kWarpMma) {
-    // ----------------------------------------------------------------- issuer
+  } else if (warp >= kWarpMma) {
+    // ----------------------------------------------------- issuers, one a warpgroup
+    const int g = warp - kWarpMma;
     constexpr uint32_t idesc = make_idesc(kHalf, kRows, BF16, false);
-    const uint64_t k_desc = smem_desc_sw128(smem, 16, 1024);
+    // K: the same 8 rows of each of 16 chunks, one product's; from 8-token blocks a chunk is two boxes
+    const uint64_t k_desc = smem_desc_sw128(smem, 16, C::kChunkBytes);
+    const uint32_t k_half = half_blocks ? C::kChunkBytes / 2 : 1024, k_group = half_blocks ? 1024 : 2048;
     const uint64_t q_desc = smem_desc_sw128(smem + C::kOffQ, 16, 1024);
+    // only the address, in the lower word, differs from product to product
+    const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32), q_hi = static_cast<uint32_t>(q_desc >> 32);
     bool ok = true;
-    int held_seq = -1, held_head = -1, held = 0;  // resident tiles: q loads before theirs
     int steps = 0;
-    bool more = walk.next();
-    while (ok && more) {
-      const Item now = it;
-      const bool fresh = !p.resident || now.seq != held_seq || now.head != held_head;
-      if (fresh) {
-        held_seq = now.seq;
-        held_head = now.head;
-        held = q_loads;
-        q_loads += p.resident ? now.tiles : now.tiles - now.first;
-      }
-      more = walk.next();
-      const bool last_use = !p.resident || !more || it.seq != now.seq || it.head != now.head;
+    while (ok && walk.next()) {
       if (lane == 0) {
-        const int ks = k_loads % KS;
-        ok = mbar_wait_bounded(&bars->k_full[ks], (k_loads / KS) & 1);
-        // (every load is waited for, its tile used or not, before its stage is handed back)
-        for (int q = held; ok && fresh && p.resident && q < held + now.first; ++q)
-          ok = mbar_wait_bounded(&bars->q_full[q % QS], (q / QS) & 1);
-        for (int j = now.first; ok && j < now.tiles; ++j, ++steps) {
-          const int q = held + (p.resident ? j : j - now.first), qs = q % QS, b = steps & 1;
-          ok = mbar_wait_bounded(&bars->q_full[qs], (q / QS) & 1);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (ok && steps >= 2) ok = mbar_wait_bounded(&bars->s_free[g][b], ((steps >> 1) - 1) & 1);
+        const int held = q_loads;  // loads before the first of this run
+        if (p.resident) {
+          q_loads += run.row_tiles;
+          // (every load is waited for, its tile used or not, before its stage is handed back)
+          for (int q = held; ok && q < q_loads; ++q) ok = mbar_wait_bounded(&bars->q_full[q % QS], (q / QS) & 1);
+        }
+        for (int tile = run.tile; ok && tile < run.end; ++tile) {
+          const int first = run.first(p, tile * kTokens) + rank;
+          if (first >= run.row_tiles) break;
+          const int ks = k_loads % KS;
+          const uint32_t k_lo = static_cast<uint32_t>(k_desc) + ((ks * C::kKBytes + g * k_half) >> 4);
+          ok = mbar_wait_bounded(&bars->k_full[ks], (k_loads / KS) & 1);
+          ++k_loads;
+          for (int j = first; ok && j < run.row_tiles; j += ranks, ++steps) {
+            const int q = p.resident ? held + j : q_loads++, qs = q % QS, b = steps & 1;
+            if (!p.resident) ok = mbar_wait_bounded(&bars->q_full[qs], (q / QS) & 1);
+            const uint32_t q_lo = static_cast<uint32_t>(q_desc) + (qs * C::kQBytes >> 4);
+            if (ok && steps >= 2) ok = mbar_wait_bounded(&bars->s_free[b][g], ((steps >> 1) - 1) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t a = k_desc + static_cast<uint64_t>(
-                  (ks * C::kKBytes + (kk >> 2) * (kTokens * 128) + g * (kHalf * 128) + (kk & 3) * 32) >> 4);
-              const uint64_t bd = q_desc + static_cast<uint64_t>(
-                  (qs * C::kQBytes + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4);
-              mma_f16(tmem + (g * 2 + b) * kRows, a, bd, idesc, kk > 0);
-            }
-            mma_commit(&bars->s_full[g][b]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_f16(tmem + (b * 2 + g) * kRows, k_hi, k_lo + (kk >> 2) * (k_group >> 4) + (kk & 3) * 2, q_hi,
+                      q_lo + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            mma_commit(&bars->s_full[b][g]);
             mma_started = 1;
+            if (!p.resident) mma_commit(&bars->q_free[qs]);
           }
-          if (ok && !p.resident) mma_commit(&bars->q_free[qs]);
+          if (ok) mma_commit(&bars->k_free[ks]);
         }
-        if (ok) mma_commit(&bars->k_free[ks]);
-        if (ok && p.resident && last_use)
-          for (int j = 0; j < now.tiles; ++j) mma_commit(&bars->q_free[(held + j) % QS]);
+        if (ok && p.resident)
+          for (int q = held; q < q_loads; ++q) mma_commit(&bars->q_free[q % QS]);
       }
-      ++k_loads;
       ok = __shfl_sync(kFullMask, ok, 0);
-      steps = __shfl_sync(kFullMask, steps, 0);
-      mma_started = __shfl_sync(kFullMask, mma_started, 0);
     }
+    mma_started = __shfl_sync(kFullMask, mma_started, 0);
     if (!ok && lane == 0) {
       *abort_flag = 1;
       report_error(p.err, PA_ERR_TIMEOUT, -1, -1);
@@ -379,77 +416,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------------- softmax
     const int wg = warp >> 2, r = threadIdx.x & (kHalf - 1);
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * kRows;
+    const int at = (r >> 3) * 16 + wg * 8 + (r & 7);  // this thread's token of an item
     float* lse_wg = lse_s + wg * 2 * kRows;
-    int steps = 0, held_seq = -1, held_head = -1, lse_loads = 0;
-    const float* lse = lse_wg;
+    auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    int steps = 0, items = 0, lse_loads = 0;
     bool ok = true;
     while (ok && walk.next()) {
-      const int t = it.t0 + wg * kHalf + r;
-      const size_t sh = static_cast<size_t>(it.seq) * p.num_kv_heads + it.head;
-      float* to = p.weights + sh * p.weights_row + t;
-      const float before = t < it.s.L ? *to : 0.f;
-      float total = 0.f;
-      for (int j = it.first; j < it.tiles; ++j, ++steps) {
-        const int b = steps & 1;
-        const int here = min(p.tile_tokens, it.s.W - j * p.tile_tokens), cols = here * p.group;
-        // a key head's only tile: its rows' lse stay where they are
-        if (!p.resident || it.tiles > 1 || it.seq != held_seq || it.head != held_head) {
-          held_seq = it.seq;
-          held_head = it.head;
-          float v = 0.f;
-          if (r < cols) {
-            const int tok = r * p.inv_group >> 16;
-            v = -kLog2e * p.lse[static_cast<size_t>(it.s.row0 + j * p.tile_tokens + tok) * p.num_heads +
-                                it.head * p.group + (r - tok * p.group)];
-          }
-          // two buffers in turn: whoever is past the barrier of one load has done with the load before
-          float* to = lse_wg + (lse_loads++ & 1) * kRows;
-          to[r] = v;
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
-          lse = to;
-        }
-        ok = __all_sync(kFullMask, mbar_wait_bounded(&bars->s_full[wg][b], (steps >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        // the first row's place in the sequence: rows before it see less
-        const int pos = it.s.L - it.s.W + j * p.tile_tokens;
-        const bool seen = it.t0 + wg * kHalf + kHalf - 1 <= pos;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 32) {
-          float s[32];
-          tmem_ld32(tmem + lanes + (wg * 2 + b) * kRows + c0, s);
-          const float4* nl = reinterpret_cast<const float4*>(lse + c0);
-          if (seen && c0 + 32 <= cols) {
+      const size_t sh = static_cast<size_t>(run.seq) * p.num_kv_heads + run.head;
+      const int tok = r * p.inv_group >> 16;  // of row r of a tile
+      const float* lse_row = p.lse + (static_cast<size_t>(run.s.row0) + tok) * p.num_heads +
+                             run.head * p.group + (r - tok * p.group);
+      // -lse in base 2 of row r of tile j; 0 past the window's last, and where r only fills the tile up
+      auto row_lse = [&](int j) {
+        if (tok >= min(p.tile_tokens, run.s.W - j * p.tile_tokens)) return 0.f;
+        return -kLog2e * __ldg(lse_row + static_cast<size_t>(j) * p.tile_tokens * p.num_heads);
+      };
+      if (p.resident) {
+        float v[QS];
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 v = nl[c / 4];
-              const float e0 = ex2_approx(fmaf(s[c], p.qscale, v.x));
-              const float e1 = ex2_approx(fmaf(s[c + 1], p.qscale, v.y));
-              const float e2 = ex2_approx(fmaf(s[c + 2], p.qscale, v.z));
-              const float e3 = ex2_approx(fmaf(s[c + 3], p.qscale, v.w));
-              add2(sum[0], sum[1], e0, e1);
-              add2(sum[2], sum[3], e2, e3);
-            }
-          } else {
+        for (int j = 0; j < QS; ++j) v[j] = j < run.row_tiles ? row_lse(j) : 0.f;
+        sync();  // the last run's are read
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float e = ex2_approx(fmaf(s[c], p.qscale, lse[c0 + c]));
-              const bool counts = c0 + c < cols && t <= pos + ((c0 + c) * p.inv_group >> 16);
-              sum[c & 3] += counts ? e : 0.f;
-            }
-          }
-        }
-        total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc_fence_before();
-        mbar_arrive(&bars->s_free[wg][b]);
-        if (__shfl_sync(kFullMask, *abort_flag, 0)) {
-          ok = false;
-          break;
-        }
+        for (int j = 0; j < QS; ++j) lse_wg[j * kRows + r] = v[j];
+        sync();
       }
-      if (ok && t < it.s.L) *to = before + total;
+      for (int tile = run.tile; ok && tile < run.end; ++tile) {
+        const int t0 = tile * kTokens, t = t0 + at;
+        const int first = run.first(p, t0) + rank;
+        float total = 0.f, next_lse = 0.f;
+        if (!p.resident && first < run.row_tiles) next_lse = row_lse(first);
+        for (int j = first; j < run.row_tiles; j += ranks, ++steps) {
+          const int b = steps & 1;
+          const float* lse = lse_wg + j * kRows;
+          if (!p.resident) {
+            // two buffers in turn: whoever is past the barrier of one tile has done with the tile before
+            float* mine = lse_wg + (lse_loads++ & 1) * kRows;
+            mine[r] = next_lse;
+            if (j + ranks < run.row_tiles) next_lse = row_lse(j + ranks);
+            sync();
+            lse = mine;
+          }
+          // the first row's place in the sequence: rows before it see less
+          const int pos = run.s.L - run.s.W + j * p.tile_tokens;
+          const int cols = min(p.tile_tokens, run.s.W - j * p.tile_tokens) * p.group;
+          const int whole = t0 + kTokens - 1 <= pos ? cols & ~31 : 0;  // columns without masks
+          const uint32_t from = lanes + b * 2 * kRows;
+          uint32_t nl = smem_addr(lse);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          ok = __all_sync(kFullMask, mbar_wait_bounded(&bars->s_full[b][wg], (steps >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          int c = 0;
+#pragma unroll 1
+          for (; c < whole; c += 32, nl += 128) {
+            float s[32];
+            tmem_ld32(from + c, s);
+            add_weights(s, nl, p.qscale, sum);
+          }
+#pragma unroll 1
+          for (; c < cols; c += 32, nl += 128) {
+            float s[32];
+            tmem_ld32(from + c, s);
+            add_seen_weights(s, nl, p.qscale, c, cols, t - pos, p.inv_group, sum);
+          }
+          tc_fence_before();
+          mbar_arrive(&bars->s_free[b][wg]);
+          total += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        if (__shfl_sync(kFullMask, *abort_flag, 0)) ok = false;
+        if (ranks > 1) {
+          // The cluster's sums meet in its first block, which adds them in order.
+          const int buf = items & 1, use = items >> 1;
+          ++items;
+          float* sums = reinterpret_cast<float*>(smem + C::kOffSums) + buf * kMaxCluster * kTokens + at;
+          if (rank == 0) {
+            ok = ok && __all_sync(kFullMask, mbar_wait_cluster(&bars->sums_full[buf], use & 1));
+            for (int i = 1; i < ranks; ++i) total += sums[i * kTokens];
+            for (int i = 1; i < ranks; ++i) mbar_arrive_peer(&bars->sums_free[buf], i);
+          } else {
+            if (use > 0) ok = ok && __all_sync(kFullMask, mbar_wait_cluster(&bars->sums_free[buf], (use - 1) & 1));
+            st_peer(smem_addr(sums + rank * kTokens), 0, total);
+            mbar_arrive_peer(&bars->sums_full[buf], 0);
+          }
+        }
+        // One thread adds to a weight, once: a reduction in L2 gives the same bits as a load, an add and a
+        // store, and nothing waits for the load.
+        if (ok && rank == 0 && t < run.s.L) atomicAdd(p.weights + sh * p.weights_row + t, total);
+      }
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -468,12 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < QS && s < q_loads; ++s)
         mbar_wait_bounded(&bars->q_full[s], ((q_loads - 1 - s) / QS) & 1);
     }
-    if (warp == kWarpMma && lane == 0 && mma_started) {
-      mma_commit(&bars->drain);
-      mbar_wait_bounded(&bars->drain, 0);
+    if (warp >= kWarpMma && lane == 0 && mma_started) {
+      mma_commit(&bars->drain[warp - kWarpMma]);
+      mbar_wait_bounded(&bars->drain[warp - kWarpMma], 0);
     }
     __syncthreads();
   }
+  if (ranks > 1) cluster_sync();  // no block leaves while another may write to its memory
   tc_fence_after();
   if (warp == kWarpMma) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
@@ -496,27 +551,36 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
                                static_cast<cuuint64_t>(p.total_queries)};
   const cuuint64_t qstr[2] = {D * 2, static_cast<cuuint64_t>(D) * 2 * p.num_heads};
   const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(p.group), static_cast<cuuint32_t>(p.tile_tokens)};
-  const cuuint64_t cdims[2] = {D, cache_rows};
-  const cuuint64_t cstr[1] = {D * 2};
-  const cuuint32_t cbox[2] = {64, p.block_size >= 16 ? 16u : 8u};
+  // the cache as [D / 64][rows][64]: one box is a chunk, or half of one with 8-token blocks
+  const cuuint64_t cdims[3] = {64, cache_rows, D / 64};
+  const cuuint64_t cstr[2] = {D * 2, 128};
+  const cuuint32_t cbox[3] = {64, p.block_size >= 16 ? 16u : 8u, D / 64};
   if (!encode_tensor_map(&tq, BF16, q, 3, qdims, qstr, qbox) ||
-      !encode_tensor_map(&tk, BF16, k_cache, 2, cdims, cstr, cbox))
+      !encode_tensor_map(&tk, BF16, k_cache, 3, cdims, cstr, cbox))
     return PA_ERR_CUDA;
   if (cudaFuncSetAttribute(chunk_weights_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes) != cudaSuccess)
     return PA_ERR_CUDA;
   const long long tiles = (static_cast<long long>(p.max_blocks) * p.block_size + kTokens - 1) / kTokens;
   const long long items = p.num_seqs * tiles * p.num_kv_heads;
+  // Few items of many tiles of rows: a cluster shares out an item's tiles.
+  const int row_tiles = (most + p.tile_tokens - 1) / p.tile_tokens;
+  int ranks = 1;
+  while (!p.resident && ranks < kMaxCluster && items * ranks < 4ll * sms && row_tiles >= 8 * ranks) ranks *= 2;
+  const long long walkers = sms / ranks;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? items : sms));
+  cfg.gridDim = dim3(static_cast<unsigned>((items < walkers ? items : walkers) * ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, chunk_weights_kernel<BF16, D>, tq, tk, p) != cudaSuccess ||
       cudaGetLastError() != cudaSuccess)
     return PA_ERR_CUDA;

@@ -62,4 +62,30 @@ __device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer_addr(addr, rank)), "f"(v) : "memory");
+}
+// Arrives at a block's barrier, behind this thread's stores to its memory, and the wait for it there.
+__device__ __forceinline__ void mbar_arrive_peer(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                   peer_addr(smem_addr(bar), rank))
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  uint64_t limit_ns = kWaitLimitNs) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 15u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 }  // namespace pagedkv

@@ -45,6 +45,18 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
       : "memory");
 }
 
+// Same, the descriptors in words: in a sequence of products only the lower ones change, by a few units,
+// and one thread issues them all.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a_hi, uint32_t a_lo, uint32_t b_hi,
+                                        uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %1};\n\tmov.b64 b, {%4, %3};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_hi), "r"(a_lo), "r"(b_hi), "r"(b_lo), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Same, with A read from tensor memory (M rows = lanes, K values packed two per
 // 32-bit column).
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
@@ -88,6 +100,14 @@ __device__ __forceinline__ void fma2(float& y0, float& y1, float x0, float x1, f
       "mov.b64 c, {%5, %5};\n\tfma.rn.f32x2 d, x, s, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(y0), "=f"(y1)
       : "f"(x0), "f"(x1), "f"(s), "f"(c));
+}
+
+// (y0, y1) = (x0 s + c0, x1 s + c1).
+__device__ __forceinline__ void fma2(float& y0, float& y1, float x0, float x1, float s, float c0, float c1) {
+  asm("{\n\t.reg .b64 x, s, c, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %6};\n\tfma.rn.f32x2 d, x, s, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(s), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ void add2(float& a0, float& a1, float x0, float x1) {
