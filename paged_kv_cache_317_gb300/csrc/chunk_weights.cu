@@ -38,7 +38,7 @@ constexpr int kTokens = 2 * kHalf;         // of an item
 constexpr int kRows = 128;                 // query rows of a tile (MMA N)
 constexpr int kWarpLoad = 8, kWarpMma = 9;  // and 10: an issuer for each warpgroup
 constexpr int kThreads = 352;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 constexpr int kLists = 128;                // lists of sequences whose items are counted together
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -131,13 +131,12 @@ struct Walk {
   const ChunkWeightsParams& p;
   const int* upto;  // [kLists]: items of the first lists of sequences
   int list;         // sequences of a list
-  int m, end, step;
+  int m, end, b, n;
   Run run;
 
   __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, int list, int b, int n)
-      : p(p), upto(upto), list(list) {
+      : p(p), upto(upto), list(list), b(b), n(n) {
     const long long all = upto[kLists - 1];
-    step = n;
     m = p.resident ? static_cast<int>(all * b / n) : b;
     end = p.resident ? static_cast<int>(all * (b + 1) / n) : static_cast<int>(all);
   }
@@ -184,22 +183,32 @@ struct Walk {
       run.tile = left / p.num_kv_heads;
       run.head = left - run.tile * p.num_kv_heads;
       run.end = run.tile + 1;
-      m += step;
+      // there and back: a sequence's items get smaller
+      b = n - 1 - b;
+      m = (m / n + 1) * n + b;
     }
     return true;
   }
 };
 
-// e^(logit - lse) of 32 columns of S, added to the four sums; nl: shared address of -lse in base 2.
-__device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, float qscale, float (&sum)[4]) {
+// e^(logit - lse) of the first `cols` of 32 columns of S, or of all, added to the four sums; nl: shared
+// address of -lse in base 2.
+template <bool kAll>
+__device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, float qscale, int cols,
+                                            float (&sum)[4]) {
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
     const float4 v = ld_shared4(nl + 4 * c);
     float x0, x1, x2, x3;
     fma2(x0, x1, s[c], s[c + 1], qscale, v.x, v.y);
     fma2(x2, x3, s[c + 2], s[c + 3], qscale, v.z, v.w);
-    add2(sum[0], sum[1], ex2_approx(x0), ex2_approx(x1));
-    add2(sum[2], sum[3], ex2_approx(x2), ex2_approx(x3));
+    float e[4] = {ex2_approx(x0), ex2_approx(x1), ex2_approx(x2), ex2_approx(x3)};
+    if constexpr (!kAll) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = c + i < cols ? e[i] : 0.f;
+    }
+    add2(sum[0], sum[1], e[0], e[1]);
+    add2(sum[2], sum[3], e[2], e[3]);
   }
 }
 
@@ -460,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the first row's place in the sequence: rows before it see less
           const int pos = run.s.L - run.s.W + j * p.tile_tokens;
           const int cols = min(p.tile_tokens, run.s.W - j * p.tile_tokens) * p.group;
-          const int whole = t0 + kTokens - 1 <= pos ? cols & ~31 : 0;  // columns without masks
+          const bool seen = t0 + kTokens - 1 <= pos;  // by all of them
+          const int whole = seen ? cols & ~31 : 0;
           const uint32_t from = lanes + b * 2 * kRows;
           uint32_t nl = smem_addr(lse);
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -472,7 +482,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (; c < whole; c += 32, nl += 128) {
             float s[32];
             tmem_ld32(from + c, s);
-            add_weights(s, nl, p.qscale, sum);
+            add_weights<true>(s, nl, p.qscale, 32, sum);
+          }
+          if (seen && c < cols) {  // a tile whose rows are not a multiple of 32
+            float s[32];
+            tmem_ld32(from + c, s);
+            add_weights<false>(s, nl, p.qscale, cols - c, sum);
+            c = cols;
           }
 #pragma unroll 1
           for (; c < cols; c += 32, nl += 128) {
@@ -567,9 +583,7 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
   const int row_tiles = (most + p.tile_tokens - 1) / p.tile_tokens;
   int ranks = 1;
   while (!p.resident && ranks < kMaxCluster && items * ranks < 4ll * sms && row_tiles >= 8 * ranks) ranks *= 2;
-  const long long walkers = sms / ranks;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((items < walkers ? items : walkers) * ranks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -581,6 +595,14 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  // as many clusters as find places at a time, whose SMs have to be neighbours
+  int walkers = sms;
+  if (ranks > 1) {
+    cfg.gridDim = dim3(ranks);
+    if (cudaOccupancyMaxActiveClusters(&walkers, chunk_weights_kernel<BF16, D>, &cfg) != cudaSuccess || walkers <= 0)
+      return PA_ERR_CUDA;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>((items < walkers ? items : walkers) * ranks));
   if (cudaLaunchKernelEx(&cfg, chunk_weights_kernel<BF16, D>, tq, tk, p) != cudaSuccess ||
       cudaGetLastError() != cudaSuccess)
     return PA_ERR_CUDA;

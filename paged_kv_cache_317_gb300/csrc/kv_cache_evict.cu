@@ -2,12 +2,13 @@
 //
 // Place j of (sequence, key head) takes the row of K, of V and the weight that place kept[j] held.
 // In place this is a gather within one array, safe in order: kept[j] >= j, so a row that is still to
-// be read (for place j' > j, from a place >= j') is never one that place j overwrites.  A thread
-// block, or for few rows a cluster, takes one (sequence, key head) and goes through its list in
-// rounds: every thread loads its pieces of the round's rows into registers, a barrier, every thread
-// stores them.  Loads of later rounds may run ahead of the stores of earlier ones; only the loads of
-// a round itself have to be over, which the barrier sees to.
-// A move and nothing else: bound by HBM for batches, by the chain list entry -> block -> row for one
+// be read (for place j' > j, from a place >= j') is never one that place j overwrites.  K and V are
+// moved apart.  A thread block, or for few lists a cluster, takes one list and goes through it in
+// rounds: every thread loads its pieces of the round's rows into registers (64 KB a thread block), looks
+// up rows of the next round, a barrier, every thread stores its pieces.  Loads of later rounds may run
+// ahead of the stores of earlier ones; only the loads of a round itself have to be over, which the
+// barrier sees to.
+// A move and nothing else: bound by HBM for batches, by a round's latency (rows, barrier, stores) for one
 // sequence.
 #include <cuda_runtime.h>
 
@@ -18,7 +19,8 @@ namespace pagedkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;     // 16-byte pieces of K, and as many of V, that a thread has in flight
+constexpr int kPieces = 16;    // 16-byte pieces that a thread has in flight
+constexpr int kMaxRows = 512;  // rows of a round and thread block
 constexpr int kMaxCluster = 8;
 
 struct EvictParams {
@@ -33,84 +35,102 @@ struct EvictParams {
   long long weights_row;   // floats from (sequence, key head) to the next
   int num_kept, num_kv_heads, vecs, block_size, max_blocks, new_max_blocks, num_blocks;
   int rows;                // rows of a round and thread block
+  unsigned inv_vecs;       // i / vecs = i * inv_vecs >> 20 for i < 4096, vecs <= 128
 };
 
-__global__ void __launch_bounds__(kThreads, 4) kv_cache_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 2) kv_cache_evict_kernel(const EvictParams p) {
+  // rows of the caches seen as rows of head_dim: where a row of the round comes from (-1: it stays) and
+  // goes to, of this round and the next
+  __shared__ long long from[2][kMaxRows], to[2][kMaxRows];
   const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int sh = blockIdx.x / ranks;
+  const int list = blockIdx.x / ranks, sh = list >> 1;
+  const bool is_v = list & 1;
   const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
-  const bool first = rank == 0 && threadIdx.x == 0;
   int L = p.seq_lens[seq];
   const int cap = p.max_blocks * p.block_size;
   if (L < 0 || L > cap) {
-    if (first && head == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
+    if (rank == 0 && threadIdx.x == 0 && head == 0 && !is_v) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     L = min(max(L, 0), cap);
   }
   const int32_t* kept = p.kept + static_cast<size_t>(sh) * p.num_kept;
   const int32_t* table = p.tables + static_cast<size_t>(seq) * p.max_blocks;
   const int32_t* new_table = p.new_tables + static_cast<size_t>(seq) * p.new_max_blocks;
-  float* weights = p.weights + sh * p.weights_row;
+  float* weights = p.weights == nullptr || is_v ? nullptr : p.weights + sh * p.weights_row;
+  uint4* cache = is_v ? p.v : p.k;
   const int places = min(p.num_kept, L);
 
-  // the place that place j takes its row from, -1 if none
-  auto source = [&](int j, bool report) -> int {
-    const int s = kept[j];
-    if (s >= j && s < L) return s;
-    if (s != -1 && report) report_error(p.err, PA_ERR_BAD_POSITION, sh, s);
-    return s == -1 ? -1 : -2;
-  };
-  // the row of place j in the cache seen as rows of head_dim
-  auto row_of = [&](const int32_t* from, int blocks, int j, bool report) -> long long {
+  // the row of place j
+  auto row_of = [&](const int32_t* t, int blocks, int j) -> long long {
     const int b = j / p.block_size;
-    const int blk = b < blocks ? from[b] : -1;
+    const int blk = b < blocks ? t[b] : -1;
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-      if (report) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
+      if (!is_v) report_error(p.err, PA_ERR_BAD_BLOCK, seq, blk);
       return -1;
     }
     return (static_cast<long long>(blk) * p.num_kv_heads + head) * p.block_size + (j - b * p.block_size);
   };
-
-  for (int j0 = rank * p.rows; j0 - rank * p.rows < places; j0 += ranks * p.rows) {
-    uint4 k[kPieces], v[kPieces];
-    long long to[kPieces];
+  // The rows of this block's places j0 on; a weight is moved by the thread that looks its row up, which
+  // returns the place it was at, -1 for none (the weight becomes 0), -2 if it stays as it is.
+  auto look_up = [&](int buf, int j0, int (&places_from)[kMaxRows / kThreads]) {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int i = threadIdx.x + u * kThreads, row = i / p.vecs, c = i - row * p.vecs;
-      const int j = j0 + row;
-      to[u] = -1;
-      if (row < p.rows && j < places) {
-        const int s = source(j, c == 0);
-        if (s >= 0) {
-          const long long src = row_of(table, p.max_blocks, s, c == 0);
-          const long long dst = row_of(new_table, p.new_max_blocks, j, c == 0);
-          if (src >= 0 && dst >= 0 && src != dst) {
-            k[u] = __ldcg(p.k + src * p.vecs + c);
-            v[u] = __ldcg(p.v + src * p.vecs + c);
-            to[u] = dst * p.vecs + c;
-          }
+    for (int u = 0; u < kMaxRows / kThreads; ++u) {
+      const int i = threadIdx.x + u * kThreads, j = j0 + i;
+      long long src = -1, dst = -1;
+      places_from[u] = -2;
+      if (i < p.rows && j < places) {
+        const int s = kept[j];
+        if (s >= j && s < L) {
+          src = row_of(table, p.max_blocks, s);
+          dst = row_of(new_table, p.new_max_blocks, j);
+          if (dst < 0 || src == dst) src = -1;
+          places_from[u] = s == j ? -2 : s;
+        } else if (s == -1) {
+          places_from[u] = -1;
+        } else if (!is_v) {
+          report_error(p.err, PA_ERR_BAD_POSITION, sh, s);
         }
       }
+      if (i < p.rows) {
+        from[buf][i] = src;
+        to[buf][i] = dst;
+      }
     }
-    float w = 0.f;
-    int from = -2;
-    const int j = j0 + static_cast<int>(threadIdx.x);
-    if (p.weights != nullptr && threadIdx.x < p.rows && j < places) {
-      from = source(j, false);
-      if (from >= 0) w = __ldcg(weights + from);
+  };
+  int now[kMaxRows / kThreads], next[kMaxRows / kThreads];
+  look_up(0, rank * p.rows, now);
+  __syncthreads();
+  const int step = ranks * p.rows;
+  int buf = 0;
+  for (int j0 = rank * p.rows; j0 - rank * p.rows < places; j0 += step, buf ^= 1) {
+    uint4 piece[kPieces];
+    float w[kMaxRows / kThreads];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int i = threadIdx.x + u * kThreads, row = i * p.inv_vecs >> 20;
+      const long long src = row < p.rows ? from[buf][row] : -1;
+      if (src >= 0) piece[u] = __ldcg(cache + src * p.vecs + (i - row * p.vecs));
     }
+    if (weights != nullptr) {
+#pragma unroll
+      for (int u = 0; u < kMaxRows / kThreads; ++u) w[u] = now[u] >= 0 ? __ldcg(weights + now[u]) : 0.f;
+    }
+    look_up(buf ^ 1, j0 + step, next);
     if (ranks == 1) __syncthreads();
     else cluster_sync();
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
-      if (to[u] >= 0) {
-        p.k[to[u]] = k[u];
-        p.v[to[u]] = v[u];
-      }
+      const int i = threadIdx.x + u * kThreads, row = i * p.inv_vecs >> 20;
+      if (row < p.rows && from[buf][row] >= 0) cache[to[buf][row] * p.vecs + (i - row * p.vecs)] = piece[u];
     }
-    if (from >= -1 && from != j) weights[j] = w;
+#pragma unroll
+    for (int u = 0; u < kMaxRows / kThreads; ++u) {
+      if (weights != nullptr && now[u] != -2) weights[j0 + static_cast<int>(threadIdx.x) + u * kThreads] = w[u];
+      now[u] = next[u];
+    }
+    __syncthreads();  // the round's rows are used
   }
   // every weight has been read
-  if (p.weights != nullptr)
+  if (weights != nullptr)
     for (int j = places + rank * kThreads + static_cast<int>(threadIdx.x); j < L; j += ranks * kThreads)
       weights[j] = 0.f;
 }
@@ -157,10 +177,11 @@ extern "C" int kv_cache_evict(void* k_cache, void* v_cache, const int32_t* block
   p.block_size = block_size;
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
+  p.inv_vecs = ((1u << 20) + p.vecs - 1) / p.vecs;
   const int fit = kThreads * kPieces / p.vecs;
-  p.rows = fit < kThreads ? fit : kThreads;
-  // Few rows: clusters, as far as a round still has work for every block of them.
-  const long long lists = static_cast<long long>(num_seqs) * num_kv_heads;
+  p.rows = fit < kMaxRows ? fit : kMaxRows;
+  // Few lists: clusters, as far as a round still has work for every block of them.
+  const long long lists = 2ll * num_seqs * num_kv_heads;
   const long long longest = num_kept < cap ? num_kept : cap;
   int ranks = 1;
   while (ranks < kMaxCluster && lists * ranks < 304 && longest > static_cast<long long>(ranks) * p.rows)

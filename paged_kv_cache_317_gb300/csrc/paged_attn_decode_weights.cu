@@ -29,7 +29,7 @@ constexpr int kWarps = 4;       // warps per thread block
 constexpr int kStages = 3;
 constexpr int kAlign = 1024;    // a swizzled box must start on 1024 bytes
 constexpr int kHeader = 256;    // barriers
-constexpr int kMaxParts = 64;   // thread blocks per row
+constexpr int kMaxParts = 64;   // thread blocks per row: 8 for each warp of the join
 constexpr int kShares = 4096;   // thread blocks of all rows, where rows have several
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTokens = 1024;  // tokens of a join's thread block
@@ -236,93 +236,144 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // Joins the parts of the rows of a (sequence, key head): blocks of kJoinTokens tokens, which also share
-// out the output's heads.
+// out the output's heads.  The last rows first: theirs are the logits most likely to be in L2 yet.
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads)
     decode_weights_join_kernel(const DecodeWeightsParams p, const int shares, const float lift) {
-  constexpr int kCols = 8 * NT, kPer = kJoinTokens / kJoinThreads;
+  constexpr int kCols = 8 * NT, kPer = kJoinTokens / kJoinThreads, kWarpsJoin = kJoinThreads / 32;
+  constexpr int kVec = D / 32, kAhead = 8;
   __shared__ float2 stat[kJoinCols];
+  __shared__ __align__(16) float slice[kWarpsJoin][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sh = blockIdx.x / shares, share = blockIdx.x - sh * shares;
+  const int block = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+  const int sh = block / shares, share = block - sh * shares;
   const int seq = sh / p.num_kv_heads, head = sh - seq * p.num_kv_heads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int L = length_of(p, seq, false);
   const int t0 = share * kJoinTokens + static_cast<int>(threadIdx.x);
+  if (share * kJoinTokens >= L && share >= p.group) return;  // neither tokens nor heads
+  // (m, l) of column `col`'s parts, lane i's i and i + 32, and M and 1 / l of the whole
+  struct Column {
+    float w[2];  // 2^(m - M) of the lane's parts
+    float M, inv;
+  };
+  auto column = [&](int col, size_t at) -> Column {
+    float2 ml[2];
+    Column c;
+    c.M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
+      ml[k] = i < p.parts ? p.part_ml[at + static_cast<size_t>(i) * kCols] : make_float2(-INFINITY, 0.f);
+      c.M = max_nan(c.M, ml[k].x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) c.M = max_nan(c.M, __shfl_xor_sync(kFullMask, c.M, off));
+    float l = 0.f;
+    bool tokens = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      tokens |= ml[k].y < 0.f || ml[k].x != -INFINITY;
+      c.w[k] = ml[k].x != -INFINITY ? exp2f(ml[k].x - c.M) : 0.f;
+      if (ml[k].x != -INFINITY) l = fmaf(c.w[k], ml[k].y, l);
+    }
+    tokens = __any_sync(kFullMask, tokens);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
+    c.inv = inverse_of(c.M, l, tokens);
+    return c;
+  };
+  auto first_part = [&](int col) -> size_t {
+    const size_t row = static_cast<size_t>(sh) * p.tiles + col / kCols;
+    return row * p.parts * kCols + col % kCols;
+  };
+  // ------------------------------------------------------------------ the weights
   float sum[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) sum[k] = 0.f;
-  for (int c0 = 0; c0 < p.group; c0 += kJoinCols) {
+  for (int c0 = 0; share * kJoinTokens < L && c0 < p.group; c0 += kJoinCols) {
     const int n = min(kJoinCols, p.group - c0);
-    for (int c = warp; c < n; c += kJoinThreads / 32) {
+    __syncthreads();
+    for (int c = warp; c < n; c += kWarpsJoin) {
+      const Column col = column(c0 + c, first_part(c0 + c));
+      if (lane == 0) stat[c] = make_float2(col.M, col.inv * lift);
+    }
+    __syncthreads();
+    auto logits = [&](int c) {
       const int col = c0 + c;
       const size_t row = static_cast<size_t>(sh) * p.tiles + col / kCols;
-      const size_t at = row * p.parts * kCols + col % kCols;
-      // lane i: parts i and i + 32
-      float2 ml[2];
-      float M = -INFINITY;
+      return p.logits + (row * p.cols + col % kCols) * p.pitch + t0;
+    };
+    for (int c = 0; c < n; c += 4) {  // four columns' loads at a time
+      float s[4][kPer];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int i = lane + 32 * k;
-        ml[k] = i < p.parts ? p.part_ml[at + static_cast<size_t>(i) * kCols] : make_float2(-INFINITY, 0.f);
-        M = max_nan(M, ml[k].x);
+      for (int i = 0; i < 4; ++i) {
+        const float* from = logits(min(c + i, n - 1));
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s[i][k] = t0 + k * kJoinThreads < L ? __ldcs(from + k * kJoinThreads) : 0.f;
       }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(kFullMask, M, off));
-      float w[2], l = 0.f;
-      bool tokens = false;
+      for (int i = 0; i < 4; ++i) {
+        if (c + i < n) {
+          const float2 st = stat[c + i];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        tokens |= ml[k].y < 0.f || ml[k].x != -INFINITY;
-        w[k] = ml[k].x != -INFINITY ? exp2f(ml[k].x - M) : 0.f;
-        if (ml[k].x != -INFINITY) l = fmaf(w[k], ml[k].y, l);
-      }
-      tokens = __any_sync(kFullMask, tokens);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
-      const float inv = inverse_of(M, l, tokens);
-      if (lane == 0) stat[c] = make_float2(M, inv * lift);
-      if (col % shares == share) {
-        constexpr int kVec = D / 32;
-        float acc[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-        const float* o = p.part_o + at * D + lane * kVec;
-#pragma unroll 4
-        for (int i = 0; i < p.parts; ++i) {
-          const float f = __shfl_sync(kFullMask, i < 32 ? w[0] : w[1], i & 31);
-          if (f != 0.f) {  // (a part without tokens holds zeros; NaN is not 0)
-            const float* from = o + static_cast<size_t>(i) * kCols * D;
-#pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-              const float2 v = *reinterpret_cast<const float2*>(from + e);
-              acc[e] = fmaf(f, v.x, acc[e]);
-              acc[e + 1] = fmaf(f, v.y, acc[e + 1]);
-            }
-          }
+          for (int k = 0; k < kPer; ++k) sum[k] = fmaf(exp2f(s[i][k] - st.x), st.y, sum[k]);
         }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] *= inv;
-        const size_t to = (static_cast<size_t>(seq) * p.num_heads + head * p.group + col) * D + lane * kVec;
-        store_out<kVec>(p.out, to, acc, p.out_dtype);
       }
     }
-    __syncthreads();
-    for (int c = 0; c < n; ++c) {
-      const int col = c0 + c;
-      const size_t row = static_cast<size_t>(sh) * p.tiles + col / kCols;
-      const float* s = p.logits + (row * p.cols + col % kCols) * p.pitch + t0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        if (t0 + k * kJoinThreads < L)
-          sum[k] = fmaf(exp2f(s[k * kJoinThreads] - stat[c].x), stat[c].y, sum[k]);
-    }
-    __syncthreads();
   }
+  // One thread adds to a weight, once: a reduction in L2 gives the same bits as a load, an add and a store.
   float* weights = p.weights + sh * p.weights_row + t0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
-    if (t0 + k * kJoinThreads < L) weights[k * kJoinThreads] += sum[k];
+    if (t0 + k * kJoinThreads < L) atomicAdd(weights + k * kJoinThreads, sum[k]);
+  // ------------------------------------------------------------------- the output
+  // A head's parts are shared out over the warps, whose sums meet in shared memory.
+  for (int col = share; col < p.group; col += shares) {
+    const size_t at = first_part(col);
+    const Column c = column(col, at);
+    float acc[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+    const float* o = p.part_o + at * D + lane * kVec;
+    float v[kAhead][kVec];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = warp + k * kWarpsJoin;
+      if (i < p.parts) {
+        const float* from = o + static_cast<size_t>(i) * kCols * D;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2)
+          *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(from + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = warp + k * kWarpsJoin;
+      const float f = __shfl_sync(kFullMask, i < 32 ? c.w[0] : c.w[1], i & 31);
+      if (i < p.parts && f != 0.f) {  // (a part without tokens has no sums; NaN is not 0)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, v[k][e], acc[e]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) slice[warp][lane * kVec + e] = acc[e];
+    __syncthreads();
+    const size_t to = (static_cast<size_t>(seq) * p.num_heads + head * p.group + col) * D;
+    for (int d = threadIdx.x * 2; d < D; d += kJoinThreads * 2) {
+      float out[2] = {0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWarpsJoin; ++w) {
+        out[0] += slice[w][d];
+        out[1] += slice[w][d + 1];
+      }
+      out[0] *= c.inv;
+      out[1] *= c.inv;
+      store_out<2>(p.out, to + d, out, p.out_dtype);
+    }
+  }
 }
 
 template <int D, int NT>
