@@ -26,13 +26,14 @@ namespace {
 
 constexpr int kChunk = 16;      // tokens per stage
 constexpr int kWarps = 4;       // warps per thread block
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kAlign = 1024;    // a swizzled box must start on 1024 bytes
 constexpr int kHeader = 256;    // barriers
 constexpr int kMaxParts = 64;   // thread blocks per row: 8 for each warp of the join
-constexpr int kShares = 4096;   // thread blocks of all rows, where rows have several
+constexpr int kFew = 304;       // fewer rows are shared out over that many thread blocks, two an SM,
+constexpr int kShares = 4096;   // more over so many, for rows of unequal length
 constexpr int kJoinThreads = 256;
-constexpr int kJoinTokens = 1024;  // tokens of a join's thread block
+constexpr int kJoinTokens = 2048;  // tokens of a join's thread block
 constexpr int kJoinCols = 64;      // columns whose maxima and sums it holds at a time
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -238,10 +239,10 @@ __global__ void __launch_bounds__(kWarps * 32)
 // Joins the parts of the rows of a (sequence, key head): blocks of kJoinTokens tokens, which also share
 // out the output's heads.  The last rows first: theirs are the logits most likely to be in L2 yet.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     decode_weights_join_kernel(const DecodeWeightsParams p, const int shares, const float lift) {
   constexpr int kCols = 8 * NT, kPer = kJoinTokens / kJoinThreads, kWarpsJoin = kJoinThreads / 32;
-  constexpr int kVec = D / 32, kAhead = 8;
+  constexpr int kVec = D / 32, kAhead = D == 256 ? 4 : 8;  // parts that a warp loads at a time
   __shared__ float2 stat[kJoinCols];
   __shared__ __align__(16) float slice[kWarpsJoin][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -294,25 +295,26 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int k = 0; k < kPer; ++k) sum[k] = 0.f;
   for (int c0 = 0; share * kJoinTokens < L && c0 < p.group; c0 += kJoinCols) {
     const int n = min(kJoinCols, p.group - c0);
+    float s[4][kPer];
+    auto load = [&](int c) {  // four columns' logits
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = c0 + min(c + i, n - 1);
+        const size_t row = static_cast<size_t>(sh) * p.tiles + col / kCols;
+        const float* from = p.logits + (row * p.cols + col % kCols) * p.pitch + t0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s[i][k] = t0 + k * kJoinThreads < L ? __ldcs(from + k * kJoinThreads) : 0.f;
+      }
+    };
+    load(0);  // on their way while the maxima and sums are joined
     __syncthreads();
     for (int c = warp; c < n; c += kWarpsJoin) {
       const Column col = column(c0 + c, first_part(c0 + c));
       if (lane == 0) stat[c] = make_float2(col.M, col.inv * lift);
     }
     __syncthreads();
-    auto logits = [&](int c) {
-      const int col = c0 + c;
-      const size_t row = static_cast<size_t>(sh) * p.tiles + col / kCols;
-      return p.logits + (row * p.cols + col % kCols) * p.pitch + t0;
-    };
-    for (int c = 0; c < n; c += 4) {  // four columns' loads at a time
-      float s[4][kPer];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* from = logits(min(c + i, n - 1));
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) s[i][k] = t0 + k * kJoinThreads < L ? __ldcs(from + k * kJoinThreads) : 0.f;
-      }
+    for (int c = 0; c < n; c += 4) {
+      if (c > 0) load(c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (c + i < n) {
@@ -337,24 +339,27 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
     const float* o = p.part_o + at * D + lane * kVec;
-    float v[kAhead][kVec];
+#pragma unroll 1
+    for (int k0 = 0; k0 < kMaxParts / kWarpsJoin && k0 * kWarpsJoin < p.parts; k0 += kAhead) {
+      float v[kAhead][kVec];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = warp + k * kWarpsJoin;
-      if (i < p.parts) {
-        const float* from = o + static_cast<size_t>(i) * kCols * D;
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = warp + (k0 + k) * kWarpsJoin;
+        if (i < p.parts) {
+          const float* from = o + static_cast<size_t>(i) * kCols * D;
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2)
-          *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(from + e);
+          for (int e = 0; e < kVec; e += 2)
+            *reinterpret_cast<float2*>(&v[k][e]) = *reinterpret_cast<const float2*>(from + e);
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = warp + k * kWarpsJoin;
-      const float f = __shfl_sync(kFullMask, i < 32 ? c.w[0] : c.w[1], i & 31);
-      if (i < p.parts && f != 0.f) {  // (a part without tokens has no sums; NaN is not 0)
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = warp + (k0 + k) * kWarpsJoin;
+        const float f = __shfl_sync(kFullMask, i < 32 ? c.w[0] : c.w[1], i & 31);
+        if (i < p.parts && f != 0.f) {  // (a part without tokens has no sums; NaN is not 0)
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, v[k][e], acc[e]);
+          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, v[k][e], acc[e]);
+        }
       }
     }
     __syncthreads();
@@ -408,7 +413,7 @@ Shape shape_for(long long rows, int tiles, int group, long long cap) {
   s.pitch = padded;
   s.smem = bare;
   const long long most = (cap + 255) / 256;
-  long long parts = rows < 456 ? 456 / rows : (2048 + rows - 1) / rows;
+  long long parts = (rows < kFew ? kFew : kShares) / rows;
   if (parts > most) parts = most;
   if (parts > kMaxParts) parts = kMaxParts;
   s.parts = static_cast<int>(parts < 1 ? 1 : parts);

@@ -205,7 +205,7 @@ __device__ __forceinline__ int item_of(int r) {
   return r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
 }
 
-template <bool BF16, int D, bool kGrouped>
+template <bool BF16, int D, bool kGrouped, bool kOne>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           for (int kk = 0; kk < kKTile / 16; ++kk) {
             const uint64_t bd = v_desc + static_cast<uint64_t>((kk * 2048) >> 4);
             mma_f16_ts(tmem + kTmemO, ph + kk * 8, bd, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            mma_f16_ts(tmem + kTmemO, pl + kk * 8, bd, idesc_o, 1u);
+            if constexpr (!kOne) mma_f16_ts(tmem + kTmemO, pl + kk * 8, bd, idesc_o, 1u);
           }
           mma_commit(&bars->s_free[b]);  // also frees V stage b (two stages)
         }
@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           const float e0 = ex2_approx(x0);
           const float e1 = ex2_approx(x1);
           add2(sum4[c & 2], sum4[(c & 2) + 1], e0, e1);
-          if constexpr (BF16) {
+          if constexpr (kOne) {
+            hi_f[c / 2] = __uint_as_float(pack_half2<BF16>(e0, e1));
+          } else if constexpr (BF16) {
             // hi = the upper 16 bits of each fp32 p (a bf16 truncation), one byte
             // permute for the pair; lo = RN(p - hi), where p - hi is exact in fp32
             // and below one bf16 ulp of p, so hi + lo keeps ~16 significant bits
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
         }
         // P replaces S in this tile's buffer (S has been read into registers)
         tmem_st32(tmem + lane_base + b * kKTile, hi_f);
-        tmem_st32(tmem + lane_base + b * kKTile + kKTile / 2, lo_f);
+        if constexpr (!kOne) tmem_st32(tmem + lane_base + b * kKTile + kKTile / 2, lo_f);
         tmem_wait_st();
         // keys past the last one any row may see: zero their V rows once the tile
         // has landed (they may hold stale or unused-slot data; 0 * NaN is NaN)
@@ -709,16 +711,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
 // The kernel always needs opt-in shared memory.  The attribute belongs to the
 // module loaded in the current context and is lost with it (cudaDeviceReset,
 // another driver-API context), so it is set on every launch.
-template <bool BF16, int D, bool kGrouped>
+template <bool BF16, int D, bool kGrouped, bool kOne>
 cudaError_t ensure_prefill_smem() {
-  return cudaFuncSetAttribute(paged_prefill_kernel<BF16, D, kGrouped>,
+  return cudaFuncSetAttribute(paged_prefill_kernel<BF16, D, kGrouped, kOne>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmemBytes);
 }
 
-template <bool BF16, int D, bool kGrouped>
+template <bool BF16, int D, bool kGrouped, bool kOne>
 int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const PrefillParams& p, int num_seqs, int num_qtiles, cudaStream_t st) {
-  if (ensure_prefill_smem<BF16, D, kGrouped>() != cudaSuccess) return PA_ERR_CUDA;
+  if (ensure_prefill_smem<BF16, D, kGrouped, kOne>() != cudaSuccess) return PA_ERR_CUDA;
   // Persistent: one block per resident slot (Cfg<D>::kMinBlocks per SM), each
   // looping over its share of the (sequence, query tile, head) items.
   int device = 0, sms = 0;
@@ -729,14 +731,14 @@ int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
       static_cast<long long>(num_seqs) * (kGrouped ? p.num_kv_heads : p.num_heads) * num_qtiles;
   const long long slots = static_cast<long long>(sms) * Cfg<D>::kMinBlocks;
   const unsigned grid = static_cast<unsigned>(items < slots ? items : slots);
-  paged_prefill_kernel<BF16, D, kGrouped>
+  paged_prefill_kernel<BF16, D, kGrouped, kOne>
       <<<grid, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, tv, p, num_seqs, num_qtiles);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 // The tensor maps of a call, and its launch.  A box of the cache is one 16-key chunk, or half of one
 // with 8-token blocks; a box of q the rows of a tile, 64 channels wide.
-template <bool kGrouped>
+template <bool kGrouped, bool kOne>
 int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, const void* v_cache,
                 unsigned long long cache_rows, int num_seqs, int head_dim, int num_qtiles, bool bf16,
                 cudaStream_t st) {
@@ -756,12 +758,12 @@ int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, cons
       !encode_tensor_map(&tv, bf16, v_cache, 2, cdims, cstr, cbox))
     return PA_ERR_CUDA;
   switch ((bf16 ? 1 : 0) | (head_dim == 64 ? 0 : head_dim == 128 ? 2 : 4)) {
-    case 0: return launch_prefill<false, 64, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 1: return launch_prefill<true, 64, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 2: return launch_prefill<false, 128, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 3: return launch_prefill<true, 128, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 4: return launch_prefill<false, 256, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    default: return launch_prefill<true, 256, kGrouped>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 0: return launch_prefill<false, 64, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 1: return launch_prefill<true, 64, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 2: return launch_prefill<false, 128, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 3: return launch_prefill<true, 128, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    case 4: return launch_prefill<false, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    default: return launch_prefill<true, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
   }
 }
 
@@ -832,7 +834,7 @@ extern "C" int paged_attn_prefill_ex(const void* q, const int32_t* query_start,
   p.total_queries = total_queries;
   p.qscale = scale * kLog2e;
 
-  return run_prefill<false>(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, qtiles,
+  return run_prefill<false, false>(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, qtiles,
                             dtype == PA_BF16, static_cast<cudaStream_t>(stream));
 }
 
@@ -888,7 +890,7 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   p.tile_tokens = tile_tokens;
   p.inv_group = (65536 + group - 1) / group;
   p.lse = lse;
-  return run_prefill<true>(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim,
-                           static_cast<int>(qtiles), dtype == PA_BF16,
-                           static_cast<cudaStream_t>(stream));
+  const auto run = out_dtype == PA_F32 ? run_prefill<true, false> : run_prefill<true, true>;
+  return run(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, static_cast<int>(qtiles),
+             dtype == PA_BF16, static_cast<cudaStream_t>(stream));
 }
