@@ -672,16 +672,33 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  *   lse           NULL, or device float [total_queries][num_heads]: the natural logarithm of
  *                 a row's sum of e^(scale * <q, k_t>); rows outside every range are not written
  *   seq_order     as in pa_prefill_opts, or NULL
+ *   workspace     device, 16-byte aligned, scratch of this call alone, at least
+ *                 paged_attn_chunk_workspace_size(...) bytes; may be NULL where
+ *                 paged_attn_chunk_workspace_needed(...) is 0
+ * Arithmetic as in paged_attn_prefill where `out` is fp32.  For a half-precision `out` the
+ * probabilities enter P.V as one number of the cache's type: off by at most 2^-8 (bf16) or
+ * 2^-11 (fp16) of a weight, which is what the output's own rounding may be off by.
  * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x
  * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30.  Otherwise, checks
- * of the batch and arithmetic too, as paged_attn_prefill. */
+ * of the batch too, as paged_attn_prefill.
+ *
+ * paged_attn_chunk_workspace_size is the same for all calls that may use a workspace (few
+ * sequences with long tables): 304 x 128 rows of head_dim + 2 floats.
+ * paged_attn_chunk_workspace_needed is that size where a call of exactly these sizes uses it,
+ * and 0 where it neither touches one nor looks at its size. */
+size_t paged_attn_chunk_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int max_blocks_per_seq,
+                                       int max_query_len);
+size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int max_blocks_per_seq,
+                                         int max_query_len);
 int paged_attn_chunk(const void* q, const int32_t* query_start, int total_queries,
                      int max_query_len, const void* k_cache, const void* v_cache,
                      const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
                      int num_heads, int num_kv_heads, int head_dim, int block_size,
                      int max_blocks_per_seq, int num_blocks, float scale, int dtype, void* out,
-                     int out_dtype, float* lse, const int32_t* seq_order, int32_t* error_record,
-                     void* stream);
+                     int out_dtype, float* lse, const int32_t* seq_order, void* workspace,
+                     size_t workspace_bytes, int32_t* error_record, void* stream);
 
 /* weights[i][h][t] += sum over the last W_i of sequence i's queries, W_i = Q_i or at most
  * `window`, and the query heads of key head h, of e^(scale * <q, k_t> - lse), for the places

@@ -258,7 +258,9 @@ SIGNATURES = {
     "paged_attn_chunk": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                  c_float, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
-                                 c_void_p]),
+                                 c_size_t, c_void_p, c_void_p]),
+    "paged_attn_chunk_workspace_size": (c_size_t, [c_int] * 7),
+    "paged_attn_chunk_workspace_needed": (c_size_t, [c_int] * 7),
     "paged_chunk_weights": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p,
                                     c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                     c_float, c_int, c_int, c_void_p, c_int64, c_void_p, c_void_p]),
@@ -902,17 +904,35 @@ def _weights(t, device, rows, room):
     return t.shape[2]
 
 
+def paged_attn_chunk_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                    max_blocks_per_seq, max_query_len) -> int:
+    """Workspace bytes that serve every paged_attn_chunk call of this head_dim (0 where tables hold
+    at most 512 tokens)."""
+    return int(load_library().paged_attn_chunk_workspace_size(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_query_len))
+
+
+def paged_attn_chunk_workspace_needed(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                      max_blocks_per_seq, max_query_len) -> int:
+    """The same where a call of exactly these sizes uses a workspace (few sequences with long tables), 0
+    where it does not touch it."""
+    return int(load_library().paged_attn_chunk_workspace_needed(
+        num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, max_query_len))
+
+
 def paged_attn_chunk(q: torch.Tensor, query_start: torch.Tensor, max_query_len: int,
                      k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
                      seq_lens: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
                      out_dtype=torch.float32, lse: Optional[torch.Tensor] = None,
                      seq_order: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
                      error_record: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of each sequence's last tokens over its cached ones, query heads sharing key
     heads.  q [T,Hq,D]; query_start int32 [N+1]; caches [B,H,bs,D], Hq a multiple of H;
     block_tables int32 [N,MB]; seq_lens int32 [N], the new tokens counted; lse: optional float32
     [T,Hq], filled with the logarithm of each row's sum of exponentials; seq_order: optional int32
-    [N] dispatch order of the sequences."""
+    [N] dispatch order of the sequences; workspace: optional contiguous tensor of at least
+    paged_attn_chunk_workspace_size(...) bytes, made here if it is needed and not given."""
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape
@@ -932,12 +952,20 @@ def paged_attn_chunk(q: torch.Tensor, query_start: torch.Tensor, max_query_len: 
         out = _new_like(q, stream)
     else:
         out = _new_out((T, Hq, D), out_dtype, q.device, stream)
-    _check(load_library().paged_attn_chunk(
+    lib = load_library()
+    if workspace is None:
+        need = lib.paged_attn_chunk_workspace_needed(N, Hq, H, D, bs, MB, int(max_query_len))
+        if need:
+            workspace = _new_out((need,), torch.uint8, q.device, stream)
+    else:
+        _need_all(device, workspace.dtype, "workspace", (workspace, workspace.shape))
+        need = workspace.numel() * workspace.element_size()
+    _check(lib.paged_attn_chunk(
         q.data_ptr(), query_start.data_ptr(), T, int(max_query_len), k_cache.data_ptr(),
         v_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), N, Hq, H, D, bs, MB, B,
         float(scale), _DTYPE[dtype], out.data_ptr(), _DTYPE[out_dtype], _address(lse),
-        _address(seq_order), _record(error_record, device), _raw_stream(stream, device)),
-        "paged_attn_chunk")
+        _address(seq_order), _address(workspace), need, _record(error_record, device),
+        _raw_stream(stream, device)), "paged_attn_chunk")
     return out
 
 

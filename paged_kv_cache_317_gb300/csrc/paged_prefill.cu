@@ -64,6 +64,9 @@ constexpr int kQTile = 128;                       // query rows per block (MMA M
 constexpr int kKTile = 64;                        // keys per tile
 constexpr int kThreads = 224;                     // 4 softmax, K producer, MMA, V producer
 constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
+constexpr int kPartTiles = 8;                     // an item's keys are shared out by so many tiles
+constexpr int kMaxParts = 32;
+constexpr int kPartSlots = 304;                   // items, parts of items: two thread blocks an SM
 constexpr int kKStages = 2;                       // K ring depth (= the S buffers: a stage is freed by its S)
 constexpr int kVStages = 2;                       // V ring depth (= the S/P buffers: a stage is freed by its P.V)
 static_assert(kKStages == 2 && kVStages == 2,
@@ -135,6 +138,11 @@ struct PrefillParams {
   // r * inv_group >> 16 for r < 128, group <= 128
   int num_kv_heads, group, tile_tokens, inv_group;
   float* lse;         // [total_queries][num_heads], or NULL
+  // Grouped, with parts > 1: an item's keys are shared out over so many, each of whose O, not divided by
+  // its sum, and (reference, sum) go to [item][part][kQTile] rows of fp32.
+  int parts;
+  float* part_o;
+  float2* part_ml;
 };
 
 // One work item: 128-query tile `q0 / kQTile` of sequence `seq`, head `h`.
@@ -145,7 +153,7 @@ struct Tile {
   int rows;  // valid query rows
   int pos0;  // position of the first query
   int keys;  // keys any row of the tile sees
-  int T;     // 64-key tiles
+  int j0, T; // 64-key tiles: from j0 to before T
   bool valid;
 };
 
@@ -160,6 +168,8 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   w.valid = false;
   const int heads = kGrouped ? p.num_kv_heads : p.num_heads;
   const int tile_tokens = kGrouped ? p.tile_tokens : kQTile;
+  const int part = kGrouped ? it % p.parts : 0;
+  if (kGrouped) it /= p.parts;
   const int per_seq = heads * num_qtiles;
   const int z = it / per_seq, rem = it % per_seq;
   const int qt = num_qtiles - 1 - rem / heads;
@@ -168,7 +178,7 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   if (p.seq_order != nullptr) {
     seq = __ldg(p.seq_order + z);
     if (static_cast<unsigned>(seq) >= static_cast<unsigned>(num_seqs)) {
-      if (report && rem == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, z, seq);
+      if (report && rem == 0 && part == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, z, seq);
       return w;
     }
   }
@@ -184,7 +194,7 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   const bool bad_q = nq < 0 || nq > L || w.q_begin < 0 || w.q_begin > p.total_queries - nq ||
                      nq > num_qtiles * tile_tokens;
   if (bad_len || bad_q) {
-    if (report && rem == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
+    if (report && rem == 0 && part == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     if (bad_q) return w;
   }
   w.q0 = qt * tile_tokens;
@@ -194,6 +204,13 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   w.pos0 = L - nq + w.q0;
   w.keys = w.pos0 + tokens;
   w.T = (w.keys + kKTile - 1) / kKTile;
+  w.j0 = 0;
+  if (kGrouped && p.parts > 1) {  // (a part begins where the producers look blocks up)
+    const int runs = (w.T + kPartTiles - 1) / kPartTiles;
+    w.j0 = runs * part / p.parts * kPartTiles;
+    w.T = min(w.T, runs * (part + 1) / p.parts * kPartTiles);
+    if (w.j0 >= w.T) return w;
+  }
   w.valid = true;
   return w;
 }
@@ -257,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
-  const int n_items = num_seqs * kv_heads * num_qtiles;
+  const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
 
   // Key tiles are counted across the block's items: tile g of the block uses K
   // and V stage g & 1 and S/P buffer g & 1, and its barriers' phases are g >> 1.
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       if (!w.valid) continue;
       const int32_t* table = p.block_tables + static_cast<size_t>(w.seq) * p.max_blocks;
       int blk = 0, blk_hi = 0;
-      for (int j = 0; j < w.T; ++j) {
+      for (int j = kGrouped ? w.j0 : 0; j < w.T; ++j) {
         if ((j & 7) == 0) {
           // lane l looks up the physical block of 16-key chunk 4*j + l (8 tiles'
           // worth) (and, with 8-token blocks, that of its second half)
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           }
         }
         kv_issued = g + 1;
-        if (!is_v && j == 0) {
+        if (!is_v && j == (kGrouped ? w.j0 : 0)) {
           // This item's Q tile, once every S of the previous item has completed
           // (issued after K(0) so that tile's latency overlaps the wait).
           if (lane == 0) {
@@ -425,10 +442,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           mma_started = 1;
           return true;
         };
-        ok = issue_s(g0, w.T == 1);
-        for (int j = 0; ok && j < w.T; ++j) {
+        const int n = kGrouped ? w.T - w.j0 : w.T;  // of the item's tiles
+        ok = issue_s(g0, n == 1);
+        for (int j = 0; ok && j < n; ++j) {
           const int gg = g0 + j, b = gg & 1;
-          if (j + 1 < w.T && !issue_s(gg + 1, j + 2 == w.T)) {
+          if (j + 1 < n && !issue_s(gg + 1, j + 2 == n)) {
             ok = false;
             break;
           }
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           }
           mma_commit(&bars->s_free[b]);  // also frees V stage b (two stages)
         }
-        g = g0 + w.T;
+        g = g0 + n;
         ++items;
       }
       if (!ok) {
@@ -476,8 +494,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       const int token = kGrouped ? r * p.inv_group >> 16 : r;  // of the tile
       const int pos = row_valid ? w.pos0 + token : -1;
       float m_ref = -INFINITY, l = 0.f;  // reference max (log2 units) and running sum
-      for (int j = 0; j < w.T; ++j) {
-        const int gg = g + j, b = gg & 1;
+      const int j0 = kGrouped ? w.j0 : 0;
+      for (int j = j0; j < w.T; ++j) {
+        const int gg = g + j - j0, b = gg & 1;
         ok = __all_sync(kFullMask, mbar_wait_bounded(&bars->s_full[b], (gg >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
         }
         const float rowsum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
         // O must not change under a running P.V: rescaling waits for P.V(gg-1).
-        if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
+        if (j > j0 && __any_sync(kFullMask, alpha != 1.f)) {
           ok = __all_sync(kFullMask,
                           mbar_wait_bounded(&bars->s_free[(gg - 1) & 1], ((gg - 1) >> 1) & 1));
           if (!ok) break;
@@ -592,34 +611,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       if (!ok) break;
       // the item's last P.V (earlier ones finish first: they come from one thread
       // into the same accumulator), then the epilogue; O is then free
-      const int g_last = g + w.T - 1;
+      const int g_last = g + w.T - j0 - 1;
       ok = __all_sync(kFullMask,
                       mbar_wait_bounded(&bars->s_free[g_last & 1], (g_last >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool whole = !kGrouped || p.parts == 1;
+      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       // Rows leave through the warp's 2 KB of the staging buffer, 64 bytes of
       // each at a time: each lane writes its row's piece, then the warp stores
       // whole 64-byte row segments (8 rows per instruction) rather than 16
       // bytes of 32 rows.  Pieces sit at an XOR of (row / 2) % 4 so that
       // neither side has bank conflicts.
-      const int esz = p.out_dtype == PA_F32 ? 4 : 2;
+      const int esz = p.out_dtype == PA_F32 ? 4 : 2;  // (a part's: 4)
       const size_t row_bytes = static_cast<size_t>(p.num_heads) * D * esz;
       const int first_head = kGrouped ? w.h * p.group : w.h, first = kGrouped ? 0 : warp * 32;
       char* out_warp = static_cast<char*>(p.out) +
                        (static_cast<size_t>(w.q_begin + w.q0 + first) * p.num_heads + first_head) *
                            D * esz;
+      if (!whole) out_warp = reinterpret_cast<char*>(p.part_o + static_cast<size_t>(it) * kQTile * D);
       // where the warp's row begins, from out_warp
       auto row_at = [&](int row) -> size_t {
         if constexpr (kGrouped) {
           const int rr = warp * 32 + row, t = rr * p.inv_group >> 16;
+          if (!whole) return static_cast<size_t>(rr) * (D * 4);
           return t * row_bytes + static_cast<size_t>(rr - t * p.group) * (D * esz);
         } else {
           return row * row_bytes;
         }
       };
       if constexpr (kGrouped) {
-        if (p.lse != nullptr && row_valid)  // ln of the sum of e^logit
+        if (!whole) {
+          if (row_valid) p.part_ml[static_cast<size_t>(it) * kQTile + r] = make_float2(m_ref, l);
+        } else if (p.lse != nullptr && row_valid)  // ln of the sum of e^logit
           p.lse[static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + first_head +
                 (r - token * p.group)] = (m_ref + log2f(l)) * kLn2;
       }
@@ -672,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           put(v, cc * 64);
         }
       }
-      g += w.T;
+      g += w.T - j0;
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -707,6 +731,66 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   }
 }
 
+// Joins the parts of an item: a warp a row, kJoinRows rows a thread block.
+constexpr int kJoinRows = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinRows * 32)
+    paged_chunk_join_kernel(const PrefillParams p, void* out, const int out_dtype, const int num_seqs,
+                            const int num_qtiles) {
+  constexpr int kVec = D / 32, kAhead = D == 256 ? 4 : 8;
+  const int lane = threadIdx.x & 31, item = blockIdx.x / (kQTile / kJoinRows);
+  const int r = blockIdx.x % (kQTile / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  PrefillParams whole = p;
+  whole.parts = 1;
+  const Tile w = decode_tile<true>(whole, item, num_seqs, num_qtiles, false);
+  if (!w.valid || r >= w.rows) return;
+  const int runs = (w.T + kPartTiles - 1) / kPartTiles;
+  // lane i: part i, which may have had no keys
+  const size_t row0 = static_cast<size_t>(item) * p.parts * kQTile + r;
+  const bool mine = lane < p.parts && runs * lane / p.parts < runs * (lane + 1) / p.parts;
+  const float2 ml = mine ? p.part_ml[row0 + static_cast<size_t>(lane) * kQTile] : make_float2(-INFINITY, 0.f);
+  float M = ml.x;  // (a reference is a number or -infinity)
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
+  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+  float l = ml.x == -INFINITY ? 0.f : f * ml.y;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
+  float acc[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+  const float* from = p.part_o + row0 * D + lane * kVec;
+#pragma unroll 1
+  for (int i0 = 0; i0 < p.parts; i0 += kAhead) {
+    float v[kAhead][kVec], g[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      g[k] = __shfl_sync(kFullMask, f, (i0 + k) & 31);
+      if (i0 + k < p.parts && g[k] != 0.f) {
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2)
+          *reinterpret_cast<float2*>(&v[k][e]) =
+              *reinterpret_cast<const float2*>(from + static_cast<size_t>(i0 + k) * kQTile * D + e);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k < p.parts && g[k] != 0.f) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(g[k], v[k][e], acc[e]);
+      }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) acc[e] *= inv;
+  const int token = r * p.inv_group >> 16;
+  const size_t row = static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + w.h * p.group +
+                     (r - token * p.group);
+  store_out<kVec>(out, row * D + lane * kVec, acc, out_dtype);
+  if (p.lse != nullptr && lane == 0) p.lse[row] = (M + log2f(l)) * kLn2;
+}
+
 // ------------------------------------------------------------------ host side
 // The kernel always needs opt-in shared memory.  The attribute belongs to the
 // module loaded in the current context and is lost with it (cudaDeviceReset,
@@ -727,8 +811,9 @@ int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_CUDA;
-  const long long items =
-      static_cast<long long>(num_seqs) * (kGrouped ? p.num_kv_heads : p.num_heads) * num_qtiles;
+  const long long items = static_cast<long long>(num_seqs) *
+                          (kGrouped ? p.num_kv_heads * static_cast<long long>(p.parts) : p.num_heads) *
+                          num_qtiles;
   const long long slots = static_cast<long long>(sms) * Cfg<D>::kMinBlocks;
   const unsigned grid = static_cast<unsigned>(items < slots ? items : slots);
   paged_prefill_kernel<BF16, D, kGrouped, kOne>
@@ -765,6 +850,19 @@ int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, cons
     case 4: return launch_prefill<false, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
     default: return launch_prefill<true, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
   }
+}
+
+// The parts that an item's keys are shared out into: as many as fill the card, where there are few items
+// and tables are long.
+int chunk_parts(long long items, long long cap) {
+  const long long runs = (cap + kPartTiles * kKTile - 1) / (kPartTiles * kKTile);
+  long long parts = items > 0 ? kPartSlots / items : 1;
+  if (parts > runs) parts = runs;
+  if (parts > kMaxParts) parts = kMaxParts;
+  return static_cast<int>(parts < 1 ? 1 : parts);
+}
+size_t chunk_workspace(int head_dim) {
+  return static_cast<size_t>(kPartSlots) * kQTile * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
@@ -838,13 +936,38 @@ extern "C" int paged_attn_prefill_ex(const void* q, const int32_t* query_start,
                             dtype == PA_BF16, static_cast<cudaStream_t>(stream));
 }
 
+extern "C" size_t paged_attn_chunk_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                  int head_dim, int block_size, int max_blocks_per_seq,
+                                                  int max_query_len) {
+  if (num_seqs <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || max_query_len <= 0 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return 0;
+  // enough for the one sequence that a smaller call may have, whatever this one uses
+  return chunk_parts(1, static_cast<long long>(max_blocks_per_seq) * block_size) > 1 ? chunk_workspace(head_dim) : 0;
+}
+
+extern "C" size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
+                                                    int head_dim, int block_size, int max_blocks_per_seq,
+                                                    int max_query_len) {
+  const size_t most = paged_attn_chunk_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                      max_blocks_per_seq, max_query_len);
+  const int group = most ? num_heads / num_kv_heads : 1;
+  if (most == 0 || group > kQTile) return 0;
+  const int tile_tokens = kQTile / group;
+  const long long tiles = (static_cast<long long>(max_query_len) + tile_tokens - 1) / tile_tokens;
+  return chunk_parts(num_seqs * tiles * num_kv_heads, static_cast<long long>(max_blocks_per_seq) * block_size) > 1
+             ? most : 0;
+}
+
 extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int total_queries,
                                 int max_query_len, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
                                 int num_heads, int num_kv_heads, int head_dim, int block_size,
                                 int max_blocks_per_seq, int num_blocks, float scale, int dtype,
                                 void* out, int out_dtype, float* lse, const int32_t* seq_order,
-                                int32_t* error_record, void* stream) {
+                                void* workspace, size_t workspace_bytes, int32_t* error_record,
+                                void* stream) {
   NvtxRange range("paged_attn_chunk");
   if (num_seqs < 0 || total_queries < 0 || max_query_len < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
       num_heads % num_kv_heads != 0 || block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
@@ -869,7 +992,8 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   if (num_seqs == 0 || total_queries == 0 || max_query_len == 0) return PA_OK;
   if (!q || !query_start || !k_cache || !v_cache || !block_tables || !seq_lens || !out)
     return PA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned16(workspace))
     return PA_ERR_INVALID_ARG;
   PrefillParams p{};
   p.seq_order = seq_order;
@@ -890,7 +1014,25 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   p.tile_tokens = tile_tokens;
   p.inv_group = (65536 + group - 1) / group;
   p.lse = lse;
+  p.parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads * qtiles,
+                        static_cast<long long>(max_blocks_per_seq) * block_size);
+  if (p.parts > 1) {
+    if (!workspace || workspace_bytes < chunk_workspace(head_dim)) return PA_ERR_INVALID_ARG;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(kPartSlots) * kQTile * head_dim);
+    p.out_dtype = PA_F32;
+  }
   const auto run = out_dtype == PA_F32 ? run_prefill<true, false> : run_prefill<true, true>;
-  return run(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, static_cast<int>(qtiles),
-             dtype == PA_BF16, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int tiles = static_cast<int>(qtiles);
+  const int status = run(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, tiles, dtype == PA_BF16, st);
+  if (status != PA_OK || p.parts == 1) return status;
+  const unsigned grid = static_cast<unsigned>(num_seqs) * num_kv_heads * tiles * (kQTile / kJoinRows);
+  if (head_dim == 64)
+    paged_chunk_join_kernel<64><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, num_seqs, tiles);
+  else if (head_dim == 128)
+    paged_chunk_join_kernel<128><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, num_seqs, tiles);
+  else
+    paged_chunk_join_kernel<256><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, num_seqs, tiles);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -20,7 +20,7 @@ def binding(lib):
 def test_chunk_refuses(lib):
     def call(**kw):
         a = dict(q=P, start=P, T=64, most=8, kc=P, vc=P, bt=P, sl=P, N=4, Hq=8, H=2, D=64, bs=16, MB=4, B=64,
-                 scale=0.125, dt=0, out=P, odt=2, lse=P, order=None, err=None, stream=None)
+                 scale=0.125, dt=0, out=P, odt=2, lse=P, order=None, ws=None, wsb=0, err=None, stream=None)
         a.update(kw)
         return lib.paged_attn_chunk(*a.values())
 
@@ -29,10 +29,18 @@ def test_chunk_refuses(lib):
                dict(B=0), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(MB=1 << 28),
                dict(B=1 << 27), dict(N=1 << 20, most=1 << 16), dict(q=None), dict(start=None), dict(kc=None),
                dict(vc=None), dict(bt=None), dict(sl=None), dict(out=None), dict(q=P + 8), dict(kc=P + 8),
-               dict(vc=P + 8), dict(out=P + 8)):
+               dict(vc=P + 8), dict(out=P + 8), dict(ws=P + 8, wsb=1 << 30)):
         assert call(**kw) == INV, kw
     for kw in (dict(D=96), dict(dt=2), dict(odt=3), dict(bs=24), dict(bs=4), dict(Hq=258)):
         assert call(**kw) == UNS, kw
+    # few sequences with long tables: no workspace, and one that is a byte short
+    long = dict(N=1, MB=4096, B=8192)
+    size, needed = lib.paged_attn_chunk_workspace_size, lib.paged_attn_chunk_workspace_needed
+    need = needed(1, 8, 2, 64, 16, 4096, 8)
+    assert need == size(1, 8, 2, 64, 16, 4096, 8) == size(500, 8, 2, 64, 16, 4096, 800) > 0
+    assert call(**long) == INV and call(ws=P, wsb=need - 1, **long) == INV
+    assert needed(500, 8, 2, 64, 16, 4096, 800) == needed(1, 8, 2, 64, 16, 32, 8) == size(1, 8, 2, 64, 16, 32, 8) == 0
+    assert size(0, 8, 2, 64, 16, 4096, 8) == size(1, 7, 2, 64, 16, 4096, 8) == size(1, 8, 2, 96, 16, 4096, 8) == 0
 
 
 def test_chunk_weights_refuse(lib):

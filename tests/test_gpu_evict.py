@@ -12,6 +12,8 @@ the scaling to base 2 and the subtraction of a maximum.  Over n tokens:
 * outputs: twice the weights' bound and 2^-16 (bf16) or 2^-21 (fp16), the two half-precision numbers of a
   probability, of sum_t w_t |v_t|; fp16 numbers have steps of 2^-24 at least, so that each token may be off
   by 2^-25 of a largest weight of at least 1; a half-precision output is rounded by half a step on top.
+  Chunks with half-precision outputs have probabilities in one number: 2^-8 (bf16) or 2^-11 (fp16), the half
+  step of its rounding, in place of 2^-16 and 2^-21.
 """
 
 import numpy as np
@@ -56,10 +58,12 @@ def close(got, want, tol, what):
     assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3].tolist(), got[bad][:3], want[bad][:3])
 
 
-def out_bound(b, w, reach, n, table, length, dtype, out_dtype):
+def out_bound(b, w, reach, n, table, length, dtype, out_dtype, one=False):
     want, spread, size = OE.weighted(w, f64(b["vc"]), table, length)
     d = (b["D"] + 8) * U * reach
     half = 2.0 ** -16 if dtype is BF else 2.0 ** -21
+    if one and out_dtype is not torch.float32:
+        half = 2.0 ** -8 if dtype is BF else 2.0 ** -11
     tol = (4 * (d + (n + 16) * U) + half)[..., None] * spread + (2.0 ** -25 * size if dtype is FH else 0)
     if out_dtype is not torch.float32:
         tol = tol + half_ulp(np.abs(want) + tol, out_dtype)
@@ -98,7 +102,8 @@ def check_chunk(b, out, lse, skip=()):
         places = int(length) - (e - a) + np.arange(e - a)
         w, want_lse, reach = OE.softmax_rows(q[a:e], kc, b["tables"][i], int(length), places, b["scale"])
         n = (places + 1)[:, None]
-        want, tol = out_bound(b, w, reach, n, b["tables"][i], int(length), b["q"].dtype, out.dtype)
+        want, tol = out_bound(b, w, reach, n, b["tables"][i], int(length), b["q"].dtype, out.dtype,
+                              one=True)
         close(out[a:e], want, tol, f"out of sequence {i}")
         close(lse[a:e], want_lse, (b["D"] + 8) * U * reach + (n + 16) * U + 2 * U * np.abs(want_lse),
               f"lse of sequence {i}")
@@ -123,13 +128,18 @@ def test_chunk_matches_the_oracle(B, shape, lens, news):
     check_chunk(b, out, lse)
 
 
-def test_chunk_with_a_head_of_its_own_each_equals_the_prefill(B):
-    b = chunk_batch(5, [300, 40, 777], [129, 7, 500], 4, 4, 128, 16, BF)
+@pytest.mark.parametrize("lens", [[300, 40, 777], [300, 40, 512]])
+def test_chunk_with_a_head_of_its_own_each_agrees_with_the_prefill(B, lens):
+    """Where tables hold at most 512 tokens, so that no item's keys are shared out, bit for bit."""
+    b = chunk_batch(5, lens, [129, 7, 500], 4, 4, 128, 16, BF)
     out, lse, _ = run_chunk(B, b)
     want = torch.full_like(out, 7)
     B.paged_attn_prefill(b["q"], dev(b["start"]), b["most"], b["kc"], b["vc"], dev(b["tables"]), dev(b["lens"]),
                          b["scale"], out=want)
-    assert torch.equal(out, want)
+    check_chunk(b, out, lse)
+    check_chunk(b, want, lse)
+    if max(lens) <= 512:
+        assert torch.equal(out, want)
     # in another dispatch order, and without lse, the same bits
     again, _, _ = run_chunk(B, b, seq_order=dev([2, 0, 1]))
     assert torch.equal(out, again)
@@ -143,6 +153,25 @@ def test_few_rows_over_a_long_context(B):
     for lens, news in (([20011], [3]), ([9000, 17, 12345], [1, 5, 2]), ([30000], [40])):
         b = chunk_batch(11, lens, news, 8, 1, 64, 16, BF)
         out, lse, rec = run_chunk(B, b)
+        assert rec == [0, 0, 0, 0]
+        check_chunk(b, out, lse)
+        out, lse, _ = run_chunk(B, b, out_dtype=BF)
+        check_chunk(b, out, lse)
+        need = B.paged_attn_chunk_workspace_needed(len(lens), 8, 1, 64, 16, b["tables"].shape[1], b["most"])
+        assert need == B.paged_attn_chunk_workspace_size(len(lens), 8, 1, 64, 16, b["tables"].shape[1], b["most"]) > 0
+        given = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        again, _, _ = run_chunk(B, b, out_dtype=BF, workspace=given)
+        assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_chunks_shared_out_over_parts(B, shape):
+    """Lengths around the ends of parts, one sequence without queries, with an order."""
+    Hq, H, D, bs, dtype = shape
+    lens, news = [2049, 511, 512, 513, 1000, 3000], [2, 3, 5, 1, 0, 4]
+    b = chunk_batch(12, lens, news, Hq, H, D, bs, dtype)
+    for kw in ({}, dict(seq_order=dev([5, 4, 3, 2, 1, 0]))):
+        out, lse, rec = run_chunk(B, b, **kw)
         assert rec == [0, 0, 0, 0]
         check_chunk(b, out, lse)
 
