@@ -26,12 +26,16 @@ namespace {
 
 constexpr int kChunk = 16;      // tokens per stage
 constexpr int kWarps = 4;       // warps per thread block
-constexpr int kStages = 2;
+// 256 channels: one stage of 16 KB a warp lets three thread blocks onto an SM, two stages one (16 x 8 rows of
+// up to 8000 tokens: 122 us, 168); 128 channels: two (64 x 40 rows of up to 2048: 206 us, with three 219).
+template <int D>
+constexpr int kStagesOf = D == 256 ? 1 : 2;
 constexpr int kAlign = 1024;    // a swizzled box must start on 1024 bytes
 constexpr int kHeader = 256;    // barriers
 constexpr int kMaxParts = 64;   // thread blocks per row: 8 for each warp of the join
-constexpr int kFew = 304;       // fewer rows are shared out over that many thread blocks, two an SM,
-constexpr int kShares = 4096;   // more over so many, for rows of unequal length
+constexpr int kFew = 304;       // thread blocks of a few rows, and of more of them, which may be of unequal
+constexpr int kShares = 4096;   // length (52 x 3 rows of up to 21,000 tokens, 16 heads: 200 us; over 304: 491)
+constexpr int kFewRows = 19;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTokens = 2048;  // tokens of a join's thread block
 constexpr int kJoinCols = 64;      // columns whose maxima and sums it holds at a time
@@ -73,12 +77,21 @@ __device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
   return 1.f / l;
 }
 
+// The rings, or the joined sums, which take their place.
+template <int D, int NT>
+constexpr size_t ring_bytes() {
+  const size_t ring = static_cast<size_t>(kWarps) * kStagesOf<D> * 2 * kChunk * D * 2;
+  const size_t join = static_cast<size_t>(kWarps) * 8 * NT * (D + 4) * sizeof(float) +
+                      (kWarps + 1) * 8 * NT * sizeof(float2);
+  return ring > join ? ring : join;
+}
+
 template <class Tag, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32)
     decode_weights_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const DecodeWeightsParams p) {
   using Attn = WarpAttn<Tag, D, NT>;
-  constexpr int kCols = 8 * NT, kPitch = D + 4, kTile = Attn::kTileBytes;
+  constexpr int kCols = 8 * NT, kPitch = D + 4, kTile = Attn::kTileBytes, kStages = kStagesOf<D>;
   if (threadIdx.x == 0) {
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
@@ -154,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const uint32_t ring_addr = smem_addr(ring);
   float* logits = p.logits != nullptr
                       ? p.logits + static_cast<size_t>(row) * p.cols * p.pitch
-                      : reinterpret_cast<float*>(ring0 + kWarps * kStages * 2 * kTile);
+                      : reinterpret_cast<float*>(ring0 + ring_bytes<D, NT>());
   bool aborted = false;
   int done = 0;
   for (; done < mine; ++done) {
@@ -381,14 +394,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   }
 }
 
-template <int D, int NT>
-constexpr size_t ring_bytes() {
-  const size_t ring = static_cast<size_t>(kWarps) * kStages * 2 * kChunk * D * 2;
-  const size_t join = static_cast<size_t>(kWarps) * 8 * NT * (D + 4) * sizeof(float) +
-                      (kWarps + 1) * 8 * NT * sizeof(float2);
-  return ring > join ? ring : join;
-}
-
 struct Shape {
   bool inside;       // logits in shared memory
   int parts, pitch;
@@ -403,7 +408,9 @@ Shape shape_for(long long rows, int tiles, int group, long long cap) {
   const size_t bare = kHeader + kAlign + ring_bytes<D, NT>();
   // + 4: the columns of a warp's stores in different banks
   const size_t held = static_cast<size_t>(cols) * (padded + 4) * sizeof(float);
-  if (tiles == 1 && bare + held <= 113 * 1024 && (rows >= 152 || cap <= 1024)) {
+  // Only where there are many rows, or short ones: 32 x 8 rows of up to 4000 tokens of 64 channels take 75 us
+  // so, 47 us in parts, 128 x 8 of up to 1000 of 128 channels 66 and 75.
+  if (tiles == 1 && bare + held <= 113 * 1024 && (rows >= 1024 || cap <= 1024)) {
     s.inside = true;
     s.parts = 1;
     s.pitch = padded + 4;
@@ -413,7 +420,7 @@ Shape shape_for(long long rows, int tiles, int group, long long cap) {
   s.pitch = padded;
   s.smem = bare;
   const long long most = (cap + 255) / 256;
-  long long parts = (rows < kFew ? kFew : kShares) / rows;
+  long long parts = (rows <= kFewRows ? kFew : kShares) / rows;
   if (parts > most) parts = most;
   if (parts > kMaxParts) parts = kMaxParts;
   s.parts = static_cast<int>(parts < 1 ? 1 : parts);
