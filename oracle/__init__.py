@@ -26,6 +26,9 @@ Modules:
                  block table; per-partition partials and their log-sum-exp merge;
                  several causal query tokens per sequence (chunked prefill).
   cache_ops      slot-mapped append and whole-block copy, element by element.
+  sparse         rotary append, key bounds, block scores and lists, attention over
+                 listed blocks.
+  evict          softmax weights of cached tokens with shared key heads, and eviction.
   allocator_model  reference model of the block allocator (free list, refcounts,
                  fork, copy-on-write append, free) and its invariants.
   content        logical token contents of sequences under add/fork/append/free.

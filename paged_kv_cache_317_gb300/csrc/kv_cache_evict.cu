@@ -4,10 +4,9 @@
 // In place this is a gather within one array, safe in order: kept[j] >= j, so a row that is still to
 // be read (for place j' > j, from a place >= j') is never one that place j overwrites.  K and V are
 // moved apart.  A thread block, or for few lists a cluster, takes one list and goes through it in
-// rounds: every thread loads its pieces of the round's rows into registers (64 KB a thread block), looks
-// up rows of the next round, a barrier, every thread stores its pieces.  Loads of later rounds may run
-// ahead of the stores of earlier ones; only the loads of a round itself have to be over, which the
-// barrier sees to.
+// rounds: every thread loads its pieces of the round's rows into registers and looks up rows of the
+// next round, a barrier, every thread stores its pieces.  Loads of later rounds may run ahead of the
+// stores of earlier ones; only the loads of a round itself have to be over, which the barrier sees to.
 // A move and nothing else: bound by HBM for batches, by a round's latency (rows, barrier, stores) for one
 // sequence.
 #include <cuda_runtime.h>
@@ -27,8 +26,12 @@ struct Round {
   static constexpr int kMaxRows = 2 * kThreads;  // rows that it looks up at most
   static constexpr int kBlocks = 512 / kThreads; // an SM, as registers allow
 };
-using Long = Round<256, 16>;  // 64 KB
-using Short = Round<64, 8>;   // 8 KB: 27 x 40 lists of 19 rows of 64 channels 7.6 us, with the long one 23
+// Few lists: 64 KB, in clusters besides (8 + 8 lists of 4096 rows of 128 channels: 11.5 us, 29 with the other).
+// Many: 16 KB, of which an SM has eight thread blocks whose loads and stores take turns (1024 lists of 1024 rows:
+// 94 us, 99 with the other; 2048 of 128: 21 us, 31).
+using Few = Round<256, 16>;
+using Many = Round<64, 16>;
+constexpr int kMany = 608;  // lists, four an SM
 
 struct EvictParams {
   uint4* k;
@@ -212,8 +215,7 @@ extern "C" int kv_cache_evict(void* k_cache, void* v_cache, const int32_t* block
   p.num_blocks = num_blocks;
   p.inv_vecs = ((1u << 20) + p.vecs - 1) / p.vecs;
   const long long longest = num_kept < cap ? num_kept : cap;
-  // a list that two short rounds hold
-  const bool fits = longest * p.vecs <= 2 * Short::kThreads * Short::kPieces;
-  return fits ? launch<Short>(p, num_seqs, longest, static_cast<cudaStream_t>(stream))
-              : launch<Long>(p, num_seqs, longest, static_cast<cudaStream_t>(stream));
+  return 2ll * num_seqs * num_kv_heads >= kMany
+             ? launch<Many>(p, num_seqs, longest, static_cast<cudaStream_t>(stream))
+             : launch<Few>(p, num_seqs, longest, static_cast<cudaStream_t>(stream));
 }

@@ -222,3 +222,11 @@ def test_batch_evict_is_all_or_nothing(binding):
     a.batch_evict([1, 2], 3)
     assert a.num_free() == 7 and a.length(1) == a.length(2) == 3
     a.check()
+
+
+def test_the_example_is_the_one_shown():
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = open(os.path.join(root, "paged_kv_cache_317_gb300", "examples", "bounded_step.py")).read()
+    body = code.split('"""', 2)[2].strip()
+    assert body in open(os.path.join(root, "README.md")).read()

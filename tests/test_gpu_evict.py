@@ -740,3 +740,20 @@ def test_the_largest_batch(B):
                  lambda: B.kv_cache_evict(kc, vc, tables, lens, kept)):
         with pytest.raises(B.PagedKVError, match="INVALID_ARG"):
             call()
+
+
+def test_the_example_runs(B):
+    """paged_kv_cache_317_gb300/examples/bounded_step.py: its last step is the oracle's for the cache it has."""
+    import os
+    import runpy
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = runpy.run_path(os.path.join(root, "paged_kv_cache_317_gb300", "examples", "bounded_step.py"))
+    lens = env["lengths"].cpu().numpy()
+    assert lens.tolist() == [512 + 100 % 64, 300 + 100] and env["alloc"].num_free() == 1024 - 35 - 25
+    b = dict(lens=lens, tables=env["tables"].cpu().numpy(), kc=env["kc"], vc=env["vc"], q=env["q"], bs=16,
+             scale=128 ** -0.5, D=128, H=8)
+    w = torch.zeros_like(env["weights"])
+    out = B.paged_attn_decode_weights(env["q"], env["kc"], env["vc"], env["tables"], env["lengths"], b["scale"], w)
+    assert torch.equal(out, env["out"])
+    check_decode(b, torch.zeros_like(w), w, out)
+    assert bool(torch.isfinite(env["weights"]).all()) and not bool(env["weights"][0, :, 548:].any())
