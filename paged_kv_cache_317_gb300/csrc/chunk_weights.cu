@@ -5,21 +5,27 @@
 // with the rows' lse from the chunk's attention, so one pass over the keys does.
 //
 //  * Work item = (sequence, key head, 256 tokens).  S^T = K.Q^T: the tokens are the rows of the product
-//    (TMEM lanes), so that a token's sum over rows is one thread's.  Two warpgroups take 128 tokens each
-//    (of every 16 the first and the last 8: a box of 16 rows then is one copy, whatever head_dim);
-//    the query rows, (token, head) packed 128 to a tile, go by as columns.  Every token is one thread's of
-//    one item: no atomics, the same bits on every run.
+//    (TMEM lanes), so that a token's sum over rows is one thread's.  Two warpgroups take 128 tokens each, of
+//    every 16 the first and the last 8 (a box of 16 rows then is one copy, whatever head_dim: 25 % faster
+//    loads than a box for each 64 channels); the query rows, (token, head) packed 128 to a tile, go by as
+//    columns.  A token's weight is added to by one thread, once: the same bits on every run.
 //  * Persistent, one thread block an SM.  The items that exist are counted from the lengths, so that none
 //    is dealt out in vain.  Where the window's tiles stay in shared memory a block takes a contiguous run
-//    of items and loads them once a key head; else block b takes items b, b + grid, ...: heads innermost,
-//    so that the items of a causal triangle are shared out alike.
+//    of items and loads them once a key head; else block b takes items b, 2 grid - 1 - b, 2 grid + b, ...,
+//    heads innermost, so that the items of a causal triangle are shared out alike; few items of many tiles
+//    are a cluster's each, whose blocks take its tiles in turn.
 //  * 11 warps: two softmax warpgroups, a producer (TMA boxes of 16 rows of K through the block table, boxes
-//    of whole tiles of Q), an issuer of products for each warpgroup (one thread issues a product in about
-//    the time that it runs, and has barriers to wait for besides).  Each warpgroup has two 128-column buffers of S in
-//    TMEM: one is read while the next product runs.
+//    of whole tiles of Q), an issuer of products for each warpgroup (one thread issues a product in about the
+//    time that it runs, and has barriers to wait for besides: 32 sequences, 64 heads, window 32: 186 us with
+//    one issuer, 165 with two).  Each warpgroup has two 128-column buffers of S in TMEM: one is read while
+//    the next product runs.
 //  * Masks only where a tile of rows meets tokens that some of its rows do not see, or ends short.
 //  * Every wait is bounded (one second); on a timeout the block records PA_ERR_TIMEOUT, waits (bounded) for
 //    its copies and products, frees its TMEM and returns.
+// Bound by the exchange between products and softmax: a step of 256 tokens x 128 rows takes about 2500
+// clocks, of which the products run for 1026 and the exponentials for 1024; read beside the products, which
+// use up what shared memory gives, the lse alone cost some 700 (2134 clocks for the arithmetic of a step,
+// 1401 without them).  The same case, 652 MB and 157 TFLOP: 162 us, 4.0 TB/s, 970 TFLOP/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -48,28 +54,28 @@ struct Cfg {
   static constexpr int kKBytes = kTokens * D * 2;         // 32 / 64 / 128 KB
   static constexpr int kChunkBytes = 16 * D * 2;          // a box: 16 tokens of K
   static constexpr int kQBytes = kRows * D * 2;           // 16 / 32 / 64 KB
-  static constexpr int kKStages = D <= 128 ? 2 : 1;
-  static constexpr int kQStages = D <= 128 ? 2 : 1;
+  static constexpr int kKStages = D == 64 ? 4 : D == 128 ? 2 : 1;
+  static constexpr int kQStages = D == 256 ? 1 : 2;
   static constexpr int kOffQ = kKStages * kKBytes;
   static constexpr int kOffLse = kOffQ + kQStages * kQBytes;       // [warpgroup][2][kRows] floats
   static constexpr int kOffSums = kOffLse + 2 * 2 * kRows * 4;  // [2][kMaxCluster][kTokens] floats
   static constexpr int kOffCount = kOffSums + 2 * kMaxCluster * kTokens * 4;  // [kLists] ints
   static constexpr int kOffBar = kOffCount + kLists * 4;
-  static constexpr int kUsed = kOffBar + 256 + 1024;               // 1 KB to align the base
+  static constexpr int kUsed = kOffBar + 512 + 1024;               // 1 KB to align the base
   // one block an SM, which takes all 512 TMEM columns
   static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
   static_assert(kSmemBytes <= 227 * 1024, "one block per SM");
 };
 
 struct Bars {
-  uint64_t k_full[2], k_free[2], q_full[2], q_free[2];
+  uint64_t k_full[4], k_free[4], q_full[4], q_free[4];
   uint64_t s_full[2][2], s_free[2][2];  // [buffer][warpgroup]
   uint64_t sums_full[2], sums_free[2];  // the cluster's sums of even and odd items: all there; read
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Bars) <= 256, "barrier block");
+static_assert(sizeof(Bars) <= 512, "barrier block");
 
 struct ChunkWeightsParams {
   const float* lse;
@@ -82,7 +88,6 @@ struct ChunkWeightsParams {
   int num_seqs, num_heads, num_kv_heads, block_size, max_blocks, num_blocks;
   int total_queries, max_query_len, window;
   int group, tile_tokens, inv_group;  // r / group = r * inv_group >> 16 for r < 128
-  int resident;                       // the window's tiles stay in shared memory
   float qscale;                       // scale * log2(e)
 };
 
@@ -124,9 +129,11 @@ struct Run {
   }
 };
 
-// The items of a thread block or cluster, b of n, decoded alike by every warp.  All of them look up what
-// is next only from run to run: the loops over a run's items have to be small, for code that every role
-// goes through once an item costs a fetch of instructions each time.
+// The items of a thread block or cluster, b of n, decoded alike by every warp, which look up what is next
+// only from run to run: what each does once an item adds to every item's time.
+// kResident: the window's tiles of rows stay in shared memory while a key head's tokens go by; else they go
+// by for every item.
+template <bool kResident>
 struct Walk {
   const ChunkWeightsParams& p;
   const int* upto;  // [kLists]: items of the first lists of sequences
@@ -137,8 +144,8 @@ struct Walk {
   __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, int list, int b, int n)
       : p(p), upto(upto), list(list), b(b), n(n) {
     const long long all = upto[kLists - 1];
-    m = p.resident ? static_cast<int>(all * b / n) : b;
-    end = p.resident ? static_cast<int>(all * (b + 1) / n) : static_cast<int>(all);
+    m = kResident ? static_cast<int>(all * b / n) : b;
+    end = kResident ? static_cast<int>(all * (b + 1) / n) : static_cast<int>(all);
   }
 
   // The next run; false past the last.  By whole warps.
@@ -173,7 +180,7 @@ struct Walk {
       }
       left -= __shfl_sync(kFullMask, sum, 31);
     }
-    if (p.resident) {  // a key head's tokens one after the other
+    if constexpr (kResident) {  // a key head's tokens one after the other
       const int tiles = tiles_of(run.s);
       run.head = left / tiles;
       run.tile = left - run.head * tiles;
@@ -229,7 +236,7 @@ __device__ __forceinline__ void add_seen_weights(const float (&s)[32], uint32_t 
   }
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool kResident>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k, const ChunkWeightsParams p) {
@@ -246,11 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_free[s], 2);  // both issuers
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_free[s], 2);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->drain[s], 1);
       mbar_init(&bars->sums_full[s], ranks > 1 ? (ranks - 1) * kTokens : 1);
       mbar_init(&bars->sums_free[s], kTokens);
@@ -296,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (ranks > 1) cluster_sync();  // peers' barriers are set up
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  Walk walk(p, upto, list, static_cast<int>(blockIdx.x) / ranks, static_cast<int>(gridDim.x) / ranks);
+  Walk<kResident> walk(p, upto, list, static_cast<int>(blockIdx.x) / ranks, static_cast<int>(gridDim.x) / ranks);
   const Run& run = walk.run;
 
   int k_loads = 0, q_loads = 0;  // producer, issuer: tiles begun so far
@@ -335,10 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return (blk * p.num_kv_heads + run.head) * p.block_size + (t - b * p.block_size);
       };
-      bool with_q = p.resident != 0;
+      bool with_q = kResident;
       for (int tile = run.tile; ok && tile < run.end; ++tile) {
         const int t0 = tile * kTokens;
-        const int j0 = p.resident ? 0 : run.first(p, t0) + rank;
+        const int j0 = kResident ? 0 : run.first(p, t0) + rank;
         if (j0 >= run.row_tiles) break;  // other blocks of the cluster have its tiles
         int y = -1, y_hi = -1;
         if (lane < 16) {
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (y_hi >= 0) tma_load_3d(dst + C::kChunkBytes / 2, &tm_k, 0, y_hi, 0, &bars->k_full[ks]);
         ++k_loads;
         if (__shfl_sync(kFullMask, *abort_flag, 0)) ok = false;
-        if (!p.resident || with_q)
+        if (!kResident || with_q)
           for (int j = j0; ok && j < run.row_tiles; j += ranks) ok = load_q(j);
         with_q = false;
       }
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next()) {
       if (lane == 0) {
         const int held = q_loads;  // loads before the first of this run
-        if (p.resident) {
+        if constexpr (kResident) {
           q_loads += run.row_tiles;
           // (every load is waited for, its tile used or not, before its stage is handed back)
           for (int q = held; ok && q < q_loads; ++q) ok = mbar_wait_bounded(&bars->q_full[q % QS], (q / QS) & 1);
@@ -396,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_bounded(&bars->k_full[ks], (k_loads / KS) & 1);
           ++k_loads;
           for (int j = first; ok && j < run.row_tiles; j += ranks, ++steps) {
-            const int q = p.resident ? held + j : q_loads++, qs = q % QS, b = steps & 1;
-            if (!p.resident) ok = mbar_wait_bounded(&bars->q_full[qs], (q / QS) & 1);
+            const int q = kResident ? held + j : q_loads++, qs = q % QS, b = steps & 1;
+            if (!kResident) ok = mbar_wait_bounded(&bars->q_full[qs], (q / QS) & 1);
             const uint32_t q_lo = static_cast<uint32_t>(q_desc) + (qs * C::kQBytes >> 4);
             if (ok && steps >= 2) ok = mbar_wait_bounded(&bars->s_free[b][g], ((steps >> 1) - 1) & 1);
             if (!ok) break;
@@ -408,11 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                       q_lo + (((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
             mma_commit(&bars->s_full[b][g]);
             mma_started = 1;
-            if (!p.resident) mma_commit(&bars->q_free[qs]);
+            if (!kResident) mma_commit(&bars->q_free[qs]);
           }
           if (ok) mma_commit(&bars->k_free[ks]);
         }
-        if (ok && p.resident)
+        if (ok && kResident)
           for (int q = held; q < q_loads; ++q) mma_commit(&bars->q_free[q % QS]);
       }
       ok = __shfl_sync(kFullMask, ok, 0);
@@ -441,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tok >= min(p.tile_tokens, run.s.W - j * p.tile_tokens)) return 0.f;
         return -kLog2e * __ldg(lse_row + static_cast<size_t>(j) * p.tile_tokens * p.num_heads);
       };
-      if (p.resident) {
+      if constexpr (kResident) {
         float v[QS];
 #pragma unroll
         for (int j = 0; j < QS; ++j) v[j] = j < run.row_tiles ? row_lse(j) : 0.f;
@@ -454,11 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = tile * kTokens, t = t0 + at;
         const int first = run.first(p, t0) + rank;
         float total = 0.f, next_lse = 0.f;
-        if (!p.resident && first < run.row_tiles) next_lse = row_lse(first);
+        if (!kResident && first < run.row_tiles) next_lse = row_lse(first);
         for (int j = first; j < run.row_tiles; j += ranks, ++steps) {
           const int b = steps & 1;
           const float* lse = lse_wg + j * kRows;
-          if (!p.resident) {
+          if constexpr (!kResident) {
             // two buffers in turn: whoever is past the barrier of one tile has done with the tile before
             float* mine = lse_wg + (lse_loads++ & 1) * kRows;
             mine[r] = next_lse;
@@ -552,16 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool BF16, int D>
-int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned long long cache_rows,
-           cudaStream_t stream) {
+template <bool BF16, int D, bool kResident>
+int launch(const ChunkWeightsParams& p, int most, const void* q, const void* k_cache,
+           unsigned long long cache_rows, cudaStream_t stream) {
   using C = Cfg<D>;
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return PA_ERR_CUDA;
-  const int most = p.window > 0 && p.window < p.max_query_len ? p.window : p.max_query_len;
-  p.resident = most <= C::kQStages * p.tile_tokens;
   CUtensorMap tq, tk;
   const cuuint64_t qdims[3] = {D, static_cast<cuuint64_t>(p.num_heads),
                                static_cast<cuuint64_t>(p.total_queries)};
@@ -574,7 +581,7 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
   if (!encode_tensor_map(&tq, BF16, q, 3, qdims, qstr, qbox) ||
       !encode_tensor_map(&tk, BF16, k_cache, 3, cdims, cstr, cbox))
     return PA_ERR_CUDA;
-  if (cudaFuncSetAttribute(chunk_weights_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(chunk_weights_kernel<BF16, D, kResident>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::kSmemBytes) != cudaSuccess)
     return PA_ERR_CUDA;
   const long long tiles = (static_cast<long long>(p.max_blocks) * p.block_size + kTokens - 1) / kTokens;
@@ -582,7 +589,7 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
   // Few items of many tiles of rows: a cluster shares out an item's tiles.
   const int row_tiles = (most + p.tile_tokens - 1) / p.tile_tokens;
   int ranks = 1;
-  while (!p.resident && ranks < kMaxCluster && items * ranks < 4ll * sms && row_tiles >= 8 * ranks) ranks *= 2;
+  while (!kResident && ranks < kMaxCluster && items * ranks < 4ll * sms && row_tiles >= 8 * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
@@ -599,14 +606,24 @@ int launch(ChunkWeightsParams p, const void* q, const void* k_cache, unsigned lo
   int walkers = sms;
   if (ranks > 1) {
     cfg.gridDim = dim3(ranks);
-    if (cudaOccupancyMaxActiveClusters(&walkers, chunk_weights_kernel<BF16, D>, &cfg) != cudaSuccess || walkers <= 0)
+    if (cudaOccupancyMaxActiveClusters(&walkers, chunk_weights_kernel<BF16, D, kResident>, &cfg) != cudaSuccess ||
+        walkers <= 0)
       return PA_ERR_CUDA;
   }
   cfg.gridDim = dim3(static_cast<unsigned>((items < walkers ? items : walkers) * ranks));
-  if (cudaLaunchKernelEx(&cfg, chunk_weights_kernel<BF16, D>, tq, tk, p) != cudaSuccess ||
+  if (cudaLaunchKernelEx(&cfg, chunk_weights_kernel<BF16, D, kResident>, tq, tk, p) != cudaSuccess ||
       cudaGetLastError() != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
+}
+
+template <bool BF16, int D>
+int launch(const ChunkWeightsParams& p, const void* q, const void* k_cache, unsigned long long cache_rows,
+           cudaStream_t stream) {
+  const int most = p.window > 0 && p.window < p.max_query_len ? p.window : p.max_query_len;
+  return most <= Cfg<D>::kQStages * p.tile_tokens
+             ? launch<BF16, D, true>(p, most, q, k_cache, cache_rows, stream)
+             : launch<BF16, D, false>(p, most, q, k_cache, cache_rows, stream);
 }
 
 }  // namespace

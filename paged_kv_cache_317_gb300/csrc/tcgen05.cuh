@@ -28,17 +28,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p, uint32_t lbo,
   return d;
 }
 
-// The same for rows of 32 bytes, 16 channels, one after the other, with 32-byte swizzle: the two 16-byte
-// halves of a row change places where bit 2 of the row is set.  Starts on 256 bytes.
-__device__ __forceinline__ uint64_t smem_desc_sw32(const void* p) {
-  uint64_t d = static_cast<uint64_t>((smem_addr(p) >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>(256 >> 4) << 32;
-  d |= 1ull << 46;
-  d |= 6ull << 61;
-  return d;
-}
-
 // Instruction descriptor for kind::f16: fp32 accumulator, A and B both bf16 (or
 // both fp16), A K-major, B K-major or MN-major, shape M x N.
 __host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool bf16, bool b_mn_major) {
