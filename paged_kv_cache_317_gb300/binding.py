@@ -953,8 +953,9 @@ def paged_attn_chunk(q: torch.Tensor, query_start: torch.Tensor, max_query_len: 
     else:
         out = _new_out((T, Hq, D), out_dtype, q.device, stream)
     lib = load_library()
-    if workspace is None:
-        need = lib.paged_attn_chunk_workspace_needed(N, Hq, H, D, bs, MB, int(max_query_len))
+    if workspace is None:   # (tables of up to 512 tokens never need one)
+        need = (lib.paged_attn_chunk_workspace_needed(N, Hq, H, D, bs, MB, int(max_query_len))
+                if MB * bs > 512 else 0)
         if need:
             workspace = _new_out((need,), torch.uint8, q.device, stream)
     else:
@@ -1037,8 +1038,9 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     else:
         out = _new_out((N, Hq, D), out_dtype, q.device, stream)
     lib = load_library()
-    if workspace is None:
-        need = lib.paged_attn_decode_weights_workspace_needed(N, Hq, H, D, bs, MB)
+    if workspace is None:   # (8 heads a key head and tables of up to 1024 tokens never need one)
+        need = (lib.paged_attn_decode_weights_workspace_needed(N, Hq, H, D, bs, MB)
+                if MB * bs > 1024 or Hq > 8 * H else 0)
         if need:
             workspace = _new_out((need,), torch.uint8, q.device, stream)
     else:

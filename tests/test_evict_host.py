@@ -112,6 +112,17 @@ def test_workspace_sizes_never_fall(lib):
     assert size(0, 8, 2, 64, 16, 64) == size(1, 7, 2, 64, 16, 64) == size(1, 8, 2, 96, 16, 64) == 0
 
 
+def test_sizes_that_never_need_a_workspace(lib):
+    """What the binding relies on where it does not ask."""
+    for n in (1, 2, 7, 100, 1000, 65535):
+        for kv in (1, 2, 8, 40):
+            for dim in (64, 128, 256):
+                for bs, mb in ((8, 128), (16, 64), (64, 16), (16, 1)):
+                    for group in (1, 3, 8):
+                        assert lib.paged_attn_decode_weights_workspace_needed(n, kv * group, kv, dim, bs, mb) == 0
+                    assert lib.paged_attn_chunk_workspace_needed(n, kv, kv, dim, bs, mb // 2 or 1, 5) == 0
+
+
 def test_the_binding_refuses_tensors_that_are_not_on_the_gpu(binding, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     h = torch.zeros(4, 2, 16, 64, dtype=torch.float16)

@@ -164,6 +164,33 @@ def test_few_rows_over_a_long_context(B):
         assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_many_small_weights_next_to_a_large_one(B, dtype):
+    """A first key that has nearly all of the weight, and thousands of 2^-25 of it each, whose values are
+    all there is to see: none of them may be lost.  The bound is that of the outputs above, with 2^-32 of
+    the largest weight for each token, as fp16 numbers are kept 2^7 larger."""
+    n, D = 6000, 64
+    b = chunk_batch(14, [n], [3], 4, 1, D, 16, dtype)
+    b["q"][:] = 1.0
+    b["kc"][:], b["vc"][:] = 0.0, 1.0
+    first = int(b["tables"][0, 0])
+    b["kc"][first, 0, 0, 0], b["vc"][first, 0, 0] = 140.0, 0.0   # a logit of 17.5
+    for out_dtype in (torch.float32, dtype):
+        out, lse, rec = run_chunk(B, b, out_dtype=out_dtype)
+        assert rec == [0, 0, 0, 0]
+        for j in range(3):
+            small = (n - 3 + j) * np.exp(-17.5)
+            want = small / (1 + small)
+            one = out_dtype is not torch.float32
+            half = (2.0 ** -8 if dtype is BF else 2.0 ** -11) if one else 2.0 ** -16
+            tol = (4 * ((D + 8) * U * 17.5 + (n + 16) * U) + half) * want + 2.0 ** -32 * n
+            if one:
+                tol += float(half_ulp(np.array(want + tol), dtype))
+            assert float((out[j].double() - want).abs().max()) <= tol
+            assert float((lse[j].double() - (17.5 + np.log1p(small))).abs().max()) <= (
+                (D + 8) * U * 17.5 + (n + 16) * U + 2 * U * 17.5)
+
+
 @pytest.mark.parametrize("shape", SHAPES)
 def test_chunks_shared_out_over_parts(B, shape):
     """Lengths around the ends of parts, one sequence without queries, with an order."""
@@ -649,6 +676,24 @@ def test_two_captured_steps_replay_side_by_side(B):
         torch.cuda.synchronize()
         for b, w in zip(two, want):
             assert all(torch.equal(x, y) for x, y in zip(state(b), w))
+
+
+def test_captured_weights_of_whole_prompts(B):
+    """The launch in clusters, captured and replayed."""
+    b = chunk_batch(75, [600, 500], [600, 400], 14, 2, 64, 8, BF)
+    lse = given_lse(b)
+    before, want, _ = run_weights(B, b, lse, 0)
+    start, tables, lens = dev(b["start"]), dev(b["tables"]), dev(b["lens"])
+    w = before.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.paged_chunk_weights(b["q"], lse, start, b["most"], b["kc"], tables, lens, b["scale"], w)
+    for _ in range(3):
+        w.copy_(before)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(w.nan_to_num(9), want.nan_to_num(9))
 
 
 def test_the_same_call_gives_the_same_bits(B):
