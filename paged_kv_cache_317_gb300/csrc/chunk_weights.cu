@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // One thread adds to a weight, once: a reduction in L2 gives the same bits as a load, an add and a
-        // store, and nothing waits for the load.
+        // store (but for numbers below 2^-126, which it may take for 0), and nothing waits for the load.
         if (ok && rank == 0 && t < run.s.L) atomicAdd(p.weights + sh * p.weights_row + t, total);
       }
     }
@@ -675,7 +675,7 @@ extern "C" int paged_chunk_weights(const void* q, const float* lse, const int32_
   p.max_blocks = max_blocks_per_seq;
   p.num_blocks = num_blocks;
   p.total_queries = total_queries;
-  p.max_query_len = max_query_len;
+  p.max_query_len = max_query_len < cap ? max_query_len : static_cast<int>(cap);  // (no more queries than tokens)
   p.window = window;
   p.group = group;
   p.tile_tokens = kRows / group;

@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
   // (m, l) of column `col`'s parts, lane i's i and i + 32, and M and 1 / l of the whole
   struct Column {
     float w[2];  // 2^(m - M) of the lane's parts
+    unsigned seen[2];  // the parts that have a weight: a NaN in them counts, however small it is
     float M, inv;
   };
   auto column = [&](int col, size_t at) -> Column {
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       tokens |= ml[k].y < 0.f || ml[k].x != -INFINITY;
+      c.seen[k] = __ballot_sync(kFullMask, ml[k].x != -INFINITY);
       c.w[k] = ml[k].x != -INFINITY ? exp2f(ml[k].x - c.M) : 0.f;
       if (ml[k].x != -INFINITY) l = fmaf(c.w[k], ml[k].y, l);
     }
@@ -338,7 +340,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       }
     }
   }
-  // One thread adds to a weight, once: a reduction in L2 gives the same bits as a load, an add and a store.
+  // One thread adds to a weight, once: a reduction in L2 gives the same bits as a load, an add and a store,
+  // but for numbers below 2^-126, which it may take for 0.
   float* weights = p.weights + sh * p.weights_row + t0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k)
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
       for (int k = 0; k < kAhead; ++k) {
         const int i = warp + (k0 + k) * kWarpsJoin;
         const float f = __shfl_sync(kFullMask, i < 32 ? c.w[0] : c.w[1], i & 31);
-        if (i < p.parts && f != 0.f) {  // (a part without tokens has no sums; NaN is not 0)
+        if ((i < 32 ? c.seen[0] : c.seen[1]) >> (i & 31) & 1) {  // (i < p.parts; one without tokens has no sums)
 #pragma unroll
           for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, v[k][e], acc[e]);
         }

@@ -653,7 +653,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       };
       if constexpr (kGrouped) {
         if (!whole) {
-          if (row_valid) p.part_ml[static_cast<size_t>(it) * kQTile + r] = make_float2(m_ref, l);
+          // (a row whose every logit was NaN has no reference: any number lets its NaN sum be seen)
+          if (row_valid)
+            p.part_ml[static_cast<size_t>(it) * kQTile + r] = make_float2(l != l && m_ref == -INFINITY ? 0.f : m_ref, l);
         } else if (p.lse != nullptr && row_valid)  // ln of the sum of e^logit
           p.lse[static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + first_head +
                 (r - token * p.group)] = (m_ref - kLift + log2f(l)) * kLn2;
@@ -765,6 +767,8 @@ __global__ void __launch_bounds__(kJoinRows * 32)
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
   const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+  // parts that the row sees keys of: a NaN in them counts, however small their weight
+  const unsigned seen = __ballot_sync(kFullMask, ml.x != -INFINITY);
   float l = ml.x == -INFINITY ? 0.f : f * ml.y;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kJoinRows * 32)
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       g[k] = __shfl_sync(kFullMask, f, (i0 + k) & 31);
-      if (i0 + k < p.parts && g[k] != 0.f) {
+      if (seen >> (i0 + k) & 1) {
 #pragma unroll
         for (int e = 0; e < kVec; e += 2)
           *reinterpret_cast<float2*>(&v[k][e]) =
@@ -787,12 +791,12 @@ __global__ void __launch_bounds__(kJoinRows * 32)
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (i0 + k < p.parts && g[k] != 0.f) {
+      if (seen >> (i0 + k) & 1) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) acc[e] = fmaf(g[k], v[k][e], acc[e]);
       }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l > 0.f ? 1.f / l : l;  // NaN: every channel
 #pragma unroll
   for (int e = 0; e < kVec; ++e) acc[e] *= inv;
   const int token = r * p.inv_group >> 16;
@@ -863,14 +867,20 @@ int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, cons
   }
 }
 
-// The parts that an item's keys are shared out into: as many as fill the card, where there are few items
-// and tables are long.
-int chunk_parts(long long items, long long cap) {
+// The parts that an item's keys are shared out into, for so many (sequence, key head) and tiles of each: as
+// many as fill the card, where there are few items and tables are long.
+int chunk_parts(long long rows, long long tiles, long long cap) {
+  const long long items = rows > kPartSlots ? rows : rows * tiles;
   const long long runs = (cap + kPartTiles * kKTile - 1) / (kPartTiles * kKTile);
   long long parts = items > 0 ? kPartSlots / items : 1;
   if (parts > runs) parts = runs;
   if (parts > kMaxParts) parts = kMaxParts;
   return static_cast<int>(parts < 1 ? 1 : parts);
+}
+// Tiles of a sequence's rows; it has no more queries than tokens.
+long long chunk_tiles(int max_query_len, int group, long long cap) {
+  const int tile_tokens = kQTile / group;
+  return ((max_query_len < cap ? max_query_len : cap) + tile_tokens - 1) / tile_tokens;
 }
 size_t chunk_workspace(int head_dim) {
   return static_cast<size_t>(kPartSlots) * kQTile * (head_dim * sizeof(float) + sizeof(float2));
@@ -955,7 +965,7 @@ extern "C" size_t paged_attn_chunk_workspace_size(int num_seqs, int num_heads, i
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   // enough for the one sequence that a smaller call may have, whatever this one uses
-  return chunk_parts(1, static_cast<long long>(max_blocks_per_seq) * block_size) > 1 ? chunk_workspace(head_dim) : 0;
+  return chunk_parts(1, 1, static_cast<long long>(max_blocks_per_seq) * block_size) > 1 ? chunk_workspace(head_dim) : 0;
 }
 
 extern "C" size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
@@ -965,9 +975,8 @@ extern "C" size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads,
                                                       max_blocks_per_seq, max_query_len);
   const int group = most ? num_heads / num_kv_heads : 1;
   if (most == 0 || group > kQTile) return 0;
-  const int tile_tokens = kQTile / group;
-  const long long tiles = (static_cast<long long>(max_query_len) + tile_tokens - 1) / tile_tokens;
-  return chunk_parts(num_seqs * tiles * num_kv_heads, static_cast<long long>(max_blocks_per_seq) * block_size) > 1
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+  return chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, chunk_tiles(max_query_len, group, cap), cap) > 1
              ? most : 0;
 }
 
@@ -993,12 +1002,11 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   if (!std::isfinite(scale) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
   const unsigned long long cache_rows =
       static_cast<unsigned long long>(num_blocks) * num_kv_heads * block_size;
-  const int tile_tokens = kQTile / group;
-  const long long qtiles = (static_cast<long long>(max_query_len) + tile_tokens - 1) / tile_tokens;
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+  const long long most = chunk_tiles(max_query_len, group, max_query_len);
   // items are numbered in an int inside the kernel (with a grid's worth of headroom)
-  if (cache_rows >= (1ull << 31) ||
-      static_cast<long long>(max_blocks_per_seq) * block_size > (1ll << 30) ||
-      static_cast<long long>(num_seqs) * num_kv_heads * qtiles >= (1ll << 30))
+  if (cache_rows >= (1ull << 31) || cap > (1ll << 30) ||
+      static_cast<long long>(num_seqs) * num_kv_heads >= ((1ll << 30) + most - 1) / (most > 0 ? most : 1))
     return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_queries == 0 || max_query_len == 0) return PA_OK;
   if (!q || !query_start || !k_cache || !v_cache || !block_tables || !seq_lens || !out)
@@ -1006,6 +1014,7 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
       !aligned16(workspace))
     return PA_ERR_INVALID_ARG;
+  const long long qtiles = chunk_tiles(max_query_len, group, cap);
   PrefillParams p{};
   p.seq_order = seq_order;
   p.query_start = query_start;
@@ -1022,11 +1031,10 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   p.qscale = scale * kLog2e;
   p.num_kv_heads = num_kv_heads;
   p.group = group;
-  p.tile_tokens = tile_tokens;
+  p.tile_tokens = kQTile / group;
   p.inv_group = (65536 + group - 1) / group;
   p.lse = lse;
-  p.parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads * qtiles,
-                        static_cast<long long>(max_blocks_per_seq) * block_size);
+  p.parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, qtiles, cap);
   if (p.parts > 1) {
     if (!workspace || workspace_bytes < chunk_workspace(head_dim)) return PA_ERR_INVALID_ARG;
     p.part_o = static_cast<float*>(workspace);

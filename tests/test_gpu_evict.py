@@ -203,6 +203,52 @@ def test_chunks_shared_out_over_parts(B, shape):
         check_chunk(b, out, lse)
 
 
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_a_nan_far_from_the_large_weights_is_seen(B, dtype):
+    """Over parts, a NaN counts in every row that sees it, though its part's weight is 0 in fp32."""
+    b = chunk_batch(15, [5000], [4], 4, 2, 64, 16, dtype)
+    b["q"][:] = 1.0
+    b["kc"][:] = 0.0
+    b["kc"][int(b["tables"][0, 0]), :, 0] = 40.0      # a logit of 320, the others' 0
+    at = int(b["tables"][0, 4000 // 16]), 0, 4000 % 16
+    for which, channel in (("kc", slice(None)), ("vc", 9), ("q", slice(None))):
+        c = {k: b[k].clone() for k in ("q", "kc", "vc")}
+        if which == "q":
+            c["q"][1, 2] = NAN
+        else:
+            c[which][(*at, channel)] = NAN
+        out, lse, rec = run_chunk(B, {**b, **c})
+        assert rec == [0, 0, 0, 0]
+        want = torch.zeros(b["q"].shape, dtype=torch.bool)
+        if which == "q":
+            want[1, 2] = True
+        else:
+            want[:4, :2, channel] = True
+        assert torch.equal(torch.isnan(out).cpu(), want), which
+        assert torch.equal(torch.isnan(lse).cpu(), want.all(2)), which
+        if which != "q":
+            w = torch.zeros(1, 2, b["tables"].shape[1] * 16, device="cuda")
+            out = B.paged_attn_decode_weights(b["q"][:1], c["kc"], c["vc"], dev(b["tables"]), dev(b["lens"]),
+                                              b["scale"], w)
+            assert torch.equal(torch.isnan(out).cpu(), want[:1]), which
+            assert bool(torch.isnan(w[0, 0, :5000]).all()) == (which == "kc") and not bool(torch.isnan(w[0, 1]).any())
+
+
+def test_more_queries_allowed_than_there_can_be(B):
+    """max_query_len is a bound, however large."""
+    b = chunk_batch(16, [3000, 70], [3, 70], 6, 2, 64, 16, BF)
+    out, lse, rec = run_chunk(B, b)
+    wide = {**b, "most": 2 ** 31 - 1}
+    again, wlse, wrec = run_chunk(B, wide)
+    assert rec == wrec == [0, 0, 0, 0]
+    check_chunk(wide, again, wlse)
+    w = [torch.zeros(2, 2, b["tables"].shape[1] * 16, device="cuda") for _ in range(2)]
+    for most, to in ((b["most"], w[0]), (2 ** 31 - 1, w[1])):
+        B.paged_chunk_weights(b["q"], lse, dev(b["start"]), most, b["kc"], dev(b["tables"]), dev(b["lens"]), b["scale"],
+                              to, window=4)
+    assert torch.equal(w[0], w[1])
+
+
 def test_chunk_leaves_out_inconsistent_sequences(B):
     b = chunk_batch(7, [50, 30, 60, 40], [5, 4, 8, 3], 6, 2, 64, 16, FH)
     b["lens"] = b["lens"].copy()
