@@ -198,11 +198,24 @@ struct Walk {
   }
 };
 
-// e^(logit - lse) of the first `cols` of 32 columns of S, or of all, added to the four sums; nl: shared
-// address of -lse in base 2.
-template <bool kAll>
-__device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, float qscale, int cols,
-                                            float (&sum)[4]) {
+// e^(logit - lse) of 32 columns of S, added to the four sums; nl: shared address of -lse in base 2.
+__device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, float qscale, float (&sum)[4]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4) {
+    const float4 v = ld_shared4(nl + 4 * c);
+    float x0, x1, x2, x3;
+    fma2(x0, x1, s[c], s[c + 1], qscale, v.x, v.y);
+    fma2(x2, x3, s[c + 2], s[c + 3], qscale, v.z, v.w);
+    add2(sum[0], sum[1], ex2_approx(x0), ex2_approx(x1));
+    add2(sum[2], sum[3], ex2_approx(x2), ex2_approx(x3));
+  }
+}
+
+// The same for the columns from `from` to before `cols` alone.  Others may hold anything.
+__device__ __forceinline__ void add_seen_weights(const float (&s)[32], uint32_t nl, float qscale, int from, int cols,
+                                                 float (&sum)[4]) {
+  // bit c: column c is one of them
+  const uint32_t seen = (from < 32 ? kFullMask << max(from, 0) : 0u) & (cols < 32 ? ~(kFullMask << cols) : kFullMask);
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
     const float4 v = ld_shared4(nl + 4 * c);
@@ -210,29 +223,10 @@ __device__ __forceinline__ void add_weights(const float (&s)[32], uint32_t nl, f
     fma2(x0, x1, s[c], s[c + 1], qscale, v.x, v.y);
     fma2(x2, x3, s[c + 2], s[c + 3], qscale, v.z, v.w);
     float e[4] = {ex2_approx(x0), ex2_approx(x1), ex2_approx(x2), ex2_approx(x3)};
-    if constexpr (!kAll) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = c + i < cols ? e[i] : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) e[i] = seen & 1u << (c + i) ? e[i] : 0.f;
     add2(sum[0], sum[1], e[0], e[1]);
     add2(sum[2], sum[3], e[2], e[3]);
-  }
-}
-
-// The same for the columns c0 + c < cols whose token, c / group tokens after the tile's first, is not
-// before this thread's, `ahead` after it.  Others may hold anything.
-__device__ __forceinline__ void add_seen_weights(const float (&s)[32], uint32_t nl, float qscale, int c0, int cols,
-                                                 int ahead, int inv_group, float (&sum)[4]) {
-#pragma unroll
-  for (int c = 0; c < 32; c += 4) {
-    const float4 v = ld_shared4(nl + 4 * c);
-    const float l[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = ex2_approx(fmaf(s[c + i], qscale, l[i]));
-      const int col = c0 + c + i;
-      sum[i] += col < cols && ahead <= (col * inv_group >> 16) ? e : 0.f;
-    }
   }
 }
 
@@ -478,32 +472,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the first row's place in the sequence: rows before it see less
           const int pos = run.s.L - run.s.W + j * p.tile_tokens;
           const int cols = min(p.tile_tokens, run.s.W - j * p.tile_tokens) * p.group;
-          const bool seen = t0 + kTokens - 1 <= pos;  // by all of them
-          const int whole = seen ? cols & ~31 : 0;
-          const uint32_t from = lanes + b * 2 * kRows;
-          uint32_t nl = smem_addr(lse);
+          // Token t is seen from column (t - pos) group on; those of the warp lie between its first lane's,
+          // from which all before are left out, and its last one's, from which on no column needs a mask.
+          const int from = max(t - pos, 0) * p.group, warp_from = __shfl_sync(kFullMask, from, 0);
+          const int warp_all = __shfl_sync(kFullMask, from, 31);
+          const uint32_t at_s = lanes + b * 2 * kRows;
+          const uint32_t nl = smem_addr(lse);
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
           ok = __all_sync(kFullMask, mbar_wait_bounded(&bars->s_full[b][wg], (steps >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          int c = 0;
+          int c = warp_from & ~31;
 #pragma unroll 1
-          for (; c < whole; c += 32, nl += 128) {
+          for (; c < min(warp_all, cols); c += 32) {
             float s[32];
-            tmem_ld32(from + c, s);
-            add_weights<true>(s, nl, p.qscale, 32, sum);
-          }
-          if (seen && c < cols) {  // a tile whose rows are not a multiple of 32
-            float s[32];
-            tmem_ld32(from + c, s);
-            add_weights<false>(s, nl, p.qscale, cols - c, sum);
-            c = cols;
+            tmem_ld32(at_s + c, s);
+            add_seen_weights(s, nl + 4 * c, p.qscale, from - c, cols - c, sum);
           }
 #pragma unroll 1
-          for (; c < cols; c += 32, nl += 128) {
+          for (; c + 32 <= cols; c += 32) {
             float s[32];
-            tmem_ld32(from + c, s);
-            add_seen_weights(s, nl, p.qscale, c, cols, t - pos, p.inv_group, sum);
+            tmem_ld32(at_s + c, s);
+            add_weights(s, nl + 4 * c, p.qscale, sum);
+          }
+          if (c < cols) {  // a tile whose rows are not a multiple of 32
+            float s[32];
+            tmem_ld32(at_s + c, s);
+            add_seen_weights(s, nl + 4 * c, p.qscale, 0, cols - c, sum);
           }
           tc_fence_before();
           mbar_arrive(&bars->s_free[b][wg]);
