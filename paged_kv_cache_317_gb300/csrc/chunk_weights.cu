@@ -46,6 +46,7 @@ constexpr int kWarpLoad = 8, kWarpMma = 9;  // and 10: an issuer for each warpgr
 constexpr int kThreads = 352;
 constexpr int kMaxCluster = 4;
 constexpr int kLists = 128;                // lists of sequences whose items are counted together
+constexpr int kSorted = 256;               // (sequence, token tile) that are put in order
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -57,10 +58,11 @@ struct Cfg {
   static constexpr int kKStages = D == 64 ? 4 : D == 128 ? 2 : 1;
   static constexpr int kQStages = D == 256 ? 1 : 2;
   static constexpr int kOffQ = kKStages * kKBytes;
-  static constexpr int kOffLse = kOffQ + kQStages * kQBytes;       // [warpgroup][2][kRows] floats
-  static constexpr int kOffSums = kOffLse + 2 * 2 * kRows * 4;  // [2][kMaxCluster][kTokens] floats
+  static constexpr int kOffLse = kOffQ + kQStages * kQBytes;       // [warp][2][kRows] floats
+  static constexpr int kOffSums = kOffLse + 8 * 2 * kRows * 4;  // [2][kMaxCluster][kTokens] floats
   static constexpr int kOffCount = kOffSums + 2 * kMaxCluster * kTokens * 4;  // [kLists] ints
-  static constexpr int kOffBar = kOffCount + kLists * 4;
+  static constexpr int kOffOrder = kOffCount + kLists * 4;         // [kSorted] ints
+  static constexpr int kOffBar = kOffOrder + kSorted * 4;
   static constexpr int kUsed = kOffBar + 512 + 1024;               // 1 KB to align the base
   // one block an SM, which takes all 512 TMEM columns
   static constexpr int kSmemBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
@@ -116,17 +118,19 @@ __device__ __forceinline__ int tiles_of(const Seq& s) {
   return s.W > 0 ? (s.L + kTokens - 1) / kTokens : 0;
 }
 
+// The first tile of rows that sees a token of the tile at t0.
+__device__ __forceinline__ int first_seeing(const ChunkWeightsParams& p, const Seq& s, int t0) {
+  const int before = s.L - s.W;
+  return t0 > before ? (t0 - before) / p.tile_tokens : 0;
+}
+
 // Items of one key head: its token tiles from `tile` to before `end`.
 struct Run {
   Seq s;
   int seq, head, tile, end;
   int row_tiles;  // tiles of query rows
 
-  // The first tile of rows that sees a token of the tile at t0.
-  __device__ __forceinline__ int first(const ChunkWeightsParams& p, int t0) const {
-    const int before = s.L - s.W;
-    return t0 > before ? (t0 - before) / p.tile_tokens : 0;
-  }
+  __device__ __forceinline__ int first(const ChunkWeightsParams& p, int t0) const { return first_seeing(p, s, t0); }
 };
 
 // The items of a thread block or cluster, b of n, decoded alike by every warp, which look up what is next
@@ -137,12 +141,14 @@ template <bool kResident>
 struct Walk {
   const ChunkWeightsParams& p;
   const int* upto;  // [kLists]: items of the first lists of sequences
+  const int* order; // (sequence, token tile), as 256 sequence + tile, in the order that they are dealt out; or NULL
   int list;         // sequences of a list
   int m, end, b, n;
   Run run;
 
-  __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, int list, int b, int n)
-      : p(p), upto(upto), list(list), b(b), n(n) {
+  __device__ __forceinline__ Walk(const ChunkWeightsParams& p, const int* upto, const int* order, int list, int b,
+                                  int n)
+      : p(p), upto(upto), order(order), list(list), b(b), n(n) {
     const long long all = upto[kLists - 1];
     m = kResident ? static_cast<int>(all * b / n) : b;
     end = kResident ? static_cast<int>(all * (b + 1) / n) : static_cast<int>(all);
@@ -151,6 +157,17 @@ struct Walk {
   // The next run; false past the last.  By whole warps.
   __device__ __forceinline__ bool next() {
     if (m >= end) return false;
+    if (!kResident && order != nullptr) {
+      const int unit = m / p.num_kv_heads, u = order[unit];
+      run.seq = u >> 8;
+      run.s = sequence(p, run.seq, false);
+      run.row_tiles = (run.s.W + p.tile_tokens - 1) / p.tile_tokens;
+      run.head = m - unit * p.num_kv_heads;
+      run.tile = u & 255;
+      run.end = run.tile + 1;
+      there_and_back();
+      return true;
+    }
     const int lane = threadIdx.x & 31;
     const int4 u = reinterpret_cast<const int4*>(upto)[lane];
     const int r = __reduce_add_sync(kFullMask, (u.x <= m) + (u.y <= m) + (u.z <= m) + (u.w <= m));
@@ -190,11 +207,14 @@ struct Walk {
       run.tile = left / p.num_kv_heads;
       run.head = left - run.tile * p.num_kv_heads;
       run.end = run.tile + 1;
-      // there and back: a sequence's items get smaller
-      b = n - 1 - b;
-      m = (m / n + 1) * n + b;
+      there_and_back();
     }
     return true;
+  }
+
+  __device__ __forceinline__ void there_and_back() {  // a sequence's items get smaller
+    b = n - 1 - b;
+    m = (m / n + 1) * n + b;
   }
 };
 
@@ -241,12 +261,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float* lse_s = reinterpret_cast<float*>(smem + C::kOffLse);
   int* upto = reinterpret_cast<int*>(smem + C::kOffCount);
+  int* order = reinterpret_cast<int*>(smem + C::kOffOrder);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBar);
   volatile int* abort_flag = &bars->abort;
   const bool half_blocks = p.block_size < 16;
   const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
   if (threadIdx.x == 0) {
+    prefetch_tensor_map(&tm_q);
+    prefetch_tensor_map(&tm_k);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_free[s], 2);  // both issuers
@@ -296,10 +319,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // Passing rows: a few items a block are dealt out longest first (12 sequences of 800 rows, 28 heads on 4: 58 us,
+  // 71 in the order of sequences; 76 of 512, 17 items a cluster: 139 and 133).
+  bool sorted = false;
+  if constexpr (!kResident) {
+    const int n = upto[kLists - 1] / p.num_kv_heads;  // (sequence, token tile)
+    const int items = upto[kLists - 1], walkers = static_cast<int>(gridDim.x) / ranks;
+    sorted = list == 1 && n <= kSorted && items > walkers && items <= 8 * walkers;
+    if (sorted) {
+      int* rows = reinterpret_cast<int*>(smem);  // tiles of rows of each; K's place, which nothing is in yet
+      int* what = rows + kSorted;
+      if (threadIdx.x < p.num_seqs) {
+        const int seq = threadIdx.x, end = upto[seq] / p.num_kv_heads;
+        const Seq s = sequence(p, seq, false);
+        const int tiles = tiles_of(s), row_tiles = (s.W + p.tile_tokens - 1) / p.tile_tokens;
+        for (int tile = 0; tile < tiles; ++tile) {
+          rows[end - tiles + tile] = row_tiles - first_seeing(p, s, tile * kTokens);
+          what[end - tiles + tile] = seq << 8 | tile;
+        }
+      }
+      __syncthreads();
+      if (threadIdx.x < n) {
+        const int mine = rows[threadIdx.x];
+        int place = 0;
+        for (int i = 0; i < n; ++i) place += rows[i] > mine || (rows[i] == mine && i < threadIdx.x);
+        order[place] = what[threadIdx.x];
+      }
+      fence_async_smem();  // TMA writes there
+      __syncthreads();
+    }
+  }
   if (ranks > 1) cluster_sync();  // peers' barriers are set up
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  Walk<kResident> walk(p, upto, list, static_cast<int>(blockIdx.x) / ranks, static_cast<int>(gridDim.x) / ranks);
+  Walk<kResident> walk(p, upto, sorted ? order : nullptr, list, static_cast<int>(blockIdx.x) / ranks,
+                       static_cast<int>(gridDim.x) / ranks);
   const Run& run = walk.run;
 
   int k_loads = 0, q_loads = 0;  // producer, issuer: tiles begun so far
@@ -430,43 +484,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2, r = threadIdx.x & (kHalf - 1);
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * kRows;
     const int at = (r >> 3) * 16 + wg * 8 + (r & 7);  // this thread's token of an item
-    float* lse_wg = lse_s + wg * 2 * kRows;
-    auto sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory"); };
+    float* lse_warp = lse_s + warp * 2 * kRows;
     int steps = 0, items = 0, lse_loads = 0;
     bool ok = true;
     while (ok && walk.next()) {
       const size_t sh = static_cast<size_t>(run.seq) * p.num_kv_heads + run.head;
-      const int tok = r * p.inv_group >> 16;  // of row r of a tile
-      const float* lse_row = p.lse + (static_cast<size_t>(run.s.row0) + tok) * p.num_heads +
-                             run.head * p.group + (r - tok * p.group);
-      // -lse in base 2 of row r of tile j; 0 past the window's last, and where r only fills the tile up
-      auto row_lse = [&](int j) {
-        if (tok >= min(p.tile_tokens, run.s.W - j * p.tile_tokens)) return 0.f;
-        return -kLog2e * __ldg(lse_row + static_cast<size_t>(j) * p.tile_tokens * p.num_heads);
+      // -lse in base 2 of rows lane, lane + 32, ... of tile j; 0 past the window's last, and where a row only
+      // fills the tile up
+      int tok[4];
+      long long from_row[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = lane + 32 * k;
+        tok[k] = row * p.inv_group >> 16;
+        from_row[k] = (static_cast<long long>(run.s.row0) + tok[k]) * p.num_heads + run.head * p.group +
+                      (row - tok[k] * p.group);
+      }
+      auto row_lse = [&](int j, float (&v)[4]) {
+        const int tokens = min(p.tile_tokens, run.s.W - j * p.tile_tokens);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = tok[k] < tokens
+                     ? -kLog2e * __ldg(p.lse + from_row[k] + static_cast<long long>(j) * p.tile_tokens * p.num_heads)
+                     : 0.f;
       };
       if constexpr (kResident) {
-        float v[QS];
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < QS; ++j) v[j] = j < run.row_tiles ? row_lse(j) : 0.f;
-        sync();  // the last run's are read
+        for (int j = 0; j < QS; ++j) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          if (j < run.row_tiles) row_lse(j, v);
 #pragma unroll
-        for (int j = 0; j < QS; ++j) lse_wg[j * kRows + r] = v[j];
-        sync();
+          for (int k = 0; k < 4; ++k) lse_warp[j * kRows + lane + 32 * k] = v[k];
+        }
+        __syncwarp();
       }
       for (int tile = run.tile; ok && tile < run.end; ++tile) {
         const int t0 = tile * kTokens, t = t0 + at;
         const int first = run.first(p, t0) + rank;
-        float total = 0.f, next_lse = 0.f;
-        if (!kResident && first < run.row_tiles) next_lse = row_lse(first);
+        float total = 0.f, next_lse[4];
+        if (!kResident && first < run.row_tiles) row_lse(first, next_lse);
         for (int j = first; j < run.row_tiles; j += ranks, ++steps) {
           const int b = steps & 1;
-          const float* lse = lse_wg + j * kRows;
+          const float* lse = lse_warp + j * kRows;
           if constexpr (!kResident) {
-            // two buffers in turn: whoever is past the barrier of one tile has done with the tile before
-            float* mine = lse_wg + (lse_loads++ & 1) * kRows;
-            mine[r] = next_lse;
-            if (j + ranks < run.row_tiles) next_lse = row_lse(j + ranks);
-            sync();
+            __syncwarp();  // the tile before the last is read
+            float* mine = lse_warp + (lse_loads++ & 1) * kRows;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mine[lane + 32 * k] = next_lse[k];
+            if (j + ranks < run.row_tiles) row_lse(j + ranks, next_lse);
+            __syncwarp();
             lse = mine;
           }
           // the first row's place in the sequence: rows before it see less
@@ -581,10 +648,14 @@ int launch(const ChunkWeightsParams& p, int most, const void* q, const void* k_c
     return PA_ERR_CUDA;
   const long long tiles = (static_cast<long long>(p.max_blocks) * p.block_size + kTokens - 1) / kTokens;
   const long long items = p.num_seqs * tiles * p.num_kv_heads;
-  // Few items of many tiles of rows: a cluster shares out an item's tiles.
+  // Few items of many tiles of rows: a cluster shares out an item's tiles.  Two tiles a block are enough where
+  // every cluster has a place at once (4 key heads, 200 rows of 7 heads: 10.5 us, 13.1 with eight; of 12 such
+  // sequences, where they do not: 18.1 us with two, 13.8 with eight).
   const int row_tiles = (most + p.tile_tokens - 1) / p.tile_tokens;
   int ranks = 1;
-  while (!kResident && ranks < kMaxCluster && items * ranks < 4ll * sms && row_tiles >= 8 * ranks) ranks *= 2;
+  while (!kResident && ranks < kMaxCluster && items * ranks < 4ll * sms &&
+         row_tiles >= (items * 2 * ranks <= sms ? 2 : 8) * ranks)
+    ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;

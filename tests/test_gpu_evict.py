@@ -337,6 +337,17 @@ def test_weights_of_whole_prompts(B, news, window, group):
     check_chunk_weights(b, lse, before, got, window)
 
 
+def test_weights_of_prompts_of_all_lengths(B):
+    """Enough of them that some thread blocks have several, dealt out longest first; two without rows."""
+    news = [37 * i % 331 for i in range(50)]
+    news[7], news[31] = 0, 700
+    b = chunk_batch(18, [max(n, 1) + (i % 3) * 64 for i, n in enumerate(news)], news, 40, 2, 64, 8, FH)
+    lse = given_lse(b)
+    before, got, rec = run_weights(B, b, lse, 0)
+    assert rec == [0, 0, 0, 0]
+    check_chunk_weights(b, lse, before, got, 0)
+
+
 def test_weights_of_many_sequences(B):
     """More sequences than are counted together at a time, some with nothing to do."""
     rng = np.random.default_rng(2)
