@@ -49,7 +49,7 @@
 //    whole tokens as 128 rows hold, so that a few drafted tokens fill a tile with all heads' rows and K and
 //    V are read once for them.  Half-precision outputs take P as one number, rounded to nearest: its error
 //    is the output's own rounding (16 chunks of 512 rows, 40 heads on 8, contexts of up to 2048: 255 us with
-//    two numbers, 210 us with one, 880 TFLOP/s).  Where there are fewer items than places, an item's keys are
+//    two numbers, 205 us with one, 900 TFLOP/s).  Where there are fewer items than places, an item's keys are
 //    shared out over several blocks, whose O and sums a second kernel joins (3 tokens over 30,000: 35 us).
 //  * Every mbarrier wait is bounded (one second); on a timeout the block
 //    records PA_ERR_TIMEOUT, waits (bounded) for its copies and MMAs, frees its
@@ -503,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       if (!w.valid) continue;
       const bool row_valid = r < w.rows;
       const int token = kGrouped ? r * p.inv_group >> 16 : r;  // of the tile
-      const int pos = row_valid ? w.pos0 + token : -1;
+      // (grouped, rows that only fill the tile up are not masked, so that their warp need not mask every tile:
+      // 16 chunks of 512 rows, 40 heads on 8: 205 us, 210 with it)
+      const int pos = row_valid ? w.pos0 + token : kGrouped ? 0x7fffffff : -1;
       float m_ref = -INFINITY, l = 0.f;  // reference max (log2 units) and running sum
       const int j0 = kGrouped ? w.j0 : 0;
       for (int j = j0; j < w.T; ++j) {
