@@ -13,19 +13,24 @@
 //    is dealt out in vain.  Where the window's tiles stay in shared memory a block takes a contiguous run
 //    of items and loads them once a key head; else block b takes items b, 2 grid - 1 - b, 2 grid + b, ...,
 //    heads innermost, so that the items of a causal triangle are shared out alike; few items of many tiles
-//    are a cluster's each, whose blocks take its tiles in turn.
+//    are a cluster's each, whose blocks take its tiles in turn; some items a block go longest first.
 //  * 11 warps: two softmax warpgroups, a producer (TMA boxes of 16 rows of K through the block table, boxes
 //    of whole tiles of Q), an issuer of products for each warpgroup (one thread issues a product in about the
 //    time that it runs, and has barriers to wait for besides: 32 sequences, 64 heads, window 32: 186 us with
 //    one issuer, 165 with two).  Each warpgroup has two 128-column buffers of S in TMEM: one is read while
 //    the next product runs.
-//  * Masks only where a tile of rows meets tokens that some of its rows do not see, or ends short.
+//  * A token is seen from a column of a tile on: 32 columns are masked only where that column of one of the
+//    warp's tokens lies among them, or the tile ends, and left out where no token is seen (the prompts below:
+//    74 us, 92 with every tile of the diagonal masked).  Each warp has a copy of the rows' lse, so that it
+//    waits for its products alone (72 prompts of 1500 rows: 772 us, 805 with a barrier a tile).
 //  * Every wait is bounded (one second); on a timeout the block records PA_ERR_TIMEOUT, waits (bounded) for
 //    its copies and products, frees its TMEM and returns.
-// Bound by the exchange between products and softmax: a step of 256 tokens x 128 rows takes about 2500
-// clocks, of which the products run for 1026 and the exponentials for 1024; read beside the products, which
-// use up what shared memory gives, the lse alone cost some 700 (2134 clocks for the arithmetic of a step,
-// 1401 without them).  The same case, 652 MB and 157 TFLOP: 162 us, 4.0 TB/s, 970 TFLOP/s.
+// Bound by the hand-over between loads, products and softmax: a step of 256 tokens x 128 rows takes about 2300
+// clocks (64 channels and passing rows: 2600), of which the products run for 1026 (513) and the exponentials
+// for 1024.  Without exponentials and lse it still takes 85 % of the time, without any arithmetic on S 75-82 %;
+// loads of S further ahead, of 16 or of 64 columns, make it slower.  32 sequences of up to 16384 tokens, 64
+// heads on 8, window 32, 652 MB and 157 GFLOP: 151 us, 4.3 TB/s, 1.04 PFLOP/s.  12 whole prompts of up to 1500
+// rows, 28 heads on 4, 64 channels, 17 GFLOP: 68 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

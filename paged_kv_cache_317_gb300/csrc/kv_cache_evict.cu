@@ -7,8 +7,9 @@
 // rounds: every thread loads its pieces of the round's rows into registers and looks up rows of the
 // next round, a barrier, every thread stores its pieces.  Loads of later rounds may run ahead of the
 // stores of earlier ones; only the loads of a round itself have to be over, which the barrier sees to.
-// A move and nothing else: bound by HBM for batches, by a round's latency (rows, barrier, stores) for one
-// sequence.
+// A move and nothing else: bound by HBM for batches (64 contexts of up to 16384 tokens, 8 heads, 1024 kept:
+// 94 us for 556 MB, 5.9 TB/s), by a round's latency (list, tables, rows, barrier, stores) for one sequence (4096
+// kept of 30,000: 11.4 us for 35 MB, two rounds a cluster).
 #include <cuda_runtime.h>
 
 #include "cluster.cuh"
