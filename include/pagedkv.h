@@ -671,7 +671,8 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  *   k_cache, v_cache  device [num_blocks][num_kv_heads][block_size][head_dim]
  *   lse           NULL, or device float [total_queries][num_heads]: the natural logarithm of
  *                 a row's sum of e^(scale * <q, k_t>); rows outside every range are not written
- *   seq_order     as in pa_prefill_opts, or NULL
+ *   seq_order     as in pa_prefill_opts, or NULL: up to 224 sequences go longest first, more as
+ *                 they come.  Results do not depend on it
  *   workspace     device, 16-byte aligned, scratch of this call alone, at least
  *                 paged_attn_chunk_workspace_size(...) bytes; may be NULL where
  *                 paged_attn_chunk_workspace_needed(...) is 0

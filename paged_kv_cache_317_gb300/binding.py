@@ -931,8 +931,9 @@ def paged_attn_chunk(q: torch.Tensor, query_start: torch.Tensor, max_query_len: 
     heads.  q [T,Hq,D]; query_start int32 [N+1]; caches [B,H,bs,D], Hq a multiple of H;
     block_tables int32 [N,MB]; seq_lens int32 [N], the new tokens counted; lse: optional float32
     [T,Hq], filled with the logarithm of each row's sum of exponentials; seq_order: optional int32
-    [N] dispatch order of the sequences; workspace: optional contiguous tensor of at least
-    paged_attn_chunk_workspace_size(...) bytes, made here if it is needed and not given."""
+    [N] dispatch order of the sequences (up to 224 go longest first without it); workspace: optional
+    contiguous tensor of at least paged_attn_chunk_workspace_size(...) bytes, made here if it is needed
+    and not given."""
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape

@@ -48,8 +48,8 @@
 //  * Grouped (query heads sharing key heads): a tile's rows are (token, query head of a key head), as many
 //    whole tokens as 128 rows hold, so that a few drafted tokens fill a tile with all heads' rows and K and
 //    V are read once for them.  Half-precision outputs take P as one number, rounded to nearest: its error
-//    is the output's own rounding (16 chunks of 512 rows, 40 heads on 8, contexts of up to 2048: 255 us with
-//    two numbers, 205 us with one, 900 TFLOP/s).  Where there are fewer items than places, an item's keys are
+//    is the output's own rounding (16 chunks of 512 rows, 40 heads on 8, contexts of up to 2048: 245 us with
+//    two numbers, 193 us with one, 960 TFLOP/s).  Where there are fewer items than places, an item's keys are
 //    shared out over several blocks, whose O and sums a second kernel joins (3 tokens over 30,000: 35 us).
 //  * Every mbarrier wait is bounded (one second); on a timeout the block
 //    records PA_ERR_TIMEOUT, waits (bounded) for its copies and MMAs, frees its
@@ -73,6 +73,7 @@ constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr int kPartTiles = 8;                     // an item's keys are shared out by so many tiles
 constexpr int kMaxParts = 32;
 constexpr int kPartSlots = 304;                   // items, parts of items: two thread blocks an SM
+constexpr int kSorted = kThreads;                 // sequences that are put in order, grouped
 constexpr int kKStages = 2;                       // K ring depth (= the S buffers: a stage is freed by its S)
 constexpr int kVStages = 2;                       // V ring depth (= the S/P buffers: a stage is freed by its P.V)
 static_assert(kKStages == 2 && kVStages == 2,
@@ -94,7 +95,8 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + kQBytes;
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffStage = kOffV + kVStages * kTileBytes;  // 4 warps x 2 KB
-  static constexpr int kOffBar = kOffStage + 8192;
+  static constexpr int kOffOrder = kOffStage + 8192;  // kSorted ints
+  static constexpr int kOffBar = kOffOrder + kSorted * 4;
   // 1 KB is left for aligning the dynamic shared-memory base to 1 KB (the
   // kernel checks it); at D <= 128 two blocks still fit an SM (228 KB, less 1 KB
   // reserved per block).
@@ -164,6 +166,7 @@ struct Tile {
   int pos0;  // position of the first query
   int keys;  // keys any row of the tile sees
   int j0, T; // 64-key tiles: from j0 to before T
+  int place; // of the item in part_o and part_ml, whatever the order
   bool valid;
 };
 
@@ -171,8 +174,9 @@ struct Tile {
 // later (longer) query tiles of that sequence first, heads innermost.  Every
 // thread decodes the same items from the same device values, so all roles
 // agree on which items exist.
+// order: where the sequences' order is in shared memory, or NULL.
 template <bool kGrouped>
-__device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int num_seqs,
+__device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* order, int it, int num_seqs,
                                             int num_qtiles, bool report) {
   Tile w;
   w.valid = false;
@@ -185,7 +189,9 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
   const int qt = num_qtiles - 1 - rem / heads;
   w.h = rem % heads;
   int seq = z;
-  if (p.seq_order != nullptr) {
+  if (kGrouped && order != nullptr) {
+    seq = order[z];
+  } else if (p.seq_order != nullptr) {
     seq = __ldg(p.seq_order + z);
     if (static_cast<unsigned>(seq) >= static_cast<unsigned>(num_seqs)) {
       if (report && rem == 0 && part == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, z, seq);
@@ -193,6 +199,7 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
     }
   }
   w.seq = seq;
+  if (kGrouped) w.place = (seq * per_seq + rem) * p.parts + part;
   int L = __ldg(p.seq_lens + seq);
   w.q_begin = __ldg(p.query_start + seq);
   const int nq = __ldg(p.query_start + seq + 1) - w.q_begin;
@@ -228,7 +235,12 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, int it, int 
 // The r-th item of this block: block b takes items b, b + gridDim.x, ...
 // (Dealing every other round in reverse, to even out long and short items per
 // block, measured 2 % slower: the two blocks sharing an SM already even out.)
+// Grouped, every other round is dealt in reverse: sequences of drafted tokens, of one tile each, are of
+// unequal lengths (64 of 64 to 2048 tokens, 32 heads on 8: 52 us, 61 without; 2 of 2529 and 15337, 1354 rows:
+// 227 and 304; the chunks of prompts above: 193 and 190).
+template <bool kGrouped>
 __device__ __forceinline__ int item_of(int r) {
+  if (kGrouped && (r & 1)) return (r + 1) * static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   return r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
 }
 
@@ -279,12 +291,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
+  const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
+  // Grouped, without an order from the caller: more items than blocks are dealt out the longest sequence
+  // first (40 sequences of 50 to 3641 tokens with 6 drafted, 32 heads on 8: 68 us, 86 as they come).
+  const int* order = nullptr;
+  if constexpr (kGrouped) {
+    if (p.seq_order == nullptr && num_seqs <= kSorted && n_items > static_cast<int>(gridDim.x)) {
+      int* lens = reinterpret_cast<int*>(Qs);  // which nothing is in yet
+      int* places = reinterpret_cast<int*>(smem + C::kOffOrder);
+      const int i = threadIdx.x;
+      if (i < num_seqs) lens[i] = __ldg(p.seq_lens + i);
+      __syncthreads();
+      if (i < num_seqs) {
+        int place = 0;
+        for (int k = 0; k < num_seqs; ++k) place += lens[k] > lens[i] || (lens[k] == lens[i] && k < i);
+        places[place] = i;
+      }
+      fence_async_smem();  // TMA writes there
+      order = places;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
-  const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
 
   // Key tiles are counted across the block's items: tile g of the block uses K
   // and V stage g & 1 and S/P buffer g & 1, and its barriers' phases are g >> 1.
@@ -296,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     const bool is_v = (warp == kWarpV);
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     bool ok = true;
-    for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-      const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, !is_v && lane == 0);
+    for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+      const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, !is_v && lane == 0);
       if (!w.valid) continue;
       const int32_t* table = p.block_tables + static_cast<size_t>(w.seq) * p.max_blocks;
       int blk = 0, blk_hi = 0;
@@ -422,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       const uint64_t v_desc0 = smem_desc_sw128(v_tile(0), kHalfBytes, 1024);
       int g = 0, items = 0;
       bool ok = true;
-      for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-        const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, false);
+      for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+        const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, false);
         if (!w.valid) continue;
         if (!mbar_wait_bounded(&bars->q_full, items & 1)) {
           ok = false;
@@ -498,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     int g = 0;
     bool ok = true;
-    for (int turn = 0, it = item_of(0); ok && it < n_items; it = item_of(++turn)) {
-      const Tile w = decode_tile<kGrouped>(p, it, num_seqs, num_qtiles, false);
+    for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+      const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, false);
       if (!w.valid) continue;
       const bool row_valid = r < w.rows;
       const int token = kGrouped ? r * p.inv_group >> 16 : r;  // of the tile
@@ -642,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       char* out_warp = static_cast<char*>(p.out) +
                        (static_cast<size_t>(w.q_begin + w.q0 + first) * p.num_heads + first_head) *
                            D * esz;
-      if (!whole) out_warp = reinterpret_cast<char*>(p.part_o + static_cast<size_t>(it) * kQTile * D);
+      if (!whole) out_warp = reinterpret_cast<char*>(p.part_o + static_cast<size_t>(w.place) * kQTile * D);
       // where the warp's row begins, from out_warp
       auto row_at = [&](int row) -> size_t {
         if constexpr (kGrouped) {
@@ -657,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
         if (!whole) {
           // (a row whose every logit was NaN has no reference: any number lets its NaN sum be seen)
           if (row_valid)
-            p.part_ml[static_cast<size_t>(it) * kQTile + r] = make_float2(l != l && m_ref == -INFINITY ? 0.f : m_ref, l);
+            p.part_ml[static_cast<size_t>(w.place) * kQTile + r] =
+                make_float2(l != l && m_ref == -INFINITY ? 0.f : m_ref, l);
         } else if (p.lse != nullptr && row_valid)  // ln of the sum of e^logit
           p.lse[static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + first_head +
                 (r - token * p.group)] = (m_ref - kLift + log2f(l)) * kLn2;
@@ -758,11 +790,11 @@ __global__ void __launch_bounds__(kJoinRows * 32)
   const int r = blockIdx.x % (kQTile / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
   PrefillParams whole = p;
   whole.parts = 1;
-  const Tile w = decode_tile<true>(whole, item, num_seqs, num_qtiles, false);
+  const Tile w = decode_tile<true>(whole, nullptr, item, num_seqs, num_qtiles, false);
   if (!w.valid || r >= w.rows) return;
   const int runs = (w.T + kPartTiles - 1) / kPartTiles;
   // lane i: part i, which may have had no keys
-  const size_t row0 = static_cast<size_t>(item) * p.parts * kQTile + r;
+  const size_t row0 = static_cast<size_t>(w.place) * p.parts * kQTile + r;  // (place: of the item as a whole)
   const bool mine = lane < p.parts && runs * lane / p.parts < runs * (lane + 1) / p.parts;
   const float2 ml = mine ? p.part_ml[row0 + static_cast<size_t>(lane) * kQTile] : make_float2(-INFINITY, 0.f);
   float M = ml.x;  // (a reference is a number or -infinity)

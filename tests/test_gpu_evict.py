@@ -249,6 +249,25 @@ def test_more_queries_allowed_than_there_can_be(B):
     assert torch.equal(w[0], w[1])
 
 
+@pytest.mark.parametrize("n,Hq,H,D,most", [(60, 16, 8, 64, 200), (6, 16, 8, 256, 3000), (300, 4, 2, 64, 90)])
+def test_the_order_of_sequences_changes_nothing(B, n, Hq, H, D, most):
+    """More items than thread blocks, as they are dealt out by themselves and in given orders."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, most + 1, n)
+    lens[1] = most
+    news = np.minimum(lens, rng.integers(0, 5, n))
+    b = chunk_batch(21, lens, news, Hq, H, D, 16, BF)
+    b["lens"] = b["lens"].copy()
+    skip = int(np.flatnonzero(news > 1)[0])
+    b["lens"][skip] = news[skip] - 1
+    want, wlse, rec = run_chunk(B, b)
+    assert rec == [BAD_SEQ_LEN, 1, skip, news[skip] - 1]
+    check_chunk(b, want, wlse, skip=(skip,))
+    for order in (np.arange(n), rng.permutation(n)):
+        out, lse, _ = run_chunk(B, b, seq_order=dev(order.astype(np.int32)))
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
 def test_chunk_leaves_out_inconsistent_sequences(B):
     b = chunk_batch(7, [50, 30, 60, 40], [5, 4, 8, 3], 6, 2, 64, 16, FH)
     b["lens"] = b["lens"].copy()
