@@ -686,7 +686,7 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  * of the batch too, as paged_attn_prefill.
  *
  * paged_attn_chunk_workspace_size is the same for all calls that may use a workspace (few
- * sequences with long tables): 304 x 128 rows of head_dim + 2 floats.
+ * sequences with long tables): 608 x 128 rows of head_dim + 2 floats.
  * paged_attn_chunk_workspace_needed is that size where a call of exactly these sizes uses it,
  * and 0 where it neither touches one nor looks at its size. */
 size_t paged_attn_chunk_workspace_size(int num_seqs, int num_heads, int num_kv_heads,

@@ -73,6 +73,7 @@ constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr int kPartTiles = 8;                     // an item's keys are shared out by so many tiles
 constexpr int kMaxParts = 32;
 constexpr int kPartSlots = 304;                   // items, parts of items: two thread blocks an SM
+constexpr int kPartPlaces = 2 * kPartSlots;       // parts in the workspace: smaller ones too, one an item
 constexpr int kSorted = kThreads;                 // sequences that are put in order, grouped
 constexpr int kKStages = 2;                       // K ring depth (= the S buffers: a stage is freed by its S)
 constexpr int kVStages = 2;                       // V ring depth (= the S/P buffers: a stage is freed by its P.V)
@@ -152,7 +153,9 @@ struct PrefillParams {
   float* lse;         // [total_queries][num_heads], or NULL
   // Grouped, with parts > 1: an item's keys are shared out over so many, each of whose O, not divided by
   // its sum, and (reference, sum) go to [item][part][kQTile] rows of fp32.
-  int parts;
+  // Part i begins at run i share / units of an item's runs of tiles; few > 0: a last, smaller part, which so
+  // many blocks at the grid's end deal out among them.
+  int parts, share, units, few;
   float* part_o;
   float2* part_ml;
 };
@@ -167,8 +170,14 @@ struct Tile {
   int keys;  // keys any row of the tile sees
   int j0, T; // 64-key tiles: from j0 to before T
   int place; // of the item in part_o and part_ml, whatever the order
+  bool whole; // no other part has keys
   bool valid;
 };
+
+// The run of tiles where part i begins, or the last one ends.
+__device__ __forceinline__ int part_begin(const PrefillParams& p, int runs, int i) {
+  return i >= p.parts ? runs : min(runs, (runs * p.share * i + p.units - 1) / p.units);
+}
 
 // Item `it` of the launch: dispatch position z (through seq_order), then the
 // later (longer) query tiles of that sequence first, heads innermost.  Every
@@ -182,9 +191,13 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* o
   w.valid = false;
   const int heads = kGrouped ? p.num_kv_heads : p.num_heads;
   const int tile_tokens = kGrouped ? p.tile_tokens : kQTile;
-  const int part = kGrouped ? it % p.parts : 0;
-  if (kGrouped) it /= p.parts;
   const int per_seq = heads * num_qtiles;
+  int part = 0;
+  if (kGrouped && p.parts > 1) {
+    const int n = num_seqs * per_seq;  // with a smaller last part: part by part
+    part = p.few > 0 ? it / n : it % p.parts;
+    it = p.few > 0 ? it - part * n : it / p.parts;
+  }
   const int z = it / per_seq, rem = it % per_seq;
   const int qt = num_qtiles - 1 - rem / heads;
   w.h = rem % heads;
@@ -222,10 +235,12 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* o
   w.keys = w.pos0 + tokens;
   w.T = (w.keys + kKTile - 1) / kKTile;
   w.j0 = 0;
+  w.whole = true;
   if (kGrouped && p.parts > 1) {  // (a part begins where the producers look blocks up)
     const int runs = (w.T + kPartTiles - 1) / kPartTiles;
-    w.j0 = runs * part / p.parts * kPartTiles;
-    w.T = min(w.T, runs * (part + 1) / p.parts * kPartTiles);
+    w.whole = part_begin(p, runs, 1) >= runs;
+    w.j0 = part_begin(p, runs, part) * kPartTiles;
+    w.T = min(w.T, part_begin(p, runs, part + 1) * kPartTiles);
     if (w.j0 >= w.T) return w;
   }
   w.valid = true;
@@ -239,7 +254,11 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* o
 // unequal lengths (64 of 64 to 2048 tokens, 32 heads on 8: 52 us, 61 without; 2 of 2529 and 15337, 1354 rows:
 // 227 and 304; the chunks of prompts above: 193 and 190).
 template <bool kGrouped>
-__device__ __forceinline__ int item_of(int r) {
+__device__ __forceinline__ int item_of(const PrefillParams& p, int r) {
+  if (kGrouped && p.few > 0) {  // a part of the full size, or smaller ones in turn
+    const int b = static_cast<int>(blockIdx.x);
+    return b + (b < static_cast<int>(gridDim.x) - p.few ? r * (1 << 30) : r * p.few);
+  }
   if (kGrouped && (r & 1)) return (r + 1) * static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   return r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
 }
@@ -291,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // (the join behind this launch, which waits for its end)
+  if (kGrouped && p.parts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
   const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
   // Grouped, without an order from the caller: more items than blocks are dealt out the longest sequence
@@ -327,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     const bool is_v = (warp == kWarpV);
     const CUtensorMap* map = is_v ? &tm_v : &tm_k;
     bool ok = true;
-    for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+    for (int turn = 0, it = item_of<kGrouped>(p, 0); ok && it < n_items; it = item_of<kGrouped>(p, ++turn)) {
       const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, !is_v && lane == 0);
       if (!w.valid) continue;
       const int32_t* table = p.block_tables + static_cast<size_t>(w.seq) * p.max_blocks;
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       const uint64_t v_desc0 = smem_desc_sw128(v_tile(0), kHalfBytes, 1024);
       int g = 0, items = 0;
       bool ok = true;
-      for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+      for (int turn = 0, it = item_of<kGrouped>(p, 0); ok && it < n_items; it = item_of<kGrouped>(p, ++turn)) {
         const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, false);
         if (!w.valid) continue;
         if (!mbar_wait_bounded(&bars->q_full, items & 1)) {
@@ -529,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     int g = 0;
     bool ok = true;
-    for (int turn = 0, it = item_of<kGrouped>(0); ok && it < n_items; it = item_of<kGrouped>(++turn)) {
+    for (int turn = 0, it = item_of<kGrouped>(p, 0); ok && it < n_items; it = item_of<kGrouped>(p, ++turn)) {
       const Tile w = decode_tile<kGrouped>(p, order, it, num_seqs, num_qtiles, false);
       if (!w.valid) continue;
       const bool row_valid = r < w.rows;
@@ -660,14 +681,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
                       mbar_wait_bounded(&bars->s_free[g_last & 1], (g_last >> 1) & 1));
       if (!ok) break;
       tc_fence_after();
-      const bool whole = !kGrouped || p.parts == 1;
+      const bool whole = !kGrouped || w.whole;
       const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
       // Rows leave through the warp's 2 KB of the staging buffer, 64 bytes of
       // each at a time: each lane writes its row's piece, then the warp stores
       // whole 64-byte row segments (8 rows per instruction) rather than 16
       // bytes of 32 rows.  Pieces sit at an XOR of (row / 2) % 4 so that
       // neither side has bank conflicts.
-      const int esz = p.out_dtype == PA_F32 ? 4 : 2;  // (a part's: 4)
+      const int esz = !whole || p.out_dtype == PA_F32 ? 4 : 2;
       const size_t row_bytes = static_cast<size_t>(p.num_heads) * D * esz;
       const int first_head = kGrouped ? w.h * p.group : w.h, first = kGrouped ? 0 : warp * 32;
       char* out_warp = static_cast<char*>(p.out) +
@@ -778,66 +799,71 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   }
 }
 
-// Joins the parts of an item: a warp a row, kJoinRows rows a thread block.
-constexpr int kJoinRows = 8;
+// Joins the parts of an item, a warp a row, kJoinRows rows a thread block in turns of eight.
+constexpr int kJoinRows = 16, kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinRows * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     paged_chunk_join_kernel(const PrefillParams p, void* out, const int out_dtype, const float lift,
                             const int num_seqs, const int num_qtiles) {
   constexpr int kVec = D / 32, kAhead = D == 256 ? 4 : 8;
   const int lane = threadIdx.x & 31, item = blockIdx.x / (kQTile / kJoinRows);
-  const int r = blockIdx.x % (kQTile / kJoinRows) * kJoinRows + (threadIdx.x >> 5);
+  const int r0 = blockIdx.x % (kQTile / kJoinRows) * kJoinRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   PrefillParams whole = p;
   whole.parts = 1;
+  whole.few = 0;
   const Tile w = decode_tile<true>(whole, nullptr, item, num_seqs, num_qtiles, false);
-  if (!w.valid || r >= w.rows) return;
+  if (!w.valid) return;
   const int runs = (w.T + kPartTiles - 1) / kPartTiles;
-  // lane i: part i, which may have had no keys
-  const size_t row0 = static_cast<size_t>(w.place) * p.parts * kQTile + r;  // (place: of the item as a whole)
-  const bool mine = lane < p.parts && runs * lane / p.parts < runs * (lane + 1) / p.parts;
-  const float2 ml = mine ? p.part_ml[row0 + static_cast<size_t>(lane) * kQTile] : make_float2(-INFINITY, 0.f);
-  float M = ml.x;  // (a reference is a number or -infinity)
+  if (part_begin(p, runs, 1) >= runs) return;  // written already
+  for (int r = r0 + static_cast<int>(threadIdx.x >> 5); r < min(w.rows, r0 + kJoinRows); r += kJoinWarps) {
+    // lane i: part i, which may have had no keys
+    const size_t row0 = static_cast<size_t>(w.place) * p.parts * kQTile + r;  // (place: of the item as a whole)
+    const bool mine = lane < p.parts && part_begin(p, runs, lane) < part_begin(p, runs, lane + 1);
+    const float2 ml = mine ? p.part_ml[row0 + static_cast<size_t>(lane) * kQTile] : make_float2(-INFINITY, 0.f);
+    float M = ml.x;  // (a reference is a number or -infinity)
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
-  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-  // parts that the row sees keys of: a NaN in them counts, however small their weight
-  const unsigned seen = __ballot_sync(kFullMask, ml.x != -INFINITY);
-  float l = ml.x == -INFINITY ? 0.f : f * ml.y;
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, off));
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    // parts that the row sees keys of: a NaN in them counts, however small their weight
+    const unsigned seen = __ballot_sync(kFullMask, ml.x != -INFINITY);
+    float l = ml.x == -INFINITY ? 0.f : f * ml.y;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
-  float acc[kVec];
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(kFullMask, l, off);
+    float acc[kVec];
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-  const float* from = p.part_o + row0 * D + lane * kVec;
+    for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+    const float* from = p.part_o + row0 * D + lane * kVec;
 #pragma unroll 1
-  for (int i0 = 0; i0 < p.parts; i0 += kAhead) {
-    float v[kAhead][kVec], g[kAhead];
+    for (int i0 = 0; i0 < p.parts; i0 += kAhead) {
+      float v[kAhead][kVec], g[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      g[k] = __shfl_sync(kFullMask, f, (i0 + k) & 31);
-      if (seen >> (i0 + k) & 1) {
+      for (int k = 0; k < kAhead; ++k) {
+        g[k] = __shfl_sync(kFullMask, f, (i0 + k) & 31);
+        if (seen >> (i0 + k) & 1) {
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2)
-          *reinterpret_cast<float2*>(&v[k][e]) =
-              *reinterpret_cast<const float2*>(from + static_cast<size_t>(i0 + k) * kQTile * D + e);
+          for (int e = 0; e < kVec; e += 2)
+            *reinterpret_cast<float2*>(&v[k][e]) =
+                *reinterpret_cast<const float2*>(from + static_cast<size_t>(i0 + k) * kQTile * D + e);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (seen >> (i0 + k) & 1) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(g[k], v[k][e], acc[e]);
+        }
     }
+    const float inv = l > 0.f ? 1.f / l : l;  // NaN: every channel
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (seen >> (i0 + k) & 1) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(g[k], v[k][e], acc[e]);
-      }
+    for (int e = 0; e < kVec; ++e) acc[e] *= inv;
+    const int token = r * p.inv_group >> 16;
+    const size_t row = static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + w.h * p.group +
+                       (r - token * p.group);
+    store_out<kVec>(out, row * D + lane * kVec, acc, out_dtype);
+    if (p.lse != nullptr && lane == 0) p.lse[row] = (M - lift + log2f(l)) * kLn2;
   }
-  const float inv = l > 0.f ? 1.f / l : l;  // NaN: every channel
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) acc[e] *= inv;
-  const int token = r * p.inv_group >> 16;
-  const size_t row = static_cast<size_t>(w.q_begin + w.q0 + token) * p.num_heads + w.h * p.group +
-                     (r - token * p.group);
-  store_out<kVec>(out, row * D + lane * kVec, acc, out_dtype);
-  if (p.lse != nullptr && lane == 0) p.lse[row] = (M - lift + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host side
@@ -864,7 +890,9 @@ int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
                           (kGrouped ? p.num_kv_heads * static_cast<long long>(p.parts) : p.num_heads) *
                           num_qtiles;
   const long long slots = static_cast<long long>(sms) * Cfg<D>::kMinBlocks;
-  const unsigned grid = static_cast<unsigned>(items < slots ? items : slots);
+  unsigned grid = static_cast<unsigned>(items < slots ? items : slots);
+  if (kGrouped && p.few > 0)  // the full parts, and who share the smaller ones
+    grid = static_cast<unsigned>(items / p.parts * (p.parts - 1) + p.few);
   paged_prefill_kernel<BF16, D, kGrouped, kOne>
       <<<grid, kThreads, Cfg<D>::kSmemBytes, st>>>(tq, tk, tv, p, num_seqs, num_qtiles);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -903,13 +931,27 @@ int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, cons
 
 // The parts that an item's keys are shared out into, for so many (sequence, key head) and tiles of each: as
 // many as fill the card, where there are few items and tables are long.
-int chunk_parts(long long rows, long long tiles, long long cap) {
+// The places left over take a smaller last part of each item, `share` of which make one of the others
+// (1024 tokens over 30,000, 32 heads on 8, 256 items: 411 us, 440 without; 700 of 64 channels: 264 and 361).
+// That an item then has parts at all has to pay for the second kernel, which costs 5 us where lengths are short
+// and only tables long: items whose first part has all their keys are written by the first kernel.
+struct Parts {
+  int parts, share, units, few;
+};
+Parts chunk_parts(long long rows, long long tiles, long long cap, int head_dim) {
   const long long items = rows > kPartSlots ? rows : rows * tiles;
   const long long runs = (cap + kPartTiles * kKTile - 1) / (kPartTiles * kKTile);
-  long long parts = items > 0 ? kPartSlots / items : 1;
+  const long long full = items > 0 ? kPartSlots / items : 0;
+  if (full >= 1 && full < runs && full < kMaxParts && head_dim <= 128) {
+    const int f = static_cast<int>(full), few = static_cast<int>(kPartSlots - full * items);
+    const int share = few > 0 ? static_cast<int>((items + few - 1) / few) : kPartSlots;
+    if (f == 1 ? share <= 9 && runs >= 3 * (share + 1) : share <= 4) return {f + 1, share, f * share + 1, few};
+  }
+  long long parts = full;
   if (parts > runs) parts = runs;
   if (parts > kMaxParts) parts = kMaxParts;
-  return static_cast<int>(parts < 1 ? 1 : parts);
+  const int n = static_cast<int>(parts < 1 ? 1 : parts);
+  return {n, 1, n, 0};
 }
 // Tiles of a sequence's rows; it has no more queries than tokens.
 long long chunk_tiles(int max_query_len, int group, long long cap) {
@@ -917,7 +959,7 @@ long long chunk_tiles(int max_query_len, int group, long long cap) {
   return ((max_query_len < cap ? max_query_len : cap) + tile_tokens - 1) / tile_tokens;
 }
 size_t chunk_workspace(int head_dim) {
-  return static_cast<size_t>(kPartSlots) * kQTile * (head_dim * sizeof(float) + sizeof(float2));
+  return static_cast<size_t>(kPartPlaces) * kQTile * (head_dim * sizeof(float) + sizeof(float2));
 }
 
 }  // namespace
@@ -999,7 +1041,8 @@ extern "C" size_t paged_attn_chunk_workspace_size(int num_seqs, int num_heads, i
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   // enough for the one sequence that a smaller call may have, whatever this one uses
-  return chunk_parts(1, 1, static_cast<long long>(max_blocks_per_seq) * block_size) > 1 ? chunk_workspace(head_dim) : 0;
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
+  return chunk_parts(1, 1, cap, head_dim).parts > 1 ? chunk_workspace(head_dim) : 0;
 }
 
 extern "C" size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads, int num_kv_heads,
@@ -1010,8 +1053,8 @@ extern "C" size_t paged_attn_chunk_workspace_needed(int num_seqs, int num_heads,
   const int group = most ? num_heads / num_kv_heads : 1;
   if (most == 0 || group > kQTile) return 0;
   const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
-  return chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, chunk_tiles(max_query_len, group, cap), cap) > 1
-             ? most : 0;
+  const long long tiles = chunk_tiles(max_query_len, group, cap);
+  return chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, tiles, cap, head_dim).parts > 1 ? most : 0;
 }
 
 extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int total_queries,
@@ -1068,12 +1111,15 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   p.tile_tokens = kQTile / group;
   p.inv_group = (65536 + group - 1) / group;
   p.lse = lse;
-  p.parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, qtiles, cap);
+  const Parts parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, qtiles, cap, head_dim);
+  p.parts = parts.parts;
+  p.share = parts.share;
+  p.units = parts.units;
+  p.few = parts.few;
   if (p.parts > 1) {
     if (!workspace || workspace_bytes < chunk_workspace(head_dim)) return PA_ERR_INVALID_ARG;
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(kPartSlots) * kQTile * head_dim);
-    p.out_dtype = PA_F32;
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(kPartPlaces) * kQTile * head_dim);
   }
   const auto run = out_dtype == PA_F32 ? run_prefill<true, false> : run_prefill<true, true>;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1081,12 +1127,18 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   const int status = run(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, tiles, dtype == PA_BF16, st);
   if (status != PA_OK || p.parts == 1) return status;
   const float lift = dtype == PA_BF16 ? lift_of<true, true>() : lift_of<false, true>();
-  const unsigned grid = static_cast<unsigned>(num_seqs) * num_kv_heads * tiles * (kQTile / kJoinRows);
-  if (head_dim == 64)
-    paged_chunk_join_kernel<64><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, lift, num_seqs, tiles);
-  else if (head_dim == 128)
-    paged_chunk_join_kernel<128><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, lift, num_seqs, tiles);
-  else
-    paged_chunk_join_kernel<256><<<grid, kJoinRows * 32, 0, st>>>(p, out, out_dtype, lift, num_seqs, tiles);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(num_seqs) * num_kv_heads * tiles * (kQTile / kJoinRows));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const auto join = head_dim == 64    ? paged_chunk_join_kernel<64>
+                    : head_dim == 128 ? paged_chunk_join_kernel<128>
+                                      : paged_chunk_join_kernel<256>;
+  if (cudaLaunchKernelEx(&cfg, join, p, out, out_dtype, lift, num_seqs, tiles) != cudaSuccess) return PA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

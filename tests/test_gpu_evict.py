@@ -268,6 +268,22 @@ def test_the_order_of_sequences_changes_nothing(B, n, Hq, H, D, most):
         assert torch.equal(out, want) and torch.equal(lse, wlse)
 
 
+@pytest.mark.parametrize("lens,news,Hq,H,cap", [
+    ([5003], [640], 32, 2, 5200),                                   # 160 items: a part and half a part each
+    ([5000, 17, 4096, 4097, 3, 2900, 1] + [600] * 25, [3] * 32, 8, 2, 5000),   # 64: four and half a part
+    ([9000] + [40] * 39, [3] * 40, 16, 4, 9000),                    # 160, of which only four have a second part
+])
+@pytest.mark.parametrize("out_dtype", [torch.float32, FH])
+def test_parts_of_two_sizes(B, lens, news, Hq, H, cap, out_dtype):
+    news = [min(n, length) for n, length in zip(news, lens)]
+    b = chunk_batch(22, lens, news, Hq, H, 64, 16, FH, wide=max(0, cap // 16 - (max(lens) + 15) // 16))
+    out, lse, rec = run_chunk(B, b, out_dtype=out_dtype)
+    assert rec == [0, 0, 0, 0]
+    check_chunk(b, out, lse)
+    again, wlse, _ = run_chunk(B, b, out_dtype=out_dtype)
+    assert torch.equal(again, out) and torch.equal(wlse, lse)
+
+
 def test_chunk_leaves_out_inconsistent_sequences(B):
     b = chunk_batch(7, [50, 30, 60, 40], [5, 4, 8, 3], 6, 2, 64, 16, FH)
     b["lens"] = b["lens"].copy()
