@@ -770,6 +770,42 @@ def test_two_captured_steps_replay_side_by_side(B):
             assert all(torch.equal(x, y) for x, y in zip(state(b), w))
 
 
+@pytest.mark.parametrize("lens,news,Hq,H", [([9000, 17], [3, 2], 8, 1), ([5003], [640], 32, 2)])
+def test_captured_chunks_in_parts(B, lens, news, Hq, H):
+    """Replayed with other queries and lengths, two calls behind each other through one workspace."""
+    b = chunk_batch(24, lens, news, Hq, H, 64, 16, BF)
+    start, tables, lengths = dev(b["start"]), dev(b["tables"]), dev(b["lens"])
+    need = B.paged_attn_chunk_workspace_needed(len(lens), Hq, H, 64, 16, b["tables"].shape[1], b["most"])
+    assert need > 0
+    space = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.full_like(b["q"], 7) for _ in range(2)]
+
+    def step():
+        for out, v in zip(outs, (b["vc"], b["kc"])):
+            B.paged_attn_chunk(b["q"], start, b["most"], b["kc"], v, tables, lengths, b["scale"], out=out,
+                               workspace=space)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for shorter in (0, 1500):
+        b["q"].copy_(torch.randn(b["q"].shape, device="cuda"))
+        lengths.copy_(dev(b["lens"]) - torch.tensor([shorter] + [0] * (len(lens) - 1), device="cuda", dtype=torch.int32))
+        graph.replay()
+        got = [out.clone() for out in outs]
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, outs))
+        lse = torch.full(b["q"].shape[:2], 7.0, device="cuda")
+        B.paged_attn_chunk(b["q"], start, b["most"], b["kc"], b["vc"], tables, lengths, b["scale"], out=outs[0], lse=lse)
+        assert torch.equal(outs[0], got[0])
+        check_chunk({**b, "lens": lengths.cpu().numpy()}, got[0], lse)
+
+
 def test_captured_weights_of_whole_prompts(B):
     """The launch in clusters, captured and replayed."""
     b = chunk_batch(75, [600, 500], [600, 400], 14, 2, 64, 8, BF)
