@@ -933,8 +933,9 @@ int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, cons
 // many as fill the card, where there are few items and tables are long.
 // The places left over take a smaller last part of each item, `share` of which make one of the others
 // (1024 tokens over 30,000, 32 heads on 8, 256 items: 411 us, 440 without; 700 of 64 channels: 264 and 361).
-// That an item then has parts at all has to pay for the second kernel, which costs 5 us where lengths are short
-// and only tables long: items whose first part has all their keys are written by the first kernel.
+// That an item then has parts at all has to pay for the second kernel and the sums' way to it: 1024 tokens over
+// 13,000 take 197 us so, 193 without, over 16,000 236 and 237, 700 over 8000 102 and 119.  Where lengths are
+// short and only tables long it costs 5 us: items of one part are written by the first kernel.
 struct Parts {
   int parts, share, units, few;
 };
@@ -945,7 +946,7 @@ Parts chunk_parts(long long rows, long long tiles, long long cap, int head_dim) 
   if (full >= 1 && full < runs && full < kMaxParts && head_dim <= 128) {
     const int f = static_cast<int>(full), few = static_cast<int>(kPartSlots - full * items);
     const int share = few > 0 ? static_cast<int>((items + few - 1) / few) : kPartSlots;
-    if (f == 1 ? share <= 9 && runs >= 3 * (share + 1) : share <= 4) return {f + 1, share, f * share + 1, few};
+    if (f == 1 ? share <= 9 && 2 * runs >= 9 * (share + 1) : share <= 4) return {f + 1, share, f * share + 1, few};
   }
   long long parts = full;
   if (parts > runs) parts = runs;

@@ -269,7 +269,7 @@ def test_the_order_of_sequences_changes_nothing(B, n, Hq, H, D, most):
 
 
 @pytest.mark.parametrize("lens,news,Hq,H,cap", [
-    ([5003], [640], 32, 2, 5200),                                   # 160 items: a part and half a part each
+    ([7003], [640], 32, 2, 7200),                                   # 160 items: a part and half a part each
     ([5000, 17, 4096, 4097, 3, 2900, 1] + [600] * 25, [3] * 32, 8, 2, 5000),   # 64: four and half a part
     ([9000] + [40] * 39, [3] * 40, 16, 4, 9000),                    # 160, of which only four have a second part
 ])
@@ -770,7 +770,7 @@ def test_two_captured_steps_replay_side_by_side(B):
             assert all(torch.equal(x, y) for x, y in zip(state(b), w))
 
 
-@pytest.mark.parametrize("lens,news,Hq,H", [([9000, 17], [3, 2], 8, 1), ([5003], [640], 32, 2)])
+@pytest.mark.parametrize("lens,news,Hq,H", [([9000, 17], [3, 2], 8, 1), ([7003], [640], 32, 2)])
 def test_captured_chunks_in_parts(B, lens, news, Hq, H):
     """Replayed with other queries and lengths, two calls behind each other through one workspace."""
     b = chunk_batch(24, lens, news, Hq, H, 64, 16, BF)
