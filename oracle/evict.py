@@ -59,7 +59,8 @@ def by_key_head(w, kv_heads):
 
 def evict(k_cache, v_cache, tables, seq_lens, kept, weights=None, new_tables=None):
     """In place: place j of (sequence, key head) takes the rows and the weight that place
-    kept[i][h][j] held; the weights of places without an entry become 0."""
+    kept[i][h][j] held; places without an entry keep their rows, in a new block too, and their
+    weights become 0."""
     old_k, old_v, bs = k_cache.copy(), v_cache.copy(), k_cache.shape[2]
     to = tables if new_tables is None else new_tables
     for i, length in enumerate(seq_lens):
@@ -68,11 +69,10 @@ def evict(k_cache, v_cache, tables, seq_lens, kept, weights=None, new_tables=Non
                 old_w = weights[i, h].copy()
                 weights[i, h, :int(length)] = 0
             for j in range(min(int(length), kept.shape[2])):
-                s = int(kept[i, h, j])
-                if s < 0:
-                    continue
+                entry = int(kept[i, h, j])
+                s = j if entry < 0 else entry
                 a, b = int(tables[i][s // bs]), int(to[i][j // bs])
                 k_cache[b, h, j % bs] = old_k[a, h, s % bs]
                 v_cache[b, h, j % bs] = old_v[a, h, s % bs]
-                if weights is not None:
+                if weights is not None and entry >= 0:
                     weights[i, h, j] = old_w[s]

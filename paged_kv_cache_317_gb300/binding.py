@@ -1061,11 +1061,12 @@ def kv_cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                    new_tables: Optional[torch.Tensor] = None,
                    error_record: Optional[torch.Tensor] = None, stream=None) -> None:
     """Place j of each (sequence, key head) takes the rows of K and V, and the weight, that place
-    kept[i,h,j] held; the weights of the other places become 0.  caches [B,H,bs,D]; block_tables
-    int32 [N,MB]; seq_lens int32 [N], the lengths before; kept int32 [N,H,K], ascending places, then
-    -1 (paged_block_select over the weights, block size 1); weights: optional float32 [N,H,places];
-    new_tables: optional int32 [N,MB'], the tables after BlockAllocator.batch_evict, where other
-    sequences hold blocks of these."""
+    kept[i,h,j] held; the other places keep their rows, and their weights become 0.  caches
+    [B,H,bs,D]; block_tables int32 [N,MB]; seq_lens int32 [N], the lengths before; kept int32 [N,H,K],
+    ascending places, then -1 (paged_block_select over the weights, block size 1); weights: optional
+    float32 [N,H,places]; new_tables: optional int32 [N,MB'], the tables after
+    BlockAllocator.batch_evict, where other sequences hold blocks of these: a sequence of at most K
+    tokens keeps its blocks in it, and its list has to keep every place."""
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape

@@ -2,8 +2,8 @@
 //
 // Place j of (sequence, key head) takes the row of K, of V and the weight that place kept[j] held.
 // In place this is a gather within one array, safe in order: kept[j] >= j, so a row that is still to
-// be read (for place j' > j, from a place >= j') is never one that place j overwrites.  K and V are
-// moved apart.  A thread block, or for few lists a cluster, takes one list and goes through it in
+// be read (for place j' > j, from a place >= j') is never one that place j overwrites.  Into other
+// blocks, places without an entry take their own rows along.  K and V are moved apart.  A thread block, or for few lists a cluster, takes one list and goes through it in
 // rounds: every thread loads its pieces of the round's rows into registers and looks up rows of the
 // next round, a barrier, every thread stores its pieces.  Loads of later rounds may run ahead of the
 // stores of earlier ones; only the loads of a round itself have to be over, which the barrier sees to.
@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(R::kThreads, R::kBlocks) kv_cache_evict_kernel
   float* weights = p.weights == nullptr || is_v ? nullptr : p.weights + sh * p.weights_row;
   uint4* cache = is_v ? p.v : p.k;
   const int places = min(p.num_kept, L);
+  const bool renewed = p.new_tables != p.tables, uncut = renewed && L <= p.num_kept;
 
   // the row of place j
   auto row_of = [&](const int32_t* t, int blocks, int j) -> long long {
@@ -91,11 +92,16 @@ __global__ void __launch_bounds__(R::kThreads, R::kBlocks) kv_cache_evict_kernel
       long long src = -1, dst = -1;
       places_from[u] = -2;
       if (i < p.rows && j < places) {
-        const int s = kept[j];
-        if (s >= j && s < L) {
-          src = row_of(table, p.max_blocks, s);
+        const int s = kept[j], b = j / p.block_size;
+        bool moves = s >= j && s < L;
+        // (a sequence that loses no tokens keeps its table, whose blocks a fork may read: its rows stay)
+        if (uncut && s != j && b < p.max_blocks && b < p.new_max_blocks && table[b] == new_table[b]) moves = false;
+        if (moves || renewed) {
+          src = row_of(table, p.max_blocks, moves ? s : j);
           dst = row_of(new_table, p.new_max_blocks, j);
           if (dst < 0 || src == dst) src = -1;
+        }
+        if (moves) {
           places_from[u] = s == j ? -2 : s;
         } else if (s == -1) {
           places_from[u] = -1;

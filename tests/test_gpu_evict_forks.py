@@ -1,0 +1,89 @@
+"""kv_cache_evict where lists have places without an entry and entries that are refused, over blocks that
+forks hold too: bit for bit what oracle.evict moves."""
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_evict as E
+import test_gpu_sparse as S
+
+pytestmark = pytest.mark.gpu
+
+BAD_POSITION = 12
+
+
+@pytest.fixture(scope="module")
+def B(lib):
+    from paged_kv_cache_317_gb300 import binding
+    return binding
+
+
+def forked(B, keep, bs=16, H=2, D=64, blocks=80):
+    """Sequences 0, 1 (a fork that has grown) and 2 of which the first two are cut to `keep` tokens; 3 and 4
+    are forks of 0 and 2 that are not listed.  Every block holds something."""
+    alloc = B.BlockAllocator(blocks, bs, np.random.default_rng(0).permutation(blocks))
+    alloc.add(0, 100)
+    alloc.fork(0, 1)
+    alloc.add(2, 50)
+    alloc.fork(0, 3)
+    alloc.fork(2, 4)
+    slots, pairs = alloc.batch_append([1])
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randn((blocks, H, bs, D), generator=gen, device="cuda").half() for _ in range(2))
+    B.block_copy([kc], [vc], torch.from_numpy(pairs).cuda())
+    tables, lens = alloc.batch_block_tables([0, 1, 2], 110 // bs + 1)
+    alloc.batch_evict([0, 1, 2], keep)
+    new, _ = alloc.batch_block_tables([0, 1, 2], 110 // bs + 1)
+    assert np.array_equal(new[2], tables[2])            # of at most `keep` tokens: as it was, its fork's too
+    return dict(kc=kc, vc=vc, tables=tables, lens=lens, bs=bs, H=H), new
+
+
+@pytest.mark.parametrize("bs", [1, 8, 16])
+@pytest.mark.parametrize("holes", [0.2, 1.0])
+def test_places_without_an_entry_keep_their_rows_in_fresh_blocks(B, bs, holes):
+    b, new = forked(B, 60, bs=bs, blocks=80 * 16 // bs)
+    rng = np.random.default_rng(bs)
+    kept = E.pick(rng, b["lens"], 2, 60)
+    kept[rng.random(kept.shape) < holes] = -1
+    E.check_evict(B, b, kept, new_tables=new)
+
+
+def test_a_refused_entry_keeps_its_row_in_a_fresh_block(B):
+    b, new = forked(B, 60)
+    kept = E.pick(np.random.default_rng(4), b["lens"], 2, 60)
+    kept[0, 1, 7] = 200                                 # past the last token
+    E.check_evict(B, b, kept, new_tables=new, expect=(BAD_POSITION, 1, 1, 200), skip=[(0, 1, 7)])
+
+
+def test_rows_that_a_fork_reads_are_not_moved(B):
+    """Sequence 2 keeps its table, which sequence 4 holds too: a list that would move rows in it is refused."""
+    b, new = forked(B, 60)
+    kept = E.pick(np.random.default_rng(5), b["lens"], 2, 60)
+    assert np.array_equal(kept[2, 1, :50], np.arange(50))
+    kept[2, 1, 20] = 21
+    E.check_evict(B, b, kept, new_tables=new, expect=(BAD_POSITION, 1, 5, 21), skip=[(2, 1, 20)])
+    # in place, where the caller holds the blocks alone, the same list moves the row
+    b, _ = forked(B, 60)
+    own = {k: (v[2:] if k in ("tables", "lens") else v) for k, v in b.items()}
+    E.check_evict(B, own, kept[2:])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_lists_into_blocks_of_their_own(B, seed):
+    """Lists with holes, one sequence shorter than the list, into tables of which some blocks stay."""
+    rng = np.random.default_rng(1200 + seed)
+    H, D, bs = int(rng.choice([1, 3, 40])), int(rng.choice([8, 64, 128])), int(rng.choice([1, 8, 16, 48]))
+    lens = rng.integers(1, 900, 4).astype(np.int32)
+    K = int(rng.choice([5, 129, 400, 1000]))
+    b = S.make(1300 + seed, lens, H, H, D, bs, torch.bfloat16, wide=int(rng.integers(0, 3)))
+    kept = E.pick(rng, lens, H, K)
+    kept[rng.random(kept.shape) < 0.3] = -1
+    own, total = -(-min(K, int(lens.max())) // bs), len(b["kc"])
+    fresh = rng.permutation(len(lens) * own).reshape(len(lens), own).astype(np.int32) + total
+    for k in ("kc", "vc"):
+        more = torch.full((len(lens) * own, *b[k].shape[1:]), 9, dtype=b[k].dtype, device="cuda")
+        b[k] = torch.cat([b[k], more])
+    held = b["tables"][:, :own]
+    new = np.where((rng.random(fresh.shape) < 0.3) & (held >= 0), held, fresh)
+    E.check_evict(B, b, kept, new_tables=new, weights=bool(seed % 4))
