@@ -767,9 +767,9 @@ int paged_attn_decode_weights(const void* q, const void* k_cache, const void* v_
  *                 their sequence.
  *   weights       may be NULL
  *   head_dim      a multiple of 8, at most 1024;  block_size: any
- * A block number out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and the row is left out;
- * a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.  Key bounds are left alone:
- * after it, kv_block_bounds. */
+ * A block number out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and the row is left out,
+ * its weight with it; a length out of range is recorded as PA_ERR_BAD_SEQ_LEN and clamped.  Key bounds
+ * are left alone: after it, kv_block_bounds. */
 int kv_cache_evict(void* k_cache, void* v_cache, const int32_t* block_tables,
                    const int32_t* new_tables, const int32_t* seq_lens, const int32_t* kept,
                    int num_kept, float* weights, int64_t weights_tokens, int num_seqs,

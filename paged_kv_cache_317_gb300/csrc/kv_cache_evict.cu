@@ -99,15 +99,15 @@ __global__ void __launch_bounds__(R::kThreads, R::kBlocks) kv_cache_evict_kernel
         if (moves || renewed) {
           src = row_of(table, p.max_blocks, moves ? s : j);
           dst = row_of(new_table, p.new_max_blocks, j);
-          if (dst < 0 || src == dst) src = -1;
         }
         if (moves) {
-          places_from[u] = s == j ? -2 : s;
+          if (src >= 0 && dst >= 0 && s != j) places_from[u] = s;  // a weight goes with its row, or stays
         } else if (s == -1) {
           places_from[u] = -1;
         } else if (!is_v) {
           report_error(p.err, PA_ERR_BAD_POSITION, sh, s);
         }
+        if (dst < 0 || src == dst) src = -1;
       }
       if (i < p.rows) {
         from[buf][i] = src;

@@ -1,5 +1,5 @@
-"""kv_cache_evict where lists have places without an entry and entries that are refused, over blocks that
-forks hold too: bit for bit what oracle.evict moves."""
+"""kv_cache_evict where lists have places without an entry, entries that are refused and rows that are left
+out, over blocks that forks hold too: bit for bit what oracle.evict moves."""
 
 import numpy as np
 import pytest
@@ -10,7 +10,7 @@ import test_gpu_sparse as S
 
 pytestmark = pytest.mark.gpu
 
-BAD_POSITION = 12
+BAD_BLOCK, BAD_POSITION = 4, 12
 
 
 @pytest.fixture(scope="module")
@@ -87,3 +87,34 @@ def test_random_lists_into_blocks_of_their_own(B, seed):
     held = b["tables"][:, :own]
     new = np.where((rng.random(fresh.shape) < 0.3) & (held >= 0), held, fresh)
     E.check_evict(B, b, kept, new_tables=new, weights=bool(seed % 4))
+
+
+def left_out(B, tables, kept, new=None, bad=10 ** 6):
+    """A call with a block out of range, and what is to come of it: rows and weights that it leaves out are
+    as they were."""
+    b = S.make(67, [64], 1, 1, 64, 16, torch.float16)
+    k, w = E.bits(b["kc"]).copy(), E.place(b)
+    before = w.cpu().numpy().copy()
+    t = b["tables"].copy()
+    t[0, tables] = bad
+    if new is not None:
+        new = np.array([[b["tables"][0, n] if n is not None else bad for n in new]], np.int32)
+    rec = B.new_error_record()
+    B.kv_cache_evict(b["kc"], b["vc"], E.dev(t), E.dev([64]), E.dev(kept[None, None]), weights=w, error_record=rec,
+                     new_tables=None if new is None else E.dev(new))
+    return B.pa_error_read(rec), k, E.bits(b["kc"]), before[0, 0], w.cpu().numpy()[0, 0], b["tables"][0]
+
+
+def test_a_weight_stays_where_its_row_is_left_out(B):
+    # places 32 to 47, which 0 to 15 are to take, sit in the bad block
+    rec, k, after, before, w, t = left_out(B, [2], np.arange(32, 64))
+    assert rec == [BAD_BLOCK, 16, 0, 10 ** 6]
+    assert np.array_equal(after[t[0]], k[t[0]]) and np.array_equal(after[t[1]], k[t[3]])
+    assert np.array_equal(w[:16], before[:16]) and np.array_equal(w[16:32], before[48:64])
+    assert not w[32:64].any()
+    # the new places 16 to 31 have no block
+    rec, k, after, before, w, t = left_out(B, [], np.arange(32, 64), new=[0, None])
+    assert rec == [BAD_BLOCK, 16, 0, 10 ** 6]
+    assert np.array_equal(after[t[0]], k[t[2]]) and np.array_equal(after[t[1:]], k[t[1:]])
+    assert np.array_equal(w[:16], before[32:48]) and np.array_equal(w[16:32], before[16:32])
+    assert not w[32:64].any()
