@@ -58,6 +58,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tcgen05.cuh"
@@ -147,18 +148,32 @@ struct PrefillParams {
   int num_heads, block_size, max_blocks, num_blocks, out_dtype;
   int total_queries;  // rows of q and out
   float qscale;
-  // grouped: query heads per key head, tokens per tile, and ceil(2^16 / group): r / group is
+};
+
+// Each form has parameters of its own: with the grouped ones' behind them the dense kernel of 128 channels in
+// bf16 spills four registers (16 chunks of 512 rows, 40 heads, contexts of up to 2048: 209 us, 203.6 without).
+struct DenseParams : PrefillParams {
+  static constexpr int num_kv_heads = 0, group = 1, tile_tokens = kQTile, inv_group = 65536;
+  static constexpr int parts = 1, share = 1, units = 1, few = 0;
+  static constexpr float *lse = nullptr, *part_o = nullptr;
+  static constexpr float2* part_ml = nullptr;
+};
+struct GroupedParams : PrefillParams {
+  // query heads per key head, tokens per tile, and ceil(2^16 / group): r / group is
   // r * inv_group >> 16 for r < 128, group <= 128
   int num_kv_heads, group, tile_tokens, inv_group;
   float* lse;         // [total_queries][num_heads], or NULL
-  // Grouped, with parts > 1: an item's keys are shared out over so many, each of whose O, not divided by
-  // its sum, and (reference, sum) go to [item][part][kQTile] rows of fp32.
+  // With parts > 1: an item's keys are shared out over so many, each of whose O, not divided by its sum,
+  // and (reference, sum) go to [item][part][kQTile] rows of fp32.
   // Part i begins at run i share / units of an item's runs of tiles; few > 0: a last, smaller part, which so
   // many blocks at the grid's end deal out among them.
   int parts, share, units, few;
   float* part_o;
   float2* part_ml;
 };
+static_assert(sizeof(DenseParams) == sizeof(PrefillParams), "nothing of the grouped form");
+template <bool kGrouped>
+using ParamsOf = std::conditional_t<kGrouped, GroupedParams, DenseParams>;
 
 // One work item: 128-query tile `q0 / kQTile` of sequence `seq`, head `h`.
 // Grouped, `h` is a key head, the tile's rows are (token, query head of the key head), heads innermost,
@@ -175,7 +190,8 @@ struct Tile {
 };
 
 // The run of tiles where part i begins, or the last one ends.
-__device__ __forceinline__ int part_begin(const PrefillParams& p, int runs, int i) {
+template <class Params>
+__device__ __forceinline__ int part_begin(const Params& p, int runs, int i) {
   return i >= p.parts ? runs : min(runs, (runs * p.share * i + p.units - 1) / p.units);
 }
 
@@ -185,7 +201,7 @@ __device__ __forceinline__ int part_begin(const PrefillParams& p, int runs, int 
 // agree on which items exist.
 // order: where the sequences' order is in shared memory, or NULL.
 template <bool kGrouped>
-__device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* order, int it, int num_seqs,
+__device__ __forceinline__ Tile decode_tile(const ParamsOf<kGrouped>& p, const int* order, int it, int num_seqs,
                                             int num_qtiles, bool report) {
   Tile w;
   w.valid = false;
@@ -254,7 +270,7 @@ __device__ __forceinline__ Tile decode_tile(const PrefillParams& p, const int* o
 // unequal lengths (64 of 64 to 2048 tokens, 32 heads on 8: 52 us, 61 without; 2 of 2529 and 15337, 1354 rows:
 // 227 and 304; the chunks of prompts above: 193 and 190).
 template <bool kGrouped>
-__device__ __forceinline__ int item_of(const PrefillParams& p, int r) {
+__device__ __forceinline__ int item_of(const ParamsOf<kGrouped>& p, int r) {
   if (kGrouped && p.few > 0) {  // a part of the full size, or smaller ones in turn
     const int b = static_cast<int>(blockIdx.x);
     return b + (b < static_cast<int>(gridDim.x) - p.few ? r * (1 << 30) : r * p.few);
@@ -267,7 +283,7 @@ template <bool BF16, int D, bool kGrouped, bool kOne>
 __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const PrefillParams p,
+                         const __grid_constant__ CUtensorMap tm_v, const ParamsOf<kGrouped> p,
                          const int num_seqs, const int num_qtiles) {
   using C = Cfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -804,13 +820,13 @@ constexpr int kJoinRows = 16, kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    paged_chunk_join_kernel(const PrefillParams p, void* out, const int out_dtype, const float lift,
+    paged_chunk_join_kernel(const GroupedParams p, void* out, const int out_dtype, const float lift,
                             const int num_seqs, const int num_qtiles) {
   constexpr int kVec = D / 32, kAhead = D == 256 ? 4 : 8;
   const int lane = threadIdx.x & 31, item = blockIdx.x / (kQTile / kJoinRows);
   const int r0 = blockIdx.x % (kQTile / kJoinRows) * kJoinRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  PrefillParams whole = p;
+  GroupedParams whole = p;
   whole.parts = 1;
   whole.few = 0;
   const Tile w = decode_tile<true>(whole, nullptr, item, num_seqs, num_qtiles, false);
@@ -878,7 +894,7 @@ cudaError_t ensure_prefill_smem() {
 
 template <bool BF16, int D, bool kGrouped, bool kOne>
 int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const PrefillParams& p, int num_seqs, int num_qtiles, cudaStream_t st) {
+                   const ParamsOf<kGrouped>& p, int num_seqs, int num_qtiles, cudaStream_t st) {
   if (ensure_prefill_smem<BF16, D, kGrouped, kOne>() != cudaSuccess) return PA_ERR_CUDA;
   // Persistent: one block per resident slot (Cfg<D>::kMinBlocks per SM), each
   // looping over its share of the (sequence, query tile, head) items.
@@ -901,7 +917,7 @@ int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 // The tensor maps of a call, and its launch.  A box of the cache is one 16-key chunk, or half of one
 // with 8-token blocks; a box of q the rows of a tile, 64 channels wide.
 template <bool kGrouped, bool kOne>
-int run_prefill(const PrefillParams& p, const void* q, const void* k_cache, const void* v_cache,
+int run_prefill(const ParamsOf<kGrouped>& p, const void* q, const void* k_cache, const void* v_cache,
                 unsigned long long cache_rows, int num_seqs, int head_dim, int num_qtiles, bool bf16,
                 cudaStream_t st) {
   CUtensorMap tq, tk, tv;
@@ -1015,7 +1031,7 @@ extern "C" int paged_attn_prefill_ex(const void* q, const int32_t* query_start,
   if (static_cast<long long>(num_seqs) * num_heads * qtiles >= (1ll << 30))
     return PA_ERR_INVALID_ARG;
 
-  PrefillParams p{};
+  DenseParams p{};
   p.seq_order = opts ? opts->seq_order : nullptr;
   p.query_start = query_start;
   p.seq_lens = seq_lens;
@@ -1093,7 +1109,7 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
       !aligned16(workspace))
     return PA_ERR_INVALID_ARG;
   const long long qtiles = chunk_tiles(max_query_len, group, cap);
-  PrefillParams p{};
+  GroupedParams p{};
   p.seq_order = seq_order;
   p.query_start = query_start;
   p.seq_lens = seq_lens;
