@@ -155,8 +155,7 @@ struct PrefillParams {
 struct DenseParams : PrefillParams {
   static constexpr int num_kv_heads = 0, group = 1, tile_tokens = kQTile, inv_group = 65536;
   static constexpr int parts = 1, share = 1, units = 1, few = 0;
-  static constexpr float *lse = nullptr, *part_o = nullptr;
-  static constexpr float2* part_ml = nullptr;
+  static constexpr float* part_o = nullptr;
 };
 struct GroupedParams : PrefillParams {
   // query heads per key head, tokens per tile, and ceil(2^16 / group): r / group is
