@@ -680,7 +680,8 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  * probabilities enter P.V as one number of the cache's type: off by at most 2^-8 (bf16) or
  * 2^-11 (fp16) of a weight, which is what the output's own rounding may be off by (fp16: and
  * by 2^-32 of the row's largest weight).  A NaN or infinity in V of a token may reach rows before
- * it in the chunk, whose weight for it is 0.
+ * it in the chunk, whose weight for it is 0.  A row whose every logit is -infinity is NaN, as in
+ * softmax, and its lse -infinity.
  * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x
  * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30.  Otherwise, checks
  * of the batch too, as paged_attn_prefill.

@@ -697,7 +697,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       if (!ok) break;
       tc_fence_after();
       const bool whole = !kGrouped || w.whole;
-      const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      // (grouped, a row whose every logit was -infinity is 0 / 0)
+      const float inv = whole ? (l > 0.f ? 1.f / l : kGrouped ? NAN : 0.f) : 1.f;
       // Rows leave through the warp's 2 KB of the staging buffer, 64 bytes of
       // each at a time: each lane writes its row's piece, then the warp stores
       // whole 64-byte row segments (8 rows per instruction) rather than 16
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
           for (int e = 0; e < kVec; ++e) acc[e] = fmaf(g[k], v[k][e], acc[e]);
         }
     }
-    const float inv = l > 0.f ? 1.f / l : l;  // NaN: every channel
+    const float inv = l > 0.f ? 1.f / l : NAN;  // every logit -infinity, or a NaN among them
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] *= inv;
     const int token = r * p.inv_group >> 16;

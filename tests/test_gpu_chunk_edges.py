@@ -1,0 +1,64 @@
+"""Corners of the grouped chunk attention and the attention weights."""
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_evict as E
+import test_gpu_sparse as S
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+BF, FH = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def B(lib):
+    from paged_kv_cache_317_gb300 import binding
+    return binding
+
+
+@pytest.mark.parametrize("lens,news", [([150, 40], [100, 3]), ([9000, 700], [3, 2])])   # one part, several
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_of_minus_infinity_alone(B, lens, news, dtype, D):
+    """softmax over logits that are all -infinity is 0 / 0: the outputs are NaN, the logarithm of the sum
+    -infinity, the weights NaN.  Rows with one number among them are as ever."""
+    b = E.chunk_batch(31, lens, news, 4, 2, D, 16, dtype)
+    b["q"].abs_()
+    where = [(int(b["tables"][0, t // 16]), t % 16) for t in range(lens[0])]
+    at, row = (torch.tensor(x, device="cuda") for x in zip(*where))
+    b["kc"][at, 1, row] = -INF                          # sequence 0, key head 1: query heads 2 and 3
+    first = lens[0] - news[0]
+    for out_dtype in (torch.float32, dtype):
+        out, lse, rec = E.run_chunk(B, b, out_dtype=out_dtype)
+        assert rec == [0, 0, 0, 0]
+        n = news[0]
+        assert bool(torch.isnan(out[:n, 2:]).all()) and bool((lse[:n, 2:] == -INF).all())
+        assert bool(torch.isfinite(out[:n, :2]).all()) and bool(torch.isfinite(lse[:n, :2]).all())
+        assert bool(torch.isfinite(out[n:]).all()) and bool(torch.isfinite(lse[n:]).all())
+        w = torch.zeros((2, 2, b["tables"].shape[1] * 16), device="cuda")
+        B.paged_chunk_weights(b["q"], lse, E.dev(b["start"]), b["most"], b["kc"], E.dev(b["tables"]), E.dev(b["lens"]),
+                              b["scale"], w)
+        assert bool(torch.isnan(w[0, 1, :lens[0]]).all()) and bool(torch.isfinite(w[0, 0]).all())
+        assert bool(torch.isfinite(w[1]).all()) and not bool(w[0, 1, lens[0]:].any())
+    # decode of the last rows: the same
+    last = torch.stack([b["q"][news[0] - 1], b["q"][sum(news) - 1]])
+    w = torch.zeros((2, 2, b["tables"].shape[1] * 16), device="cuda")
+    out = B.paged_attn_decode_weights(last, b["kc"], b["vc"], E.dev(b["tables"]), E.dev(b["lens"]), b["scale"], w)
+    assert bool(torch.isnan(out[0, 2:]).all()) and bool(torch.isfinite(out[0, :2]).all())
+    # One number, at the last token before the chunk: the row is that token's.  Its probability p is near 1, as
+    # the reference is its logit rounded; the two halves of p are within 2^-16 (bf16) or 2^-21 (fp16) of it, the sum
+    # is p, their products, sum, quotient and product add 8 u.
+    t = first - 1
+    b["kc"][at[t], 1, row[t]] = 0.5
+    out, lse, _ = E.run_chunk(B, b)
+    v = b["vc"][at[t], 1, row[t]].float()
+    tol = (2.0 ** (-16 if dtype is BF else -21) + 8 * E.U) * v.abs()
+    assert bool(((out[:news[0], 2:] - v).abs() <= tol).all())
+    assert bool(torch.isfinite(lse[:news[0], 2:]).all())
+    # infinity among them: NaN, as inf - inf is
+    b["kc"][at[t], 1, row[t]] = INF
+    out, lse, _ = E.run_chunk(B, b)
+    assert bool(torch.isnan(out[:news[0], 2:]).all()) and bool(torch.isfinite(out[:news[0], :2]).all())
