@@ -404,8 +404,9 @@ int pa_decode_share_plan_ex(const int32_t* block_tables, const int32_t* seq_lens
  *                 chunk is then loaded as two 8-row boxes)
  *   out           device [total_queries][num_heads][head_dim] in `out_dtype`
  * Rows of out outside every sequence's query range are not written.  A sequence
- * whose range is inconsistent (Q_i > L, range outside q, Q_i > max_query_len) is
- * recorded as PA_ERR_BAD_SEQ_LEN and skipped.  scale must be > 0.  Other
+ * whose range is inconsistent (Q_i > L, range outside q, Q_i > max_query_len, here
+ * rounded up to a multiple of 128) is recorded as PA_ERR_BAD_SEQ_LEN and skipped.
+ * scale must be > 0.  Other
  * arguments as for paged_attn_decode; num_blocks * num_heads * block_size must
  * be < 2^31.  Launch: one block per resident slot on the current device, each
  * looping over its share of the items (it reads the device's SM count on every
@@ -684,7 +685,7 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  * softmax, and its lse -infinity.
  * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x
  * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30.  Otherwise, checks
- * of the batch too, as paged_attn_prefill.
+ * of the batch too, as paged_attn_prefill; max_query_len is not rounded up.
  *
  * paged_attn_chunk_workspace_size is the same for all calls that may use a workspace (few
  * sequences with long tables): 608 x 128 rows of head_dim + 2 floats.

@@ -153,7 +153,7 @@ struct PrefillParams {
 // Each form has parameters of its own: with the grouped ones' behind them the dense kernel of 128 channels in
 // bf16 spills four registers (16 chunks of 512 rows, 40 heads, contexts of up to 2048: 209 us, 203.6 without).
 struct DenseParams : PrefillParams {
-  static constexpr int num_kv_heads = 0, group = 1, tile_tokens = kQTile, inv_group = 65536;
+  static constexpr int num_kv_heads = 0, group = 1, tile_tokens = kQTile, inv_group = 65536, max_query_len = 0;
   static constexpr int parts = 1, share = 1, units = 1, few = 0;
   static constexpr float* part_o = nullptr;
 };
@@ -161,6 +161,7 @@ struct GroupedParams : PrefillParams {
   // query heads per key head, tokens per tile, and ceil(2^16 / group): r / group is
   // r * inv_group >> 16 for r < 128, group <= 128
   int num_kv_heads, group, tile_tokens, inv_group;
+  int max_query_len;  // at most the tokens of a table
   float* lse;         // [total_queries][num_heads], or NULL
   // With parts > 1: an item's keys are shared out over so many, each of whose O, not divided by its sum,
   // and (reference, sum) go to [item][part][kQTile] rows of fp32.
@@ -237,7 +238,7 @@ __device__ __forceinline__ Tile decode_tile(const ParamsOf<kGrouped>& p, const i
   const bool bad_len = L < 0 || L > cap;
   L = L < 0 ? 0 : (L > cap ? cap : L);
   const bool bad_q = nq < 0 || nq > L || w.q_begin < 0 || w.q_begin > p.total_queries - nq ||
-                     nq > num_qtiles * tile_tokens;
+                     nq > (kGrouped ? p.max_query_len : num_qtiles * tile_tokens);
   if (bad_len || bad_q) {
     if (report && rem == 0 && part == 0) report_error(p.err, PA_ERR_BAD_SEQ_LEN, seq, L);
     if (bad_q) return w;
@@ -1127,6 +1128,7 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   p.group = group;
   p.tile_tokens = kQTile / group;
   p.inv_group = (65536 + group - 1) / group;
+  p.max_query_len = max_query_len < cap ? max_query_len : static_cast<int>(cap);
   p.lse = lse;
   const Parts parts = chunk_parts(static_cast<long long>(num_seqs) * num_kv_heads, qtiles, cap, head_dim);
   p.parts = parts.parts;

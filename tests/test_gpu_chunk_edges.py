@@ -9,6 +9,7 @@ import test_gpu_sparse as S
 
 pytestmark = pytest.mark.gpu
 
+BAD_SEQ_LEN = 6
 INF = float("inf")
 BF, FH = torch.bfloat16, torch.float16
 
@@ -62,3 +63,18 @@ def test_rows_of_minus_infinity_alone(B, lens, news, dtype, D):
     b["kc"][at[t], 1, row[t]] = INF
     out, lse, _ = E.run_chunk(B, b)
     assert bool(torch.isnan(out[:news[0], 2:]).all()) and bool(torch.isfinite(out[:news[0], :2]).all())
+
+
+@pytest.mark.parametrize("lens,news,most", [([50, 60, 40, 70], [5, 8, 3, 7], 7), ([9000, 40], [3, 2], 2)])
+def test_more_queries_than_the_call_allows(B, lens, news, most):
+    """One query over max_query_len, though a tile would hold it: left out by both calls."""
+    b = E.chunk_batch(7, lens, news, 6, 2, 64, 16, FH)
+    b["most"] = most
+    skip = int(np.argmax(news))
+    out, lse, rec = E.run_chunk(B, b)
+    assert rec == [BAD_SEQ_LEN, 1, skip, lens[skip]]
+    E.check_chunk(b, out, lse, skip=(skip,))
+    lse = E.given_lse(b)
+    before, got, rec = E.run_weights(B, b, lse, 0)
+    assert rec == [BAD_SEQ_LEN, 1, skip, lens[skip]]
+    E.check_chunk_weights(b, lse, before, got, 0, skip=(skip,))
