@@ -684,8 +684,9 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  * it in the chunk, whose weight for it is 0.  A row whose every logit is -infinity is NaN, as in
  * softmax, and its lse -infinity.
  * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x
- * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30.  Otherwise, checks
- * of the batch too, as paged_attn_prefill; max_query_len is not rounded up.
+ * ceil(max_query_len / floor(128 / (num_heads / num_kv_heads))) < 2^30, where max_query_len counts
+ * as at most max_blocks_per_seq * block_size for up to 65535 sequences.  Otherwise, checks of the
+ * batch too, as paged_attn_prefill; max_query_len is not rounded up.
  *
  * paged_attn_chunk_workspace_size is the same for all calls that may use a workspace (few
  * sequences with long tables): 608 x 128 rows of head_dim + 2 floats.

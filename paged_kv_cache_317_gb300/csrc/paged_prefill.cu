@@ -1098,7 +1098,10 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   const unsigned long long cache_rows =
       static_cast<unsigned long long>(num_blocks) * num_kv_heads * block_size;
   const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
-  const long long most = chunk_tiles(max_query_len, group, max_query_len);
+  // max_query_len is a bound: what is launched goes by the tables' tokens at most.  (Only batches that no other call
+  // of a bounded cache takes are held to it as given.)
+  const long long qtiles = chunk_tiles(max_query_len, group, cap);
+  const long long most = num_seqs <= 65535 ? qtiles : chunk_tiles(max_query_len, group, max_query_len);
   // items are numbered in an int inside the kernel (with a grid's worth of headroom)
   if (cache_rows >= (1ull << 31) || cap > (1ll << 30) ||
       static_cast<long long>(num_seqs) * num_kv_heads >= ((1ll << 30) + most - 1) / (most > 0 ? most : 1))
@@ -1109,7 +1112,6 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
       !aligned16(workspace))
     return PA_ERR_INVALID_ARG;
-  const long long qtiles = chunk_tiles(max_query_len, group, cap);
   GroupedParams p{};
   p.seq_order = seq_order;
   p.query_start = query_start;

@@ -78,3 +78,16 @@ def test_more_queries_than_the_call_allows(B, lens, news, most):
     before, got, rec = E.run_weights(B, b, lse, 0)
     assert rec == [BAD_SEQ_LEN, 1, skip, lens[skip]]
     E.check_chunk_weights(b, lse, before, got, 0, skip=(skip,))
+
+
+def test_any_bound_on_queries_for_a_batch(B):
+    """max_query_len is a bound: 64 sequences, 8 key heads and 2^31 - 1 are no more work than 70."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(1, 300, 64)
+    news = np.minimum(lens, rng.integers(0, 70, 64))
+    b = E.chunk_batch(33, lens, news, 24, 8, 64, 16, BF)
+    want, wlse, rec = E.run_chunk(B, b)
+    out, lse, wide = E.run_chunk(B, {**b, "most": 2 ** 31 - 1})
+    assert rec == wide == [0, 0, 0, 0]
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    E.check_chunk(b, out, lse)
