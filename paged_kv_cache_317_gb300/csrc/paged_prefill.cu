@@ -73,7 +73,7 @@ constexpr int kThreads = 224;                     // 4 softmax, K producer, MMA,
 constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr int kPartTiles = 8;                     // an item's keys are shared out by so many tiles
 constexpr int kMaxParts = 32;
-constexpr int kPartSlots = 304;                   // items, parts of items: two thread blocks an SM
+constexpr int kPartSlots = 304;                   // items, parts of items: two thread blocks an SM (D <= 128)
 constexpr int kPartPlaces = 2 * kPartSlots;       // parts in the workspace: smaller ones too, one an item
 constexpr int kSorted = kThreads;                 // sequences that are put in order, grouped
 constexpr int kKStages = 2;                       // K ring depth (= the S buffers: a stage is freed by its S)
@@ -953,16 +953,19 @@ int run_prefill(const ParamsOf<kGrouped>& p, const void* q, const void* k_cache,
 // That an item then has parts at all has to pay for the second kernel and the sums' way to it: 1024 tokens over
 // 13,000 take 197 us so, 193 without, over 16,000 236 and 237, 700 over 8000 102 and 119.  Where lengths are
 // short and only tables long it costs 5 us: items of one part are written by the first kernel.
+// 256 channels have one thread block an SM, half the places (4 tokens, 32 heads on 8, contexts of 2000 / 8000: 80
+// items 44 / 128 us, 57 / 139 in parts for all; 120 49 / 164 and 61 / 182; 48 31 / 79 and 34 / 85).
 struct Parts {
   int parts, share, units, few;
 };
 Parts chunk_parts(long long rows, long long tiles, long long cap, int head_dim) {
   const long long items = rows > kPartSlots ? rows : rows * tiles;
   const long long runs = (cap + kPartTiles * kKTile - 1) / (kPartTiles * kKTile);
-  const long long full = items > 0 ? kPartSlots / items : 0;
-  if (full >= 1 && full < runs && full < kMaxParts && head_dim <= 128) {
-    const int f = static_cast<int>(full), few = static_cast<int>(kPartSlots - full * items);
-    const int share = few > 0 ? static_cast<int>((items + few - 1) / few) : kPartSlots;
+  const int places = kPartSlots / (head_dim <= 128 ? 1 : 2);
+  const long long full = items > 0 ? places / items : 0;
+  if (full >= 1 && full < runs && full < kMaxParts) {
+    const int f = static_cast<int>(full), few = static_cast<int>(places - full * items);
+    const int share = few > 0 ? static_cast<int>((items + few - 1) / few) : places;
     if (f == 1 ? share <= 9 && 2 * runs >= 9 * (share + 1) : share <= 4) return {f + 1, share, f * share + 1, few};
   }
   long long parts = full;

@@ -91,3 +91,19 @@ def test_any_bound_on_queries_for_a_batch(B):
     assert rec == wide == [0, 0, 0, 0]
     assert torch.equal(out, want) and torch.equal(lse, wlse)
     E.check_chunk(b, out, lse)
+
+
+@pytest.mark.parametrize("N,lens,wide,shared", [(50, 700, 100, True), (80, 700, 100, False), (80, 700, 600, True),
+                                                (120, 700, 100, False), (152, 1300, 600, False), (77, 2600, 300, True)])
+def test_parts_of_wide_heads(B, N, lens, wide, shared):
+    """256 channels, one thread block an SM: 50 items are shared out, 80 and more where tables are long, 152 and
+    one a place are not."""
+    rng = np.random.default_rng(N)
+    lens = rng.integers(500, lens, N)
+    b = E.chunk_batch(35, lens, [2] * N, 4, 1, 256, 16, BF, wide=wide)
+    need = B.paged_attn_chunk_workspace_needed(N, 4, 1, 256, 16, b["tables"].shape[1], 2)
+    assert (need > 0) == shared
+    for out_dtype in (torch.float32, BF):
+        out, lse, rec = E.run_chunk(B, b, out_dtype=out_dtype)
+        assert rec == [0, 0, 0, 0]
+        E.check_chunk(b, out, lse)
