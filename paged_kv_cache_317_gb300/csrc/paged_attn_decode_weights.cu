@@ -75,12 +75,6 @@ __device__ __forceinline__ int length_of(const DecodeWeightsParams& p, int seq, 
   return L;
 }
 
-// 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
-__device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
-  if (M == -INFINITY) return tokens ? NAN : 0.f;
-  return 1.f / l;
-}
-
 // The rings, or the joined sums, which take their place.
 template <int D, int NT>
 constexpr size_t ring_bytes() {

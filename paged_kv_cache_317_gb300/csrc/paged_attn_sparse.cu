@@ -9,11 +9,9 @@
 //    chunk (a 3-D TMA box of 16 rows x D channels in 128-byte swizzled columns) into the
 //    warp's ring of stages, and the warp waits on the stage's barrier.  No warp waits for
 //    another before the end.
-//  * Per chunk, on mma.sync m16n8k16 with the 16 tokens as the rows and the query heads as
-//    the columns: S^T = K.Q^T in fp32, the running maximum and sum of each column in log2
-//    units, O^T += V^T.P^T with P as a high and a low half-precision number (off by at most 2^-17
-//    of a weight in bf16, 2^-23 in fp16; with one number it would be 2^-8, 2^-11).  Up to 8 query
-//    heads cost one product, up to 16 two; K and V are read once for all of them.
+//  * Per chunk the products and the softmax of warp_attn.cuh, tokens as the rows and query heads as
+//    the columns.  Up to 8 query heads cost one product, up to 16 two; K and V are read once for all
+//    of them.
 //  * At the end the warps' (m, l, O) are joined in shared memory, and those of the cluster's
 //    blocks over distributed shared memory, in a fixed order: the same bits on every run.  Only
 //    where a few rows have long lists are a row's chunks spread over several clusters, whose sums
@@ -31,8 +29,8 @@
 
 #include "cluster.cuh"
 #include "common.cuh"
-#include "mma.cuh"
 #include "tma.cuh"
+#include "warp_attn.cuh"
 
 namespace pagedkv {
 namespace {
@@ -64,15 +62,6 @@ struct SparseParams {
   float qscale;         // scale * log2(e)
 };
 
-// Partials of a column: m = running maximum (NaN once a logit was), l = sum of the weights;
-// m = -infinity with l = 0 (no token) or l = -1 (tokens, every logit -infinity), which have
-// no weight in a join.
-// 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
-__device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
-  if (M == -INFINITY) return tokens ? NAN : 0.f;
-  return 1.f / l;
-}
-
 template <int D>
 struct Geo {
   static constexpr int kTileBytes = kChunk * D * 2;  // one chunk of K or V
@@ -84,11 +73,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     paged_attn_sparse_kernel(const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v, const SparseParams p) {
   using Gm = Geo<D>;
-  using T = typename Tag::T;
+  using Attn = WarpAttn<Tag, D, NT>;
   constexpr int kCols = 8 * NT;
-  // Weights are kept as 2^(s - m + kLift), sums and products alike: fp16 has no numbers below
-  // 2^-24, and a long list's many small weights would be lost next to one of 1.
-  constexpr float kLift = std::is_same<Tag, F16>::value ? 12.f : 0.f;
   if (threadIdx.x == 0) {  // arguments, not memory of the kernel before
     prefetch_tensor_map(&tm_k);
     prefetch_tensor_map(&tm_v);
@@ -221,40 +207,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   int issued = 0, done = 0;
   while (issued < S && issue(issued)) ++issued;
 
-  // -------------------------------------------------------------- the queries
-  // Q^T as B fragments: column g of an 8-column tile is query head g of the tile.
-  const int g = lane >> 2, tq = lane & 3;
-  uint32_t qf[NT][D / 16][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const bool have = t * 8 + g < cols;
-    const T* src = static_cast<const T*>(p.q) + (q0 + (have ? t * 8 + g : 0)) * D + 2 * tq;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      qf[t][kk][0] = have ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
-      qf[t][kk][1] = have ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
-    }
-  }
-  float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int dd = 0; dd < D / 16; ++dd) o[t][dd][0] = o[t][dd][1] = o[t][dd][2] = o[t][dd][3] = 0.f;
-    m[t][0] = m[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.f;
-  }
-
-  // ldmatrix rows of this lane.  A tile is [D / 64 column groups][16 rows][128 bytes], with
-  // 8-token blocks two of [D / 64][8][128]; token t's 16-byte piece c of a column group sits
-  // at c ^ (t & 7).  K (A operand): matrices (tokens 0-7, d + 0..7), (8-15, d + 0..7), (0-7,
-  // d + 8..15), (8-15, d + 8..15).  V (A operand of V^T, transposed): (tokens 0-7, d + 0..7),
-  // (0-7, d + 8..15), (8-15, d + 0..7), (8-15, d + 8..15).
-  const int mi = lane >> 3, r8 = lane & 7;
-  const uint32_t group_bytes = small ? 1024u : 2048u;
-  const uint32_t half_bytes = small ? Gm::kTileBytes / 2 : 1024u;
-  const uint32_t k_row = (mi & 1) * half_bytes + r8 * 128, v_row = (mi >> 1) * half_bytes + r8 * 128;
-  const int k_half = mi >> 1, v_half = mi & 1;
+  Attn at;
+  at.init(static_cast<const typename Tag::T*>(p.q) + q0 * D, cols, small, lane);
   const uint32_t ring_addr = smem_addr(ring);
 
   bool aborted = false;
@@ -269,84 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int rlo = rows & 255, rhi = rows >> 8;
     const uint32_t kt = ring_addr + s * 2 * Gm::kTileBytes, vt = kt + Gm::kTileBytes;
 
-    float sc[NT][4];  // (token g, column 2 tq), (g, 2 tq + 1), (g + 8, ...)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t a[4];
-      const int c = ((kk & 3) << 1) | k_half;
-      ldsm_x4(kt + (kk >> 2) * group_bytes + k_row + ((c ^ r8) << 4), a);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) mma(sc[t], a, qf[t][kk][0], qf[t][kk][1], Tag{});
-    }
-    const bool partial = rlo + rhi < kChunk;
-    uint32_t bh[NT][2], bl[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[t][e] *= p.qscale;
-      if (partial) {
-        if (g >= rlo) sc[t][0] = sc[t][1] = -INFINITY;
-        if (g >= rhi) sc[t][2] = sc[t][3] = -INFINITY;
-      }
-      float c0 = max_nan(sc[t][0], sc[t][2]), c1 = max_nan(sc[t][1], sc[t][3]);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        c0 = max_nan(c0, __shfl_xor_sync(kFullMask, c0, off));
-        c1 = max_nan(c1, __shfl_xor_sync(kFullMask, c1, off));
-      }
-      const float n0 = max_nan(m[t][0], c0), n1 = max_nan(m[t][1], c1);
-      // all -infinity so far: any finite base gives them the weight 0
-      const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-      const float a0 = exp2f(m[t][0] - b0), a1 = exp2f(m[t][1] - b1);
-      const float s0 = kLift - b0, s1 = kLift - b1;
-      const float p0 = exp2f(sc[t][0] + s0), p1 = exp2f(sc[t][1] + s1);
-      const float p2 = exp2f(sc[t][2] + s0), p3 = exp2f(sc[t][3] + s1);
-      l[t][0] = fmaf(l[t][0], a0, p0 + p2);
-      l[t][1] = fmaf(l[t][1], a1, p1 + p3);
-      if (__any_sync(kFullMask, a0 != 1.f || a1 != 1.f)) {
-#pragma unroll
-        for (int dd = 0; dd < D / 16; ++dd) {
-          o[t][dd][0] *= a0;
-          o[t][dd][1] *= a1;
-          o[t][dd][2] *= a0;
-          o[t][dd][3] *= a1;
-        }
-      }
-      m[t][0] = n0;
-      m[t][1] = n1;
-      uint32_t hi_a, lo_a, hi_b, lo_b;
-      split2(p0, p1, hi_a, lo_a, Tag{});
-      split2(p2, p3, hi_b, lo_b, Tag{});
-      bh[t][0] = movmatrix_trans(hi_a);
-      bh[t][1] = movmatrix_trans(hi_b);
-      bl[t][0] = movmatrix_trans(lo_a);
-      bl[t][1] = movmatrix_trans(lo_b);
-    }
-    // rows without a token may hold anything, NaN too: 0 in the product
-    uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (partial) {
-      keep_lo = (2 * tq < rlo ? 0xffffu : 0u) | (2 * tq + 1 < rlo ? 0xffff0000u : 0u);
-      keep_hi = (2 * tq < rhi ? 0xffffu : 0u) | (2 * tq + 1 < rhi ? 0xffff0000u : 0u);
-    }
-#pragma unroll
-    for (int dd = 0; dd < D / 16; ++dd) {
-      uint32_t a[4];
-      const int c = ((dd & 3) << 1) | v_half;
-      ldsm_x4_trans(vt + (dd >> 2) * group_bytes + v_row + ((c ^ r8) << 4), a);
-      if (partial) {
-        a[0] &= keep_lo;
-        a[1] &= keep_lo;
-        a[2] &= keep_hi;
-        a[3] &= keep_hi;
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mma(o[t][dd], a, bh[t][0], bh[t][1], Tag{});
-        mma(o[t][dd], a, bl[t][0], bl[t][1], Tag{});
-      }
-    }
+    at.step(kt, vt, rlo, rhi, p.qscale, lane, [](int, const float (&)[4]) {});
     __syncwarp();  // the stage is read
     ++done;
     if (issue(s)) ++issued;
@@ -361,24 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   __syncthreads();
   float* jo = reinterpret_cast<float*>(ring0);
   float2* jml = reinterpret_cast<float2*>(jo + kWarps * kCols * Gm::kPitch);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float sum = l[t][e];
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
-      const int col = t * 8 + 2 * tq + e;
-      if (m[t][e] == -INFINITY && done > 0) sum = -1.f;  // tokens, but no weight
-      if (g == 0) jml[warp * kCols + col] = make_float2(m[t][e], sum);
-      float* dst = jo + (warp * kCols + col) * Gm::kPitch + g;
-#pragma unroll
-      for (int dd = 0; dd < D / 16; ++dd) {
-        dst[dd * 16] = o[t][dd][e];
-        dst[dd * 16 + 8] = o[t][dd][2 + e];
-      }
-    }
-  }
+  at.put(jo + warp * kCols * Gm::kPitch, Gm::kPitch, jml + warp * kCols, done > 0, lane);
   __syncthreads();
   // Column col, channels d .. d + 3 of the first n of up to kMost partials; their loads do not
   // wait for one another.

@@ -1,7 +1,7 @@
 // One warp's attention over chunks of 16 cached tokens, on mma.sync m16n8k16 with the tokens as the
 // rows and 8 NT query heads as the columns: S^T = K.Q^T in fp32, the running maximum and sum of each
 // column in log2 units, O^T += V^T.P^T with P as a high and a low half-precision number (off by at
-// most 2^-17 of a weight in bf16, 2^-23 in fp16).
+// most 2^-17 of a weight in bf16, 2^-23 in fp16; with one number it would be 2^-8, 2^-11).
 #pragma once
 
 #include <type_traits>
@@ -10,6 +10,12 @@
 #include "mma.cuh"
 
 namespace pagedkv {
+
+// 1 / l of a joined column; NaN where every logit was -infinity, 0 where there was no token.
+__device__ __forceinline__ float inverse_of(float M, float l, bool tokens) {
+  if (M == -INFINITY) return tokens ? NAN : 0.f;
+  return 1.f / l;
+}
 
 // A chunk of K or V in shared memory, as TMA leaves it: [D / 64 column groups][16 rows][128 bytes],
 // from 8-token blocks two of [D / 64][8][128]; token t's 16-byte piece c of a column group sits at
