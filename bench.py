@@ -49,6 +49,7 @@ METRIC = "paged-attn decode KV GB/s (% of HBM peak), seq-tokens/s at 13B shape"
 UNIT = "GB/s"
 FALLBACK_HBM_GBS = 6800.0
 PREFILL_SOURCES = ("paged_kv_cache_317_gb300/csrc/paged_prefill.cu",
+                   "paged_kv_cache_317_gb300/csrc/tcgen05.cuh",
                    "paged_kv_cache_317_gb300/csrc/tma.cuh",
                    "paged_kv_cache_317_gb300/csrc/common.cuh")
 DECODE_SOURCES = ("paged_kv_cache_317_gb300/csrc/decode_partition.cuh",
