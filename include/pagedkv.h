@@ -677,10 +677,9 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  *   workspace     device, 16-byte aligned, scratch of this call alone, at least
  *                 paged_attn_chunk_workspace_size(...) bytes; may be NULL where
  *                 paged_attn_chunk_workspace_needed(...) is 0
- * Arithmetic as in paged_attn_prefill where `out` is fp32.  For a half-precision `out` the
- * probabilities enter P.V as one number of the cache's type: off by at most 2^-8 (bf16) or
- * 2^-11 (fp16) of a weight, which is what the output's own rounding may be off by (fp16: and
- * by 2^-32 of the row's largest weight).  A NaN or infinity in V of a token may reach rows before
+ * Arithmetic as in paged_attn_prefill, but for fp16 caches with a half-precision `out`: their
+ * probabilities enter P.V as one fp16 number, off by at most 2^-11 of a weight and 2^-32 of the
+ * row's largest.  A NaN or infinity in V of a token may reach rows before
  * it in the chunk, whose weight for it is 0.  A row whose every logit is -infinity is NaN, as in
  * softmax, and its lse -infinity.
  * num_blocks * num_kv_heads * block_size must be < 2^31, num_seqs x num_kv_heads x

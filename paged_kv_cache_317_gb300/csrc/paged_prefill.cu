@@ -47,10 +47,12 @@
 //    each store instruction writes whole 64-byte row segments.
 //  * Grouped (query heads sharing key heads): a tile's rows are (token, query head of a key head), as many
 //    whole tokens as 128 rows hold, so that a few drafted tokens fill a tile with all heads' rows and K and
-//    V are read once for them.  Half-precision outputs take P as one number, rounded to nearest: its error
-//    is the output's own rounding (16 chunks of 512 rows, 40 heads on 8, contexts of up to 2048: 245 us with
-//    two numbers, 193 us with one, 960 TFLOP/s).  Where there are fewer items than places, an item's keys are
-//    shared out over several blocks, whose O and sums a second kernel joins (3 tokens over 30,000: 35 us).
+//    V are read once for them.  From fp16 caches half-precision outputs take P as one number, rounded to
+//    nearest: off by 2^-11 of a weight at most, which the 2e-3 bound allows (1024 tokens over 30,000, 32 heads
+//    on 8: 412 us, 496 with two numbers).  bf16 keeps two: with one, 2^-8, outputs of N(0, 1) values were up to
+//    1.3 times the bound off (16 chunks of 512 rows, 40 heads on 8: 193 us with one, 244 with two).  Where there
+//    are fewer items than places, an item's keys are shared out over several blocks, whose O and sums a second
+//    kernel joins (3 tokens over 30,000: 35 us).
 //  * Every mbarrier wait is bounded (one second); on a timeout the block
 //    records PA_ERR_TIMEOUT, waits (bounded) for its copies and MMAs, frees its
 //    TMEM and returns.  Nothing traps.
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
   const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
   // Grouped, without an order from the caller: more items than blocks are dealt out the longest sequence
-  // first (40 sequences of 50 to 3641 tokens with 6 drafted, 32 heads on 8: 68 us, 86 as they come).
+  // first (40 sequences of 50 to 3641 tokens with 6 drafted, 32 heads on 8: 70 us, 104 as they come).
   const int* order = nullptr;
   if constexpr (kGrouped) {
     if (p.seq_order == nullptr && num_seqs <= kSorted && n_items > static_cast<int>(gridDim.x)) {
@@ -625,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
           const float e1 = ex2_approx(x1);
           add2(sum4[c & 2], sum4[(c & 2) + 1], e0, e1);
           if constexpr (kOne) {
-            hi_f[c / 2] = __uint_as_float(pack_half2<BF16>(e0, e1));
+            static_assert(!BF16, "one bf16 number a probability is too few");
+            hi_f[c / 2] = __uint_as_float(pack_half2<false>(e0, e1));
           } else if constexpr (BF16) {
             // hi = the upper 16 bits of each fp32 p (a bf16 truncation), one byte
             // permute for the pair; lo = RN(p - hi), where p - hi is exact in fp32
@@ -936,13 +939,16 @@ int run_prefill(const ParamsOf<kGrouped>& p, const void* q, const void* k_cache,
       !encode_tensor_map(&tk, bf16, k_cache, 2, cdims, cstr, cbox) ||
       !encode_tensor_map(&tv, bf16, v_cache, 2, cdims, cstr, cbox))
     return PA_ERR_CUDA;
-  switch ((bf16 ? 1 : 0) | (head_dim == 64 ? 0 : head_dim == 128 ? 2 : 4)) {
-    case 0: return launch_prefill<false, 64, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 1: return launch_prefill<true, 64, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 2: return launch_prefill<false, 128, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 3: return launch_prefill<true, 128, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    case 4: return launch_prefill<false, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
-    default: return launch_prefill<true, 256, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+  const auto sized = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if constexpr (!kOne)
+      if (bf16) return launch_prefill<true, D, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+    return launch_prefill<false, D, kGrouped, kOne>(tq, tk, tv, p, num_seqs, num_qtiles, st);
+  };
+  switch (head_dim) {
+    case 64: return sized(std::integral_constant<int, 64>{});
+    case 128: return sized(std::integral_constant<int, 128>{});
+    default: return sized(std::integral_constant<int, 256>{});
   }
 }
 
@@ -1145,7 +1151,8 @@ extern "C" int paged_attn_chunk(const void* q, const int32_t* query_start, int t
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(kPartPlaces) * kQTile * head_dim);
   }
-  const auto run = out_dtype == PA_F32 ? run_prefill<true, false> : run_prefill<true, true>;
+  const bool one = dtype == PA_F16 && out_dtype != PA_F32;
+  const auto run = one ? run_prefill<true, true> : run_prefill<true, false>;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int tiles = static_cast<int>(qtiles);
   const int status = run(p, q, k_cache, v_cache, cache_rows, num_seqs, head_dim, tiles, dtype == PA_BF16, st);

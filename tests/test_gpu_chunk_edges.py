@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import test_gpu_evict as E
-import test_gpu_sparse as S
+from gpu_util import assert_matches_oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,27 @@ def test_parts_of_wide_heads(B, N, lens, wide, shared):
         out, lse, rec = E.run_chunk(B, b, out_dtype=out_dtype)
         assert rec == [0, 0, 0, 0]
         E.check_chunk(b, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("lens,news,Hq,H,D", [([300, 200], [300, 200], 8, 8, 128), ([300, 200], [300, 200], 8, 2, 128),
+                                              ([2000], [64], 8, 2, 128), ([400], [400], 4, 4, 64),
+                                              ([300], [300], 4, 1, 256), ([9000, 5000], [3, 4], 4, 1, 128)])
+def test_half_precision_outputs_keep_the_librarys_bound(B, lens, news, Hq, H, D, dtype):
+    """2e-3 and half a step of the output's type at the oracle's value, as everywhere; and with a head of its own
+    each, a bf16 cache and keys that are not shared out, the bits of the dense prefill."""
+    b = E.chunk_batch(3, lens, news, Hq, H, D, 16, dtype)
+    q, kc = E.f64(b["q"]), E.f64(b["kc"])
+    out, _, rec = E.run_chunk(B, b, out_dtype=dtype)
+    assert rec == [0, 0, 0, 0]
+    for i, length in enumerate(lens):
+        a, e = int(b["start"][i]), int(b["start"][i + 1])
+        places = length - (e - a) + np.arange(e - a)
+        w, _, _ = E.OE.softmax_rows(q[a:e], kc, b["tables"][i], length, places, b["scale"])
+        want, _, _ = E.OE.weighted(w, E.f64(b["vc"]), b["tables"][i], length)
+        assert_matches_oracle(out[a:e], want, f"sequence {i}")
+    if Hq == H and dtype is BF:
+        dense = torch.full_like(out, 7)
+        B.paged_attn_prefill(b["q"], E.dev(b["start"]), b["most"], b["kc"], b["vc"], E.dev(b["tables"]),
+                             E.dev(b["lens"]), b["scale"], out=dense)
+        assert torch.equal(out, dense)
