@@ -658,6 +658,7 @@ int paged_attn_sparse(const void* q, const void* k_cache, const void* v_cache,
  * attention weight that the token at place t of sequence i has had from the query heads
  * of key head h; paged_block_select over them (block_size 1) lists the places to keep,
  * and kv_cache_evict moves those to the front.  Query heads may share key heads as above.
+ * (paged_block_select takes tables of up to 131072 places, the calls below of up to 2^30.)
  * Keys carry their rotation in the cache, so places may be renumbered freely; new tokens
  * keep the positions that they would have had (kv_cache_append_rope's `positions`).
  *   weights       device float [num_seqs][num_kv_heads][weights_tokens], weights_tokens >=
@@ -735,7 +736,8 @@ int paged_chunk_weights(const void* q, const float* lse, const int32_t* query_st
  *
  * paged_attn_decode_weights_workspace_size never falls as num_seqs, max_blocks_per_seq or
  * block_size grow, the others alike: a buffer sized for the largest call serves every smaller
- * one.  paged_attn_decode_weights_workspace_needed is that size where a call of exactly these
+ * one.  It goes by the tables' width, not by the lengths: about 4 bytes for each sequence, query
+ * head and place.  paged_attn_decode_weights_workspace_needed is that size where a call of exactly these
  * sizes uses a workspace, and 0 where it neither touches one nor looks at its size. */
 size_t paged_attn_decode_weights_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                                 int head_dim, int block_size,

@@ -1018,8 +1018,8 @@ def paged_attn_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     """Decode attention, query heads sharing key heads, that adds to weights float32 [N,H,places] the
     softmax weight of every cached token, summed over the query heads of its key head.  q [N,Hq,D];
     caches [B,H,bs,D], Hq a multiple of H; block_tables int32 [N,MB]; seq_lens int32 [N]; workspace:
-    optional contiguous tensor of at least paged_attn_decode_weights_workspace_size(...) bytes, made
-    here if it is needed and not given."""
+    optional contiguous tensor of at least paged_attn_decode_weights_workspace_size(...) bytes (about 4
+    N Hq MB bs, whatever the lengths), made here if it is needed and not given."""
     device, i32 = torch.cuda.current_device(), torch.int32
     (B, H, bs, D), dtype = _half("k_cache", k_cache, 4)
     N, MB = block_tables.shape

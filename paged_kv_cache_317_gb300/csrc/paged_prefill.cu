@@ -48,11 +48,11 @@
 //  * Grouped (query heads sharing key heads): a tile's rows are (token, query head of a key head), as many
 //    whole tokens as 128 rows hold, so that a few drafted tokens fill a tile with all heads' rows and K and
 //    V are read once for them.  From fp16 caches half-precision outputs take P as one number, rounded to
-//    nearest: off by 2^-11 of a weight at most, which the 2e-3 bound allows (1024 tokens over 30,000, 32 heads
-//    on 8: 412 us, 496 with two numbers).  bf16 keeps two: with one, 2^-8, outputs of N(0, 1) values were up to
-//    1.3 times the bound off (16 chunks of 512 rows, 40 heads on 8: 193 us with one, 244 with two).  Where there
-//    are fewer items than places, an item's keys are shared out over several blocks, whose O and sums a second
-//    kernel joins (3 tokens over 30,000: 35 us).
+//    nearest: off by 2^-11 of a weight at most, which the 2e-3 bound allows for values of up to 4 (1024 tokens
+//    over 30,000, 32 heads on 8: 412 us, 496 with two numbers).  bf16 keeps two: with one, 2^-8, outputs of
+//    N(0, 1) values were up to 1.3 times the bound off (16 chunks of 512 rows, 40 heads on 8: 193 us with one, 244
+//    with two).  Where there are fewer items than places, an item's keys are shared out over several blocks,
+//    whose O and sums a second kernel joins (3 tokens over 30,000: 45 us).
 //  * Every mbarrier wait is bounded (one second); on a timeout the block
 //    records PA_ERR_TIMEOUT, waits (bounded) for its copies and MMAs, frees its
 //    TMEM and returns.  Nothing traps.
@@ -269,8 +269,8 @@ __device__ __forceinline__ Tile decode_tile(const ParamsOf<kGrouped>& p, const i
 // (Dealing every other round in reverse, to even out long and short items per
 // block, measured 2 % slower: the two blocks sharing an SM already even out.)
 // Grouped, every other round is dealt in reverse: sequences of drafted tokens, of one tile each, are of
-// unequal lengths (64 of 64 to 2048 tokens, 32 heads on 8: 52 us, 61 without; 2 of 2529 and 15337, 1354 rows:
-// 227 and 304; the chunks of prompts above: 193 and 190).
+// unequal lengths (64 of 64 to 2048 tokens, 32 heads on 8: 56 us, 65 without; 2 of 2529 and 15337, 1354 rows,
+// 16 heads on 4: 275 and 356; the chunks of prompts above: 244 and 243).
 template <bool kGrouped>
 __device__ __forceinline__ int item_of(const ParamsOf<kGrouped>& p, int r) {
   if (kGrouped && p.few > 0) {  // a part of the full size, or smaller ones in turn
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
   const int kv_heads = kGrouped ? p.num_kv_heads : p.num_heads;
   const int n_items = num_seqs * kv_heads * num_qtiles * (kGrouped ? p.parts : 1);
   // Grouped, without an order from the caller: more items than blocks are dealt out the longest sequence
-  // first (40 sequences of 50 to 3641 tokens with 6 drafted, 32 heads on 8: 70 us, 104 as they come).
+  // first (40 sequences of 50 to 3641 tokens with 6 drafted, 32 heads on 8: 73 us, 113 as they come).
   const int* order = nullptr;
   if constexpr (kGrouped) {
     if (p.seq_order == nullptr && num_seqs <= kSorted && n_items > static_cast<int>(gridDim.x)) {
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D>::kMinBlocks)
       const bool row_valid = r < w.rows;
       const int token = kGrouped ? r * p.inv_group >> 16 : r;  // of the tile
       // (grouped, rows that only fill the tile up are not masked, so that their warp need not mask every tile:
-      // 16 chunks of 512 rows, 40 heads on 8: 205 us, 210 with it)
+      // 16 chunks of 512 rows, 40 heads on 8: 244 us, 261 with it)
       const int pos = row_valid ? w.pos0 + token : kGrouped ? 0x7fffffff : -1;
       float m_ref = -INFINITY, l = 0.f;  // reference max (log2 units) and running sum
       const int j0 = kGrouped ? w.j0 : 0;
@@ -955,10 +955,11 @@ int run_prefill(const ParamsOf<kGrouped>& p, const void* q, const void* k_cache,
 // The parts that an item's keys are shared out into, for so many (sequence, key head) and tiles of each: as
 // many as fill the card, where there are few items and tables are long.
 // The places left over take a smaller last part of each item, `share` of which make one of the others
-// (1024 tokens over 30,000, 32 heads on 8, 256 items: 411 us, 440 without; 700 of 64 channels: 264 and 361).
-// That an item then has parts at all has to pay for the second kernel and the sums' way to it: 1024 tokens over
-// 13,000 take 197 us so, 193 without, over 16,000 236 and 237, 700 over 8000 102 and 119.  Where lengths are
-// short and only tables long it costs 5 us: items of one part are written by the first kernel.
+// (1024 tokens over 30,000, 32 heads on 8, 256 items: fp16 412 us, 442 without, bf16 517 and 556; 700 of 64
+// channels: 264 and 365, 351 and 494).  That an item then has parts at all has to pay for the second kernel and
+// the sums' way to it: 1024 tokens over 13,000 take 200 us so, 193 without, over 16,000 237 and 238 (bf16: 244 and
+// 241, 288 and 295), 700 over 8000 105 and 120.  Where lengths are short and only tables long it costs 5 us: items
+// of one part are written by the first kernel.
 // 256 channels have one thread block an SM, half the places (4 tokens, 32 heads on 8, contexts of 2000 / 8000: 80
 // items 44 / 128 us, 57 / 139 in parts for all; 120 49 / 164 and 61 / 182; 48 31 / 79 and 34 / 85).
 struct Parts {
