@@ -756,19 +756,20 @@ int paged_attn_decode_weights(const void* q, const void* k_cache, const void* v_
 /* For every sequence i, key head h and place j < min(num_kept, L): place j takes the row of K,
  * of V and the weight that place s = kept[i][h][j] held before the call.  Places below L without
  * an entry (kept[i][h][j] = -1, or j >= num_kept) keep their rows, those below min(num_kept, L) in
- * their new blocks too, and get the weight 0.  With ascending places, then -1, the sequence is
- * afterwards min(num_kept, L) tokens long.
+ * their new blocks too, where they have one, and get the weight 0.  With ascending places, then -1,
+ * the sequence is afterwards min(num_kept, L) tokens long.
  *   kept          device int32 [num_seqs][num_kv_heads][num_kept]: -1, or j <= s < L, as any
  *                 ascending list has it.  Another entry is recorded as PA_ERR_BAD_POSITION (index =
  *                 i * num_kv_heads + h, value = s), and place j keeps its row and weight.  L is the
  *                 length before the call.
  *   new_tables    NULL: in place; or device int32 [num_seqs][new_max_blocks], the blocks of the
  *                 new places.  Each entry is the sequence's own block of those places, or a block
- *                 that no sequence of the call reads (pa_batch_evict sees to it).  A sequence with
- *                 L <= num_kept loses no tokens, and pa_batch_evict leaves it its blocks, shared
- *                 ones too: an entry other than j is recorded as PA_ERR_BAD_POSITION there, in
- *                 blocks that stay.  In place, the blocks of the new places must be private to
- *                 their sequence.
+ *                 that no sequence of the call reads (pa_batch_evict sees to it); -1 past its end.
+ *                 A sequence with L <= num_kept and a block for place L - 1 loses no tokens, and
+ *                 pa_batch_evict leaves it its blocks, shared ones too: an entry other than j is
+ *                 recorded as PA_ERR_BAD_POSITION there, in blocks that stay.  (Sequences cut to
+ *                 different lengths: lists padded with -1, or a call for each num_kept.)  In place,
+ *                 the blocks of the new places must be private to their sequence.
  *   weights       may be NULL
  *   head_dim      a multiple of 8, at most 1024;  block_size: any
  * A block number out of range is recorded as PA_ERR_BAD_BLOCK (index = i) and the row is left out,

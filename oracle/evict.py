@@ -71,6 +71,8 @@ def evict(k_cache, v_cache, tables, seq_lens, kept, weights=None, new_tables=Non
             for j in range(min(int(length), kept.shape[2])):
                 entry = int(kept[i, h, j])
                 s = j if entry < 0 else entry
+                if entry < 0 and (j // bs >= len(to[i]) or to[i][j // bs] < 0):
+                    continue                            # a place that the sequence does not keep
                 a, b = int(tables[i][s // bs]), int(to[i][j // bs])
                 k_cache[b, h, j % bs] = old_k[a, h, s % bs]
                 v_cache[b, h, j % bs] = old_v[a, h, s % bs]

@@ -71,7 +71,12 @@ __global__ void __launch_bounds__(R::kThreads, R::kBlocks) kv_cache_evict_kernel
   float* weights = p.weights == nullptr || is_v ? nullptr : p.weights + sh * p.weights_row;
   uint4* cache = is_v ? p.v : p.k;
   const int places = min(p.num_kept, L);
-  const bool renewed = p.new_tables != p.tables, uncut = renewed && L <= p.num_kept;
+  // whether place j has a block in other tables than its own: one that does not leaves the sequence
+  auto renewed = [&](int j) -> bool {
+    const int b = j / p.block_size;
+    return p.new_tables != p.tables && b < p.new_max_blocks && new_table[b] != -1;
+  };
+  const bool uncut = L > 0 && L <= p.num_kept && renewed(L - 1);
 
   // the row of place j
   auto row_of = [&](const int32_t* t, int blocks, int j) -> long long {
@@ -95,8 +100,8 @@ __global__ void __launch_bounds__(R::kThreads, R::kBlocks) kv_cache_evict_kernel
         const int s = kept[j], b = j / p.block_size;
         bool moves = s >= j && s < L;
         // (a sequence that loses no tokens keeps its table, whose blocks a fork may read: its rows stay)
-        if (uncut && s != j && b < p.max_blocks && b < p.new_max_blocks && table[b] == new_table[b]) moves = false;
-        if (moves || renewed) {
+        if (uncut && s != j && table[b] == new_table[b]) moves = false;
+        if (moves || renewed(j)) {
           src = row_of(table, p.max_blocks, moves ? s : j);
           dst = row_of(new_table, p.new_max_blocks, j);
         }

@@ -89,6 +89,35 @@ def test_random_lists_into_blocks_of_their_own(B, seed):
     E.check_evict(B, b, kept, new_tables=new, weights=bool(seed % 4))
 
 
+@pytest.mark.parametrize("bs", [1, 8, 16])
+def test_sequences_cut_to_lengths_of_their_own(B, bs):
+    """Lists of one width, padded with -1: the places behind a sequence's new end have no block, and no need of
+    one, though the sequence had fewer tokens than the list has room for."""
+    blocks = 800 // bs
+    alloc = B.BlockAllocator(blocks, bs, np.random.default_rng(0).permutation(blocks))
+    lens, keeps = [100, 50, 70, 90], [64, 20, 70, 33]
+    for i, n in enumerate(lens[:3]):
+        alloc.add(i, n)
+    alloc.fork(0, 3)
+    alloc.free(3)
+    alloc.add(3, lens[3])
+    alloc.fork(2, 4)                                    # of which 2 keeps all it has
+    alloc.fork(1, 5)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randn((blocks, 2, bs, 64), generator=gen, device="cuda").half() for _ in range(2))
+    width = 110 // bs + 1
+    tables, held = alloc.batch_block_tables(range(4), width)
+    for i, keep in enumerate(keeps):
+        alloc.batch_evict([i], keep)
+    new, after = alloc.batch_block_tables(range(4), width)
+    assert held.tolist() == lens and after.tolist() == keeps and np.array_equal(new[2], tables[2])
+    rng = np.random.default_rng(bs)
+    kept = np.full((4, 2, 80), -1, np.int32)
+    for i, keep in enumerate(keeps):
+        kept[i, :, :keep] = E.pick(rng, lens[i:i + 1], 2, keep)[0]
+    E.check_evict(B, dict(kc=kc, vc=vc, tables=tables, lens=held, bs=bs, H=2), kept, new_tables=new)
+
+
 def left_out(B, tables, kept, new=None, bad=10 ** 6):
     """A call with a block out of range, and what is to come of it: rows and weights that it leaves out are
     as they were."""
