@@ -960,8 +960,8 @@ int run_prefill(const ParamsOf<kGrouped>& p, const void* q, const void* k_cache,
 // the sums' way to it: 1024 tokens over 13,000 take 200 us so, 193 without, over 16,000 237 and 238 (bf16: 244 and
 // 241, 288 and 295), 700 over 8000 105 and 120.  Where lengths are short and only tables long it costs 5 us: items
 // of one part are written by the first kernel.
-// 256 channels have one thread block an SM, half the places (4 tokens, 32 heads on 8, contexts of 2000 / 8000: 80
-// items 44 / 128 us, 57 / 139 in parts for all; 120 49 / 164 and 61 / 182; 48 31 / 79 and 34 / 85).
+// 256 channels have one thread block an SM, half the places (4 fp16 tokens, 32 heads on 8, contexts of 2000 / 8000:
+// 80 items 44 / 127 us, 57 / 138 in parts for 304; 120 49 / 162 and 61 / 179; 48 31 / 78 and 35 / 85).
 struct Parts {
   int parts, share, units, few;
 };
